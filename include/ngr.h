@@ -231,6 +231,61 @@ int ngr_fused_linear_residual_norm(int norm, const void *x, const void *W,
                                    int dtype, void *h, void *y, void *workspace,
                                    size_t workspace_bytes, ngr_stream_t stream);
 
+/* The join of a transformer block to its residual stream, in one pass:
+ *   n = norm1(x)                                         (norm after the block)
+ *   h = residual_scale residual + block_scale gate n     (gate, residual scale)
+ *   y = norm2(h)                                         (norm before the next block)
+ * x, residual, h, y are [M, N].  norm1, norm2: ngr_norm values, each with
+ * gamma (and beta for LayerNorm) of length N and its eps; with NGR_NORM_NONE
+ * n = x, and no y is made (y may be NULL).  residual may be NULL (taken as
+ * zero).  gate may be NULL (1), else it is [G, N] with G = ceil(M /
+ * rows_per_gate) and row i uses gate row i / rows_per_gate: rows_per_gate >= M
+ * gives one gate for all tokens (a channel scale), the tokens per sample one
+ * for each sample of a batch, 1 a full gate.  stats, when not NULL, receives
+ * FP32 [M, 4] = (mean1, rstd1, mean2, rstd2) for the backward call (0 and 1
+ * where a norm has none); it is 16-byte aligned.  Statistics and all
+ * arithmetic are FP32; h and y are rounded once, y from the unrounded h.
+ * Any N up to 65536; pointers need 2-byte alignment (16-byte aligned ones
+ * with N % 8 == 0 take the vectorized kernel).  h or y may be the memory of
+ * x or residual.  Needs no workspace. */
+int ngr_fused_norm_gate_residual_norm(int norm1, int norm2, const void *x,
+                                      const void *residual, const void *gate,
+                                      int64_t rows_per_gate,
+                                      const void *gamma1, const void *beta1,
+                                      const void *gamma2, const void *beta2,
+                                      float eps1, float eps2,
+                                      float residual_scale, float block_scale,
+                                      int64_t M, int64_t N, int dtype, void *h,
+                                      void *y, float *stats,
+                                      ngr_stream_t stream);
+
+/* The gradient of ngr_fused_norm_gate_residual_norm: from dy [M, N] (the
+ * gradient of y) and dh [M, N] (of h; either may be NULL for zero, dh not
+ * without norm2), the forward's inputs (beta2 has no part) and its stats, it
+ * writes
+ *   dx, dresidual [M, N], dgate [G, N] (summed over each gate row's tokens),
+ *   dgamma1, dbeta1, dgamma2, dbeta2 [N] (summed over the tokens),
+ * all in `dtype`; the sums are FP32, taken in a fixed order (the same call
+ * gives the same bits).  Any output but dx may be NULL (not wanted).  dx or
+ * dresidual may be the memory of dy, dh, x or residual.  M == 0 zeroes the
+ * vectors.  The workspace (256-byte aligned) holds the partial sums:
+ * ngr_norm_gate_residual_norm_workspace_bytes, with rows_per_gate = 0 for no
+ * gate. */
+int ngr_fused_norm_gate_residual_norm_backward(
+    int norm1, int norm2, const void *dy, const void *dh, const void *x,
+    const void *residual, const void *gate, int64_t rows_per_gate,
+    const void *gamma1, const void *beta1, const void *gamma2,
+    const float *stats, float residual_scale, float block_scale, int64_t M,
+    int64_t N, int dtype, void *dx,
+    void *dresidual, void *dgate, void *dgamma1, void *dbeta1, void *dgamma2,
+    void *dbeta2, void *workspace, size_t workspace_bytes,
+    ngr_stream_t stream);
+
+/* Bytes of workspace of the backward call above (0 for invalid sizes). */
+size_t ngr_norm_gate_residual_norm_workspace_bytes(int norm1, int norm2,
+                                                   int64_t rows_per_gate,
+                                                   int64_t M, int64_t N);
+
 /* Inference-mode weight fold, step 1 of 2 ([LNF] §6.2: with gamma and beta
  * fixed, gamma is folded into the matmul weight once, ahead of the calls).
  * norm: 1 = LayerNorm, 2 = RMSNorm (beta ignored, may be NULL).  With K8,

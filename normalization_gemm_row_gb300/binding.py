@@ -48,6 +48,12 @@ SIGNATURES = {
     "ngr_fused_norm_swiglu": (_I, [_I, _P, _P, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _SZ, _P]),
     "ngr_fused_mlp_swiglu": (_I, [_I, _P, _P, _P, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
     "ngr_fused_linear_residual_norm": (_I, [_I, _P, _P, _P, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "ngr_fused_norm_gate_residual_norm": (
+        _I, [_I, _I, _P, _P, _P, _I64, _P, _P, _P, _P, _F, _F, _F, _F, _I64, _I64, _I, _P, _P, _P, _P]),
+    "ngr_fused_norm_gate_residual_norm_backward": (
+        _I, [_I, _I, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _F, _F, _I64, _I64, _I,
+             _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "ngr_norm_gate_residual_norm_workspace_bytes": (_SZ, [_I, _I, _I64, _I64, _I64]),
     "ngr_row_stats": (_I, [_I, _P, _F, _I64, _I64, _I, _P, _P]),
     "ngr_fold_prepare": (_I, [_I, _P, _P, _P, _P, _I64, _I64, _I, _P, _P, _P]),
     "ngr_fused_norm_linear_folded": (_I, [_I, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _SZ, _P]),
@@ -171,6 +177,30 @@ def ngr_fused_norm_linear_folded(norm, x, Wf, cb, eps, M, K, N, dtype, y, ws,
                                  ws_bytes, stream) -> int:
     return lib().ngr_fused_norm_linear_folded(norm, x, Wf, cb, eps, M, K, N, dtype,
                                               y, ws, ws_bytes, stream)
+
+
+def ngr_fused_norm_gate_residual_norm(norm1, norm2, x, residual, gate, rows_per_gate, gamma1,
+                                      beta1, gamma2, beta2, eps1, eps2, residual_scale,
+                                      block_scale, M, N, dtype, h, y, stats, stream) -> int:
+    return lib().ngr_fused_norm_gate_residual_norm(norm1, norm2, x, residual, gate, rows_per_gate,
+                                                   gamma1, beta1, gamma2, beta2, eps1, eps2,
+                                                   residual_scale, block_scale, M, N, dtype, h, y,
+                                                   stats, stream)
+
+
+def ngr_fused_norm_gate_residual_norm_backward(norm1, norm2, dy, dh, x, residual, gate,
+                                               rows_per_gate, gamma1, beta1, gamma2, stats,
+                                               residual_scale, block_scale, M, N, dtype, dx,
+                                               dresidual, dgate, dgamma1, dbeta1, dgamma2, dbeta2,
+                                               ws, ws_bytes, stream) -> int:
+    return lib().ngr_fused_norm_gate_residual_norm_backward(
+        norm1, norm2, dy, dh, x, residual, gate, rows_per_gate, gamma1, beta1, gamma2,
+        stats, residual_scale, block_scale, M, N, dtype, dx, dresidual, dgate, dgamma1, dbeta1,
+        dgamma2, dbeta2, ws, ws_bytes, stream)
+
+
+def ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rows_per_gate, M, N) -> int:
+    return int(lib().ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rows_per_gate, M, N))
 
 
 def ngr_row_stats(norm, x, eps, M, K, dtype, stats, stream) -> int:
@@ -471,6 +501,157 @@ def fused_linear_residual_norm(x, W, gamma, norm: int = NORM_RMS, beta=None, bia
                                         ws.numel() * ws.element_size(), _stream(stream))
     _raise(rc, "fused_linear_residual_norm")
     return hh.reshape(*x.shape[:-1], N), y.reshape(*x.shape[:-1], N)
+
+
+def _device_checks(x, *ts):
+    """The new operators' tensors: one CUDA device, contiguous."""
+    if not x.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors")
+    for t in ts:
+        if t is None:
+            continue
+        if t.device != x.device:
+            raise ValueError("all tensors must be on one device")
+        if not t.is_contiguous():
+            raise ValueError("all tensors must be contiguous")
+
+
+class _Launch:
+    """Makes the tensors' device current and gives the stream to launch on
+    (the current one of that device by default).  Tensors that were
+    allocated for a call on another stream are kept from reuse until that
+    stream is done with them."""
+
+    def __init__(self, device, stream):
+        self.device = device
+        self.back = None
+        self.given = stream
+
+    def __enter__(self):
+        now = torch.cuda.current_device()
+        if self.device.index is not None and now != self.device.index:
+            self.back = now
+            torch.cuda.set_device(self.device)
+        self.stream = _stream(self.given)
+        return self
+
+    def hold(self, *tensors):
+        if self.given is None or self.stream == torch.cuda.current_stream().cuda_stream:
+            return
+        s = self.given if isinstance(self.given, torch.cuda.Stream) else torch.cuda.ExternalStream(self.stream)
+        for t in tensors:
+            if t is not None:
+                t.record_stream(s)
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            torch.cuda.set_device(self.back)
+        return False
+
+
+def _join_operands(x, residual, gate, norm1, gamma1, beta1, norm2, gamma2, beta2):
+    """(x, residual, gate as 2-D, gamma1, ... without those that the norms do
+    not use, rows_per_gate)"""
+    N = x.shape[-1]
+    x2 = x.reshape(-1, N)
+    M = x2.shape[0]
+    r2 = None
+    if residual is not None:
+        if residual.shape != x.shape:
+            raise ValueError("residual must have x's shape")
+        r2 = residual.reshape(-1, N)
+    rpg = 0
+    if gate is not None:
+        if gate.shape[-1] != N:
+            raise ValueError("gate must be [N] or [G, N]")
+        gate = gate.reshape(-1, N)
+        G = gate.shape[0]
+        if G == 0 or M % G != 0:
+            raise ValueError("gate must have one row for all tokens or for each of G equal runs of them")
+        rpg = max(1, M // G)
+    vectors = [gamma1 if norm1 != NORM_NONE else None, beta1 if norm1 == NORM_LAYER else None,
+               gamma2 if norm2 != NORM_NONE else None, beta2 if norm2 == NORM_LAYER else None]
+    for v in vectors:
+        if v is not None and v.numel() != N:
+            raise ValueError("gamma and beta must have one element per column")
+    _check(x2, r2, gate, *vectors, dtype=x.dtype)
+    _device_checks(x2, r2, gate, *vectors)
+    return x2, r2, gate, vectors, rpg, M, N
+
+
+def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM_RMS, gamma1=None,
+                                  beta1=None, eps1=1e-5, norm2: int = NORM_RMS, gamma2=None,
+                                  beta2=None, eps2=1e-5, residual_scale=1.0, block_scale=1.0,
+                                  h=None, out=None, return_stats=False, stream=None):
+    """(h, y): h = residual_scale residual + block_scale gate norm1(x),
+    y = norm2(h); x [..., N].  gate is [N], or [G, N] with one row for each
+    of G equal runs of tokens.  h and y go to ``h`` and ``out`` when given
+    (which may be x or residual).  y is None without norm2.  With
+    ``return_stats`` (h, y, stats), stats float32 [M, 4] for the backward
+    call."""
+    x2, r2, g2, (ga1, be1, ga2, be2), rpg, M, N = _join_operands(
+        x, residual, gate, norm1, gamma1, beta1, norm2, gamma2, beta2)
+    for t in (h, out):
+        if t is not None and t.shape != x.shape:
+            raise ValueError("h and out must have x's shape")
+    _check(h, out, dtype=x.dtype)
+    _device_checks(x2, h, out)
+    hh = h if h is not None else torch.empty_like(x2)
+    y = None
+    if norm2 != NORM_NONE:
+        y = out if out is not None else torch.empty_like(x2)
+    st = torch.empty((M, 4), dtype=torch.float32, device=x.device) if return_stats else None
+    with _Launch(x.device, stream) as on:
+        rc = ngr_fused_norm_gate_residual_norm(
+            norm1, norm2, _ptr(x2), _ptr(r2), _ptr(g2), rpg, _ptr(ga1), _ptr(be1), _ptr(ga2),
+            _ptr(be2), eps1, eps2, residual_scale, block_scale, M, N, _dtype_code(x), _ptr(hh),
+            _ptr(y), _ptr(st), on.stream)
+        _raise(rc, "fused_norm_gate_residual_norm")
+        on.hold(x2, r2, g2, hh, y, st)
+    hh = hh.reshape(x.shape)
+    y = y.reshape(x.shape) if y is not None else None
+    return (hh, y, st) if return_stats else (hh, y)
+
+
+def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None,
+                                           norm1: int = NORM_RMS, gamma1=None, beta1=None,
+                                           eps1=None, norm2: int = NORM_RMS, gamma2=None,
+                                           beta2=None, eps2=None, residual_scale=1.0,
+                                           block_scale=1.0, workspace=None, stream=None) -> dict:
+    """The gradients of ``fused_norm_gate_residual_norm`` from those of y
+    (``dy``) and h (``dh``), either None for zero; the other arguments as in
+    the forward call (eps1, eps2 and beta2 have no part and are not read).
+    A dict: dx, dresidual, dgate, dgamma1, dbeta1, dgamma2, dbeta2 (None for
+    an input that the call does not have)."""
+    x2, r2, g2, (ga1, be1, ga2, _), rpg, M, N = _join_operands(
+        x, residual, gate, norm1, gamma1, beta1, norm2, gamma2, None)
+    for t in (dy, dh):
+        if t is not None and t.shape != x.shape:
+            raise ValueError("dy and dh must have x's shape")
+    _check(dy, dh, dtype=x.dtype)
+    if stats.dtype != torch.float32 or stats.numel() != 4 * M:
+        raise ValueError("stats must be the float32 [M, 4] of the forward call")
+    _device_checks(x2, dy, dh, stats)
+    new = torch.empty_like
+    dx = new(x2)
+    dr = new(r2) if r2 is not None else None
+    dg = (new(g2) if M > 0 else torch.zeros_like(g2)) if g2 is not None else None
+    dv = [new(v) if v is not None else None
+          for v in (ga1, be1, ga2, ga2 if norm2 == NORM_LAYER else None)]
+    ws = _workspace(ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rpg, M, N), x.device,
+                    workspace)
+    _device_checks(x2, ws)
+    with _Launch(x.device, stream) as on:
+        rc = ngr_fused_norm_gate_residual_norm_backward(
+            norm1, norm2, _ptr(dy), _ptr(dh), _ptr(x2), _ptr(r2), _ptr(g2), rpg, _ptr(ga1),
+            _ptr(be1), _ptr(ga2), _ptr(stats), residual_scale, block_scale, M, N,
+            _dtype_code(x), _ptr(dx), _ptr(dr), _ptr(dg), *[_ptr(v) for v in dv], _ptr(ws),
+            ws.numel() * ws.element_size(), on.stream)
+        _raise(rc, "fused_norm_gate_residual_norm_backward")
+        on.hold(x2, r2, g2, dx, dr, dg, *dv, ws)
+    return {"dx": dx.reshape(x.shape), "dresidual": dr.reshape(x.shape) if dr is not None else None,
+            "dgate": dg.reshape(gate.shape) if gate is not None else None,
+            "dgamma1": dv[0], "dbeta1": dv[1], "dgamma2": dv[2], "dbeta2": dv[3]}
 
 
 def fold_prepare(norm: int, gamma, beta, W, bias=None, stream=None):

@@ -382,6 +382,30 @@ int finish(int rc, void *ws, cudaStream_t stream)
     return NGR_OK;
 }
 
+}  // namespace
+
+int device_sms(int *sms)
+{
+    DevInfo di;
+    const int rc = current_device_info(&di);
+    *sms = di.sms;
+    return rc;
+}
+void call_begin() { events_reset(); }
+void kernel_begin(cudaStream_t stream) { event_before(stream); }
+void kernel_end(cudaStream_t stream) { event_after(stream); }
+int call_end(int rc, void *ws, cudaStream_t stream)
+{
+    if (rc != NGR_OK) return rc;
+    events_call_done();
+    if (ws) return finish(rc, ws, stream);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess && debug_mode()) e = cudaStreamSynchronize(stream);
+    return e == cudaSuccess ? NGR_OK : record_cuda_error("kernel launch", e, cudaGetErrorString(e));
+}
+
+namespace {
+
 // One linear layer y = act(norm(x) W^T + bias) on its own, given the
 // workspace regions.  `stats_ready` says whether a preceding grid on the
 // stream produced what this one reads (then it is launched as a

@@ -151,6 +151,16 @@ constexpr int kMinKbPerSplitSingle = 16;
 // ngr_last_error).  Returns -7 (NGR_ERR_CUDA) for use in return statements.
 int record_cuda_error(const char *what, int code, const char *detail);
 
+// What the entry points outside ngr_api.cu share with those in it: the
+// current device's SM count (NGR_OK, or NGR_ERR_ARCH / NGR_ERR_CUDA), the
+// kernel timing (begin, then a pair around each launch), and the end of a
+// call (launch errors; with NGR_DEBUG the error word, `ws` may be null).
+int device_sms(int *sms);
+void call_begin();
+void kernel_begin(cudaStream_t stream);
+void kernel_end(cudaStream_t stream);
+int call_end(int rc, void *ws, cudaStream_t stream);
+
 // NGR_DEBUG set (and not "0"): every entry point synchronizes its stream
 // after launching and reports the device error word.
 bool debug_mode();
