@@ -286,6 +286,53 @@ size_t ngr_norm_gate_residual_norm_workspace_bytes(int norm1, int norm2,
                                                    int64_t rows_per_gate,
                                                    int64_t M, int64_t N);
 
+/* Softmax cross entropy of a linear head over a large vocabulary, the logits
+ * never kept: with z[i, v] = logit_scale x[i, :] . W[v, :],
+ *   lse[i] = log sum_v exp(z[i, v]),  loss[i] = lse[i] - z[i, target[i]].
+ * x is [M, K], W [V, K] (`dtype`), target [M] int64, loss and lse FP32 [M].
+ * A token whose target is negative does not count: its loss and lse are 0,
+ * its row of x is not looked at (it may hold anything).  A target of V or
+ * more is an error: the token does not count, and the workspace's error word
+ * reports NGR_ERR_ARG (ngr_workspace_error).  The logits are formed a tile
+ * at a time in FP32 on chip, and each tile leaves a (maximum, sum) pair per
+ * token.  Any K and V; W must be 16-byte aligned when K is a multiple of 8
+ * (otherwise the call copies it into the workspace with padded rows), x and
+ * an unaligned W 2-byte aligned.  M == 0 is a no-op.  The workspace is
+ * 256-byte aligned, ngr_linear_cross_entropy_workspace_bytes(0, M, K, V). */
+int ngr_fused_linear_cross_entropy(const void *x, const void *W,
+                                   const int64_t *target, float logit_scale,
+                                   int64_t M, int64_t K, int64_t V, int dtype,
+                                   float *loss, float *lse, void *workspace,
+                                   size_t workspace_bytes,
+                                   ngr_stream_t stream);
+
+/* The gradient of ngr_fused_linear_cross_entropy: from dloss and dlse (FP32
+ * [M], the gradients of loss and lse; either may be NULL for zero, not both),
+ * the forward's inputs and its lse,
+ *   dz[i, v] = logit_scale ((dloss[i] + dlse[i]) p[i, v] - dloss[i] [v = target[i]]),
+ *   p = exp(z - lse),   dx = dz W [M, K],   dW = dz^T x [V, K]   (`dtype`).
+ * (dlse gives the gradient of a penalty on lse.)  Tokens that do not count
+ * have dx = 0 and add nothing to dW.  The logits are computed again a piece
+ * of the vocabulary at a time; dz of one piece is held in the workspace,
+ * rounded to `dtype` after scaling by a power of two that keeps it inside
+ * fp16's range; the products accumulate in FP32 and dx and dW are rounded
+ * once.  The order of every sum is fixed (the same call gives the same
+ * bits).  dx or dW may be NULL (not wanted).  M == 0 zeroes dW.  Alignment
+ * as in the forward call, dx and dW 2 bytes.  Workspace:
+ * ngr_linear_cross_entropy_workspace_bytes(1, M, K, V). */
+int ngr_fused_linear_cross_entropy_backward(
+    const float *dloss, const float *dlse, const float *lse, const void *x,
+    const void *W, const int64_t *target, float logit_scale, int64_t M,
+    int64_t K, int64_t V, int dtype, void *dx, void *dW, void *workspace,
+    size_t workspace_bytes, ngr_stream_t stream);
+
+/* Bytes of workspace of the two calls above (0 for invalid sizes): the
+ * counted tokens' rows, and forward 8 bytes per token and 128 vocabulary
+ * entries, backward dz of a piece of the vocabulary (256 MB, or 4096 entries
+ * if that is more) and FP32 sums of dx where it is not made in one go. */
+size_t ngr_linear_cross_entropy_workspace_bytes(int backward, int64_t M,
+                                                int64_t K, int64_t V);
+
 /* Inference-mode weight fold, step 1 of 2 ([LNF] §6.2: with gamma and beta
  * fixed, gamma is folded into the matmul weight once, ahead of the calls).
  * norm: 1 = LayerNorm, 2 = RMSNorm (beta ignored, may be NULL).  With K8,
@@ -369,8 +416,8 @@ int ngr_row_stats(int norm, const void *x, float eps, int64_t M, int64_t K,
                   int dtype, float *stats, ngr_stream_t stream);
 
 /* Synchronize `stream`, then return and clear the error word kept in
- * `workspace` (NGR_OK, or NGR_ERR_TIMEOUT when a kernel's bounded wait ran
- * out).  NGR_ERR_CUDA if the synchronization itself fails. */
+ * `workspace` (NGR_OK, NGR_ERR_TIMEOUT when a kernel's bounded wait ran
+ * out, or NGR_ERR_ARG for a target outside the vocabulary).  NGR_ERR_CUDA if the synchronization itself fails. */
 int ngr_workspace_error(void *workspace, ngr_stream_t stream);
 
 /* Launch one tiny kernel whose mbarrier wait can never complete, bounded by
@@ -408,7 +455,7 @@ int ngr_tile_plan(int op, int64_t M, int64_t K, int64_t N, int *plan);
 /* Profiling aid: time every kernel of this thread's next `n_calls` calls.
  * Each such call records CUDA events (the library's own, created here; no
  * device memory) on its stream just before and just after each kernel it
- * launches, at most NGR_MAX_KERNELS_PER_CALL per call.  Recording between a
+ * launches, at most the first NGR_MAX_KERNELS_PER_CALL per call.  Recording between a
  * call's kernels keeps them from overlapping, so time whole calls with this
  * off.  Returns NGR_OK, NGR_ERR_ARG for n_calls <= 0, NGR_ERR_CUDA if
  * events cannot be created. */

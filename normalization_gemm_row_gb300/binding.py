@@ -54,6 +54,10 @@ SIGNATURES = {
         _I, [_I, _I, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _F, _F, _I64, _I64, _I,
              _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "ngr_norm_gate_residual_norm_workspace_bytes": (_SZ, [_I, _I, _I64, _I64, _I64]),
+    "ngr_fused_linear_cross_entropy": (_I, [_P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "ngr_fused_linear_cross_entropy_backward": (
+        _I, [_P, _P, _P, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "ngr_linear_cross_entropy_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64]),
     "ngr_row_stats": (_I, [_I, _P, _F, _I64, _I64, _I, _P, _P]),
     "ngr_fold_prepare": (_I, [_I, _P, _P, _P, _P, _I64, _I64, _I, _P, _P, _P]),
     "ngr_fused_norm_linear_folded": (_I, [_I, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _SZ, _P]),
@@ -201,6 +205,23 @@ def ngr_fused_norm_gate_residual_norm_backward(norm1, norm2, dy, dh, x, residual
 
 def ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rows_per_gate, M, N) -> int:
     return int(lib().ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rows_per_gate, M, N))
+
+
+def ngr_fused_linear_cross_entropy(x, W, target, logit_scale, M, K, V, dtype, loss, lse, ws,
+                                   ws_bytes, stream) -> int:
+    return lib().ngr_fused_linear_cross_entropy(x, W, target, logit_scale, M, K, V, dtype, loss,
+                                                lse, ws, ws_bytes, stream)
+
+
+def ngr_fused_linear_cross_entropy_backward(dloss, dlse, lse, x, W, target, logit_scale, M, K, V,
+                                            dtype, dx, dW, ws, ws_bytes, stream) -> int:
+    return lib().ngr_fused_linear_cross_entropy_backward(dloss, dlse, lse, x, W, target,
+                                                         logit_scale, M, K, V, dtype, dx, dW, ws,
+                                                         ws_bytes, stream)
+
+
+def ngr_linear_cross_entropy_workspace_bytes(backward, M, K, V) -> int:
+    return int(lib().ngr_linear_cross_entropy_workspace_bytes(backward, M, K, V))
 
 
 def ngr_row_stats(norm, x, eps, M, K, dtype, stats, stream) -> int:
@@ -652,6 +673,71 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     return {"dx": dx.reshape(x.shape), "dresidual": dr.reshape(x.shape) if dr is not None else None,
             "dgate": dg.reshape(gate.shape) if gate is not None else None,
             "dgamma1": dv[0], "dbeta1": dv[1], "dgamma2": dv[2], "dbeta2": dv[3]}
+
+
+def _ce_operands(x, W, target):
+    """(x as [M, K], target as [M], M, K, V)"""
+    K = x.shape[-1]
+    if W.dim() != 2 or W.shape[1] != K:
+        raise ValueError("W must be [V, K]")
+    if target.dtype != torch.int64:
+        raise TypeError("target must be int64")
+    if target.shape != x.shape[:-1]:
+        raise ValueError("target must have one entry per row of x")
+    x2 = x.reshape(-1, K)
+    t1 = target.reshape(-1)
+    _check(x2, W, dtype=x.dtype)
+    _device_checks(x2, W, t1)
+    return x2, t1, x2.shape[0], K, W.shape[0]
+
+
+def _row_vector(t, M, device):
+    """A float32 vector of one element per token (None stays None)."""
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != M or t.device != device:
+        raise ValueError("dloss, dlse and lse must be float32 with one element per token")
+    return t.reshape(-1).contiguous()
+
+
+def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, stream=None):
+    """(loss, lse), float32 of target's shape: z = logit_scale x . W^T,
+    lse = log sum exp z, loss = lse - z[target], both 0 where target is
+    negative; x [..., K], W [V, K], target [...] int64.  The logits are not
+    kept."""
+    x2, t1, M, K, V = _ce_operands(x, W, target)
+    loss = torch.empty(M, dtype=torch.float32, device=x.device)
+    lse = torch.empty(M, dtype=torch.float32, device=x.device)
+    ws = _workspace(ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
+    _device_checks(x2, ws)
+    with _Launch(x.device, stream) as on:
+        rc = ngr_fused_linear_cross_entropy(_ptr(x2), _ptr(W), _ptr(t1), logit_scale, M, K, V,
+                                            _dtype_code(x), _ptr(loss), _ptr(lse), _ptr(ws),
+                                            ws.numel() * ws.element_size(), on.stream)
+        _raise(rc, "fused_linear_cross_entropy")
+        on.hold(x2, t1, loss, lse, ws)
+    return loss.reshape(target.shape), lse.reshape(target.shape)
+
+
+def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.0, dlse=None,
+                                        need_dx=True, need_dW=True, workspace=None, stream=None):
+    """(dx, dW) of ``fused_linear_cross_entropy`` from the gradients of its
+    loss (``dloss``) and, if given, of its lse (``dlse``), float32 per token;
+    either output is None when not needed."""
+    x2, t1, M, K, V = _ce_operands(x, W, target)
+    g, gl, l1 = (_row_vector(t, M, x.device) for t in (dloss, dlse, lse))
+    dx = torch.empty_like(x2) if need_dx else None
+    dW = torch.empty_like(W) if need_dW else None
+    ws = _workspace(ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
+    _device_checks(x2, ws)
+    with _Launch(x.device, stream) as on:
+        rc = ngr_fused_linear_cross_entropy_backward(
+            _ptr(g), _ptr(gl), _ptr(l1), _ptr(x2), _ptr(W), _ptr(t1), logit_scale, M, K, V,
+            _dtype_code(x), _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(),
+            on.stream)
+        _raise(rc, "fused_linear_cross_entropy_backward")
+        on.hold(x2, t1, g, gl, l1, dx, dW, ws)
+    return dx.reshape(x.shape) if dx is not None else None, dW
 
 
 def fold_prepare(norm: int, gamma, beta, W, bias=None, stream=None):

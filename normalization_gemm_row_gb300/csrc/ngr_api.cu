@@ -301,7 +301,7 @@ EncodeTiledFn encode_fn()
 bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 bool map_2d(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t cols,
-            uint32_t box_rows)
+            uint32_t box_rows, int64_t pitch)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) {
@@ -309,7 +309,7 @@ bool map_2d(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t co
         return false;
     }
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols) * 2};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch < 0 ? cols : pitch) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), box_rows};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,
@@ -1306,7 +1306,7 @@ int ngr_workspace_error(void *workspace, ngr_stream_t stream)
     if (cudaMemcpy(&v, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
         return NGR_ERR_CUDA;
     if (v != 0 && cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return NGR_ERR_CUDA;
-    return v == 0 ? NGR_OK : NGR_ERR_TIMEOUT;
+    return v == 0 ? NGR_OK : v == kDevErrTarget ? NGR_ERR_ARG : NGR_ERR_TIMEOUT;
 }
 
 int ngr_debug_bounded_wait(void *workspace, uint32_t timeout_us, ngr_stream_t stream_)

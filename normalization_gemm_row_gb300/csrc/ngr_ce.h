@@ -1,0 +1,88 @@
+// ngr_ce.h -- argument blocks of the linear cross entropy's kernels.  Not
+// installed.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace ngr {
+
+// The four products of the operator.  z = x W^T by tiles, reduced to each
+// row's (max, sum) in the epilogue or turned into dz; dx = dz W; dW = dz^T x.
+enum { kCeLse = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
+
+constexpr int kCeTile = 256;      // rows and columns of a CTA pair's output tile
+constexpr int kCeStages = 6;      // pipeline stages of 32 KB a CTA
+
+// What the kernels of a call learn of its tokens (device memory): `count`
+// tokens have a target; the weights of their gradients times `up` (a power
+// of two) are at most 2^14, so that dz in 16 bits neither overflows nor
+// loses small probabilities among fp16's subnormals; `down` = 1 / up.
+struct CeInfo {
+    int count;
+    float up, down;
+};
+
+// Per counted token: lse in powers of two, the weights of p and of the
+// target's -1 (scaled by `up`), and the target.
+struct CeRow {
+    float lse2, weight_p, weight_t;
+    int target;
+};
+
+struct alignas(128) CeGemmArgs {
+    CUtensorMap map_a, map_b;
+    const CeInfo *info;
+    int *err;
+    unsigned long long timeout_ns;
+    int rows;               // kCeDw: vocabulary entries of the piece (output rows)
+    int cols;               // output columns: vocabulary entries of the piece, or K
+    int depth;              // contracted length (kCeDw: the counted tokens, from info)
+    int splits;             // kCeDx: ranges of the contracted length, each with its own sums
+    float scale2;           // kCeLse, kCeGrad: logit scale times log2(e)
+    float scale;            // kCeLse: logit scale
+    int v0;                 // first vocabulary entry of the piece
+    const int *target;      // kCeLse: [count] targets of the counted tokens
+    float2 *part;           // kCeLse: [2 column tiles][part_pitch] (max, sum) in powers of two
+    int64_t part_pitch;
+    float *z_target;        // kCeLse: [count] the target's logit
+    const CeRow *row;       // kCeGrad
+    void *out;              // kCeGrad: dz [rows][pitch]; kCeDw: dW at v0; kCeDx: dx (finish)
+    int64_t pitch;          // elements between rows of `out`
+    float *sums;            // kCeDx: FP32 [splits][sums_rows][cols]
+    int64_t sums_rows;
+    int add;                // kCeDx: add to the sums of the pieces before
+    int finish;             // kCeDx: this is the last piece and splits == 1: write dx itself
+    const int *index;       // kCeDx (finish): a counted token's row of x
+};
+
+int launch_ce_gemm(int mode, bool bf16, const CeGemmArgs &a, int64_t units, cudaStream_t stream);
+
+struct CeTokens {
+    const void *x;          // [M, K] rows of K elements
+    const int64_t *target;  // [M]
+    const float *dloss;     // [M] or null (forward)
+    const float *dlse;      // [M] or null
+    const float *lse;       // [M] (backward)
+    void *dx;               // [M, K] or null: rows of tokens that do not count are zeroed
+    float logit_scale;
+    int64_t M, K, V, K8;
+    CeInfo *info;
+    int *err;
+    int *index;             // [M] counted tokens in order, the others behind them
+    int *ctarget;           // [M] targets of the counted tokens
+    CeRow *row;             // [M up to a tile] (backward)
+    void *xc;               // [M up to 64][K8] the counted tokens' rows, zeros behind
+};
+
+int launch_ce_index(const CeTokens &t, cudaStream_t stream);
+int launch_ce_gather(const CeTokens &t, cudaStream_t stream);
+int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, int parts,
+                   const float *z_target, float *loss, float *lse, cudaStream_t stream);
+int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_rows, int splits,
+                 cudaStream_t stream);
+int ce_clusters();          // resident CTA pairs of the product kernels
+
+}  // namespace ngr

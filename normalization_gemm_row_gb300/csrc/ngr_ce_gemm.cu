@@ -1,0 +1,456 @@
+// ngr_ce_gemm.cu -- the products of the linear cross entropy on CTA pairs
+// (tcgen05 cta_group::2), 256 x 256 output tiles, with the softmax's work in
+// the epilogue:
+//
+//   kCeLse   z = x W^T by tiles; a tile leaves (max, sum exp) of each row's
+//            columns and the target's logit, so no logit reaches HBM;
+//   kCeGrad  the same product again over a piece of the vocabulary, turned
+//            into dz = weight_p p - weight_t [v = target] with p = exp(z - lse);
+//   kCeDx    dx (+)= dz W over the piece;
+//   kCeDw    dW = dz^T x for the piece's rows of W.
+//
+// Operands are read as they lie: x and W rows are K-major for z; W's rows
+// are the contracted index of dx, dz's and x's rows that of dW, so those
+// operands are MN-major, which the tensor core reads through a transposed
+// shared-memory descriptor; nothing is transposed in memory.
+//
+// Bound by the tensor cores for batches of tokens, by reading W (or writing
+// dW) for a few tokens.  Per CTA a stage is 16 KB of A and 16 KB of B, six
+// stages deep; the two 256-column accumulators take turns, so a tile's
+// epilogue (8 warps, two per tensor-memory lane quarter) runs under the next
+// tile's products.
+//
+// Warp roles: 0 TMA producer, 1 MMA issuer (even CTA), 2 tensor memory, 4-11
+// epilogue.  Barriers as in the CTA-pair tile kernel without a norm: full[s]
+// on the leader, on which both CTAs' copies complete; empty[s] the leader's
+// commit to both; acc_full[a] the same at a tile's end; acc_empty[a] on the
+// leader, one arrival per epilogue warp of both CTAs.
+#include "ngr_ce.h"
+#include "ngr_gemm_kernel.cuh"
+
+namespace ngr {
+
+namespace {
+
+constexpr int kCeThreads = 384;
+constexpr int kCeEpilogueWarp0 = 4;
+constexpr int kCeEpilogueWarps = 8;
+constexpr int kCeOperand = kBM * kBK * 2;                 // 16 KB: a CTA's half of A or B
+constexpr int kCeBox = 64 * kBK * 2;                      // an MN-major box of 64 x 64
+constexpr int kCeSmem = kCeStages * 2 * kCeOperand + 8 * (2 * kCeStages + 5) + 16 + 1024;
+
+__device__ __forceinline__ float exp2_approx(float v)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ void ld_global_v8(const float *p, float (&v)[8])
+{
+    asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]),
+                   "=f"(v[7])
+                 : "l"(p)
+                 : "memory");
+}
+
+// Columns [c, min(c + 32, cols)) of a row of 16-bit values that starts at
+// `row`: whole sectors, 16-byte pieces or single elements by the alignment
+// of the row.
+template <bool BF16>
+__device__ __forceinline__ void store16_32(const float (&v)[32], uint16_t *row, int c, int cols)
+{
+    uint32_t o[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) o[j] = from_float2<BF16>(v[2 * j], v[2 * j + 1]);
+    uint16_t *p = row + c;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (c + 32 <= cols && (at & 31u) == 0) {
+        st_global_v8(p, *reinterpret_cast<const uint32_t(*)[8]>(&o[0]));
+        st_global_v8(p + 16, *reinterpret_cast<const uint32_t(*)[8]>(&o[8]));
+    } else if (c + 32 <= cols && (at & 15u) == 0) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            reinterpret_cast<uint4 *>(p)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (c + j < cols) p[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+    }
+}
+
+// The output tiles of a call and the order they run in.
+template <int MODE>
+struct CeUnits {
+    int tiles, slow, kb_all, splits, kb_per_split;   // `fast` dimension first
+    int fast;
+    __device__ __forceinline__ CeUnits(const CeGemmArgs &a)
+    {
+        // (no counted token: one tile of zero rows, so that dW is written)
+        const int n = max(a.info->count, 1);
+        const int m_tiles = ((MODE == kCeDw ? a.rows : n) + kCeTile - 1) / kCeTile;
+        const int n_tiles = (a.cols + kCeTile - 1) / kCeTile;
+        // z: the row tiles of one column tile run together, so W is read
+        // once; dx, dW: the column tiles of one row tile, so dz is.
+        constexpr bool kRowsFast = MODE == kCeLse || MODE == kCeGrad;
+        fast = kRowsFast ? m_tiles : n_tiles;
+        slow = kRowsFast ? n_tiles : m_tiles;
+        tiles = m_tiles * n_tiles;
+        kb_all = ((MODE == kCeDw ? n : a.depth) + kBK - 1) / kBK;
+        splits = MODE == kCeDx ? a.splits : 1;
+        kb_per_split = (kb_all + splits - 1) / splits;
+    }
+    __device__ __forceinline__ int count() const { return tiles * splits; }
+    __device__ __forceinline__ int m0(int u) const
+    {
+        const int t = u / splits;
+        return ((MODE == kCeLse || MODE == kCeGrad) ? t % fast : t / fast) * kCeTile;
+    }
+    __device__ __forceinline__ int n0(int u) const
+    {
+        const int t = u / splits;
+        return ((MODE == kCeLse || MODE == kCeGrad) ? t / fast : t % fast) * kCeTile;
+    }
+    __device__ __forceinline__ int split(int u) const { return u % splits; }
+    __device__ __forceinline__ int kb0(int u) const { return min(kb_all, split(u) * kb_per_split); }
+    __device__ __forceinline__ int kb1(int u) const { return min(kb_all, (split(u) + 1) * kb_per_split); }
+};
+
+template <int MODE, bool BF16>
+__global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_constant__ CeGemmArgs args)
+{
+    constexpr bool kAMn = MODE == kCeDw;
+    constexpr bool kBMn = MODE == kCeDx || MODE == kCeDw;
+    constexpr uint32_t kIdesc = idesc_f16_major(BF16, kCeTile, kCeTile, kAMn, kBMn);
+    constexpr uint32_t kStageBytes = 2u * 2u * kCeOperand;   // both CTAs' copies
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+    uint8_t *sA = smem;
+    uint8_t *sB = smem + kCeStages * kCeOperand;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + 2 * kCeStages * kCeOperand);
+    uint64_t *empty = full + kCeStages;
+    uint64_t *acc_full = empty + kCeStages;
+    uint64_t *acc_empty = acc_full + 2;
+    uint64_t *drain = acc_empty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(drain + 1);
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_ctarank();
+    const bool leader = rank == 0;
+    __shared__ int abort_flag;
+    const WaitCtx wc{&abort_flag, args.err, args.timeout_ns};
+
+    if (threadIdx.x == 0) {
+        abort_flag = 0;
+        prefetch_tmap(&args.map_a);
+        prefetch_tmap(&args.map_b);
+        for (int s = 0; s < kCeStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&acc_full[i], 1);
+            mbar_init(&acc_empty[i], 2 * kCeEpilogueWarps);
+        }
+        mbar_init(drain, 1);
+        fence_mbarrier_init();
+    }
+    if (warp == 2) {
+        tmem_alloc_pair(tmem_slot, 512);
+        tmem_relinquish_pair();
+    }
+    tc_fence_before();
+    cluster_sync_all();
+    tc_fence_after();
+    const uint32_t tmem_base = *tmem_slot;
+
+    const CeUnits<MODE> units(args);
+    const int n_units = units.count();
+    const int first = blockIdx.x >> 1, step = gridDim.x >> 1;
+    const uint32_t full_leader = mapa_shared(smem_u32(full), 0);
+    const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
+            // z: x stays in L2, W streams through; dx: W's piece stays; dW: x.
+            const uint64_t pol_a = (MODE == kCeLse || MODE == kCeGrad) ? keep : stream;
+            const uint64_t pol_b = (MODE == kCeLse || MODE == kCeGrad) ? stream : keep;
+            int stage = 0;
+            uint32_t phase = 0;
+            long long fills = 0;
+            bool ok = true;
+            for (int u = first; ok && u < n_units; u += step) {
+                const int m0 = units.m0(u) + static_cast<int>(rank) * kBM;
+                const int n0 = units.n0(u) + static_cast<int>(rank) * kBM;
+                for (int kb = units.kb0(u), end = units.kb1(u); kb < end; ++kb) {
+                    if (!mbar_wait_ahead(&empty[stage], phase ^ 1u, wc)) { ok = false; break; }
+                    const int kc = kb * kBK;
+                    uint8_t *a = sA + stage * kCeOperand, *b = sB + stage * kCeOperand;
+                    const uint32_t fb = full_leader + 8u * static_cast<uint32_t>(stage);
+                    if (leader) mbar_arrive_expect_tx(&full[stage], kStageBytes);
+                    if constexpr (kAMn) {
+                        tma_load_2d_pair(a, &args.map_a, fb, m0, kc, pol_a);
+                        tma_load_2d_pair(a + kCeBox, &args.map_a, fb, m0 + 64, kc, pol_a);
+                    } else {
+                        tma_load_2d_pair(a, &args.map_a, fb, kc, m0, pol_a);
+                    }
+                    if constexpr (kBMn) {
+                        tma_load_2d_pair(b, &args.map_b, fb, n0, kc, pol_b);
+                        tma_load_2d_pair(b + kCeBox, &args.map_b, fb, n0 + 64, kc, pol_b);
+                    } else {
+                        tma_load_2d_pair(b, &args.map_b, fb, kc, n0, pol_b);
+                    }
+                    ++fills;
+                    if (++stage == kCeStages) { stage = 0; phase ^= 1u; }
+                }
+            }
+            // All copies complete on the leader's barriers: it waits for the
+            // last fills before the pair leaves.
+            if (leader) {
+                const int outstanding = fills < kCeStages ? static_cast<int>(fills) : kCeStages;
+                for (int j = 1; j <= outstanding; ++j) {
+                    int s = stage - j;
+                    uint32_t p = phase;
+                    if (s < 0) { s += kCeStages; p ^= 1u; }
+                    mbar_wait(&full[s], p, wc);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            int stage = 0;
+            uint32_t phase = 0;
+            int acc = 0;
+            uint32_t acc_phase = 0;
+            bool ok = true;
+            for (int u = first; ok && u < n_units; u += step) {
+                if (!mbar_wait_spin(&acc_empty[acc], acc_phase ^ 1u, wc)) break;
+                tc_fence_after();
+                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kCeTile);
+                const int kb0 = units.kb0(u);
+                for (int kb = kb0, end = units.kb1(u); kb < end; ++kb) {
+                    if (!mbar_wait_spin(&full[stage], phase, wc)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(sA + stage * kCeOperand);
+                    const uint32_t b = smem_u32(sB + stage * kCeOperand);
+#pragma unroll
+                    for (int k = 0; k < kBK / kUmmaK; ++k) {
+                        const uint64_t da = kAMn ? sdesc_mnmajor_sw128(a + k * 2048, kCeBox)
+                                                 : sdesc_kmajor_sw128(a + k * 32);
+                        const uint64_t db = kBMn ? sdesc_mnmajor_sw128(b + k * 2048, kCeBox)
+                                                 : sdesc_kmajor_sw128(b + k * 32);
+                        umma_f16_ss_pair(d, da, db, kIdesc, (kb != kb0 || k != 0) ? 1u : 0u);
+                    }
+                    umma_commit_pair(&empty[stage], 0x3);
+                    if (++stage == kCeStages) { stage = 0; phase ^= 1u; }
+                }
+                if (!ok) break;
+                umma_commit_pair(&acc_full[acc], 0x3);
+                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            }
+            umma_commit_pair(drain, 0x1);
+            mbar_wait_long(drain, 0, wc);
+        }
+    } else if (warp >= kCeEpilogueWarp0) {
+        const int q = warp & 3;                               // tensor-memory lane quarter
+        const int half = (warp - kCeEpilogueWarp0) >> 2;      // columns [128 half, +128) of the tile
+        const int count = args.info->count;
+        const float down = args.info->down;
+        int acc = 0;
+        uint32_t acc_phase = 0;
+        for (int u = first; u < n_units; u += step) {
+            const int row = units.m0(u) + static_cast<int>(rank) * kBM + q * 32 + lane;
+            const int c0 = units.n0(u) + half * 128;
+            const bool empty_range = units.kb0(u) >= units.kb1(u);   // nothing was multiplied
+            CeRow cr{0.0f, 0.0f, 0.0f, -1};
+            int target = -1;
+            if constexpr (MODE == kCeGrad) {
+                if (row < count) cr = args.row[row];
+                target = cr.target - args.v0 - c0;
+            }
+            if constexpr (MODE == kCeLse) {
+                if (row < count) target = args.target[row] - c0;
+            }
+            if (!mbar_wait_warp_long(&acc_full[acc], acc_phase, wc)) break;
+            tc_fence_after();
+            const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                static_cast<uint32_t>(acc * kCeTile + half * 128);
+            float top = -INFINITY, sum = 0.0f;
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 32) {
+                const int col = c0 + c;
+                if (col >= args.cols) break;
+                uint32_t r[32];
+                tmem_ld32(t0 + static_cast<uint32_t>(c), r);
+                tmem_ld_wait();
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) v[j] = empty_range ? 0.0f : __uint_as_float(r[j]);
+                if constexpr (MODE == kCeLse) {
+                    const int t = target - c;
+                    if (t >= 0 && t < 32) {
+                        float z = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) z = t == j ? v[j] : z;
+                        args.z_target[row] = z * args.scale;
+                    }
+                    float m = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        v[j] = col + j < args.cols ? v[j] * args.scale2 : -INFINITY;
+                        m = fmaxf(m, v[j]);
+                    }
+                    m = fmaxf(m, top);
+                    // (every logit so far -inf: their sum stays zero)
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    sum *= exp2_approx(top - base);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) sum += exp2_approx(v[j] - base);
+                    top = m;
+                } else if constexpr (MODE == kCeGrad) {
+                    const int t = target - c;
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        v[j] = exp2_approx(fmaf(v[j], args.scale2, -cr.lse2)) * cr.weight_p;
+                        if (t == j) v[j] -= cr.weight_t;
+                        // rows behind the counted tokens: x there may be anything
+                        if (row >= count) v[j] = 0.0f;
+                    }
+                    store16_32<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch,
+                                     col, args.cols);
+                } else if constexpr (MODE == kCeDw) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] *= down;
+                    if (row < args.rows)
+                        store16_32<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch,
+                                         col, args.cols);
+                } else if (row < count) {
+                    float *s = args.sums + (units.split(u) * args.sums_rows + row) * static_cast<int64_t>(args.cols) + col;
+                    const bool whole = col + 32 <= args.cols && (reinterpret_cast<uintptr_t>(s) & 31u) == 0;
+                    if (args.add) {
+                        if (whole) {
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float o[8];
+                                ld_global_v8(s + 8 * j, o);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) v[8 * j + i] += o[i];
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (col + j < args.cols) v[j] += s[j];
+                        }
+                    }
+                    if (args.finish) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] *= down;
+                        store16_32<BF16>(v, static_cast<uint16_t *>(args.out) +
+                                                static_cast<int64_t>(args.index[row]) * args.pitch,
+                                         col, args.cols);
+                    } else if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            uint32_t o[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[8 * j + i]);
+                            st_global_v8(s + 8 * j, o);
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (col + j < args.cols) s[j] = v[j];
+                    }
+                }
+            }
+            if constexpr (MODE == kCeLse) {
+                if (row < count && c0 < args.cols)
+                    args.part[static_cast<int64_t>(c0 / 128) * args.part_pitch + row] = make_float2(top, sum);
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8u * static_cast<uint32_t>(acc));
+            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+        }
+    }
+
+    // Neither CTA frees its tensor memory or leaves while the pair may still
+    // touch it.
+    tc_fence_before();
+    cluster_sync_all();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem_base, 512);
+    }
+}
+
+template <int MODE, bool BF16>
+int run(const CeGemmArgs &a, int grid, cudaStream_t stream)
+{
+    auto kern = ce_gemm_kernel<MODE, BF16>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem);
+    if (e != cudaSuccess)
+        return record_cuda_error("cudaFuncSetAttribute(max dynamic smem)", e, cudaGetErrorString(e));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kCeThreads);
+    cfg.dynamicSmemBytes = kCeSmem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, a);
+    return e == cudaSuccess ? 0 : record_cuda_error("cudaLaunchKernelEx (cross entropy)", e, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+int ce_clusters()
+{
+    auto kern = ce_gemm_kernel<kCeLse, true>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem) != cudaSuccess) return 0;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2);
+    cfg.blockDim = dim3(kCeThreads);
+    cfg.dynamicSmemBytes = kCeSmem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
+}
+
+int launch_ce_gemm(int mode, bool bf16, const CeGemmArgs &a, int64_t units, cudaStream_t stream)
+{
+    // The kernel is persistent and its CTA pairs wait for nothing of one
+    // another, so any number of them is right; as many as fit are fastest.
+    static thread_local int clusters = 0;
+    if (clusters == 0) clusters = ce_clusters();
+    const int64_t most = clusters > 0 ? clusters : 64;
+    const int grid = 2 * static_cast<int>(units < most ? units : most);
+#define NGR_CE(M_)      \
+    case M_: return bf16 ? run<M_, true>(a, grid, stream) : run<M_, false>(a, grid, stream);
+    switch (mode) {
+        NGR_CE(kCeLse)
+        NGR_CE(kCeGrad)
+        NGR_CE(kCeDx)
+        NGR_CE(kCeDw)
+    }
+#undef NGR_CE
+    return -9;
+}
+
+}  // namespace ngr

@@ -167,10 +167,10 @@ bool debug_mode();
 // Bound on every in-kernel barrier wait: NGR_WAIT_TIMEOUT_MS, default 2 s.
 unsigned long long wait_timeout_ns();
 // Tensor maps (record the reason in ngr_last_error on failure):
-// row-major [rows, cols] 16-bit matrix, box {64 columns, box_rows rows},
-// 128-byte swizzle;
+// row-major [rows, cols] 16-bit matrix (rows `pitch` elements apart, cols if
+// negative), box {64 columns, box_rows rows}, 128-byte swizzle;
 bool map_2d(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t cols,
-            uint32_t box_rows);
+            uint32_t box_rows, int64_t pitch = -1);
 // FP32 gamma and beta as the two rows of a [2, K] matrix whose rows are
 // `row_stride` bytes apart, box {64 columns, 2 rows}, no swizzle.
 bool map_gb(CUtensorMap *m, const float *gamma_f, int64_t K, size_t row_stride);

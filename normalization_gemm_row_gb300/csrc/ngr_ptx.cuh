@@ -10,7 +10,7 @@
 namespace ngr {
 
 // Device error word values (kept in the first 4 bytes of the workspace).
-enum : int { kDevErrTimeout = 1 };
+enum : int { kDevErrTimeout = 1, kDevErrTarget = 2 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void *p)
 {
@@ -458,6 +458,23 @@ __device__ __forceinline__ uint64_t sdesc_kmajor_sw128(uint32_t saddr)
     return d;
 }
 
+// Shared-memory matrix descriptor for an MN-major operand tile (the rows or
+// columns of the output are contiguous, K strides) in the 128-byte swizzle
+// layout: each TMA box is 64 output rows (128 bytes) x 64 k, k rows 128
+// bytes apart, so 8-k groups lie 1024 bytes apart (the stride byte offset)
+// and the boxes of further 64 output rows `box_bytes` apart (the leading
+// byte offset).  Advancing K by 16 adds 2048 bytes to the start address.
+__device__ __forceinline__ uint64_t sdesc_mnmajor_sw128(uint32_t saddr, uint32_t box_bytes)
+{
+    uint64_t d = 0;
+    d |= static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4);
+    d |= static_cast<uint64_t>(box_bytes >> 4) << 16;
+    d |= static_cast<uint64_t>(1024u >> 4) << 32;
+    d |= static_cast<uint64_t>(1u) << 46;
+    d |= static_cast<uint64_t>(2u) << 61;
+    return d;
+}
+
 // Instruction descriptor for kind::f16 with FP32 accumulation, both operands
 // K-major, dense: D format F32 (bits 4-5 = 1), A and B format F16 = 0 or
 // BF16 = 1 (bits 7-9, 10-12), N >> 3 (bits 17-22), M >> 4 (bits 24-28).
@@ -466,6 +483,12 @@ __host__ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N)
     return (1u << 4) | ((bf16 ? 1u : 0u) << 7) | ((bf16 ? 1u : 0u) << 10) |
            (static_cast<uint32_t>(N >> 3) << 17) |
            (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+// The same with A and/or B MN-major (the transpose bits 15 and 16).
+__host__ __device__ constexpr uint32_t idesc_f16_major(bool bf16, int M, int N, bool a_mn, bool b_mn)
+{
+    return idesc_f16(bf16, M, N) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16);
 }
 
 // ------------------------------------------------- programmatic dependent launch
