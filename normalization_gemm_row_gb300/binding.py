@@ -524,17 +524,33 @@ def fused_linear_residual_norm(x, W, gamma, norm: int = NORM_RMS, beta=None, bia
     return hh.reshape(*x.shape[:-1], N), y.reshape(*x.shape[:-1], N)
 
 
-def _device_checks(x, *ts):
-    """The new operators' tensors: one CUDA device, contiguous."""
+def _uniform(x, *ts):
+    """x is a 16-bit CUDA tensor, and the others (None left out) share its
+    type and device; all are contiguous.  Returns x's dtype code."""
+    dtype, device = x.dtype, x.device
+    code = _dtype_code(x)
     if not x.is_cuda:
         raise ValueError("all tensors must be CUDA tensors")
+    if not x.is_contiguous():
+        raise ValueError("all tensors must be contiguous")
     for t in ts:
         if t is None:
             continue
-        if t.device != x.device:
-            raise ValueError("all tensors must be on one device")
+        if t.dtype != dtype:
+            raise TypeError("all tensors must share one dtype")
+        if t.device != device:
+            raise ValueError("all tensors must be on one CUDA device")
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
+    return code
+
+
+def _tokens(x, what, *ts):
+    """The others (None left out) have x's shape."""
+    shape = x.shape
+    for t in ts:
+        if t is not None and t.shape != shape:
+            raise ValueError(f"{what} must have x's shape")
 
 
 class _Launch:
@@ -543,14 +559,14 @@ class _Launch:
     allocated for a call on another stream are kept from reuse until that
     stream is done with them."""
 
+    __slots__ = ("device", "given", "back", "stream")
+
     def __init__(self, device, stream):
-        self.device = device
-        self.back = None
-        self.given = stream
+        self.device, self.given, self.back = device, stream, None
 
     def __enter__(self):
         now = torch.cuda.current_device()
-        if self.device.index is not None and now != self.device.index:
+        if now != self.device.index:
             self.back = now
             torch.cuda.set_device(self.device)
         self.stream = _stream(self.given)
@@ -570,34 +586,36 @@ class _Launch:
         return False
 
 
-def _join_operands(x, residual, gate, norm1, gamma1, beta1, norm2, gamma2, beta2):
-    """(x, residual, gate as 2-D, gamma1, ... without those that the norms do
-    not use, rows_per_gate)"""
+def _scratch(nbytes, device, workspace):
+    """A workspace of at least nbytes on the device."""
+    if workspace is not None and (workspace.device != device or not workspace.is_contiguous()):
+        raise ValueError("the workspace must be contiguous and on the tensors' device")
+    return _workspace(nbytes, device, workspace)
+
+
+def _join_operands(x, gate, norm1, gamma1, beta1, norm2, gamma2, beta2):
+    """(M, N, rows_per_gate, gamma1, beta1, gamma2, beta2), the vectors that
+    the norms do not use as None."""
     N = x.shape[-1]
-    x2 = x.reshape(-1, N)
-    M = x2.shape[0]
-    r2 = None
-    if residual is not None:
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
-        r2 = residual.reshape(-1, N)
+    M = x.numel() // N if N else 0
     rpg = 0
     if gate is not None:
-        if gate.shape[-1] != N:
-            raise ValueError("gate must be [N] or [G, N]")
-        gate = gate.reshape(-1, N)
-        G = gate.shape[0]
-        if G == 0 or M % G != 0:
-            raise ValueError("gate must have one row for all tokens or for each of G equal runs of them")
+        G = gate.numel() // N if N else 0
+        if gate.shape[-1] != N or G == 0 or M % G != 0:
+            raise ValueError("gate must be [N], or [G, N] with a row for each of G equal runs of tokens")
         rpg = max(1, M // G)
-    vectors = [gamma1 if norm1 != NORM_NONE else None, beta1 if norm1 == NORM_LAYER else None,
-               gamma2 if norm2 != NORM_NONE else None, beta2 if norm2 == NORM_LAYER else None]
-    for v in vectors:
+    if norm1 != NORM_LAYER:
+        beta1 = None
+        if norm1 == NORM_NONE:
+            gamma1 = None
+    if norm2 != NORM_LAYER:
+        beta2 = None
+        if norm2 == NORM_NONE:
+            gamma2 = None
+    for v in (gamma1, beta1, gamma2, beta2):
         if v is not None and v.numel() != N:
             raise ValueError("gamma and beta must have one element per column")
-    _check(x2, r2, gate, *vectors, dtype=x.dtype)
-    _device_checks(x2, r2, gate, *vectors)
-    return x2, r2, gate, vectors, rpg, M, N
+    return M, N, rpg, gamma1, beta1, gamma2, beta2
 
 
 def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM_RMS, gamma1=None,
@@ -610,28 +628,25 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
     (which may be x or residual).  y is None without norm2.  With
     ``return_stats`` (h, y, stats), stats float32 [M, 4] for the backward
     call."""
-    x2, r2, g2, (ga1, be1, ga2, be2), rpg, M, N = _join_operands(
-        x, residual, gate, norm1, gamma1, beta1, norm2, gamma2, beta2)
-    for t in (h, out):
-        if t is not None and t.shape != x.shape:
-            raise ValueError("h and out must have x's shape")
-    _check(h, out, dtype=x.dtype)
-    _device_checks(x2, h, out)
-    hh = h if h is not None else torch.empty_like(x2)
-    y = None
-    if norm2 != NORM_NONE:
-        y = out if out is not None else torch.empty_like(x2)
+    M, N, rpg, gamma1, beta1, gamma2, beta2 = _join_operands(
+        x, gate, norm1, gamma1, beta1, norm2, gamma2, beta2)
+    _tokens(x, "residual, h and out", residual, h, out)
+    code = _uniform(x, residual, gate, gamma1, beta1, gamma2, beta2, h, out)
+    if h is None:
+        h = torch.empty_like(x)
+    if norm2 == NORM_NONE:
+        out = None
+    elif out is None:
+        out = torch.empty_like(x)
     st = torch.empty((M, 4), dtype=torch.float32, device=x.device) if return_stats else None
     with _Launch(x.device, stream) as on:
-        rc = ngr_fused_norm_gate_residual_norm(
-            norm1, norm2, _ptr(x2), _ptr(r2), _ptr(g2), rpg, _ptr(ga1), _ptr(be1), _ptr(ga2),
-            _ptr(be2), eps1, eps2, residual_scale, block_scale, M, N, _dtype_code(x), _ptr(hh),
-            _ptr(y), _ptr(st), on.stream)
+        rc = lib().ngr_fused_norm_gate_residual_norm(
+            norm1, norm2, _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1), _ptr(beta1),
+            _ptr(gamma2), _ptr(beta2), eps1, eps2, residual_scale, block_scale, M, N, code, _ptr(h),
+            _ptr(out), _ptr(st), on.stream)
         _raise(rc, "fused_norm_gate_residual_norm")
-        on.hold(x2, r2, g2, hh, y, st)
-    hh = hh.reshape(x.shape)
-    y = y.reshape(x.shape) if y is not None else None
-    return (hh, y, st) if return_stats else (hh, y)
+        on.hold(h, out, st)
+    return (h, out, st) if return_stats else (h, out)
 
 
 def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None,
@@ -644,39 +659,39 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     the forward call (eps1, eps2 and beta2 have no part and are not read).
     A dict: dx, dresidual, dgate, dgamma1, dbeta1, dgamma2, dbeta2 (None for
     an input that the call does not have)."""
-    x2, r2, g2, (ga1, be1, ga2, _), rpg, M, N = _join_operands(
-        x, residual, gate, norm1, gamma1, beta1, norm2, gamma2, None)
-    for t in (dy, dh):
-        if t is not None and t.shape != x.shape:
-            raise ValueError("dy and dh must have x's shape")
-    _check(dy, dh, dtype=x.dtype)
-    if stats.dtype != torch.float32 or stats.numel() != 4 * M:
+    M, N, rpg, gamma1, beta1, gamma2, _ = _join_operands(
+        x, gate, norm1, gamma1, beta1, norm2, gamma2, None)
+    _tokens(x, "residual, dy and dh", residual, dy, dh)
+    code = _uniform(x, dy, dh, residual, gate, gamma1, beta1, gamma2)
+    if (stats.dtype != torch.float32 or stats.numel() != 4 * M or stats.device != x.device
+            or not stats.is_contiguous()):
         raise ValueError("stats must be the float32 [M, 4] of the forward call")
-    _device_checks(x2, dy, dh, stats)
-    new = torch.empty_like
-    dx = new(x2)
-    dr = new(r2) if r2 is not None else None
-    dg = (new(g2) if M > 0 else torch.zeros_like(g2)) if g2 is not None else None
-    dv = [new(v) if v is not None else None
-          for v in (ga1, be1, ga2, ga2 if norm2 == NORM_LAYER else None)]
-    ws = _workspace(ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rpg, M, N), x.device,
-                    workspace)
-    _device_checks(x2, ws)
+    like = torch.empty_like
+    dx = like(x)
+    dr = like(residual) if residual is not None else None
+    dg = None
+    if gate is not None:
+        dg = like(gate) if M > 0 else torch.zeros_like(gate)
+    dg1 = like(gamma1) if gamma1 is not None else None
+    db1 = like(beta1) if beta1 is not None else None
+    dg2 = like(gamma2) if gamma2 is not None else None
+    db2 = like(gamma2) if norm2 == NORM_LAYER else None
+    ws = _scratch(lib().ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rpg, M, N),
+                  x.device, workspace)
     with _Launch(x.device, stream) as on:
-        rc = ngr_fused_norm_gate_residual_norm_backward(
-            norm1, norm2, _ptr(dy), _ptr(dh), _ptr(x2), _ptr(r2), _ptr(g2), rpg, _ptr(ga1),
-            _ptr(be1), _ptr(ga2), _ptr(stats), residual_scale, block_scale, M, N,
-            _dtype_code(x), _ptr(dx), _ptr(dr), _ptr(dg), *[_ptr(v) for v in dv], _ptr(ws),
+        rc = lib().ngr_fused_norm_gate_residual_norm_backward(
+            norm1, norm2, _ptr(dy), _ptr(dh), _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1),
+            _ptr(beta1), _ptr(gamma2), _ptr(stats), residual_scale, block_scale, M, N, code, _ptr(dx),
+            _ptr(dr), _ptr(dg), _ptr(dg1), _ptr(db1), _ptr(dg2), _ptr(db2), _ptr(ws),
             ws.numel() * ws.element_size(), on.stream)
         _raise(rc, "fused_norm_gate_residual_norm_backward")
-        on.hold(x2, r2, g2, dx, dr, dg, *dv, ws)
-    return {"dx": dx.reshape(x.shape), "dresidual": dr.reshape(x.shape) if dr is not None else None,
-            "dgate": dg.reshape(gate.shape) if gate is not None else None,
-            "dgamma1": dv[0], "dbeta1": dv[1], "dgamma2": dv[2], "dbeta2": dv[3]}
+        on.hold(dx, dr, dg, dg1, db1, dg2, db2, ws)
+    return {"dx": dx, "dresidual": dr, "dgate": dg, "dgamma1": dg1, "dbeta1": db1, "dgamma2": dg2,
+            "dbeta2": db2}
 
 
 def _ce_operands(x, W, target):
-    """(x as [M, K], target as [M], M, K, V)"""
+    """(M, K, V, dtype code)"""
     K = x.shape[-1]
     if W.dim() != 2 or W.shape[1] != K:
         raise ValueError("W must be [V, K]")
@@ -684,20 +699,18 @@ def _ce_operands(x, W, target):
         raise TypeError("target must be int64")
     if target.shape != x.shape[:-1]:
         raise ValueError("target must have one entry per row of x")
-    x2 = x.reshape(-1, K)
-    t1 = target.reshape(-1)
-    _check(x2, W, dtype=x.dtype)
-    _device_checks(x2, W, t1)
-    return x2, t1, x2.shape[0], K, W.shape[0]
+    code = _uniform(x, W)
+    if target.device != x.device or not target.is_contiguous():
+        raise ValueError("target must be contiguous and on x's device")
+    return target.numel(), K, W.shape[0], code
 
 
-def _row_vector(t, M, device):
-    """A float32 vector of one element per token (None stays None)."""
-    if t is None:
-        return None
-    if t.dtype != torch.float32 or t.numel() != M or t.device != device:
-        raise ValueError("dloss, dlse and lse must be float32 with one element per token")
-    return t.reshape(-1).contiguous()
+def _row_vectors(M, device, *ts):
+    """The others (None left out) are float32 with one element per token."""
+    for t in ts:
+        if t is not None and (t.dtype != torch.float32 or t.numel() != M or t.device != device
+                              or not t.is_contiguous()):
+            raise ValueError("dloss, dlse and lse must be contiguous float32 with one element per token")
 
 
 def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, stream=None):
@@ -705,18 +718,17 @@ def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, st
     lse = log sum exp z, loss = lse - z[target], both 0 where target is
     negative; x [..., K], W [V, K], target [...] int64.  The logits are not
     kept."""
-    x2, t1, M, K, V = _ce_operands(x, W, target)
-    loss = torch.empty(M, dtype=torch.float32, device=x.device)
-    lse = torch.empty(M, dtype=torch.float32, device=x.device)
-    ws = _workspace(ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
-    _device_checks(x2, ws)
+    M, K, V, code = _ce_operands(x, W, target)
+    loss = torch.empty(target.shape, dtype=torch.float32, device=x.device)
+    lse = torch.empty_like(loss)
+    ws = _scratch(lib().ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
     with _Launch(x.device, stream) as on:
-        rc = ngr_fused_linear_cross_entropy(_ptr(x2), _ptr(W), _ptr(t1), logit_scale, M, K, V,
-                                            _dtype_code(x), _ptr(loss), _ptr(lse), _ptr(ws),
-                                            ws.numel() * ws.element_size(), on.stream)
+        rc = lib().ngr_fused_linear_cross_entropy(_ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
+                                                  code, _ptr(loss), _ptr(lse), _ptr(ws),
+                                                  ws.numel() * ws.element_size(), on.stream)
         _raise(rc, "fused_linear_cross_entropy")
-        on.hold(x2, t1, loss, lse, ws)
-    return loss.reshape(target.shape), lse.reshape(target.shape)
+        on.hold(loss, lse, ws)
+    return loss, lse
 
 
 def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.0, dlse=None,
@@ -724,20 +736,18 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
     """(dx, dW) of ``fused_linear_cross_entropy`` from the gradients of its
     loss (``dloss``) and, if given, of its lse (``dlse``), float32 per token;
     either output is None when not needed."""
-    x2, t1, M, K, V = _ce_operands(x, W, target)
-    g, gl, l1 = (_row_vector(t, M, x.device) for t in (dloss, dlse, lse))
-    dx = torch.empty_like(x2) if need_dx else None
+    M, K, V, code = _ce_operands(x, W, target)
+    _row_vectors(M, x.device, dloss, dlse, lse)
+    dx = torch.empty_like(x) if need_dx else None
     dW = torch.empty_like(W) if need_dW else None
-    ws = _workspace(ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
-    _device_checks(x2, ws)
+    ws = _scratch(lib().ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
     with _Launch(x.device, stream) as on:
-        rc = ngr_fused_linear_cross_entropy_backward(
-            _ptr(g), _ptr(gl), _ptr(l1), _ptr(x2), _ptr(W), _ptr(t1), logit_scale, M, K, V,
-            _dtype_code(x), _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(),
-            on.stream)
+        rc = lib().ngr_fused_linear_cross_entropy_backward(
+            _ptr(dloss), _ptr(dlse), _ptr(lse), _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
+            code, _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(), on.stream)
         _raise(rc, "fused_linear_cross_entropy_backward")
-        on.hold(x2, t1, g, gl, l1, dx, dW, ws)
-    return dx.reshape(x.shape) if dx is not None else None, dW
+        on.hold(dx, dW, ws)
+    return dx, dW
 
 
 def fold_prepare(norm: int, gamma, beta, W, bias=None, stream=None):

@@ -19,13 +19,14 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kDzUnit = 8192.0f;   // dz's largest weight
 constexpr int kIndexThreads = 1024, kIndexEach = 8;
 constexpr int kGatherThreads = 128;
 constexpr int kLossThreads = 1024;
 
 // One CTA: a prefix sum over the tokens gives each counted token its place
 // (their order kept) and the others theirs from the end; the largest weight
-// sets the power of two that dz is scaled by.
+// is the unit of dz.
 __global__ void __launch_bounds__(kIndexThreads) ce_index_kernel(const __grid_constant__ CeTokens t)
 {
     __shared__ int warp_sum[kIndexThreads / 32];
@@ -89,12 +90,12 @@ __global__ void __launch_bounds__(kIndexThreads) ce_index_kernel(const __grid_co
     if (threadIdx.x == 0) {
         for (int w = 0; w < kIndexThreads / 32; ++w) top = fmaxf(top, warp_max[w]);
         top *= fabsf(t.logit_scale);
-        int e = 13;
-        if (top > 0.0f && top <= 3.0e38f) e = max(-100, min(100, ilogbf(top)));
+        // (no weight, or one that is not finite: unscaled)
+        if (!(top >= 1.0e-30f && top <= 1.0e38f)) top = kDzUnit;
         CeInfo info;
         info.count = static_cast<int>(base);
-        info.up = ldexpf(1.0f, 13 - e);
-        info.down = ldexpf(1.0f, e - 13);
+        info.weight = top;
+        info.down = top / kDzUnit;
         *t.info = info;
         *t.err = bad ? kDevErrTarget : 0;
     }
@@ -138,9 +139,10 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const __grid_
             }
         }
         if (t.row && r < count && threadIdx.x == 0) {
-            const float up = t.info->up * t.logit_scale;
+            const float top = t.info->weight;
             const float g = t.dloss ? t.dloss[token] : 0.0f, l = t.dlse ? t.dlse[token] : 0.0f;
-            t.row[r] = CeRow{t.lse[token] * kLog2e, (g + l) * up, g * up, t.ctarget[r]};
+            t.row[r] = CeRow{t.lse[token] * kLog2e, (g + l) * t.logit_scale / top * kDzUnit,
+                             g * t.logit_scale / top * kDzUnit, t.ctarget[r]};
         }
         if (t.dx && r >= count && r < t.M) {
             uint16_t *dst = static_cast<uint16_t *>(t.dx) + token * t.K;

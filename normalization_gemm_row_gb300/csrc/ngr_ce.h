@@ -17,16 +17,19 @@ constexpr int kCeTile = 256;      // rows and columns of a CTA pair's output til
 constexpr int kCeStages = 6;      // pipeline stages of 32 KB a CTA
 
 // What the kernels of a call learn of its tokens (device memory): `count`
-// tokens have a target; the weights of their gradients times `up` (a power
-// of two) are at most 2^14, so that dz in 16 bits neither overflows nor
-// loses small probabilities among fp16's subnormals; `down` = 1 / up.
+// tokens have a target, and `weight` is the largest size of a gradient
+// weight logit_scale dloss or logit_scale (dloss + dlse).  dz is held in 16
+// bits as a multiple of weight / 2^13: it neither overflows nor loses small
+// probabilities among fp16's subnormals, and where all tokens weigh the same
+// (a mean) the target's -1 is exact.  `down` = weight / 2^13 undoes it in
+// FP32.
 struct CeInfo {
     int count;
-    float up, down;
+    float weight, down;
 };
 
 // Per counted token: lse in powers of two, the weights of p and of the
-// target's -1 (scaled by `up`), and the target.
+// target's -1 in that unit, and the target.
 struct CeRow {
     float lse2, weight_p, weight_t;
     int target;

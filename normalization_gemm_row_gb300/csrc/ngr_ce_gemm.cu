@@ -14,6 +14,15 @@
 // operands are MN-major, which the tensor core reads through a transposed
 // shared-memory descriptor; nothing is transposed in memory.
 //
+// The tensor core adds each step's products to the FP32 accumulator without
+// rounding to nearest, so over a long contracted length an element loses up
+// to a part in 2^24 a step, always towards zero (measured: 6e-5 of a logit
+// after the 256 steps of K = 4096).  Every kChunk k blocks the accumulator is
+// therefore handed to the epilogue, which keeps the output in registers
+// (128 columns a thread) and adds the pieces there, rounding to nearest; the
+// loss's error against 64 bits falls from 5e-6 to below 1e-6, and the reads
+// hide under the products of the next piece.
+//
 // Bound by the tensor cores for batches of tokens, by reading W (or writing
 // dW) for a few tokens.  Per CTA a stage is 16 KB of A and 16 KB of B, six
 // stages deep; the two 256-column accumulators take turns, so a tile's
@@ -35,6 +44,10 @@ namespace {
 constexpr int kCeThreads = 384;
 constexpr int kCeEpilogueWarp0 = 4;
 constexpr int kCeEpilogueWarps = 8;
+// k blocks per accumulator: short for the logits, whose error shows in the
+// loss and, through the exponential, in dz; dx and dW are rounded to 16 bits.
+template <int MODE>
+__device__ __forceinline__ constexpr int ce_chunk() { return MODE == kCeLse || MODE == kCeGrad ? 8 : 32; }
 constexpr int kCeOperand = kBM * kBK * 2;                 // 16 KB: a CTA's half of A or B
 constexpr int kCeBox = 64 * kBK * 2;                      // an MN-major box of 64 x 64
 constexpr int kCeSmem = kCeStages * 2 * kCeOperand + 8 * (2 * kCeStages + 5) + 16 + 1024;
@@ -59,7 +72,7 @@ __device__ __forceinline__ void ld_global_v8(const float *p, float (&v)[8])
 // `row`: whole sectors, 16-byte pieces or single elements by the alignment
 // of the row.
 template <bool BF16>
-__device__ __forceinline__ void store16_32(const float (&v)[32], uint16_t *row, int c, int cols)
+__device__ __forceinline__ void store16_32(const float *v, uint16_t *row, int c, int cols)
 {
     uint32_t o[16];
 #pragma unroll
@@ -124,6 +137,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
     constexpr bool kBMn = MODE == kCeDx || MODE == kCeDw;
     constexpr uint32_t kIdesc = idesc_f16_major(BF16, kCeTile, kCeTile, kAMn, kBMn);
     constexpr uint32_t kStageBytes = 2u * 2u * kCeOperand;   // both CTAs' copies
+    constexpr int kChunk = ce_chunk<MODE>();
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
@@ -229,13 +243,16 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             uint32_t acc_phase = 0;
             bool ok = true;
             for (int u = first; ok && u < n_units; u += step) {
-                if (!mbar_wait_spin(&acc_empty[acc], acc_phase ^ 1u, wc)) break;
-                tc_fence_after();
-                const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kCeTile);
-                const int kb0 = units.kb0(u);
-                for (int kb = kb0, end = units.kb1(u); kb < end; ++kb) {
+                int left = 0;   // k blocks until the accumulator is handed over
+                for (int kb = units.kb0(u), end = units.kb1(u); kb < end; ++kb) {
+                    const bool fresh = left == 0;
+                    if (fresh) {
+                        if (!mbar_wait_spin(&acc_empty[acc], acc_phase ^ 1u, wc)) { ok = false; break; }
+                        left = min(kChunk, end - kb);
+                    }
                     if (!mbar_wait_spin(&full[stage], phase, wc)) { ok = false; break; }
                     tc_fence_after();
+                    const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kCeTile);
                     const uint32_t a = smem_u32(sA + stage * kCeOperand);
                     const uint32_t b = smem_u32(sB + stage * kCeOperand);
 #pragma unroll
@@ -244,14 +261,15 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
                                                  : sdesc_kmajor_sw128(a + k * 32);
                         const uint64_t db = kBMn ? sdesc_mnmajor_sw128(b + k * 2048, kCeBox)
                                                  : sdesc_kmajor_sw128(b + k * 32);
-                        umma_f16_ss_pair(d, da, db, kIdesc, (kb != kb0 || k != 0) ? 1u : 0u);
+                        umma_f16_ss_pair(d, da, db, kIdesc, (!fresh || k != 0) ? 1u : 0u);
                     }
                     umma_commit_pair(&empty[stage], 0x3);
                     if (++stage == kCeStages) { stage = 0; phase ^= 1u; }
+                    if (--left == 0) {
+                        umma_commit_pair(&acc_full[acc], 0x3);
+                        if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+                    }
                 }
-                if (!ok) break;
-                umma_commit_pair(&acc_full[acc], 0x3);
-                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
             }
             umma_commit_pair(drain, 0x1);
             mbar_wait_long(drain, 0, wc);
@@ -266,7 +284,6 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
         for (int u = first; u < n_units; u += step) {
             const int row = units.m0(u) + static_cast<int>(rank) * kBM + q * 32 + lane;
             const int c0 = units.n0(u) + half * 128;
-            const bool empty_range = units.kb0(u) >= units.kb1(u);   // nothing was multiplied
             CeRow cr{0.0f, 0.0f, 0.0f, -1};
             int target = -1;
             if constexpr (MODE == kCeGrad) {
@@ -276,106 +293,115 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             if constexpr (MODE == kCeLse) {
                 if (row < count) target = args.target[row] - c0;
             }
-            if (!mbar_wait_warp_long(&acc_full[acc], acc_phase, wc)) break;
-            tc_fence_after();
-            const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                static_cast<uint32_t>(acc * kCeTile + half * 128);
-            float top = -INFINITY, sum = 0.0f;
-#pragma unroll 1
-            for (int c = 0; c < 128; c += 32) {
-                const int col = c0 + c;
-                if (col >= args.cols) break;
-                uint32_t r[32];
-                tmem_ld32(t0 + static_cast<uint32_t>(c), r);
-                tmem_ld_wait();
-                float v[32];
+            float v[128];
 #pragma unroll
-                for (int j = 0; j < 32; ++j) v[j] = empty_range ? 0.0f : __uint_as_float(r[j]);
-                if constexpr (MODE == kCeLse) {
-                    const int t = target - c;
-                    if (t >= 0 && t < 32) {
-                        float z = 0.0f;
+            for (int j = 0; j < 128; ++j) v[j] = 0.0f;
+            bool ok = true;
+            for (int kb = units.kb0(u), end = units.kb1(u); kb < end; kb += kChunk) {
+                if (!mbar_wait_warp_long(&acc_full[acc], acc_phase, wc)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                                    static_cast<uint32_t>(acc * kCeTile + half * 128);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) z = t == j ? v[j] : z;
-                        args.z_target[row] = z * args.scale;
-                    }
-                    float m = -INFINITY;
+                for (int c = 0; c < 128; c += 16) {
+                    uint32_t r[16];
+                    tmem_ld16(t0 + static_cast<uint32_t>(c), r);
+                    tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        v[j] = col + j < args.cols ? v[j] * args.scale2 : -INFINITY;
-                        m = fmaxf(m, v[j]);
-                    }
-                    m = fmaxf(m, top);
-                    // (every logit so far -inf: their sum stays zero)
-                    const float base = m == -INFINITY ? 0.0f : m;
-                    sum *= exp2_approx(top - base);
+                    for (int j = 0; j < 16; ++j) v[c + j] += __uint_as_float(r[j]);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8u * static_cast<uint32_t>(acc));
+                if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
+            }
+            if (!ok) break;
+            const int cols = min(128, args.cols - c0);   // this warp's columns of the tile (may be <= 0)
+            if constexpr (MODE == kCeLse) {
+                if (target >= 0 && target < cols) {
+                    float z = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) sum += exp2_approx(v[j] - base);
-                    top = m;
-                } else if constexpr (MODE == kCeGrad) {
-                    const int t = target - c;
+                    for (int j = 0; j < 128; ++j) z = target == j ? v[j] : z;
+                    args.z_target[row] = z * args.scale;
+                }
+                float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
+                for (int j = 0; j < 128; ++j) {
+                    v[j] = j < cols ? v[j] * args.scale2 : -INFINITY;
+                    top = fmaxf(top, v[j]);
+                }
+                // (every logit -inf: their sum stays zero)
+                const float base = top == -INFINITY ? 0.0f : top;
+#pragma unroll
+                for (int j = 0; j < 128; ++j) sum += exp2_approx(v[j] - base);
+                if (row < count && cols > 0)
+                    args.part[static_cast<int64_t>(c0 / 128) * args.part_pitch + row] = make_float2(top, sum);
+            } else if constexpr (MODE == kCeGrad) {
+                uint16_t *out = static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= cols) break;
+#pragma unroll
+                    for (int j = c; j < c + 32; ++j) {
                         v[j] = exp2_approx(fmaf(v[j], args.scale2, -cr.lse2)) * cr.weight_p;
-                        if (t == j) v[j] -= cr.weight_t;
+                        if (target == j) v[j] -= cr.weight_t;
                         // rows behind the counted tokens: x there may be anything
                         if (row >= count) v[j] = 0.0f;
                     }
-                    store16_32<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch,
-                                     col, args.cols);
-                } else if constexpr (MODE == kCeDw) {
+                    store16_32<BF16>(v + c, out, c0 + c, args.cols);
+                }
+            } else if constexpr (MODE == kCeDw) {
+                uint16_t *out = static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] *= down;
-                    if (row < args.rows)
-                        store16_32<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch,
-                                         col, args.cols);
-                } else if (row < count) {
-                    float *s = args.sums + (units.split(u) * args.sums_rows + row) * static_cast<int64_t>(args.cols) + col;
-                    const bool whole = col + 32 <= args.cols && (reinterpret_cast<uintptr_t>(s) & 31u) == 0;
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= cols || row >= args.rows) break;
+#pragma unroll
+                    for (int j = c; j < c + 32; ++j) v[j] *= down;
+                    store16_32<BF16>(v + c, out, c0 + c, args.cols);
+                }
+            } else if (row < count) {
+                float *s = args.sums + (units.split(u) * args.sums_rows + row) * static_cast<int64_t>(args.cols) + c0;
+                const bool sectors = (reinterpret_cast<uintptr_t>(s) & 31u) == 0;
+#pragma unroll
+                for (int c = 0; c < 128; c += 32) {
+                    if (c >= cols) break;
+                    const bool whole = c + 32 <= cols && sectors;
                     if (args.add) {
                         if (whole) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
+                            for (int j = c; j < c + 32; j += 8) {
                                 float o[8];
-                                ld_global_v8(s + 8 * j, o);
+                                ld_global_v8(s + j, o);
 #pragma unroll
-                                for (int i = 0; i < 8; ++i) v[8 * j + i] += o[i];
+                                for (int i = 0; i < 8; ++i) v[j + i] += o[i];
                             }
                         } else {
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (col + j < args.cols) v[j] += s[j];
+                            for (int j = c; j < c + 32; ++j)
+                                if (j < cols) v[j] += s[j];
                         }
                     }
                     if (args.finish) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] *= down;
-                        store16_32<BF16>(v, static_cast<uint16_t *>(args.out) +
-                                                static_cast<int64_t>(args.index[row]) * args.pitch,
-                                         col, args.cols);
+                        for (int j = c; j < c + 32; ++j) v[j] *= down;
+                        store16_32<BF16>(v + c, static_cast<uint16_t *>(args.out) +
+                                                    static_cast<int64_t>(args.index[row]) * args.pitch,
+                                         c0 + c, args.cols);
                     } else if (whole) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
+                        for (int j = c; j < c + 32; j += 8) {
                             uint32_t o[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[8 * j + i]);
-                            st_global_v8(s + 8 * j, o);
+                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[j + i]);
+                            st_global_v8(s + j, o);
                         }
                     } else {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (col + j < args.cols) s[j] = v[j];
+                        for (int j = c; j < c + 32; ++j)
+                            if (j < cols) s[j] = v[j];
                     }
                 }
             }
-            if constexpr (MODE == kCeLse) {
-                if (row < count && c0 < args.cols)
-                    args.part[static_cast<int64_t>(c0 / 128) * args.part_pitch + row] = make_float2(top, sum);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_cluster(acc_empty_leader + 8u * static_cast<uint32_t>(acc));
-            if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
         }
     }
 
