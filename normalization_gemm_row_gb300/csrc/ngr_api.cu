@@ -396,7 +396,10 @@ void kernel_begin(cudaStream_t stream) { event_before(stream); }
 void kernel_end(cudaStream_t stream) { event_after(stream); }
 int call_end(int rc, void *ws, cudaStream_t stream)
 {
-    if (rc != NGR_OK) return rc;
+    if (rc != NGR_OK) {
+        (void)cudaGetLastError();   // recorded already; not the next call's
+        return rc;
+    }
     events_call_done();
     if (ws) return finish(rc, ws, stream);
     cudaError_t e = cudaGetLastError();

@@ -142,7 +142,7 @@ int64_t tiles_of(int64_t rows, int64_t cols)
         kernel_begin(stream);    \
         rc = (CALL);             \
         kernel_end(stream);      \
-        if (rc != NGR_OK) return rc; \
+        if (rc != NGR_OK) return call_end(rc, nullptr, stream); \
     } while (0)
 
 int ce_forward(const void *x, const void *W, const int64_t *target, float logit_scale, int64_t M, int64_t K,

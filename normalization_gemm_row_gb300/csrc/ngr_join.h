@@ -11,19 +11,29 @@ namespace ngr {
 
 constexpr int kJoinThreads = 512;      // threads per CTA at most
 constexpr int kJoinMaxCluster = 8;     // CTAs that share one row at most
-constexpr int kJoinMaxVecs = 4;        // 8-element vectors per thread and row at most
 constexpr int64_t kJoinMaxN = 65536;   // widest row
-// Shared memory for the backward kernel's column sums, at most (of 227 KB).
-constexpr int kJoinSumBytes = 200 * 1024;
-// CTAs the backward kernel runs at most (its partial sums are one row per
-// CTA, so their number is fixed here and not by the device: sizing needs no GPU).
-constexpr int kJoinCtas = 152;
+constexpr int64_t kJoinSmem = 224 * 1024;   // shared memory of an SM for its CTAs' rings and sums
+constexpr int kJoinForwardCols = 8192;    // columns a CTA takes at most: 256 threads x 4 vectors
+constexpr int kJoinBackwardCols = 8192;   // 512 threads x 2 vectors
+// Both kernels are persistent, per_sm CTAs on each SM.  The backward's
+// partial sums are rows per CTA, so the number of SMs is fixed here and not
+// asked of the device: sizing needs no GPU.
+constexpr int kJoinSms = 152;
+
+// How a row's elements are reached, by the alignment of the call's pointers.
+//   kJoinAligned  every row starts on a 16-byte boundary and has whole
+//                 8-element vectors;
+//   kJoinWindow   the [M, N] arrays have the same offset from a 16-byte
+//                 boundary but N % 8 != 0 (or the offset is not 0): a row is
+//                 covered by aligned vectors, those at its ends in part;
+//   kJoinScalar   anything else, one 2-byte access per element.
+enum { kJoinAligned = 0, kJoinWindow = 1, kJoinScalar = 2 };
 
 // How rows map to CTAs: `cluster` CTAs share a row, `cols` columns each (a
 // multiple of 8); a CTA of tpr * slots threads works on `slots` rows at a
 // time, tpr threads (a multiple of 32) of `vecs` vectors on each.
 struct JoinShape {
-    int cluster, cols, vecs, tpr, slots;
+    int cluster, cols, vecs, tpr, slots, per_sm;
 };
 
 struct JoinArgs {
@@ -34,38 +44,44 @@ struct JoinArgs {
     void *dx, *dresidual, *dgate;               // backward outputs
     float4 *stats;                              // [M] (mu1, rstd1, mu2, rstd2)
     int *err;                                   // backward: the workspace's error word, cleared
-    float *partials;                            // backward: per-CTA sums ([arrays but dgate][CTAs][N])
     int64_t M, rows_per_gate;
     int N, norm1, norm2;
     float eps1, eps2, residual_scale, block_scale;
+    int shift;                                  // kJoinWindow: the arrays' offset in elements
     JoinShape shape;
     // Backward: the rows are cut into items of item_rows rows that lie in
     // one gate group each; group g has items [g * items_per_group, +items_per_group).
     int64_t items, item_rows;
     int items_per_group;
-    // Row sums kept in shared memory and written to `partials`, -1 = not wanted:
-    // the place of each among a CTA's `arrays` rows.
-    // (dgate's, kept for one item at a time, is the last).
-    int a_dgamma1, a_dbeta1, a_dgamma2, a_dbeta2, a_dgate, arrays;
-    int dgate_direct;                           // one item per group: dgate is written by its CTA
-    float *gate_partials;                       // [items][N] otherwise
+    // Column sums, -1 = not wanted: their places among the `arrays` sums a
+    // CTA keeps in shared memory.  Over an item: p = sum u1 D, q = sum D
+    // (D the gradient of h), written to item_p, item_q [items][N].  Over a
+    // CTA: dgamma2, dbeta2, written to cta_sums [2][CTAs][N].  With
+    // fold_gate (small gate groups) p = sum gate u1 D and q = sum gate D run
+    // over the CTA too (cta_sums [4]), and dgate is summed over its group
+    // and written by the CTA itself.
+    int a_p, a_q, a_dgamma2, a_dbeta2, a_dgate, arrays;
+    int fold_gate;
+    int depth;                                  // rows under way per CTA slot (1 to 3)
+    float *item_p, *item_q, *cta_sums;
 };
 
-// What ngr_join_backward's second kernel adds up.
+// The second kernel of the backward call: vectors of N from the rows of sums.
 struct JoinReduce {
-    const float *src[5];        // rows of N floats
-    int64_t row_stride[5];      // floats between the rows of one sum
-    int rows[5];                // rows per sum
-    void *dst[5];               // rows of N of the call's type, one per sum
-    int64_t first[5];           // index of the first output row of source i among all
-    int sources, N;
-    int64_t total_outs;
+    const float *p, *q;          // [items][N] (or [CTAs][N] with fold_gate), null: not there
+    const float *dgamma2_rows, *dbeta2_rows;   // [ctas][N]
+    void *dgamma1, *dbeta1, *dgamma2, *dbeta2, *dgate;   // null: not wanted (or written already)
+    const void *gate, *gamma1, *beta1;         // null: 1, 1, 0
+    int64_t groups;
+    int items_per_group, ctas, pq_rows, N;
+    float block_scale;
+    int fold_gate;
 };
 
-JoinShape join_forward_shape(int64_t N);
-JoinShape join_backward_shape(int64_t N, int arrays);
-int launch_join_forward(bool bf16, bool vec, const JoinArgs &a, cudaStream_t stream);
-int launch_join_backward(bool bf16, bool vec, const JoinArgs &a, int ctas, cudaStream_t stream);
+JoinShape join_forward_shape(int64_t N, int mode);
+JoinShape join_backward_shape(int64_t N, int mode, int arrays);
+int launch_join_forward(bool bf16, int mode, const JoinArgs &a, cudaStream_t stream);
+int launch_join_backward(bool bf16, int mode, const JoinArgs &a, int ctas, cudaStream_t stream);
 int launch_join_reduce(bool bf16, const JoinReduce &r, cudaStream_t stream);
 
 }  // namespace ngr

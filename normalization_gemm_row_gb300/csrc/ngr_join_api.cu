@@ -15,37 +15,47 @@ namespace {
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool norm_kind(int n) { return n >= kNormNone && n <= kNormRms; }
 
+// Where the parts of the backward call's workspace lie, and how it cuts the
+// rows (see JoinArgs).
 struct JoinPlan {
     JoinShape shape;
-    int a_dgamma1 = -1, a_dbeta1 = -1, a_dgamma2 = -1, a_dbeta2 = -1, a_dgate = -1, arrays = 0;
-    int64_t groups = 1, group_rows = 0, items = 0, item_rows = 0;
+    int a_p = -1, a_q = -1, a_dgamma2 = -1, a_dbeta2 = -1, a_dgate = -1, arrays = 0;
+    int64_t groups = 1, group_rows = 0, items = 0, item_rows = 0, pq_rows = 0;
     int items_per_group = 1, ctas = 0;
-    size_t off_partials = 256, off_gate = 0, total = 256;
+    bool fold_gate = false;
+    size_t off_p = 256, off_q = 0, off_cta = 0, total = 256;
 };
+
+// A gate row of fewer tokens than this is applied row by row: writing the
+// sums p and q of an item costs 8 bytes a column, as much as two thirds of
+// a row's loads and stores, and the rows of sums would be as many as the
+// tokens.
+constexpr int64_t kFoldRows = 16;
 
 // The rows are cut so that every CTA gets the same number of rows as nearly
 // as the gate's groups allow: of the numbers of items per group, the one
 // with the least rows on the busiest CTA, an item counted as one row more
-// for writing its gate sums (N floats against a row's twelve bytes a column).
-JoinPlan join_plan(int64_t M, int64_t N, int64_t rows_per_gate, int norm1, int norm2)
+// for writing its sums.
+JoinPlan join_plan(int mode, int64_t M, int64_t N, int64_t rows_per_gate, int norm1, int norm2)
 {
     JoinPlan p;
-    if (norm1 != kNormNone) p.a_dgamma1 = p.arrays++;
-    if (norm1 == kNormLayer) p.a_dbeta1 = p.arrays++;
+    const bool gate = rows_per_gate > 0;
+    p.group_rows = gate ? std::min(rows_per_gate, M) : M;
+    p.fold_gate = gate && p.group_rows < kFoldRows && p.group_rows < M;
+    if (norm1 != kNormNone || (gate && !p.fold_gate)) p.a_p = p.arrays++;
+    if (norm1 == kNormLayer) p.a_q = p.arrays++;
     if (norm2 != kNormNone) p.a_dgamma2 = p.arrays++;
     if (norm2 == kNormLayer) p.a_dbeta2 = p.arrays++;
-    const bool gate = rows_per_gate > 0;
-    if (gate) p.a_dgate = p.arrays++;
-    p.shape = join_backward_shape(N, p.arrays);
-    p.group_rows = gate ? std::min(rows_per_gate, M) : M;
+    if (p.fold_gate) p.a_dgate = p.arrays++;
+    p.shape = join_backward_shape(N, mode, p.arrays);
     if (M == 0) return p;
     p.groups = (M + p.group_rows - 1) / p.group_rows;
-    const int64_t P = kJoinCtas / p.shape.cluster;
+    const int64_t P = std::max<int64_t>(1, kJoinSms * p.shape.per_sm / p.shape.cluster);
     const int64_t steps = (p.group_rows + p.shape.slots - 1) / p.shape.slots;
-    const int64_t most = std::min(steps, std::max<int64_t>(1, 4 * P / p.groups));
+    const int64_t most = p.fold_gate ? 1 : std::min(steps, std::max<int64_t>(1, 4 * P / p.groups));
     int64_t best = 0, best_cost = 0;
     for (int64_t c = 1; c <= most; ++c) {
-        const int64_t rows = (steps + c - 1) / c + (gate ? 1 : 0);
+        const int64_t rows = (steps + c - 1) / c + 1;
         const int64_t cost = (p.groups * c + P - 1) / P * rows;
         if (best == 0 || cost < best_cost) {
             best = c;
@@ -56,9 +66,11 @@ JoinPlan join_plan(int64_t M, int64_t N, int64_t rows_per_gate, int norm1, int n
     p.item_rows = (steps + best - 1) / best * p.shape.slots;
     p.items = p.groups * best;
     p.ctas = static_cast<int>(std::min(P, p.items));
+    p.pq_rows = p.fold_gate ? p.ctas : p.items;
     const size_t row = static_cast<size_t>(N) * sizeof(float);
-    p.off_gate = p.off_partials + static_cast<size_t>(p.arrays - (gate ? 1 : 0)) * p.ctas * row;
-    p.total = p.off_gate + (gate && best > 1 ? static_cast<size_t>(p.items) * row : 0);
+    p.off_q = p.off_p + (p.a_p >= 0 ? static_cast<size_t>(p.pq_rows) * row : 0);
+    p.off_cta = p.off_q + (p.a_q >= 0 ? static_cast<size_t>(p.pq_rows) * row : 0);
+    p.total = p.off_cta + static_cast<size_t>((p.a_dgamma2 >= 0) + (p.a_dbeta2 >= 0)) * p.ctas * row;
     return p;
 }
 
@@ -69,14 +81,26 @@ int join_sizes(int64_t M, int64_t N, int dtype)
     return NGR_OK;
 }
 
-// Whether the 16-byte kernels can run: NGR_ERR_ALIGN if not even 2-byte ones can.
-int join_alignment(std::initializer_list<const void *> ptrs, int64_t N, bool *vec)
+// How the rows can be reached (kJoin* mode, and `shift` for the window
+// mode): NGR_ERR_ALIGN if an address is not even that of a 16-bit element.
+int join_alignment(std::initializer_list<const void *> rows, std::initializer_list<const void *> vectors,
+                   int64_t N, int *mode, int *shift)
 {
-    *vec = N % 8 == 0;
-    for (const void *p : ptrs) {
+    bool same = true, vec = N % 8 == 0;
+    *shift = -1;
+    for (const void *p : rows) {
         if (!aligned(p, 2)) return NGR_ERR_ALIGN;
-        *vec = *vec && aligned(p, 16);
+        if (!p) continue;
+        const int at = static_cast<int>((reinterpret_cast<uintptr_t>(p) & 15u) / 2);
+        if (*shift < 0) *shift = at;
+        same = same && at == *shift;
     }
+    for (const void *p : vectors) {
+        if (!aligned(p, 2)) return NGR_ERR_ALIGN;
+        vec = vec && aligned(p, 16);
+    }
+    if (*shift < 0) *shift = 0;
+    *mode = !same ? kJoinScalar : vec && *shift == 0 ? kJoinAligned : kJoinWindow;
     return NGR_OK;
 }
 
@@ -154,16 +178,16 @@ int ngr_fused_norm_gate_residual_norm(int norm1, int norm2, const void *x, const
     a.h = h;
     a.y = norm2 != kNormNone ? y : nullptr;
     a.stats = reinterpret_cast<float4 *>(stats);
-    bool vec = false;
-    rc = join_alignment({x, residual, gate, a.gamma1, a.beta1, a.gamma2, a.beta2, h, a.y}, N, &vec);
+    int mode = 0;
+    rc = join_alignment({x, residual, h, a.y}, {gate, a.gamma1, a.beta1, a.gamma2, a.beta2}, N, &mode, &a.shift);
     if (rc != NGR_OK) return rc;
     int sms = 0;
     rc = device_sms(&sms);
     if (rc != NGR_OK) return rc;
-    a.shape = join_forward_shape(N);
+    a.shape = join_forward_shape(N, mode);
     call_begin();
     kernel_begin(stream);
-    rc = launch_join_forward(dtype == NGR_BF16, vec, a, stream);
+    rc = launch_join_forward(dtype == NGR_BF16, mode, a, stream);
     kernel_end(stream);
     return call_end(rc, nullptr, stream);
 }
@@ -172,7 +196,11 @@ size_t ngr_norm_gate_residual_norm_workspace_bytes(int norm1, int norm2, int64_t
                                                    int64_t N)
 {
     if (!norm_kind(norm1) || !norm_kind(norm2) || join_sizes(M, N, NGR_F16) != NGR_OK) return 0;
-    return join_plan(M, N, rows_per_gate, norm1, norm2).total;
+    // (the alignment of the pointers is not known here: the most of the modes)
+    size_t most = 0;
+    for (int mode : {kJoinAligned, kJoinWindow, kJoinScalar})
+        most = std::max(most, join_plan(mode, M, N, rows_per_gate, norm1, norm2).total);
+    return most;
 }
 
 int ngr_fused_norm_gate_residual_norm_backward(
@@ -199,13 +227,14 @@ int ngr_fused_norm_gate_residual_norm_backward(
         return NGR_ERR_NULL;
     if (norm2 == kNormNone) dy = nullptr;
     if (!aligned(stats, 16)) return NGR_ERR_ALIGN;
-    bool vec = false;
     JoinArgs a = join_args(x, residual, gate, rows_per_gate, norm1, gamma1, beta1, 0.0f, norm2, gamma2,
                            nullptr, 0.0f, residual_scale, block_scale, M, N);
-    rc = join_alignment({dy, dh, x, residual, gate, a.gamma1, a.beta1, a.gamma2, dx, dresidual,
-                         dgate, dgamma1, dbeta1, dgamma2, dbeta2}, N, &vec);
+    int mode = 0;
+    rc = join_alignment({dy, dh, x, residual, dx, dresidual},
+                        {gate, a.gamma1, a.beta1, a.gamma2, dgate, dgamma1, dbeta1, dgamma2, dbeta2}, N, &mode,
+                        &a.shift);
     if (rc != NGR_OK) return rc;
-    const JoinPlan p = join_plan(M, N, gate ? rows_per_gate : 0, norm1, norm2);
+    const JoinPlan p = join_plan(mode, M, N, gate ? rows_per_gate : 0, norm1, norm2);
     if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
     int sms = 0;
@@ -225,46 +254,49 @@ int ngr_fused_norm_gate_residual_norm_backward(
     a.dgate = dgate;
     a.stats = const_cast<float4 *>(reinterpret_cast<const float4 *>(stats));
     a.err = reinterpret_cast<int *>(ws);
-    a.partials = reinterpret_cast<float *>(ws + p.off_partials);
-    a.gate_partials = reinterpret_cast<float *>(ws + p.off_gate);
     a.shape = p.shape;
     a.items = p.items;
     a.item_rows = p.item_rows;
     a.items_per_group = p.items_per_group;
-    a.a_dgamma1 = p.a_dgamma1;
-    a.a_dbeta1 = p.a_dbeta1;
+    a.a_p = p.a_p;
+    a.a_q = p.a_q;
     a.a_dgamma2 = p.a_dgamma2;
     a.a_dbeta2 = p.a_dbeta2;
-    a.a_dgate = dgate ? p.a_dgate : -1;
-    a.arrays = p.arrays - (gate && !dgate ? 1 : 0);
-    a.dgate_direct = p.items_per_group == 1;
+    a.a_dgate = p.a_dgate;
+    a.arrays = p.arrays;
+    a.fold_gate = p.fold_gate;
+    a.item_p = reinterpret_cast<float *>(ws + p.off_p);
+    a.item_q = reinterpret_cast<float *>(ws + p.off_q);
+    a.cta_sums = reinterpret_cast<float *>(ws + p.off_cta);
 
     JoinReduce r;
     std::memset(&r, 0, sizeof(r));
+    r.p = p.a_p >= 0 ? a.item_p : nullptr;
+    r.q = p.a_q >= 0 ? a.item_q : nullptr;
+    r.dgamma2_rows = a.cta_sums;
+    r.dbeta2_rows = a.cta_sums + static_cast<int64_t>(p.ctas) * N;
+    r.dgamma1 = dgamma1;
+    r.dbeta1 = dbeta1;
+    r.dgamma2 = dgamma2;
+    r.dbeta2 = dbeta2;
+    r.dgate = p.fold_gate ? nullptr : dgate;
+    r.gate = gate;
+    r.gamma1 = a.gamma1;
+    r.beta1 = a.beta1;
+    r.groups = p.groups;
+    r.items_per_group = p.items_per_group;
+    r.ctas = p.ctas;
+    r.pq_rows = static_cast<int>(p.pq_rows);
     r.N = static_cast<int>(N);
-    auto source = [&](const float *src, int rows, void *dst, int64_t outs) {
-        if (!dst) return;
-        r.src[r.sources] = src;
-        r.row_stride[r.sources] = N;
-        r.rows[r.sources] = rows;
-        r.dst[r.sources] = dst;
-        r.first[r.sources] = r.total_outs;
-        r.total_outs += outs;
-        ++r.sources;
-    };
-    auto sum_of = [&](int k) { return a.partials + static_cast<int64_t>(k) * p.ctas * N; };
-    source(sum_of(p.a_dgamma1), p.ctas, dgamma1, 1);
-    source(sum_of(p.a_dbeta1), p.ctas, dbeta1, 1);
-    source(sum_of(p.a_dgamma2), p.ctas, dgamma2, 1);
-    source(sum_of(p.a_dbeta2), p.ctas, dbeta2, 1);
-    if (!a.dgate_direct) source(a.gate_partials, p.items_per_group, dgate, p.groups);
+    r.block_scale = block_scale;
+    r.fold_gate = p.fold_gate;
 
     const bool bf16 = dtype == NGR_BF16;
     call_begin();
     kernel_begin(stream);
-    rc = launch_join_backward(bf16, vec, a, p.ctas, stream);
+    rc = launch_join_backward(bf16, mode, a, p.ctas, stream);
     kernel_end(stream);
-    if (rc == NGR_OK && r.sources > 0) {
+    if (rc == NGR_OK && (dgamma1 || dbeta1 || dgamma2 || dbeta2 || r.dgate)) {
         kernel_begin(stream);
         rc = launch_join_reduce(bf16, r, stream);
         kernel_end(stream);

@@ -1,0 +1,203 @@
+// ngr_join_forward.cu -- the join of a block to its residual stream (see
+// ngr_join_kernel.cuh): TPR threads on a row, the row held in registers.
+//
+// The statistics are two-pass (mean, then centred squares), so a row far from
+// zero mean or with a few very large channels loses nothing.  Four vectors a
+// thread and four CTAs of 256 threads an SM (64 registers) keep enough loads
+// in flight: at 8192 x 8192, RMSNorm on both sides, three or five CTAs, two
+// or eight vectors, persistent CTAs that fetch the next row early, or a ring
+// of rows in shared memory all ran 2-60 % slower.
+#include <algorithm>
+
+#include "ngr_join_kernel.cuh"
+
+namespace ngr {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr unsigned kWave = 4 * kJoinSms;   // CTAs that run at once
+
+template <bool BF16, int MODE, int TPR, int VECS>
+__global__ void __launch_bounds__(kThreads, MODE == kJoinAligned ? 4 : 2)
+    join_forward_kernel(const __grid_constant__ JoinArgs a)
+{
+    constexpr int kSlots = kThreads / TPR;
+    __shared__ RowSumSmem sums;
+    int half = 0;
+    const int cluster = a.shape.cluster;
+    const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0u;
+    const int slot = threadIdx.x / TPR;
+    const int c0 = static_cast<int>(rank) * a.shape.cols;
+    const Place<MODE, TPR> p(c0, min(a.N, c0 + a.shape.cols), threadIdx.x % TPR);
+    const int64_t row = static_cast<int64_t>(blockIdx.x / cluster) * kSlots + slot;
+    const bool active = kSlots == 1 || row < a.M;
+    const int64_t off = active ? row * a.N : 0;
+    const int s = row_shift<MODE>(a, row);
+    const float inv_n = 1.0f / static_cast<float>(a.N);
+
+    uint4 xp[VECS], rp[VECS];
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) xp[v] = rp[v] = make_uint4(0u, 0u, 0u, 0u);
+    if (active) {
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) xp[v] = load8(elements(a.x, off), p, v, s);
+        if (a.residual) {
+#pragma unroll
+            for (int v = 0; v < VECS; ++v) rp[v] = load8(elements(a.residual, off), p, v, s);
+        }
+    }
+    const uint16_t *gate = nullptr;
+    if (a.gate) gate = elements(a.gate, a.rows_per_gate >= a.M || !active ? 0 : row / a.rows_per_gate * a.N);
+    // In a call of one wave the vectors are in no cache: they are on their way
+    // while x is reduced.  (With more rows the CTAs before have brought them,
+    // and asking again for each row tripled the time at narrow widths.)
+    if (gridDim.x <= kWave) {
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            const int c = p.col(v, 0, 0);
+            if (c < p.c1) {
+                if (gate) prefetch_l1(gate + c);
+                if (a.gamma1) prefetch_l1(elements(a.gamma1, c));
+                if (a.gamma2) prefetch_l1(elements(a.gamma2, c));
+            }
+        }
+    }
+    // Every CTA of the cluster runs before its shared memory is written.
+    if (cluster > 1) cluster_sync_all();
+
+    float mu1 = 0.0f, rs1 = 1.0f;
+    if (a.norm1 == kNormLayer) {
+        float2 t = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) sum8(t, unpack8<BF16>(xp[v]));   // zero past the row
+        float k[1] = {t.x + t.y};
+        row_sum<1, TPR>(k, sums, half, cluster, rank);
+        mu1 = k[0] * inv_n;
+    }
+    if (a.norm1 != kNormNone) {
+        float2 t = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            Vec8 d = unpack8<BF16>(xp[v]);
+            if (a.norm1 == kNormLayer) d = masked(d + -mu1, p, v, s);
+            dot8(t, d, d);
+        }
+        float k[1] = {t.x + t.y};
+        row_sum<1, TPR>(k, sums, half, cluster, rank);
+        rs1 = rsqrtf(k[0] * inv_n + a.eps1);
+    }
+
+    Vec8 h[VECS];
+#pragma unroll
+    for (int v = 0; v < VECS; ++v) {
+        Vec8 n = unpack8<BF16>(xp[v]);
+        if (a.norm1 == kNormLayer) n = n + -mu1;
+        if (a.norm1 != kNormNone) n = n * rs1 * param8<BF16>(elements(a.gamma1), p, v, s);
+        if (a.norm1 == kNormLayer) n = n + param8<BF16>(elements(a.beta1), p, v, s);
+        if (gate) n = n * param8<BF16>(gate, p, v, s);
+        h[v] = fma8(unpack8<BF16>(rp[v]), a.residual_scale, n * a.block_scale);
+        if (active) store8(elements(a.h, off), p, v, s, pack8<BF16>(h[v]));
+    }
+
+    float mu2 = 0.0f, rs2 = 1.0f;
+    if (a.norm2 == kNormLayer) {
+        float2 t = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) sum8(t, masked(h[v], p, v, s));
+        float k[1] = {t.x + t.y};
+        row_sum<1, TPR>(k, sums, half, cluster, rank);
+        mu2 = k[0] * inv_n;
+    }
+    if (a.norm2 != kNormNone) {
+        float2 t = both(0.0f);
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            if (a.norm2 == kNormLayer) h[v] = h[v] + -mu2;
+            const Vec8 d = masked(h[v], p, v, s);
+            dot8(t, d, d);
+        }
+        float k[1] = {t.x + t.y};
+        row_sum<1, TPR>(k, sums, half, cluster, rank);
+        rs2 = rsqrtf(k[0] * inv_n + a.eps2);
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            Vec8 y = h[v] * rs2 * param8<BF16>(elements(a.gamma2), p, v, s);
+            if (a.norm2 == kNormLayer) y = y + param8<BF16>(elements(a.beta2), p, v, s);
+            if (active) store8(elements(a.y, off), p, v, s, pack8<BF16>(y));
+        }
+    }
+    if (a.stats && active && threadIdx.x % TPR == 0 && rank == 0) a.stats[row] = make_float4(mu1, rs1, mu2, rs2);
+}
+
+// Threads on a row and vectors a thread, by the vectors they hold: a warp a
+// row while five vectors a lane cover it (its sums need no barrier), then
+// three or four vectors a thread.
+struct Width {
+    int tpr, vecs;
+};
+constexpr Width kWidths[] = {{32, 1}, {32, 2}, {32, 3}, {32, 4}, {32, 5}, {64, 3}, {64, 4},
+                             {128, 3}, {128, 4}, {256, 3}, {256, 4}};
+
+template <bool BF16, int MODE>
+int run(const JoinArgs &a, cudaStream_t stream)
+{
+    const int64_t ctas = (a.M + a.shape.slots - 1) / a.shape.slots;
+#define NGR_WIDTH(T, V)                           \
+    if (a.shape.tpr == T && a.shape.vecs == V)    \
+        return launch_join(join_forward_kernel<BF16, MODE, T, V>, ctas, a.shape, 0, a, stream, "join launch");
+    NGR_WIDTH(256, 4)
+    if constexpr (MODE != kJoinScalar) {
+        NGR_WIDTH(32, 1)
+        NGR_WIDTH(32, 2)
+        NGR_WIDTH(32, 3)
+        NGR_WIDTH(32, 4)
+        NGR_WIDTH(32, 5)
+        NGR_WIDTH(64, 3)
+        NGR_WIDTH(64, 4)
+        NGR_WIDTH(128, 3)
+        NGR_WIDTH(128, 4)
+        NGR_WIDTH(256, 3)
+    }
+#undef NGR_WIDTH
+    return -9;
+}
+
+}  // namespace
+
+JoinShape join_forward_shape(int64_t N, int mode)
+{
+    JoinShape s;
+    s.cluster = 1;
+    auto cols = [&] { return up8((N + s.cluster - 1) / s.cluster); };
+    while (cols() + (mode == kJoinWindow ? 8 : 0) > kJoinForwardCols) s.cluster *= 2;
+    s.cols = static_cast<int>(cols());
+    s.tpr = 256;
+    s.vecs = 4;
+    if (mode != kJoinScalar) {
+        for (const Width &w : kWidths) {
+            if (w.tpr * w.vecs < join_vectors(s, mode)) continue;
+            s.tpr = w.tpr;
+            s.vecs = w.vecs;
+            break;
+        }
+    }
+    s.slots = kThreads / s.tpr;
+    // (a cluster works on one row at a time)
+    if (s.cluster > 1) {
+        s.tpr = 256;
+        s.vecs = join_vectors(s, mode) <= 768 && mode != kJoinScalar ? 3 : 4;
+        s.slots = 1;
+    }
+    s.per_sm = 0;
+    return s;
+}
+
+int launch_join_forward(bool bf16, int mode, const JoinArgs &a, cudaStream_t stream)
+{
+    if (mode == kJoinAligned) return bf16 ? run<true, kJoinAligned>(a, stream) : run<false, kJoinAligned>(a, stream);
+    if (mode == kJoinWindow) return bf16 ? run<true, kJoinWindow>(a, stream) : run<false, kJoinWindow>(a, stream);
+    return bf16 ? run<true, kJoinScalar>(a, stream) : run<false, kJoinScalar>(a, stream);
+}
+
+}  // namespace ngr

@@ -1,0 +1,123 @@
+// ngr_join_reduce.cu -- the second kernel of the join's gradient: the vectors
+// of the row's width from the sums that the CTAs left, and the choice of the
+// first kernel's shape.
+#include "ngr_join_backward.cuh"
+
+namespace ngr {
+
+namespace {
+
+// ---------------------------------------------------------------- last sums
+constexpr int kReduceCols = 32, kReduceLanes = 16;
+
+// Output row o (0-3 dgamma1, dbeta1, dgamma2, dbeta2, then the gate's rows)
+// at 32 columns: the rows of sums are added in a fixed order, 16 lanes of
+// threads taking every 16th row.
+template <bool BF16>
+__global__ void __launch_bounds__(kReduceCols *kReduceLanes) join_reduce_kernel(const __grid_constant__ JoinReduce r)
+{
+    __shared__ float2 part[kReduceLanes][kReduceCols];
+    const int tx = threadIdx.x % kReduceCols, ty = threadIdx.x / kReduceCols;
+    const int col = blockIdx.x * kReduceCols + tx;
+    const bool in = col < r.N;
+    const uint16_t *gate = static_cast<const uint16_t *>(r.gate);
+    for (int64_t o = blockIdx.y; o < 4 + (r.dgate ? r.groups : 0); o += gridDim.y) {
+        void *dst = o == 0 ? r.dgamma1 : o == 1 ? r.dbeta1 : o == 2 ? r.dgamma2 : o == 3 ? r.dbeta2 : r.dgate;
+        if (!dst) continue;
+        float2 t = make_float2(0.0f, 0.0f);
+        if (in && o < 2) {
+            const float *src = o == 0 ? r.p : r.q;
+            for (int i = ty; i < r.pq_rows; i += kReduceLanes) {
+                const float f = src[static_cast<int64_t>(i) * r.N + col];
+                const float g = r.fold_gate ? 1.0f
+                                : gate ? r.block_scale * widen16<BF16>(gate[static_cast<int64_t>(i / r.items_per_group) * r.N + col])
+                                       : r.block_scale;
+                t.x += g * f;
+            }
+        } else if (in && o < 4) {
+            const float *src = o == 2 ? r.dgamma2_rows : r.dbeta2_rows;
+            for (int i = ty; i < r.ctas; i += kReduceLanes) t.x += src[static_cast<int64_t>(i) * r.N + col];
+        } else if (in) {
+            const int64_t i0 = (o - 4) * r.items_per_group;
+            for (int i = ty; i < r.items_per_group; i += kReduceLanes) {
+                t.x += r.p[(i0 + i) * r.N + col];
+                if (r.q) t.y += r.q[(i0 + i) * r.N + col];
+            }
+        }
+        part[ty][tx] = t;
+        __syncthreads();
+        if (ty == 0 && in) {
+            t = make_float2(0.0f, 0.0f);
+#pragma unroll
+            for (int q = 0; q < kReduceLanes; ++q) {
+                t.x += part[q][tx].x;
+                t.y += part[q][tx].y;
+            }
+            if (o >= 4) {
+                const uint16_t *g1 = static_cast<const uint16_t *>(r.gamma1), *b1 = static_cast<const uint16_t *>(r.beta1);
+                t.x *= g1 ? widen16<BF16>(g1[col]) : 1.0f;
+                if (b1) t.x += t.y * widen16<BF16>(b1[col]);
+                t.x *= r.block_scale;
+            }
+            static_cast<uint16_t *>(dst)[(o >= 4 ? (o - 4) * r.N : 0) + col] = round16<BF16>(t.x);
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace
+
+JoinShape join_backward_shape(int64_t N, int mode, int arrays)
+{
+    JoinShape s;
+    s.cluster = 1;
+    auto cols = [&] { return up8((N + s.cluster - 1) / s.cluster); };
+    while (cols() + (mode == kJoinWindow ? 8 : 0) > kJoinBackwardCols) s.cluster *= 2;
+    for (;; s.cluster *= 2) {
+        s.cols = static_cast<int>(cols());
+        const int64_t n = join_vectors(s, mode);
+        // (a cluster works on one row at a time; the scalar mode, for pointers
+        // that no other takes, has two widths only)
+        s.tpr = 512;
+        s.vecs = 2;
+        for (const Width &w : kWidths) {
+            if (w.tpr * w.vecs < n || (s.cluster > 1 && w.tpr < 256)) continue;
+            if (mode == kJoinScalar && !(w.tpr == 64 && w.vecs == 2)) continue;
+            s.tpr = w.tpr;
+            s.vecs = w.vecs;
+            break;
+        }
+        s.slots = backward_slots(s.tpr);
+        // As many CTAs as the SM has registers for, and shared memory for
+        // their sums and a row each.
+        const int64_t bytes = sum_bytes(s, arrays) + ring_row(s) + 2048;
+        s.per_sm = static_cast<int>(std::min<int64_t>(backward_ctas(s.tpr, s.vecs), kJoinSmem / bytes));
+        if (s.per_sm >= 1) return s;
+    }
+}
+
+int launch_join_backward_bf16_ln(int mode, const JoinArgs &a, int ctas, cudaStream_t stream);
+int launch_join_backward_bf16_rms(int mode, const JoinArgs &a, int ctas, cudaStream_t stream);
+int launch_join_backward_f16_ln(int mode, const JoinArgs &a, int ctas, cudaStream_t stream);
+int launch_join_backward_f16_rms(int mode, const JoinArgs &a, int ctas, cudaStream_t stream);
+
+int launch_join_backward(bool bf16, int mode, const JoinArgs &a, int ctas, cudaStream_t stream)
+{
+    if (a.norm1 == kNormLayer || a.norm2 == kNormLayer)
+        return bf16 ? launch_join_backward_bf16_ln(mode, a, ctas, stream) : launch_join_backward_f16_ln(mode, a, ctas, stream);
+    return bf16 ? launch_join_backward_bf16_rms(mode, a, ctas, stream) : launch_join_backward_f16_rms(mode, a, ctas, stream);
+}
+
+int launch_join_reduce(bool bf16, const JoinReduce &r, cudaStream_t stream)
+{
+    if (!r.dgamma1 && !r.dbeta1 && !r.dgamma2 && !r.dbeta2 && !r.dgate) return 0;
+    const int64_t outs = 4 + (r.dgate ? r.groups : 0);
+    const dim3 grid(static_cast<unsigned>((r.N + kReduceCols - 1) / kReduceCols),
+                    static_cast<unsigned>(outs < 1024 ? outs : 1024));
+    if (bf16) join_reduce_kernel<true><<<grid, kReduceCols * kReduceLanes, 0, stream>>>(r);
+    else join_reduce_kernel<false><<<grid, kReduceCols * kReduceLanes, 0, stream>>>(r);
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? 0 : record_cuda_error("join sums launch", e, cudaGetErrorString(e));
+}
+
+}  // namespace ngr

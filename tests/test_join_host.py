@@ -58,22 +58,19 @@ def test_backward_refuses(kw, expect):
 
 def test_workspace_bytes():
     f = B.ngr_norm_gate_residual_norm_workspace_bytes
-    # without a gate: one row of FP32 sums per CTA (152 at most) and sum
-    assert f(2, 2, 0, 8192, 4096) == 256 + 2 * 152 * 4096 * 4
-    assert f(1, 1, 0, 3, 64) == 256 + 4 * 1 * 64 * 4          # one CTA holds 16 rows of 64
-    assert f(0, 0, 0, 100, 64) == 256
-    # one gate: its sums once per item as well
-    assert f(2, 2, 8192, 8192, 4096) == 256 + 3 * 152 * 4096 * 4
-    # a gate row per token: written directly
-    assert f(0, 2, 1, 400, 4096) == 256 + 1 * 152 * 4096 * 4
+    # a row of FP32 sums for each CTA (two an SM at this width) and sum
+    assert f(2, 2, 0, 8192, 4096) == 256 + 2 * 304 * 4096 * 4
+    assert f(2, 2, 8192, 8192, 4096) == f(2, 2, 0, 8192, 4096)
+    assert f(0, 0, 0, 100, 64) == 256                         # no sums without a norm or a gate
+    assert f(0, 2, 1, 400, 4096) == 256 + 304 * 4096 * 4      # dgate of one token each: written directly
     for bad in ((3, 2, 0, 8, 8), (2, 2, 0, -1, 8), (2, 2, 0, 8, 0), (2, 2, 0, 8, 65537)):
         assert f(*bad) == 0
     assert f(2, 2, 0, 0, 64) == 256
-    # within a few rows of sums per CTA at any size
+    # a few rows of sums per CTA, or one per gate row of 16 tokens or more
     for M in (1, 17, 1000, 100000):
         for g in (0, 1, 7, M):
             for N in (8, 999, 16384, 65536):
-                assert f(1, 1, g, M, N) <= 256 + (4 * 152 + 4 * 152 + M) * N * 4
+                assert f(1, 1, g, M, N) <= 256 + (2 * 4 * 1520 + 2 * 1520 + 2 * M) * N * 4
 
 
 def test_helper_refuses():
