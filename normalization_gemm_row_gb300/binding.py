@@ -553,37 +553,31 @@ def _tokens(x, what, *ts):
             raise ValueError(f"{what} must have x's shape")
 
 
-class _Launch:
-    """Makes the tensors' device current and gives the stream to launch on
-    (the current one of that device by default).  Tensors that were
-    allocated for a call on another stream are kept from reuse until that
-    stream is done with them."""
+# The handle of a device's current stream.  torch.cuda.current_stream builds a
+# stream object for it first, a tenth of a short call's host time.
+_current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                 lambda index: torch.cuda.current_stream(index).cuda_stream)
 
-    __slots__ = ("device", "given", "back", "stream")
 
-    def __init__(self, device, stream):
-        self.device, self.given, self.back = device, stream, None
+def _on_device(x):
+    """Whether x's device is the current one (the library launches there)."""
+    return x.get_device() == torch.cuda.current_device()
 
-    def __enter__(self):
-        now = torch.cuda.current_device()
-        if now != self.device.index:
-            self.back = now
-            torch.cuda.set_device(self.device)
-        self.stream = _stream(self.given)
-        return self
 
-    def hold(self, *tensors):
-        if self.given is None or self.stream == torch.cuda.current_stream().cuda_stream:
-            return
-        s = self.given if isinstance(self.given, torch.cuda.Stream) else torch.cuda.ExternalStream(self.stream)
+def _launch_stream(x, stream, *tensors):
+    """The stream handle to launch on (by default the current one of x's
+    device).  The tensors that were allocated for the call are kept from
+    reuse until a stream other than the current one is done with them."""
+    current = _current_stream_handle(x.get_device())
+    if stream is None:
+        return current
+    handle = _stream(stream)
+    if handle != current:
+        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle)
         for t in tensors:
             if t is not None:
                 t.record_stream(s)
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            torch.cuda.set_device(self.back)
-        return False
+    return handle
 
 
 def _scratch(nbytes, device, workspace):
@@ -632,6 +626,11 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
         x, gate, norm1, gamma1, beta1, norm2, gamma2, beta2)
     _tokens(x, "residual, h and out", residual, h, out)
     code = _uniform(x, residual, gate, gamma1, beta1, gamma2, beta2, h, out)
+    if not _on_device(x):
+        with torch.cuda.device(x.device):
+            return fused_norm_gate_residual_norm(
+                x, residual, gate, norm1, gamma1, beta1, eps1, norm2, gamma2, beta2, eps2,
+                residual_scale, block_scale, h, out, return_stats, stream)
     if h is None:
         h = torch.empty_like(x)
     if norm2 == NORM_NONE:
@@ -639,13 +638,11 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
     elif out is None:
         out = torch.empty_like(x)
     st = torch.empty((M, 4), dtype=torch.float32, device=x.device) if return_stats else None
-    with _Launch(x.device, stream) as on:
-        rc = lib().ngr_fused_norm_gate_residual_norm(
-            norm1, norm2, _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1), _ptr(beta1),
-            _ptr(gamma2), _ptr(beta2), eps1, eps2, residual_scale, block_scale, M, N, code, _ptr(h),
-            _ptr(out), _ptr(st), on.stream)
-        _raise(rc, "fused_norm_gate_residual_norm")
-        on.hold(h, out, st)
+    rc = lib().ngr_fused_norm_gate_residual_norm(
+        norm1, norm2, _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1), _ptr(beta1),
+        _ptr(gamma2), _ptr(beta2), eps1, eps2, residual_scale, block_scale, M, N, code, _ptr(h),
+        _ptr(out), _ptr(st), _launch_stream(x, stream, h, out, st))
+    _raise(rc, "fused_norm_gate_residual_norm")
     return (h, out, st) if return_stats else (h, out)
 
 
@@ -666,6 +663,11 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     if (stats.dtype != torch.float32 or stats.numel() != 4 * M or stats.device != x.device
             or not stats.is_contiguous()):
         raise ValueError("stats must be the float32 [M, 4] of the forward call")
+    if not _on_device(x):
+        with torch.cuda.device(x.device):
+            return fused_norm_gate_residual_norm_backward(
+                dy, dh, x, residual, stats, gate, norm1, gamma1, beta1, eps1, norm2, gamma2, beta2,
+                eps2, residual_scale, block_scale, workspace, stream)
     like = torch.empty_like
     dx = like(x)
     dr = like(residual) if residual is not None else None
@@ -678,14 +680,12 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     db2 = like(gamma2) if norm2 == NORM_LAYER else None
     ws = _scratch(lib().ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rpg, M, N),
                   x.device, workspace)
-    with _Launch(x.device, stream) as on:
-        rc = lib().ngr_fused_norm_gate_residual_norm_backward(
-            norm1, norm2, _ptr(dy), _ptr(dh), _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1),
-            _ptr(beta1), _ptr(gamma2), _ptr(stats), residual_scale, block_scale, M, N, code, _ptr(dx),
-            _ptr(dr), _ptr(dg), _ptr(dg1), _ptr(db1), _ptr(dg2), _ptr(db2), _ptr(ws),
-            ws.numel() * ws.element_size(), on.stream)
-        _raise(rc, "fused_norm_gate_residual_norm_backward")
-        on.hold(dx, dr, dg, dg1, db1, dg2, db2, ws)
+    rc = lib().ngr_fused_norm_gate_residual_norm_backward(
+        norm1, norm2, _ptr(dy), _ptr(dh), _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1),
+        _ptr(beta1), _ptr(gamma2), _ptr(stats), residual_scale, block_scale, M, N, code, _ptr(dx),
+        _ptr(dr), _ptr(dg), _ptr(dg1), _ptr(db1), _ptr(dg2), _ptr(db2), _ptr(ws),
+        ws.numel() * ws.element_size(), _launch_stream(x, stream, dx, dr, dg, dg1, db1, dg2, db2, ws))
+    _raise(rc, "fused_norm_gate_residual_norm_backward")
     return {"dx": dx, "dresidual": dr, "dgate": dg, "dgamma1": dg1, "dbeta1": db1, "dgamma2": dg2,
             "dbeta2": db2}
 
@@ -719,15 +719,16 @@ def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, st
     negative; x [..., K], W [V, K], target [...] int64.  The logits are not
     kept."""
     M, K, V, code = _ce_operands(x, W, target)
+    if not _on_device(x):
+        with torch.cuda.device(x.device):
+            return fused_linear_cross_entropy(x, W, target, logit_scale, workspace, stream)
     loss = torch.empty(target.shape, dtype=torch.float32, device=x.device)
     lse = torch.empty_like(loss)
     ws = _scratch(lib().ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
-    with _Launch(x.device, stream) as on:
-        rc = lib().ngr_fused_linear_cross_entropy(_ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
-                                                  code, _ptr(loss), _ptr(lse), _ptr(ws),
-                                                  ws.numel() * ws.element_size(), on.stream)
-        _raise(rc, "fused_linear_cross_entropy")
-        on.hold(loss, lse, ws)
+    rc = lib().ngr_fused_linear_cross_entropy(
+        _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V, code, _ptr(loss), _ptr(lse), _ptr(ws),
+        ws.numel() * ws.element_size(), _launch_stream(x, stream, loss, lse, ws))
+    _raise(rc, "fused_linear_cross_entropy")
     return loss, lse
 
 
@@ -738,15 +739,18 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
     either output is None when not needed."""
     M, K, V, code = _ce_operands(x, W, target)
     _row_vectors(M, x.device, dloss, dlse, lse)
+    if not _on_device(x):
+        with torch.cuda.device(x.device):
+            return fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale, dlse,
+                                                       need_dx, need_dW, workspace, stream)
     dx = torch.empty_like(x) if need_dx else None
     dW = torch.empty_like(W) if need_dW else None
     ws = _scratch(lib().ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
-    with _Launch(x.device, stream) as on:
-        rc = lib().ngr_fused_linear_cross_entropy_backward(
-            _ptr(dloss), _ptr(dlse), _ptr(lse), _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
-            code, _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(), on.stream)
-        _raise(rc, "fused_linear_cross_entropy_backward")
-        on.hold(dx, dW, ws)
+    rc = lib().ngr_fused_linear_cross_entropy_backward(
+        _ptr(dloss), _ptr(dlse), _ptr(lse), _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
+        code, _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(),
+        _launch_stream(x, stream, dx, dW, ws))
+    _raise(rc, "fused_linear_cross_entropy_backward")
     return dx, dW
 
 

@@ -13,7 +13,7 @@ constexpr int kJoinThreads = 512;      // threads per CTA at most
 constexpr int kJoinMaxCluster = 8;     // CTAs that share one row at most
 constexpr int64_t kJoinMaxN = 65536;   // widest row
 constexpr int64_t kJoinSmem = 224 * 1024;   // shared memory of an SM for its CTAs' rings and sums
-constexpr int kJoinForwardCols = 8192;    // columns a CTA takes at most: 256 threads x 4 vectors
+constexpr int kJoinForwardCols = 16384;   // columns a CTA takes at most: 512 threads x 4 vectors
 constexpr int kJoinBackwardCols = 8192;   // 512 threads x 2 vectors
 // Both kernels are persistent, per_sm CTAs on each SM.  The backward's
 // partial sums are rows per CTA, so the number of SMs is fixed here and not

@@ -33,9 +33,9 @@ struct JoinPlan {
 constexpr int64_t kFoldRows = 16;
 
 // The rows are cut so that every CTA gets the same number of rows as nearly
-// as the gate's groups allow: of the numbers of items per group, the one
-// with the least rows on the busiest CTA, an item counted as one row more
-// for writing its sums.
+// as the gate's groups allow: of the numbers of items per group that fill the
+// CTAs one to four times over, the one with the least rows on the busiest
+// CTA, an item counted as one row more for writing its sums.
 JoinPlan join_plan(int mode, int64_t M, int64_t N, int64_t rows_per_gate, int norm1, int norm2)
 {
     JoinPlan p;
@@ -52,15 +52,11 @@ JoinPlan join_plan(int mode, int64_t M, int64_t N, int64_t rows_per_gate, int no
     p.groups = (M + p.group_rows - 1) / p.group_rows;
     const int64_t P = std::max<int64_t>(1, kJoinSms * p.shape.per_sm / p.shape.cluster);
     const int64_t steps = (p.group_rows + p.shape.slots - 1) / p.shape.slots;
-    const int64_t most = p.fold_gate ? 1 : std::min(steps, std::max<int64_t>(1, 4 * P / p.groups));
-    int64_t best = 0, best_cost = 0;
-    for (int64_t c = 1; c <= most; ++c) {
-        const int64_t rows = (steps + c - 1) / c + 1;
-        const int64_t cost = (p.groups * c + P - 1) / P * rows;
-        if (best == 0 || cost < best_cost) {
-            best = c;
-            best_cost = cost;
-        }
+    int64_t best = 1;
+    auto cost = [&](int64_t c) { return (p.groups * c + P - 1) / P * ((steps + c - 1) / c + 1); };
+    for (int64_t waves = 1; waves <= 4 && !p.fold_gate; ++waves) {
+        const int64_t c = std::min(steps, std::max<int64_t>(1, waves * P / p.groups));
+        if (cost(c) < cost(best)) best = c;
     }
     p.items_per_group = static_cast<int>(best);
     p.item_rows = (steps + best - 1) / best * p.shape.slots;

@@ -15,14 +15,15 @@ namespace ngr {
 
 namespace {
 
-constexpr int kThreads = 256;
+// Threads of a CTA: 256 (four CTAs an SM), 512 for the widest rows.
+__host__ __device__ constexpr int forward_threads(int tpr) { return tpr > 256 ? tpr : 256; }
 constexpr unsigned kWave = 4 * kJoinSms;   // CTAs that run at once
 
 template <bool BF16, int MODE, int TPR, int VECS>
-__global__ void __launch_bounds__(kThreads, MODE == kJoinAligned ? 4 : 2)
+__global__ void __launch_bounds__(forward_threads(TPR), (MODE == kJoinAligned ? 1024 : 512) / forward_threads(TPR))
     join_forward_kernel(const __grid_constant__ JoinArgs a)
 {
-    constexpr int kSlots = kThreads / TPR;
+    constexpr int kSlots = forward_threads(TPR) / TPR;
     __shared__ RowSumSmem sums;
     int half = 0;
     const int cluster = a.shape.cluster;
@@ -137,7 +138,7 @@ struct Width {
     int tpr, vecs;
 };
 constexpr Width kWidths[] = {{32, 1}, {32, 2}, {32, 3}, {32, 4}, {32, 5}, {64, 3}, {64, 4},
-                             {128, 3}, {128, 4}, {256, 3}, {256, 4}};
+                             {128, 3}, {128, 4}, {256, 3}, {256, 4}, {512, 3}, {512, 4}};
 
 template <bool BF16, int MODE>
 int run(const JoinArgs &a, cudaStream_t stream)
@@ -147,6 +148,7 @@ int run(const JoinArgs &a, cudaStream_t stream)
     if (a.shape.tpr == T && a.shape.vecs == V)    \
         return launch_join(join_forward_kernel<BF16, MODE, T, V>, ctas, a.shape, 0, a, stream, "join launch");
     NGR_WIDTH(256, 4)
+    NGR_WIDTH(512, 4)
     if constexpr (MODE != kJoinScalar) {
         NGR_WIDTH(32, 1)
         NGR_WIDTH(32, 2)
@@ -158,6 +160,7 @@ int run(const JoinArgs &a, cudaStream_t stream)
         NGR_WIDTH(128, 3)
         NGR_WIDTH(128, 4)
         NGR_WIDTH(256, 3)
+        NGR_WIDTH(512, 3)
     }
 #undef NGR_WIDTH
     return -9;
@@ -172,23 +175,15 @@ JoinShape join_forward_shape(int64_t N, int mode)
     auto cols = [&] { return up8((N + s.cluster - 1) / s.cluster); };
     while (cols() + (mode == kJoinWindow ? 8 : 0) > kJoinForwardCols) s.cluster *= 2;
     s.cols = static_cast<int>(cols());
-    s.tpr = 256;
-    s.vecs = 4;
-    if (mode != kJoinScalar) {
-        for (const Width &w : kWidths) {
-            if (w.tpr * w.vecs < join_vectors(s, mode)) continue;
-            s.tpr = w.tpr;
-            s.vecs = w.vecs;
-            break;
-        }
+    // (a cluster works on one row at a time; the scalar mode, for pointers
+    // that no other takes, has two widths only)
+    for (const Width &w : kWidths) {
+        s.tpr = w.tpr;
+        s.vecs = w.vecs;
+        if (w.tpr * w.vecs < join_vectors(s, mode) || (s.cluster > 1 && w.tpr < 256)) continue;
+        if (mode != kJoinScalar || (w.tpr >= 256 && w.vecs == 4)) break;
     }
-    s.slots = kThreads / s.tpr;
-    // (a cluster works on one row at a time)
-    if (s.cluster > 1) {
-        s.tpr = 256;
-        s.vecs = join_vectors(s, mode) <= 768 && mode != kJoinScalar ? 3 : 4;
-        s.slots = 1;
-    }
+    s.slots = forward_threads(s.tpr) / s.tpr;
     s.per_sm = 0;
     return s;
 }
