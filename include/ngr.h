@@ -327,8 +327,8 @@ int ngr_fused_linear_cross_entropy_backward(
     size_t workspace_bytes, ngr_stream_t stream);
 
 /* Bytes of workspace of the two calls above (0 for invalid sizes): the
- * counted tokens' rows, and forward 8 bytes per token and 128 vocabulary
- * entries, backward dz of a piece of the vocabulary (256 MB, or 4096 entries
+ * counted tokens' rows, and forward 16 bytes per token and tile of 128 to 256
+ * vocabulary entries, backward dz of a piece of the vocabulary (256 MB, or 4096 entries
  * if that is more) and FP32 sums of dx where it is not made in one go. */
 size_t ngr_linear_cross_entropy_workspace_bytes(int backward, int64_t M,
                                                 int64_t K, int64_t V);

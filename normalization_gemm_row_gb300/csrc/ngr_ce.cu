@@ -3,8 +3,8 @@
 //
 // Tokens whose target is negative take no part: the counted tokens' rows are
 // copied together, so that the products run over those alone, nothing a
-// masked row holds (infinities, NaN) reaches a sum, and every operand has
-// rows of a 16-byte pitch.  The copy moves 4 K bytes a token against the
+// masked row holds (infinities, NaN) reaches a sum, and the rows start on
+// 128-byte lines whatever K is.  The copy moves 4 K bytes a token against the
 // 2 K V operations of one product.
 #include "ngr_ce.h"
 #include "ngr_internal.h"
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kIndexThreads) ce_index_kernel(const __grid_co
 }
 
 // One CTA per row of the gathered matrix at a time: a counted token's row
-// (padded with zeros to K8), zero rows up to the next 64 (the contracted
+// (padded with zeros to Kx), zero rows up to the next 64 (the contracted
 // length of dW), and in the backward call each row's softmax constants and
 // zeros for the dx rows of the tokens that do not count.
 template <bool VEC>
@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const __grid_
     const int count = t.info->count;
     const int64_t filled = (static_cast<int64_t>(max(count, 1)) + 63) / 64 * 64;
     const int64_t last = filled > t.M ? filled : t.M;
-    const int vecs = static_cast<int>(t.K8 / 8);
+    const int vecs = static_cast<int>(t.Kx / 8), whole = static_cast<int>(t.K / 8);
     for (int64_t r = blockIdx.x; r < last; r += gridDim.x) {
         const int64_t token = r < t.M ? t.index[r] : 0;
         if (r < filled) {
@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const __grid_
                 uint4 d = make_uint4(0u, 0u, 0u, 0u);
                 if (r < count) {
                     if constexpr (VEC) {
-                        d = reinterpret_cast<const uint4 *>(src)[v];
+                        if (v < whole) d = reinterpret_cast<const uint4 *>(src)[v];
                     } else {
                         uint32_t w[4];
 #pragma unroll
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const __grid_
         if (t.dx && r >= count && r < t.M) {
             uint16_t *dst = static_cast<uint16_t *>(t.dx) + token * t.K;
             if constexpr (VEC) {
-                for (int v = threadIdx.x; v < vecs; v += kGatherThreads)
+                for (int v = threadIdx.x; v < whole; v += kGatherThreads)
                     reinterpret_cast<uint4 *>(dst)[v] = make_uint4(0u, 0u, 0u, 0u);
             } else {
                 for (int64_t c = threadIdx.x; c < t.K; c += kGatherThreads) dst[c] = 0;

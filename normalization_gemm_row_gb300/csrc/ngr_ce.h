@@ -13,7 +13,7 @@ namespace ngr {
 // row's (max, sum) in the epilogue or turned into dz; dx = dz W; dW = dz^T x.
 enum { kCeLse = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
 
-constexpr int kCeTile = 256;      // rows and columns of a CTA pair's output tile
+constexpr int kCeTile = 256;      // rows, and columns at most, of a CTA pair's output tile
 constexpr int kCeStages = 6;      // pipeline stages of 32 KB a CTA
 
 // What the kernels of a call learn of its tokens (device memory): `count`
@@ -48,6 +48,7 @@ struct alignas(128) CeGemmArgs {
     float scale;            // kCeLse: logit scale
     int v0;                 // first vocabulary entry of the piece
     const int *target;      // kCeLse: [count] targets of the counted tokens
+    int width;              // columns of a tile: a multiple of 32, 256 at most (256 for dx, dW)
     float2 *part;           // kCeLse: [2 column tiles][part_pitch] (max, sum) in powers of two
     int64_t part_pitch;
     float *z_target;        // kCeLse: [count] the target's logit
@@ -71,13 +72,14 @@ struct CeTokens {
     const float *lse;       // [M] (backward)
     void *dx;               // [M, K] or null: rows of tokens that do not count are zeroed
     float logit_scale;
-    int64_t M, K, V, K8;
+    int64_t M, K, V;
+    int64_t K8, Kx;         // K up to multiples of 8 (rows of W) and 64 (rows of xc)
     CeInfo *info;
     int *err;
     int *index;             // [M] counted tokens in order, the others behind them
     int *ctarget;           // [M] targets of the counted tokens
     CeRow *row;             // [M up to a tile] (backward)
-    void *xc;               // [M up to 64][K8] the counted tokens' rows, zeros behind
+    void *xc;               // [M up to 64][Kx] the counted tokens' rows, zeros behind
 };
 
 int launch_ce_index(const CeTokens &t, cudaStream_t stream);

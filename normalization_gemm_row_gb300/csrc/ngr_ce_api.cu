@@ -25,8 +25,45 @@ constexpr int64_t kPairs = 76;
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
 
+// Columns of the tiles of z (rows x cols): the width, a multiple of 32, at
+// which the CTA pairs are busiest, a tile counted as kTileCost columns more.
+constexpr int64_t kTileCost = 32;
+int tile_width(int64_t rows, int64_t cols)
+{
+    const int64_t m = (std::max<int64_t>(rows, 1) + kCeTile - 1) / kCeTile;
+    int best = kCeTile;
+    int64_t least = 0;
+    for (int w = kCeTile; w >= 128; w -= 32) {
+        const int64_t cost = (m * ((cols + w - 1) / w) + kPairs - 1) / kPairs * (w + kTileCost);
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = w;
+        }
+    }
+    return best;
+}
+
+// Few output tiles of dx: the vocabulary is cut into ranges whose sums are
+// added afterwards.  The number of ranges that leaves the busiest pair the
+// least k blocks, a tile counted as kSplitCost k blocks more (its sums are
+// written and read again), at least 8 k blocks a range.
+constexpr int64_t kSplitCost = 12;
+int64_t dx_splits(int64_t tiles, int64_t k_blocks)
+{
+    if (tiles >= 8 * kPairs) return 1;
+    int64_t best = 1, least = 0;
+    for (int64_t s = 1; s <= 32 && (s == 1 || k_blocks / s >= 8); ++s) {
+        const int64_t cost = (tiles * s + kPairs - 1) / kPairs * ((k_blocks + s - 1) / s + (s > 1 ? kSplitCost : 4));
+        if (least == 0 || cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
 struct CePlan {
-    int64_t K8, piece, pieces, splits, parts;
+    int64_t K8, Kx, piece, pieces, splits, parts;
     size_t info, index, ctarget, xc, wp, row, part, z_target, dz, sums, total;
 };
 
@@ -35,6 +72,7 @@ CePlan ce_plan(bool backward, int64_t M, int64_t K, int64_t V)
     CePlan p;
     std::memset(&p, 0, sizeof(p));
     p.K8 = up_to(K, 8);
+    p.Kx = up_to(K, kBK);
     size_t off = 256;   // error word
     auto take = [&](size_t bytes) {
         const size_t at = off;
@@ -44,10 +82,11 @@ CePlan ce_plan(bool backward, int64_t M, int64_t K, int64_t V)
     p.info = take(sizeof(CeInfo));
     p.index = take(static_cast<size_t>(M) * 4);
     p.ctarget = take(static_cast<size_t>(M) * 4);
-    p.xc = take(static_cast<size_t>(up_to(std::max<int64_t>(M, 1), 64)) * p.K8 * 2);
+    p.xc = take(static_cast<size_t>(up_to(std::max<int64_t>(M, 1), 64)) * p.Kx * 2);
     if (K % 8 != 0) p.wp = take(static_cast<size_t>(V) * p.K8 * 2);
     if (!backward) {
-        p.parts = (V + 127) / 128;
+        const int64_t w = tile_width(M, V);
+        p.parts = (V + w - 1) / w * 2;
         p.part = take(static_cast<size_t>(p.parts) * M * sizeof(float2));
         p.z_target = take(static_cast<size_t>(M) * 4);
     } else {
@@ -58,10 +97,7 @@ CePlan ce_plan(bool backward, int64_t M, int64_t K, int64_t V)
         p.pieces = (V + p.piece - 1) / p.piece;
         p.row = take(static_cast<size_t>(rows) * sizeof(CeRow));
         p.dz = take(static_cast<size_t>(rows) * p.piece * 2);
-        // Few output tiles of dx: the vocabulary is cut into ranges whose
-        // sums are added afterwards (at least 8 k blocks each).
-        const int64_t tiles = rows / kCeTile * ((K + kCeTile - 1) / kCeTile);
-        p.splits = std::max<int64_t>(1, std::min(kPairs / tiles, p.piece / kBK / 8));
+        p.splits = dx_splits(rows / kCeTile * ((K + kCeTile - 1) / kCeTile), p.piece / kBK);
         if (p.splits > 1 || p.pieces > 1)
             p.sums = take(static_cast<size_t>(p.splits) * M * K * sizeof(float));
     }
@@ -110,6 +146,7 @@ int ce_begin(CeCall *c, bool backward, const void *x, const void *W, const int64
     t.K = K;
     t.V = V;
     t.K8 = c->p.K8;
+    t.Kx = c->p.Kx;
     t.info = reinterpret_cast<CeInfo *>(ws + c->p.info);
     t.err = reinterpret_cast<int *>(ws);
     t.index = reinterpret_cast<int *>(ws + c->p.index);
@@ -129,12 +166,13 @@ CeGemmArgs ce_args(const CeCall &c)
     a.scale = c.t.logit_scale;
     a.scale2 = c.t.logit_scale * 1.4426950408889634f;
     a.splits = 1;
+    a.width = kCeTile;
     return a;
 }
 
-int64_t tiles_of(int64_t rows, int64_t cols)
+int64_t tiles_of(int64_t rows, int64_t cols, int64_t width = kCeTile)
 {
-    return (std::max<int64_t>(rows, 1) + kCeTile - 1) / kCeTile * ((cols + kCeTile - 1) / kCeTile);
+    return (std::max<int64_t>(rows, 1) + kCeTile - 1) / kCeTile * ((cols + width - 1) / width);
 }
 
 #define NGR_TIMED(CALL)          \
@@ -160,8 +198,9 @@ int ce_forward(const void *x, const void *W, const int64_t *target, float logit_
     rc = ce_begin(&c, false, x, W, target, logit_scale, M, K, V, dtype, workspace, workspace_bytes);
     if (rc != NGR_OK) return rc;
     CeGemmArgs a = ce_args(c);
-    if (!map_2d(&a.map_a, c.t.xc, c.bf16, up_to(M, 64), c.t.K8, kBM) ||
-        !map_2d(&a.map_b, c.W, c.bf16, V, c.t.K8, kBM))
+    a.width = tile_width(M, V);
+    if (!map_2d(&a.map_a, c.t.xc, c.bf16, up_to(M, 64), c.t.Kx, kBM) ||
+        !map_2d(&a.map_b, c.W, c.bf16, V, c.t.K8, static_cast<uint32_t>(a.width / 2)))
         return NGR_ERR_CUDA;
     a.cols = static_cast<int>(V);
     a.depth = static_cast<int>(c.t.K8);
@@ -172,7 +211,7 @@ int ce_forward(const void *x, const void *W, const int64_t *target, float logit_
     call_begin();
     NGR_TIMED(launch_ce_index(c.t, stream));
     NGR_TIMED(launch_ce_gather(c.t, stream));
-    NGR_TIMED(launch_ce_gemm(kCeLse, c.bf16, a, tiles_of(M, V), stream));
+    NGR_TIMED(launch_ce_gemm(kCeLse, c.bf16, a, tiles_of(M, V, a.width), stream));
     NGR_TIMED(launch_ce_loss(c.t, a.part, M, static_cast<int>(c.p.parts), a.z_target, loss, lse, stream));
     return call_end(rc, workspace, stream);
 }
@@ -215,8 +254,9 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
         const int64_t v0 = i * c.p.piece, n = std::min(c.p.piece, V - v0);
         const char *Wi = static_cast<const char *>(c.W) + v0 * c.t.K8 * 2;
         CeGemmArgs a = ce_args(c);
-        if (!map_2d(&a.map_a, c.t.xc, c.bf16, up_to(M, 64), c.t.K8, kBM) ||
-            !map_2d(&a.map_b, Wi, c.bf16, n, c.t.K8, kBM))
+        a.width = tile_width(M, n);
+        if (!map_2d(&a.map_a, c.t.xc, c.bf16, up_to(M, 64), c.t.Kx, kBM) ||
+            !map_2d(&a.map_b, Wi, c.bf16, n, c.t.K8, static_cast<uint32_t>(a.width / 2)))
             return NGR_ERR_CUDA;
         a.cols = static_cast<int>(n);
         a.depth = static_cast<int>(c.t.K8);
@@ -224,7 +264,7 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
         a.row = c.t.row;
         a.out = dz;
         a.pitch = c.p.piece;
-        NGR_TIMED(launch_ce_gemm(kCeGrad, c.bf16, a, tiles_of(M, n), stream));
+        NGR_TIMED(launch_ce_gemm(kCeGrad, c.bf16, a, tiles_of(M, n, a.width), stream));
         if (dx) {
             a = ce_args(c);
             if (!map_2d(&a.map_a, dz, c.bf16, rows, n, kBM, c.p.piece) ||
@@ -245,7 +285,7 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
         if (dW) {
             a = ce_args(c);
             if (!map_2d(&a.map_a, dz, c.bf16, rows, n, kBK, c.p.piece) ||
-                !map_2d(&a.map_b, c.t.xc, c.bf16, up_to(M, 64), c.t.K8, kBK))
+                !map_2d(&a.map_b, c.t.xc, c.bf16, up_to(M, 64), c.t.Kx, kBK))
                 return NGR_ERR_CUDA;
             a.rows = static_cast<int>(n);
             a.cols = static_cast<int>(K);

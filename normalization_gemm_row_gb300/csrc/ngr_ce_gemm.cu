@@ -19,18 +19,18 @@
 // to a part in 2^24 a step, always towards zero (measured: 6e-5 of a logit
 // after the 256 steps of K = 4096).  Every kChunk k blocks the accumulator is
 // therefore handed to the epilogue, which keeps the output in registers
-// (128 columns a thread) and adds the pieces there, rounding to nearest; the
+// (a row of up to 128 columns a thread) and adds the pieces there, rounding to nearest; the
 // loss's error against 64 bits falls from 5e-6 to below 1e-6, and the reads
 // hide under the products of the next piece.
 //
 // Bound by the tensor cores for batches of tokens, by reading W (or writing
 // dW) for a few tokens.  Per CTA a stage is 16 KB of A and 16 KB of B, six
-// stages deep; the two 256-column accumulators take turns, so a tile's
-// epilogue (8 warps, two per tensor-memory lane quarter) runs under the next
-// tile's products.
+// stages deep; the two 256-column accumulators take turns, so the epilogue (8
+// warps, two per tensor-memory lane quarter; 16 were 10 % slower) runs under
+// the next products.
 //
-// Warp roles: 0 TMA producer, 1 MMA issuer (even CTA), 2 tensor memory, 4-11
-// epilogue.  Barriers as in the CTA-pair tile kernel without a norm: full[s]
+// Warp roles: 0 TMA producer (and tensor memory), 1 MMA issuer (even CTA),
+// 4-11 epilogue.  Barriers as in the CTA-pair tile kernel without a norm: full[s]
 // on the leader, on which both CTAs' copies complete; empty[s] the leader's
 // commit to both; acc_full[a] the same at a tile's end; acc_empty[a] on the
 // leader, one arrival per epilogue warp of both CTAs.
@@ -41,9 +41,10 @@ namespace ngr {
 
 namespace {
 
-constexpr int kCeThreads = 384;
 constexpr int kCeEpilogueWarp0 = 4;
 constexpr int kCeEpilogueWarps = 8;
+constexpr int kCeThreads = 32 * (kCeEpilogueWarp0 + kCeEpilogueWarps);
+constexpr int kCePart = 128;                              // columns of a tile an epilogue warp takes at most
 // k blocks per accumulator: short for the logits, whose error shows in the
 // loss and, through the exponential, in dz; dx and dW are rounded to 16 bits.
 template <int MODE>
@@ -68,28 +69,38 @@ __device__ __forceinline__ void ld_global_v8(const float *p, float (&v)[8])
                  : "memory");
 }
 
-// Columns [c, min(c + 32, cols)) of a row of 16-bit values that starts at
-// `row`: whole sectors, 16-byte pieces or single elements by the alignment
-// of the row.
+// The first `n` of 128 values into a row of 16-bit values at `p`: whole
+// sectors, 16-byte pieces or single elements by the address and n.
 template <bool BF16>
-__device__ __forceinline__ void store16_32(const float *v, uint16_t *row, int c, int cols)
+__device__ __forceinline__ void store16(const float (&v)[kCePart], uint16_t *p, int n)
 {
-    uint32_t o[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j) o[j] = from_float2<BF16>(v[2 * j], v[2 * j + 1]);
-    uint16_t *p = row + c;
     const uintptr_t at = reinterpret_cast<uintptr_t>(p);
-    if (c + 32 <= cols && (at & 31u) == 0) {
-        st_global_v8(p, *reinterpret_cast<const uint32_t(*)[8]>(&o[0]));
-        st_global_v8(p + 16, *reinterpret_cast<const uint32_t(*)[8]>(&o[8]));
-    } else if (c + 32 <= cols && (at & 15u) == 0) {
+    if (n == kCePart && (at & 31u) == 0) {   // nearly always
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            reinterpret_cast<uint4 *>(p)[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
-    } else {
+        for (int c = 0; c < kCePart; c += 16) {
+            uint32_t o[8];
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (c + j < cols) p[j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+            for (int j = 0; j < 8; ++j) o[j] = from_float2<BF16>(v[c + 2 * j], v[c + 2 * j + 1]);
+            st_global_v8(p + c, o);
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < kCePart; c += 16) {
+        if (c >= n) break;
+        uint32_t o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[j] = from_float2<BF16>(v[c + 2 * j], v[c + 2 * j + 1]);
+        if (c + 16 <= n && (at & 31u) == 0) {
+            st_global_v8(p + c, o);
+        } else if (n % 8 == 0 && (at & 15u) == 0) {
+            *reinterpret_cast<uint4 *>(p + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            if (c + 16 <= n) *reinterpret_cast<uint4 *>(p + c + 8) = make_uint4(o[4], o[5], o[6], o[7]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j)
+                if (c + j < n) p[c + j] = static_cast<uint16_t>(o[j >> 1] >> (16 * (j & 1)));
+        }
     }
 }
 
@@ -97,13 +108,14 @@ __device__ __forceinline__ void store16_32(const float *v, uint16_t *row, int c,
 template <int MODE>
 struct CeUnits {
     int tiles, slow, kb_all, splits, kb_per_split;   // `fast` dimension first
-    int fast;
+    int fast, width;
     __device__ __forceinline__ CeUnits(const CeGemmArgs &a)
     {
         // (no counted token: one tile of zero rows, so that dW is written)
         const int n = max(a.info->count, 1);
         const int m_tiles = ((MODE == kCeDw ? a.rows : n) + kCeTile - 1) / kCeTile;
-        const int n_tiles = (a.cols + kCeTile - 1) / kCeTile;
+        width = a.width;
+        const int n_tiles = (a.cols + width - 1) / width;
         // z: the row tiles of one column tile run together, so W is read
         // once; dx, dW: the column tiles of one row tile, so dz is.
         constexpr bool kRowsFast = MODE == kCeLse || MODE == kCeGrad;
@@ -123,7 +135,7 @@ struct CeUnits {
     __device__ __forceinline__ int n0(int u) const
     {
         const int t = u / splits;
-        return ((MODE == kCeLse || MODE == kCeGrad) ? t / fast : t % fast) * kCeTile;
+        return ((MODE == kCeLse || MODE == kCeGrad) ? t / fast : t % fast) * width;
     }
     __device__ __forceinline__ int split(int u) const { return u % splits; }
     __device__ __forceinline__ int kb0(int u) const { return min(kb_all, split(u) * kb_per_split); }
@@ -135,8 +147,10 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
 {
     constexpr bool kAMn = MODE == kCeDw;
     constexpr bool kBMn = MODE == kCeDx || MODE == kCeDw;
-    constexpr uint32_t kIdesc = idesc_f16_major(BF16, kCeTile, kCeTile, kAMn, kBMn);
-    constexpr uint32_t kStageBytes = 2u * 2u * kCeOperand;   // both CTAs' copies
+    const int width = args.width;                            // columns of a tile
+    const uint32_t idesc = idesc_f16_major(BF16, kCeTile, width, kAMn, kBMn);
+    // both CTAs' copies of a stage (an MN-major B is copied in boxes of 64)
+    const uint32_t stage_bytes = 2u * (kCeOperand + (kBMn ? (width / 2 + 63) / 64 * kCeBox : width / 2 * kBK * 2));
     constexpr int kChunk = ce_chunk<MODE>();
 
     extern __shared__ uint8_t smem_raw[];
@@ -173,7 +187,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
         mbar_init(drain, 1);
         fence_mbarrier_init();
     }
-    if (warp == 2) {
+    if (warp == 0) {
+        __syncwarp();
         tmem_alloc_pair(tmem_slot, 512);
         tmem_relinquish_pair();
     }
@@ -189,7 +204,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
     const uint32_t acc_empty_leader = mapa_shared(smem_u32(acc_empty), 0);
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             const uint64_t keep = policy_evict_last(), stream = policy_evict_first();
             // z: x stays in L2, W streams through; dx: W's piece stays; dW: x.
             const uint64_t pol_a = (MODE == kCeLse || MODE == kCeGrad) ? keep : stream;
@@ -200,13 +215,13 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             bool ok = true;
             for (int u = first; ok && u < n_units; u += step) {
                 const int m0 = units.m0(u) + static_cast<int>(rank) * kBM;
-                const int n0 = units.n0(u) + static_cast<int>(rank) * kBM;
+                const int n0 = units.n0(u) + static_cast<int>(rank) * (width / 2);
                 for (int kb = units.kb0(u), end = units.kb1(u); kb < end; ++kb) {
                     if (!mbar_wait_ahead(&empty[stage], phase ^ 1u, wc)) { ok = false; break; }
                     const int kc = kb * kBK;
                     uint8_t *a = sA + stage * kCeOperand, *b = sB + stage * kCeOperand;
                     const uint32_t fb = full_leader + 8u * static_cast<uint32_t>(stage);
-                    if (leader) mbar_arrive_expect_tx(&full[stage], kStageBytes);
+                    if (leader) mbar_arrive_expect_tx(&full[stage], stage_bytes);
                     if constexpr (kAMn) {
                         tma_load_2d_pair(a, &args.map_a, fb, m0, kc, pol_a);
                         tma_load_2d_pair(a + kCeBox, &args.map_a, fb, m0 + 64, kc, pol_a);
@@ -215,7 +230,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
                     }
                     if constexpr (kBMn) {
                         tma_load_2d_pair(b, &args.map_b, fb, n0, kc, pol_b);
-                        tma_load_2d_pair(b + kCeBox, &args.map_b, fb, n0 + 64, kc, pol_b);
+                        if (width > 128) tma_load_2d_pair(b + kCeBox, &args.map_b, fb, n0 + 64, kc, pol_b);
                     } else {
                         tma_load_2d_pair(b, &args.map_b, fb, kc, n0, pol_b);
                     }
@@ -236,7 +251,11 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             }
         }
     } else if (warp == 1) {
-        if (leader && lane == 0) {
+        if (leader && elect_one()) {
+            // descriptors of stage 0; further stages and k steps add to the
+            // address field (16-byte units)
+            const uint64_t a0 = kAMn ? sdesc_mnmajor_sw128(smem_u32(sA), kCeBox) : sdesc_kmajor_sw128(smem_u32(sA));
+            const uint64_t b0 = kBMn ? sdesc_mnmajor_sw128(smem_u32(sB), kCeBox) : sdesc_kmajor_sw128(smem_u32(sB));
             int stage = 0;
             uint32_t phase = 0;
             int acc = 0;
@@ -253,15 +272,14 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
                     if (!mbar_wait_spin(&full[stage], phase, wc)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kCeTile);
-                    const uint32_t a = smem_u32(sA + stage * kCeOperand);
-                    const uint32_t b = smem_u32(sB + stage * kCeOperand);
+                    const uint64_t a = a0 + static_cast<uint32_t>(stage * (kCeOperand >> 4));
+                    const uint64_t b = b0 + static_cast<uint32_t>(stage * (kCeOperand >> 4));
 #pragma unroll
                     for (int k = 0; k < kBK / kUmmaK; ++k) {
-                        const uint64_t da = kAMn ? sdesc_mnmajor_sw128(a + k * 2048, kCeBox)
-                                                 : sdesc_kmajor_sw128(a + k * 32);
-                        const uint64_t db = kBMn ? sdesc_mnmajor_sw128(b + k * 2048, kCeBox)
-                                                 : sdesc_kmajor_sw128(b + k * 32);
-                        umma_f16_ss_pair(d, da, db, kIdesc, (!fresh || k != 0) ? 1u : 0u);
+                        // (16 k on: 2048 bytes in an MN-major tile, 32 in a K-major one)
+                        umma_f16_ss_pair(d, a + static_cast<uint32_t>(k * (kAMn ? 128 : 2)),
+                                         b + static_cast<uint32_t>(k * (kBMn ? 128 : 2)), idesc,
+                                         (!fresh || k != 0) ? 1u : 0u);
                     }
                     umma_commit_pair(&empty[stage], 0x3);
                     if (++stage == kCeStages) { stage = 0; phase ^= 1u; }
@@ -276,14 +294,15 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
         }
     } else if (warp >= kCeEpilogueWarp0) {
         const int q = warp & 3;                               // tensor-memory lane quarter
-        const int half = (warp - kCeEpilogueWarp0) >> 2;      // columns [128 half, +128) of the tile
+        const int piece = (warp - kCeEpilogueWarp0) >> 2;     // columns [piece width / 2, + width / 2)
+        const int n_piece = width >> 1;
         const int count = args.info->count;
         const float down = args.info->down;
         int acc = 0;
         uint32_t acc_phase = 0;
         for (int u = first; u < n_units; u += step) {
             const int row = units.m0(u) + static_cast<int>(rank) * kBM + q * 32 + lane;
-            const int c0 = units.n0(u) + half * 128;
+            const int c0 = units.n0(u) + piece * n_piece;
             CeRow cr{0.0f, 0.0f, 0.0f, -1};
             int target = -1;
             if constexpr (MODE == kCeGrad) {
@@ -293,17 +312,18 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             if constexpr (MODE == kCeLse) {
                 if (row < count) target = args.target[row] - c0;
             }
-            float v[128];
+            float v[kCePart];
 #pragma unroll
-            for (int j = 0; j < 128; ++j) v[j] = 0.0f;
+            for (int j = 0; j < kCePart; ++j) v[j] = 0.0f;
             bool ok = true;
             for (int kb = units.kb0(u), end = units.kb1(u); kb < end; kb += kChunk) {
                 if (!mbar_wait_warp_long(&acc_full[acc], acc_phase, wc)) { ok = false; break; }
                 tc_fence_after();
+                // (columns past the piece are read along and not used)
                 const uint32_t t0 = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
-                                    static_cast<uint32_t>(acc * kCeTile + half * 128);
+                                    static_cast<uint32_t>(acc * kCeTile + piece * n_piece);
 #pragma unroll
-                for (int c = 0; c < 128; c += 16) {
+                for (int c = 0; c < kCePart; c += 16) {
                     uint32_t r[16];
                     tmem_ld16(t0 + static_cast<uint32_t>(c), r);
                     tmem_ld_wait();
@@ -316,89 +336,82 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
                 if (++acc == 2) { acc = 0; acc_phase ^= 1u; }
             }
             if (!ok) break;
-            const int cols = min(128, args.cols - c0);   // this warp's columns of the tile (may be <= 0)
+            const int cols = min(n_piece, args.cols - c0);   // this warp's columns (may be <= 0)
+            // (kCeLse: a piece past the vocabulary leaves the pair of an empty sum)
+            if (MODE != kCeLse && cols <= 0) continue;
             if constexpr (MODE == kCeLse) {
                 if (target >= 0 && target < cols) {
                     float z = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 128; ++j) z = target == j ? v[j] : z;
+                    for (int j = 0; j < kCePart; ++j) z = target == j ? v[j] : z;
                     args.z_target[row] = z * args.scale;
                 }
-                float top = -INFINITY, sum = 0.0f;
+                float m[4], e[4];
 #pragma unroll
-                for (int j = 0; j < 128; ++j) {
-                    v[j] = j < cols ? v[j] * args.scale2 : -INFINITY;
-                    top = fmaxf(top, v[j]);
+                for (int j = 0; j < kCePart; ++j) {
+                    v[j] = cols < kCePart && j >= cols ? -INFINITY : v[j] * args.scale2;
+                    m[j & 3] = j < 4 ? v[j] : fmaxf(m[j & 3], v[j]);
                 }
+                const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
                 // (every logit -inf: their sum stays zero)
                 const float base = top == -INFINITY ? 0.0f : top;
 #pragma unroll
-                for (int j = 0; j < 128; ++j) sum += exp2_approx(v[j] - base);
-                if (row < count && cols > 0)
-                    args.part[static_cast<int64_t>(c0 / 128) * args.part_pitch + row] = make_float2(top, sum);
+                for (int j = 0; j < kCePart; ++j) {
+                    const float x = exp2_approx(v[j] - base);
+                    e[j & 3] = j < 4 ? x : e[j & 3] + x;
+                }
+                if (row < count)
+                    args.part[static_cast<int64_t>(units.n0(u) / width * 2 + piece) * args.part_pitch + row] =
+                        make_float2(top, (e[0] + e[1]) + (e[2] + e[3]));
             } else if constexpr (MODE == kCeGrad) {
-                uint16_t *out = static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    if (c >= cols) break;
-#pragma unroll
-                    for (int j = c; j < c + 32; ++j) {
-                        v[j] = exp2_approx(fmaf(v[j], args.scale2, -cr.lse2)) * cr.weight_p;
-                        if (target == j) v[j] -= cr.weight_t;
-                        // rows behind the counted tokens: x there may be anything
-                        if (row >= count) v[j] = 0.0f;
-                    }
-                    store16_32<BF16>(v + c, out, c0 + c, args.cols);
+                for (int j = 0; j < kCePart; ++j) {
+                    v[j] = exp2_approx(fmaf(v[j], args.scale2, -cr.lse2)) * cr.weight_p;
+                    if (target == j) v[j] -= cr.weight_t;
+                    // rows behind the counted tokens: x there may be anything
+                    if (row >= count) v[j] = 0.0f;
                 }
+                store16<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch + c0, cols);
             } else if constexpr (MODE == kCeDw) {
-                uint16_t *out = static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    if (c >= cols || row >= args.rows) break;
-#pragma unroll
-                    for (int j = c; j < c + 32; ++j) v[j] *= down;
-                    store16_32<BF16>(v + c, out, c0 + c, args.cols);
-                }
+                for (int j = 0; j < kCePart; ++j) v[j] *= down;
+                if (row < args.rows)
+                    store16<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch + c0, cols);
             } else if (row < count) {
                 float *s = args.sums + (units.split(u) * args.sums_rows + row) * static_cast<int64_t>(args.cols) + c0;
                 const bool sectors = (reinterpret_cast<uintptr_t>(s) & 31u) == 0;
 #pragma unroll
-                for (int c = 0; c < 128; c += 32) {
-                    if (c >= cols) break;
-                    const bool whole = c + 32 <= cols && sectors;
-                    if (args.add) {
-                        if (whole) {
-#pragma unroll
-                            for (int j = c; j < c + 32; j += 8) {
-                                float o[8];
-                                ld_global_v8(s + j, o);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) v[j + i] += o[i];
-                            }
-                        } else {
-#pragma unroll
-                            for (int j = c; j < c + 32; ++j)
-                                if (j < cols) v[j] += s[j];
-                        }
-                    }
-                    if (args.finish) {
-#pragma unroll
-                        for (int j = c; j < c + 32; ++j) v[j] *= down;
-                        store16_32<BF16>(v + c, static_cast<uint16_t *>(args.out) +
-                                                    static_cast<int64_t>(args.index[row]) * args.pitch,
-                                         c0 + c, args.cols);
-                    } else if (whole) {
-#pragma unroll
-                        for (int j = c; j < c + 32; j += 8) {
-                            uint32_t o[8];
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[j + i]);
-                            st_global_v8(s + j, o);
-                        }
+                for (int c = 0; c < kCePart; c += 8) {
+                    if (c >= cols || !args.add) break;
+                    float o[8];
+                    if (c + 8 <= cols && sectors) {
+                        ld_global_v8(s + c, o);
                     } else {
 #pragma unroll
-                        for (int j = c; j < c + 32; ++j)
-                            if (j < cols) s[j] = v[j];
+                        for (int i = 0; i < 8; ++i) o[i] = c + i < cols ? s[c + i] : 0.0f;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[c + i] += o[i];
+                }
+                if (args.finish) {
+#pragma unroll
+                    for (int j = 0; j < kCePart; ++j) v[j] *= down;
+                    store16<BF16>(v, static_cast<uint16_t *>(args.out) +
+                                         static_cast<int64_t>(args.index[row]) * args.pitch + c0, cols);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < kCePart; c += 8) {
+                        if (c >= cols) break;
+                        if (c + 8 <= cols && sectors) {
+                            uint32_t o[8];
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[c + i]);
+                            st_global_v8(s + c, o);
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                if (c + i < cols) s[c + i] = v[c + i];
+                        }
                     }
                 }
             }
@@ -409,7 +422,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
     // touch it.
     tc_fence_before();
     cluster_sync_all();
-    if (warp == 2) {
+    if (warp == 0) {
+        __syncwarp();
         tc_fence_after();
         tmem_dealloc_pair(tmem_base, 512);
     }

@@ -440,6 +440,23 @@ __device__ __forceinline__ void tmem_ld_wait()
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  A role that issues tcgen05 or TMA
+// instructions from one thread is entered through this and not through
+// "lane == 0": the compiler then knows the thread to be one, and the
+// instructions take their descriptors without a detour (measured on the
+// cross entropy's products: 500 clocks a k block to issue with lane == 0,
+// about what its products take, and 16 % off the kernel's time without).
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
+}
+
 // Shared-memory matrix descriptor for a K-major operand tile stored in the
 // 128-byte swizzle layout the TMA writes: rows of 128 bytes, 8-row groups
 // 1024 bytes apart, tile base 1024-byte aligned.  Fields: start address >> 4
