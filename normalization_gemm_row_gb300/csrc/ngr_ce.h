@@ -14,7 +14,6 @@ namespace ngr {
 enum { kCeLse = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
 
 constexpr int kCeTile = 256;      // rows, and columns at most, of a CTA pair's output tile
-constexpr int kCeStages = 6;      // pipeline stages of 32 KB a CTA
 
 // What the kernels of a call learn of its tokens (device memory): `count`
 // tokens have a target, and `weight` is the largest size of a gradient
@@ -37,6 +36,7 @@ struct CeRow {
 
 struct alignas(128) CeGemmArgs {
     CUtensorMap map_a, map_b;
+    CUtensorMap map_out;    // kCeDw: `out`, box {64 columns, 32 rows} (with `boxes`)
     const CeInfo *info;
     int *err;
     unsigned long long timeout_ns;
@@ -55,6 +55,7 @@ struct alignas(128) CeGemmArgs {
     const CeRow *row;       // kCeGrad
     void *out;              // kCeGrad: dz [rows][pitch]; kCeDw: dW at v0; kCeDx: dx (finish)
     int64_t pitch;          // elements between rows of `out`
+    int boxes;              // kCeDw: aligned rows, written as boxes (map_out)
     float *sums;            // kCeDx: FP32 [splits][sums_rows][cols]
     int64_t sums_rows;
     int add;                // kCeDx: add to the sums of the pieces before

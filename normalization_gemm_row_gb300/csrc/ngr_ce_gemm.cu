@@ -51,7 +51,18 @@ template <int MODE>
 __device__ __forceinline__ constexpr int ce_chunk() { return MODE == kCeLse || MODE == kCeGrad ? 8 : 32; }
 constexpr int kCeOperand = kBM * kBK * 2;                 // 16 KB: a CTA's half of A or B
 constexpr int kCeBox = 64 * kBK * 2;                      // an MN-major box of 64 x 64
-constexpr int kCeSmem = kCeStages * 2 * kCeOperand + 8 * (2 * kCeStages + 5) + 16 + 1024;
+constexpr int kCeOutBox = 64 * 32 * 2;                    // 64 columns of a warp's 32 rows of the output
+constexpr int kCeOut = kCeEpilogueWarps * 2 * kCeOutBox;
+// Pipeline stages of 32 KB a CTA: reading W for a few tokens takes six (177
+// us at 33 x 8192 x 65536, 208 with four); dW, which reads little then and
+// is bound by its writes, gives two of them to its output boxes.
+template <int MODE>
+__host__ __device__ constexpr int ce_stages() { return MODE == kCeDw ? 4 : 6; }
+template <int MODE>
+constexpr int ce_smem()
+{
+    return ce_stages<MODE>() * 2 * kCeOperand + (MODE == kCeDw ? kCeOut : 0) + 8 * (2 * ce_stages<MODE>() + 5) + 16 + 1024;
+}
 
 __device__ __forceinline__ float exp2_approx(float v)
 {
@@ -104,6 +115,35 @@ __device__ __forceinline__ void store16(const float (&v)[kCePart], uint16_t *p, 
     }
 }
 
+// 128 values of each of a warp's 32 rows through the warp's own shared memory
+// to the box at (c, row0): whole lines to memory, where stores by rows from
+// 32 lanes write a sector of 32 lines each (dW of 33 tokens, 65536 x 8192:
+// 317 us so).  `box` is the warp's two 4 KB boxes in the 128-byte swizzle.
+template <bool BF16>
+__device__ __forceinline__ void store_boxes(const float (&v)[kCePart], uint8_t *box, const CUtensorMap *map,
+                                            int c, int row0, int lane, int cols, int rows)
+{
+    if (lane == 0) tma_store_wait_read();   // the last tile's stores have read it
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < kCePart / 8; ++i) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = from_float2<BF16>(v[8 * i + 2 * j], v[8 * i + 2 * j + 1]);
+        *reinterpret_cast<uint4 *>(box + (i >> 3) * kCeOutBox + lane * 128 + (((i & 7) ^ (lane & 7)) << 4)) =
+            make_uint4(o[0], o[1], o[2], o[3]);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+        if (row0 < rows) {
+            tma_store_2d(map, box, c, row0);
+            if (c + 64 < cols) tma_store_2d(map, box + kCeOutBox, c + 64, row0);
+        }
+        tma_store_commit();
+    }
+}
+
 // The output tiles of a call and the order they run in.
 template <int MODE>
 struct CeUnits {
@@ -153,12 +193,14 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
     const uint32_t stage_bytes = 2u * (kCeOperand + (kBMn ? (width / 2 + 63) / 64 * kCeBox : width / 2 * kBK * 2));
     constexpr int kChunk = ce_chunk<MODE>();
 
+    constexpr int kCeStages = ce_stages<MODE>();
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
     uint8_t *sA = smem;
     uint8_t *sB = smem + kCeStages * kCeOperand;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + 2 * kCeStages * kCeOperand);
+    uint8_t *sOut = smem + 2 * kCeStages * kCeOperand;
+    uint64_t *full = reinterpret_cast<uint64_t *>(sOut + (MODE == kCeDw ? kCeOut : 0));
     uint64_t *empty = full + kCeStages;
     uint64_t *acc_full = empty + kCeStages;
     uint64_t *acc_empty = acc_full + 2;
@@ -296,6 +338,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
         const int q = warp & 3;                               // tensor-memory lane quarter
         const int piece = (warp - kCeEpilogueWarp0) >> 2;     // columns [piece width / 2, + width / 2)
         const int n_piece = width >> 1;
+        uint8_t *const out_box = sOut + (warp - kCeEpilogueWarp0) * 2 * kCeOutBox;
         const int count = args.info->count;
         const float down = args.info->down;
         int acc = 0;
@@ -375,7 +418,9 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             } else if constexpr (MODE == kCeDw) {
 #pragma unroll
                 for (int j = 0; j < kCePart; ++j) v[j] *= down;
-                if (row < args.rows)
+                if (args.boxes)
+                    store_boxes<BF16>(v, out_box, &args.map_out, c0, row - lane, lane, args.cols, args.rows);
+                else if (row < args.rows)
                     store16<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch + c0, cols);
             } else if (row < count) {
                 float *s = args.sums + (units.split(u) * args.sums_rows + row) * static_cast<int64_t>(args.cols) + c0;
@@ -418,6 +463,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
         }
     }
 
+    // The boxes of the last tiles are written out before the shared memory goes.
+    if (MODE == kCeDw && lane == 0 && warp >= kCeEpilogueWarp0) tma_store_wait();
     // Neither CTA frees its tensor memory or leaves while the pair may still
     // touch it.
     tc_fence_before();
@@ -433,13 +480,13 @@ template <int MODE, bool BF16>
 int run(const CeGemmArgs &a, int grid, cudaStream_t stream)
 {
     auto kern = ce_gemm_kernel<MODE, BF16>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (ce_smem<MODE>()));
     if (e != cudaSuccess)
         return record_cuda_error("cudaFuncSetAttribute(max dynamic smem)", e, cudaGetErrorString(e));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(kCeThreads);
-    cfg.dynamicSmemBytes = kCeSmem;
+    cfg.dynamicSmemBytes = ce_smem<MODE>();
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -457,11 +504,11 @@ int run(const CeGemmArgs &a, int grid, cudaStream_t stream)
 int ce_clusters()
 {
     auto kern = ce_gemm_kernel<kCeLse, true>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCeSmem) != cudaSuccess) return 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (ce_smem<kCeLse>())) != cudaSuccess) return 0;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(2);
     cfg.blockDim = dim3(kCeThreads);
-    cfg.dynamicSmemBytes = kCeSmem;
+    cfg.dynamicSmemBytes = ce_smem<kCeLse>();
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
