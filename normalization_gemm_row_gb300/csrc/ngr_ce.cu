@@ -32,6 +32,7 @@ __global__ void __launch_bounds__(kIndexThreads) ce_index_kernel(const __grid_co
     __shared__ int warp_sum[kIndexThreads / 32];
     __shared__ float warp_max[kIndexThreads / 32];
     __shared__ int bad;
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
@@ -108,6 +109,8 @@ __global__ void __launch_bounds__(kIndexThreads) ce_index_kernel(const __grid_co
 template <bool VEC>
 __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const __grid_constant__ CeTokens t)
 {
+    pdl_launch_dependents();
+    pdl_wait();
     const int count = t.info->count;
     const int64_t filled = (static_cast<int64_t>(max(count, 1)) + 63) / 64 * 64;
     const int64_t last = filled > t.M ? filled : t.M;
@@ -175,6 +178,7 @@ __global__ void __launch_bounds__(kLossThreads) ce_loss_kernel(
     const int lanes = kLossThreads / rows;
     const int x = threadIdx.x % rows, y = threadIdx.x / rows;
     const int64_t r = static_cast<int64_t>(blockIdx.x) * rows + x;
+    pdl_wait();
     const int count = t.info->count;
     float m = -INFINITY, s = 0.0f;
     if (r < count) {
@@ -207,6 +211,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeTokens t,
                                                     const float *__restrict__ sums, int64_t sums_rows, int splits)
 {
+    pdl_wait();
     const int count = t.info->count;
     const float down = t.info->down;
     const int64_t total = static_cast<int64_t>(count) * t.K;
@@ -222,9 +227,22 @@ __global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeTo
     }
 }
 
-int launched(const char *what)
+// A launch as a programmatic dependent of the kernel before it: it may start
+// while that one ends, and waits for it before it reads (pdl_wait).  A call's
+// first kernel is not launched so.
+template <typename... P, typename... A>
+int launch_after(const char *what, void (*kern)(P...), unsigned grid, unsigned threads, cudaStream_t stream, A... args)
 {
-    const cudaError_t e = cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
     return e == cudaSuccess ? 0 : record_cuda_error(what, e, cudaGetErrorString(e));
 }
 
@@ -235,7 +253,8 @@ unsigned blocks(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 
 int launch_ce_index(const CeTokens &t, cudaStream_t stream)
 {
     ce_index_kernel<<<1, kIndexThreads, 0, stream>>>(t);
-    return launched("cross entropy token index launch");
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? 0 : record_cuda_error("cross entropy token index launch", e, cudaGetErrorString(e));
 }
 
 int launch_ce_gather(const CeTokens &t, cudaStream_t stream)
@@ -244,9 +263,8 @@ int launch_ce_gather(const CeTokens &t, cudaStream_t stream)
                      ((reinterpret_cast<uintptr_t>(t.x) | reinterpret_cast<uintptr_t>(t.dx)) & 15u) == 0;
     const int64_t rows = (t.M + 63) / 64 * 64;
     const unsigned grid = blocks(rows, 152 * 16);
-    if (vec) ce_gather_kernel<true><<<grid, kGatherThreads, 0, stream>>>(t);
-    else ce_gather_kernel<false><<<grid, kGatherThreads, 0, stream>>>(t);
-    return launched("cross entropy gather launch");
+    return launch_after("cross entropy gather launch", vec ? ce_gather_kernel<true> : ce_gather_kernel<false>, grid,
+                        kGatherThreads, stream, t);
 }
 
 int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, int parts,
@@ -255,18 +273,16 @@ int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, in
     // A CTA per row while the rows are few, else 32 rows side by side so
     // that a warp reads whole lines of the pairs.
     const int rows = t.M < 512 ? 1 : 32;
-    ce_loss_kernel<<<static_cast<unsigned>((t.M + rows - 1) / rows), kLossThreads, 0, stream>>>(
-        t, part, part_pitch, parts, z_target, loss, lse, rows);
-    return launched("cross entropy loss launch");
+    return launch_after("cross entropy loss launch", ce_loss_kernel, static_cast<unsigned>((t.M + rows - 1) / rows),
+                        kLossThreads, stream, t, part, part_pitch, parts, z_target, loss, lse, rows);
 }
 
 int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_rows, int splits,
                  cudaStream_t stream)
 {
     const unsigned grid = blocks((t.M * t.K + 255) / 256, 152 * 8);
-    if (bf16) ce_dx_kernel<true><<<grid, 256, 0, stream>>>(t, sums, sums_rows, splits);
-    else ce_dx_kernel<false><<<grid, 256, 0, stream>>>(t, sums, sums_rows, splits);
-    return launched("cross entropy dx sums launch");
+    return launch_after("cross entropy dx sums launch", bf16 ? ce_dx_kernel<true> : ce_dx_kernel<false>, grid, 256u,
+                        stream, t, sums, sums_rows, splits);
 }
 
 }  // namespace ngr

@@ -61,6 +61,7 @@ struct alignas(128) CeGemmArgs {
     int add;                // kCeDx: add to the sums of the pieces before
     int finish;             // kCeDx: this is the last piece and splits == 1: write dx itself
     const int *index;       // kCeDx (finish): a counted token's row of x
+    int after_dx;           // kCeDw: the kernel before it is dx (and not dz, which it reads)
 };
 
 int launch_ce_gemm(int mode, bool bf16, const CeGemmArgs &a, int64_t units, cudaStream_t stream);

@@ -291,6 +291,7 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
             a.cols = static_cast<int>(K);
             a.out = static_cast<char *>(dW) + v0 * K * 2;
             a.pitch = K;
+            a.after_dx = dx != nullptr;
             a.boxes = K % 8 == 0 && aligned(dW, 16);
             if (a.boxes && !map_2d(&a.map_out, a.out, c.bf16, n, K, 32)) return NGR_ERR_CUDA;
             NGR_TIMED(launch_ce_gemm(kCeDw, c.bf16, a, tiles_of(n, K), stream));

@@ -238,6 +238,14 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
     cluster_sync_all();
     tc_fence_after();
     const uint32_t tmem_base = *tmem_slot;
+    // Launched as a programmatic dependent of the kernel before it.  dW reads
+    // nothing that dx writes, and dz is complete once dx has begun its work:
+    // launched behind dx it fills the SMs that dx's last tiles leave free and
+    // waits for dx only at its end.  (So dx lets its dependent start after its
+    // own wait for dz and not before.)
+    if constexpr (MODE == kCeDx) pdl_wait();
+    pdl_launch_dependents();
+    if constexpr (MODE == kCeLse || MODE == kCeGrad) pdl_wait();
 
     const CeUnits<MODE> units(args);
     const int n_units = units.count();
@@ -465,6 +473,7 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
 
     // The boxes of the last tiles are written out before the shared memory goes.
     if (MODE == kCeDw && lane == 0 && warp >= kCeEpilogueWarp0) tma_store_wait();
+    if (MODE == kCeDw) pdl_wait();
     // Neither CTA frees its tensor memory or leaves while the pair may still
     // touch it.
     tc_fence_before();
@@ -488,13 +497,15 @@ int run(const CeGemmArgs &a, int grid, cudaStream_t stream)
     cfg.blockDim = dim3(kCeThreads);
     cfg.dynamicSmemBytes = ce_smem<MODE>();
     cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.after_dx || MODE != kCeDw ? 2 : 1;
     e = cudaLaunchKernelEx(&cfg, kern, a);
     return e == cudaSuccess ? 0 : record_cuda_error("cudaLaunchKernelEx (cross entropy)", e, cudaGetErrorString(e));
 }
