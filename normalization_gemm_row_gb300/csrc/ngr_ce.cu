@@ -22,141 +22,196 @@ constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kDzUnit = 8192.0f;   // dz's largest weight
 constexpr int kIndexThreads = 1024, kIndexEach = 8;
 constexpr int kGatherThreads = 128;
-constexpr int kLossThreads = 1024;
+constexpr int kFewTokens = kGatherThreads * kIndexEach;   // index and gather in one kernel up to this
 
-// One CTA: a prefix sum over the tokens gives each counted token its place
-// (their order kept) and the others theirs from the end; the largest weight
-// is the unit of dz.
+// A prefix sum over the tokens [r0, r0 + THREADS x kIndexEach) gives each
+// counted token its place (their order kept) and the others theirs from the
+// end: put(place, token, target or -1).  `base` counts the tokens of the
+// rounds before and is carried on; `top` takes the largest weight of this
+// thread's tokens; *bad is set by a target outside the vocabulary.
+template <int THREADS, typename Put>
+__device__ __forceinline__ void place_tokens(const CeTokens &t, int64_t r0, int64_t &base, float &top, int *bad,
+                                             int *warp_sum, Put put)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t i0 = r0 + static_cast<int64_t>(threadIdx.x) * kIndexEach;
+    int64_t target[kIndexEach];
+    int mine = 0;
+#pragma unroll
+    for (int j = 0; j < kIndexEach; ++j) {
+        target[j] = i0 + j < t.M ? t.target[i0 + j] : -1;
+        if (target[j] >= t.V) {
+            *bad = 1;
+            target[j] = -1;
+        }
+        mine += target[j] >= 0;
+    }
+    int incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    int64_t at = base + before + incl - mine;
+#pragma unroll
+    for (int j = 0; j < kIndexEach; ++j) {
+        const int64_t i = i0 + j;
+        if (i >= t.M) continue;
+        if (target[j] >= 0) {
+            put(at, static_cast<int>(i), static_cast<int>(target[j]));
+            ++at;
+            if (t.lse) {
+                const float g = t.dloss ? t.dloss[i] : 0.0f, l = t.dlse ? t.dlse[i] : 0.0f;
+                top = fmaxf(top, fmaxf(fabsf(g), fabsf(g + l)));
+            }
+        } else {
+            put(t.M - 1 - (i - at), static_cast<int>(i), -1);
+        }
+    }
+    base += total;
+    __syncthreads();
+}
+
+// The largest weight over the CTA's threads (all get it) as the unit of dz.
+template <int THREADS>
+__device__ __forceinline__ CeInfo tokens_info(const CeTokens &t, int64_t count, float top, float *warp_max)
+{
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = top;
+    __syncthreads();
+    for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, warp_max[w]);
+    top *= fabsf(t.logit_scale);
+    // (no weight, or one that is not finite: unscaled)
+    if (!(top >= 1.0e-30f && top <= 1.0e38f)) top = kDzUnit;
+    CeInfo info;
+    info.count = static_cast<int>(count);
+    info.weight = top;
+    info.down = top / kDzUnit;
+    return info;
+}
+
 __global__ void __launch_bounds__(kIndexThreads) ce_index_kernel(const __grid_constant__ CeTokens t)
 {
     __shared__ int warp_sum[kIndexThreads / 32];
     __shared__ float warp_max[kIndexThreads / 32];
     __shared__ int bad;
     pdl_launch_dependents();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) bad = 0;
     __syncthreads();
-    int64_t base = 0;   // counted tokens before this round
+    int64_t base = 0;
     float top = 0.0f;
-    for (int64_t r0 = 0; r0 < t.M; r0 += kIndexThreads * kIndexEach) {
-        const int64_t i0 = r0 + static_cast<int64_t>(threadIdx.x) * kIndexEach;
-        int64_t target[kIndexEach];
-        int mine = 0;
-#pragma unroll
-        for (int j = 0; j < kIndexEach; ++j) {
-            target[j] = i0 + j < t.M ? t.target[i0 + j] : -1;
-            if (target[j] >= t.V) {
-                bad = 1;
-                target[j] = -1;
-            }
-            mine += target[j] >= 0;
-        }
-        int incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
-        }
-        if (lane == 31) warp_sum[warp] = incl;
-        __syncthreads();
-        int before = 0, total = 0;
-        for (int w = 0; w < kIndexThreads / 32; ++w) {
-            if (w < warp) before += warp_sum[w];
-            total += warp_sum[w];
-        }
-        int64_t at = base + before + incl - mine;
-#pragma unroll
-        for (int j = 0; j < kIndexEach; ++j) {
-            const int64_t i = i0 + j;
-            if (i >= t.M) continue;
-            if (target[j] >= 0) {
-                t.index[at] = static_cast<int>(i);
-                t.ctarget[at] = static_cast<int>(target[j]);
-                ++at;
-                if (t.lse) {
-                    const float g = t.dloss ? t.dloss[i] : 0.0f, l = t.dlse ? t.dlse[i] : 0.0f;
-                    top = fmaxf(top, fmaxf(fabsf(g), fabsf(g + l)));
-                }
-            } else {
-                t.index[t.M - 1 - (i - at)] = static_cast<int>(i);
-            }
-        }
-        base += total;
-        __syncthreads();
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) warp_max[warp] = top;
-    __syncthreads();
+    for (int64_t r0 = 0; r0 < t.M; r0 += kIndexThreads * kIndexEach)
+        place_tokens<kIndexThreads>(t, r0, base, top, &bad, warp_sum, [&](int64_t at, int token, int target) {
+            t.index[at] = token;
+            if (target >= 0) t.ctarget[at] = target;
+        });
+    const CeInfo info = tokens_info<kIndexThreads>(t, base, top, warp_max);
     if (threadIdx.x == 0) {
-        for (int w = 0; w < kIndexThreads / 32; ++w) top = fmaxf(top, warp_max[w]);
-        top *= fabsf(t.logit_scale);
-        // (no weight, or one that is not finite: unscaled)
-        if (!(top >= 1.0e-30f && top <= 1.0e38f)) top = kDzUnit;
-        CeInfo info;
-        info.count = static_cast<int>(base);
-        info.weight = top;
-        info.down = top / kDzUnit;
         *t.info = info;
         *t.err = bad ? kDevErrTarget : 0;
     }
 }
 
-// One CTA per row of the gathered matrix at a time: a counted token's row
-// (padded with zeros to Kx), zero rows up to the next 64 (the contracted
-// length of dW), and in the backward call each row's softmax constants and
-// zeros for the dx rows of the tokens that do not count.
+// Row r of the gathered matrix: a counted token's row (padded with zeros to
+// Kx), a zero row up to the next 64 (the contracted length of dW), and in the
+// backward call the row's softmax constants and zeros for the dx row of a
+// token that does not count.
+template <bool VEC>
+__device__ __forceinline__ void gather_row(const CeTokens &t, const CeInfo &info, int64_t r, int64_t token, int target)
+{
+    const int count = info.count;
+    const int vecs = static_cast<int>(t.Kx / 8), whole = static_cast<int>(t.K / 8);
+    if (r < (static_cast<int64_t>(max(count, 1)) + 63) / 64 * 64) {
+        uint4 *dst = static_cast<uint4 *>(t.xc) + r * vecs;
+        const uint16_t *src = static_cast<const uint16_t *>(t.x) + token * t.K;
+#pragma unroll 4
+        for (int v = threadIdx.x; v < vecs; v += kGatherThreads) {
+            uint4 d = make_uint4(0u, 0u, 0u, 0u);
+            if (r < count) {
+                if constexpr (VEC) {
+                    if (v < whole) d = reinterpret_cast<const uint4 *>(src)[v];
+                } else {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int64_t c = 8 * static_cast<int64_t>(v) + 2 * j;
+                        const uint32_t lo = c < t.K ? src[c] : 0u;
+                        const uint32_t hi = c + 1 < t.K ? src[c + 1] : 0u;
+                        w[j] = lo | (hi << 16);
+                    }
+                    d = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            dst[v] = d;
+        }
+    }
+    if (t.row && r < count && threadIdx.x == 0) {
+        const float g = t.dloss ? t.dloss[token] : 0.0f, l = t.dlse ? t.dlse[token] : 0.0f;
+        t.row[r] = CeRow{t.lse[token] * kLog2e, (g + l) * t.logit_scale / info.weight * kDzUnit,
+                         g * t.logit_scale / info.weight * kDzUnit, target};
+    }
+    if (t.dx && r >= count && r < t.M) {
+        uint16_t *dst = static_cast<uint16_t *>(t.dx) + token * t.K;
+        if constexpr (VEC) {
+            for (int v = threadIdx.x; v < whole; v += kGatherThreads)
+                reinterpret_cast<uint4 *>(dst)[v] = make_uint4(0u, 0u, 0u, 0u);
+        } else {
+            for (int64_t c = threadIdx.x; c < t.K; c += kGatherThreads) dst[c] = 0;
+        }
+    }
+}
+
 template <bool VEC>
 __global__ void __launch_bounds__(kGatherThreads) ce_gather_kernel(const __grid_constant__ CeTokens t)
 {
     pdl_launch_dependents();
     pdl_wait();
-    const int count = t.info->count;
-    const int64_t filled = (static_cast<int64_t>(max(count, 1)) + 63) / 64 * 64;
-    const int64_t last = filled > t.M ? filled : t.M;
-    const int vecs = static_cast<int>(t.Kx / 8), whole = static_cast<int>(t.K / 8);
-    for (int64_t r = blockIdx.x; r < last; r += gridDim.x) {
-        const int64_t token = r < t.M ? t.index[r] : 0;
-        if (r < filled) {
-            uint4 *dst = static_cast<uint4 *>(t.xc) + r * vecs;
-            const uint16_t *src = static_cast<const uint16_t *>(t.x) + token * t.K;
-#pragma unroll 4
-            for (int v = threadIdx.x; v < vecs; v += kGatherThreads) {
-                uint4 d = make_uint4(0u, 0u, 0u, 0u);
-                if (r < count) {
-                    if constexpr (VEC) {
-                        if (v < whole) d = reinterpret_cast<const uint4 *>(src)[v];
-                    } else {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int64_t c = 8 * static_cast<int64_t>(v) + 2 * j;
-                            const uint32_t lo = c < t.K ? src[c] : 0u;
-                            const uint32_t hi = c + 1 < t.K ? src[c + 1] : 0u;
-                            w[j] = lo | (hi << 16);
-                        }
-                        d = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-                dst[v] = d;
-            }
+    const CeInfo info = *t.info;
+    const int64_t rows = (t.M + 63) / 64 * 64;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        gather_row<VEC>(t, info, r, r < t.M ? t.index[r] : 0, r < info.count ? t.ctarget[r] : -1);
+}
+
+// Index and gather in one kernel for few tokens: every CTA places them all
+// for itself in shared memory, which costs less than a launch.
+template <bool VEC>
+__global__ void __launch_bounds__(kGatherThreads) ce_index_gather_kernel(const __grid_constant__ CeTokens t)
+{
+    __shared__ int index[kFewTokens], ctarget[kFewTokens];
+    __shared__ int warp_sum[kGatherThreads / 32];
+    __shared__ float warp_max[kGatherThreads / 32];
+    __shared__ int bad;
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) bad = 0;
+    __syncthreads();
+    int64_t base = 0;
+    float top = 0.0f;
+    place_tokens<kGatherThreads>(t, 0, base, top, &bad, warp_sum, [&](int64_t at, int token, int target) {
+        index[at] = token;
+        ctarget[at] = target;
+    });
+    const CeInfo info = tokens_info<kGatherThreads>(t, base, top, warp_max);
+    if (blockIdx.x == 0) {
+        for (int i = threadIdx.x; i < t.M; i += kGatherThreads) {
+            t.index[i] = index[i];
+            t.ctarget[i] = ctarget[i];
         }
-        if (t.row && r < count && threadIdx.x == 0) {
-            const float top = t.info->weight;
-            const float g = t.dloss ? t.dloss[token] : 0.0f, l = t.dlse ? t.dlse[token] : 0.0f;
-            t.row[r] = CeRow{t.lse[token] * kLog2e, (g + l) * t.logit_scale / top * kDzUnit,
-                             g * t.logit_scale / top * kDzUnit, t.ctarget[r]};
-        }
-        if (t.dx && r >= count && r < t.M) {
-            uint16_t *dst = static_cast<uint16_t *>(t.dx) + token * t.K;
-            if constexpr (VEC) {
-                for (int v = threadIdx.x; v < whole; v += kGatherThreads)
-                    reinterpret_cast<uint4 *>(dst)[v] = make_uint4(0u, 0u, 0u, 0u);
-            } else {
-                for (int64_t c = threadIdx.x; c < t.K; c += kGatherThreads) dst[c] = 0;
-            }
+        if (threadIdx.x == 0) {
+            *t.info = info;
+            *t.err = bad ? kDevErrTarget : 0;
         }
     }
+    const int64_t rows = (t.M + 63) / 64 * 64;
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x)
+        gather_row<VEC>(t, info, r, r < t.M ? index[r] : 0, r < t.M ? ctarget[r] : -1);
 }
 
 // (max, sum) pairs in powers of two, merged in a fixed order.
@@ -168,41 +223,56 @@ __device__ __forceinline__ void merge(float &m, float &s, float om, float os)
     m = top;
 }
 
-// A row's pairs over the column tiles -> its lse and loss.  `rows` rows per
-// CTA (1 or 32), the CTA's other threads along the pairs.
-__global__ void __launch_bounds__(kLossThreads) ce_loss_kernel(
+// A row's pairs over the column tiles -> its lse and loss.  ROWS 32: 32 rows
+// side by side, so that a warp reads whole lines of the pairs, and 32 threads
+// along the pairs of each; ROWS 1, while the rows are few: a CTA per row.
+template <int ROWS>
+__global__ void __launch_bounds__(ROWS == 1 ? 256 : 1024) ce_loss_kernel(
     const __grid_constant__ CeTokens t, const float2 *__restrict__ part, int64_t part_pitch, int parts,
-    const float *__restrict__ z_target, float *loss, float *lse, int rows)
+    const float *__restrict__ z_target, float *loss, float *lse)
 {
-    __shared__ float2 pair[kLossThreads];
-    const int lanes = kLossThreads / rows;
-    const int x = threadIdx.x % rows, y = threadIdx.x / rows;
-    const int64_t r = static_cast<int64_t>(blockIdx.x) * rows + x;
+    constexpr int kLanes = ROWS == 1 ? 256 : 32;   // threads along a row's pairs
+    __shared__ float2 pair[ROWS == 1 ? 8 : 32][33];
+    const int x = threadIdx.x % ROWS, y = threadIdx.x / ROWS;
+    const int64_t r = static_cast<int64_t>(blockIdx.x) * ROWS + x;
     pdl_wait();
     const int count = t.info->count;
     float m = -INFINITY, s = 0.0f;
     if (r < count) {
 #pragma unroll 4
-        for (int p = y; p < parts; p += lanes) {
+        for (int p = y; p < parts; p += kLanes) {
             const float2 v = part[p * part_pitch + r];
             merge(m, s, v.x, v.y);
         }
     }
-    pair[threadIdx.x] = make_float2(m, s);
-    __syncthreads();
-    for (int h = lanes / 2; h > 0; h >>= 1) {
-        if (y < h) {
-            const float2 o = pair[threadIdx.x + h * rows];
-            merge(m, s, o.x, o.y);
-            pair[threadIdx.x] = make_float2(m, s);
-        }
+    // ROWS 32: turn the tile round, so that a warp holds one row's 32 lanes.
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if constexpr (ROWS == 32) {
+        pair[y][x] = make_float2(m, s);
         __syncthreads();
+        const float2 v = pair[lane][warp];
+        m = v.x;
+        s = v.y;
     }
-    if (y == 0 && r < t.M) {
-        const int token = t.index[r];
-        const float l = r < count ? m * kLn2 + logf(s) : 0.0f;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const float om = __shfl_xor_sync(0xffffffffu, m, o), os = __shfl_xor_sync(0xffffffffu, s, o);
+        merge(m, s, om, os);
+    }
+    if constexpr (ROWS == 1) {
+        if (lane == 0) pair[warp][0] = make_float2(m, s);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+#pragma unroll
+            for (int w = 1; w < 8; ++w) merge(m, s, pair[w][0].x, pair[w][0].y);
+        }
+    }
+    const int64_t row = ROWS == 1 ? r : static_cast<int64_t>(blockIdx.x) * ROWS + warp;
+    if (lane == 0 && (ROWS == 32 || warp == 0) && row < t.M) {
+        const int token = t.index[row];
+        const float l = row < count ? m * kLn2 + logf(s) : 0.0f;
         lse[token] = l;
-        loss[token] = r < count ? l - z_target[r] : 0.0f;
+        loss[token] = row < count ? l - z_target[row] : 0.0f;
     }
 }
 
@@ -250,6 +320,8 @@ unsigned blocks(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 
 
 }  // namespace
 
+bool launch_ce_index_apart(const CeTokens &t) { return t.M > kFewTokens; }
+
 int launch_ce_index(const CeTokens &t, cudaStream_t stream)
 {
     ce_index_kernel<<<1, kIndexThreads, 0, stream>>>(t);
@@ -261,8 +333,13 @@ int launch_ce_gather(const CeTokens &t, cudaStream_t stream)
 {
     const bool vec = t.K % 8 == 0 &&
                      ((reinterpret_cast<uintptr_t>(t.x) | reinterpret_cast<uintptr_t>(t.dx)) & 15u) == 0;
-    const int64_t rows = (t.M + 63) / 64 * 64;
-    const unsigned grid = blocks(rows, 152 * 16);
+    const unsigned grid = blocks((t.M + 63) / 64 * 64, 152 * 16);
+    if (!launch_ce_index_apart(t)) {
+        if (vec) ce_index_gather_kernel<true><<<grid, kGatherThreads, 0, stream>>>(t);
+        else ce_index_gather_kernel<false><<<grid, kGatherThreads, 0, stream>>>(t);
+        const cudaError_t e = cudaGetLastError();
+        return e == cudaSuccess ? 0 : record_cuda_error("cross entropy gather launch", e, cudaGetErrorString(e));
+    }
     return launch_after("cross entropy gather launch", vec ? ce_gather_kernel<true> : ce_gather_kernel<false>, grid,
                         kGatherThreads, stream, t);
 }
@@ -270,11 +347,11 @@ int launch_ce_gather(const CeTokens &t, cudaStream_t stream)
 int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, int parts,
                    const float *z_target, float *loss, float *lse, cudaStream_t stream)
 {
-    // A CTA per row while the rows are few, else 32 rows side by side so
-    // that a warp reads whole lines of the pairs.
-    const int rows = t.M < 512 ? 1 : 32;
-    return launch_after("cross entropy loss launch", ce_loss_kernel, static_cast<unsigned>((t.M + rows - 1) / rows),
-                        kLossThreads, stream, t, part, part_pitch, parts, z_target, loss, lse, rows);
+    if (t.M < 1024)
+        return launch_after("cross entropy loss launch", ce_loss_kernel<1>, static_cast<unsigned>(t.M), 256u, stream,
+                            t, part, part_pitch, parts, z_target, loss, lse);
+    return launch_after("cross entropy loss launch", ce_loss_kernel<32>, static_cast<unsigned>((t.M + 31) / 32), 1024u,
+                        stream, t, part, part_pitch, parts, z_target, loss, lse);
 }
 
 int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_rows, int splits,

@@ -84,6 +84,9 @@ struct CeTokens {
     void *xc;               // [M up to 64][Kx] the counted tokens' rows, zeros behind
 };
 
+// The tokens' index and the gathered rows: two kernels, or for few tokens the
+// second alone.
+bool launch_ce_index_apart(const CeTokens &t);
 int launch_ce_index(const CeTokens &t, cudaStream_t stream);
 int launch_ce_gather(const CeTokens &t, cudaStream_t stream);
 int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, int parts,

@@ -209,7 +209,7 @@ int ce_forward(const void *x, const void *W, const int64_t *target, float logit_
     a.part_pitch = M;
     a.z_target = reinterpret_cast<float *>(c.ws + c.p.z_target);
     call_begin();
-    NGR_TIMED(launch_ce_index(c.t, stream));
+    if (launch_ce_index_apart(c.t)) NGR_TIMED(launch_ce_index(c.t, stream));
     NGR_TIMED(launch_ce_gather(c.t, stream));
     NGR_TIMED(launch_ce_gemm(kCeLse, c.bf16, a, tiles_of(M, V, a.width), stream));
     NGR_TIMED(launch_ce_loss(c.t, a.part, M, static_cast<int>(c.p.parts), a.z_target, loss, lse, stream));
@@ -245,7 +245,7 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
     if (rc != NGR_OK) return rc;
     c.t.row = reinterpret_cast<CeRow *>(c.ws + c.p.row);
     call_begin();
-    NGR_TIMED(launch_ce_index(c.t, stream));
+    if (launch_ce_index_apart(c.t)) NGR_TIMED(launch_ce_index(c.t, stream));
     NGR_TIMED(launch_ce_gather(c.t, stream));
     const int64_t rows = up_to(M, kCeTile);
     char *dz = c.ws + c.p.dz;
