@@ -49,8 +49,8 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
 {
     constexpr int kSlots = backward_slots(TPR);
     constexpr int kThreads = TPR * kSlots;
-    constexpr int kStage = 4 * VECS * kThreads;   // 16-byte slots of one stage of the ring
-    extern __shared__ uint4 ring[];   // [depth][x, residual, dy, dh][vecs][threads]
+    constexpr int kStage = (4 * VECS + 1) * kThreads;   // 16-byte slots of one stage of the ring
+    extern __shared__ uint4 ring[];   // [depth][vecs of x, residual, dy, dh; statistics][threads]
     float *const acc = reinterpret_cast<float *>(ring + a.depth * kStage);   // [arrays][slots][cols]
     __shared__ RowSumSmem sums;
     int half = 0;
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     for (int i = threadIdx.x; i < a.arrays * arr; i += kThreads) acc[i] = 0.0f;
     // an array that the call does not have is zeros
     uint4 *const mine = ring + threadIdx.x;
-    for (int i = 0; i < a.depth * 4 * VECS; ++i) mine[i * kThreads] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < a.depth * (4 * VECS + 1); ++i) mine[i * kThreads] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     if (cluster > 1) cluster_sync_all();   // every CTA runs before its shared memory is written
 
@@ -145,6 +145,7 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
             const int s = row_shift<MODE>(a, row);
             const int64_t off = row * a.N;
             const void *src[4] = {a.x, a.residual, a.dy, a.dh};
+            copy_async16(st + 4 * VECS * kThreads, a.stats + row);
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 if (src[k] == nullptr) continue;
@@ -152,14 +153,15 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
 #pragma unroll
                 for (int v = 0; v < VECS; ++v) {
                     uint4 *d = st + (k * VECS + v) * kThreads;
-                    if (p.whole(v, s)) copy_async16(d, b + p.col(v, 0, s));
-                    else if constexpr (MODE != kJoinAligned) *d = load_elements(b, p, v, s);
+                    if constexpr (MODE == kJoinScalar) *d = load_elements(b, p, v, s);
+                    else if (p.some(v, s)) copy_async16(d, b + p.col(v, 0, s));
                 }
             }
         } else {
-            // (what the slots held before may be anything)
+            // (what the slots held before may be anything; rstd 0 makes all terms
+            // of a row that is not there 0)
 #pragma unroll
-            for (int i = 0; i < 4 * VECS; ++i) st[i * kThreads] = make_uint4(0u, 0u, 0u, 0u);
+            for (int i = 0; i < 4 * VECS + 1; ++i) st[i * kThreads] = make_uint4(0u, 0u, 0u, 0u);
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
@@ -194,14 +196,13 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
         const bool active = row < now.r1;
         const int64_t off = row * a.N;
         const int s = row_shift<MODE>(a, row);
-        // (a row that is not there: rstd 0, so all its terms are 0)
-        const float4 st = active ? a.stats[row] : make_float4(0.f, 0.f, 0.f, 0.f);
         // the oldest of the rows under way has arrived (each thread reads what
         // it copied itself)
         if (a.depth == 1) asm volatile("cp.async.wait_group 0;" ::: "memory");
         else if (a.depth == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
         else asm volatile("cp.async.wait_group 2;" ::: "memory");
         uint4 *const in = mine + stage * kStage;
+        const float4 st = *reinterpret_cast<const float4 *>(in + 4 * VECS * kThreads);
         const float rs2 = norm2 ? st.w : 0.0f;
         if constexpr (MODE == kJoinWindow) params(s);
 
@@ -211,16 +212,16 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
         for (int k = 0; k < 8; ++k) t[k] = both(0.0f);
 #pragma unroll
         for (int v = 0; v < VECS; ++v) {
-            u1[v] = unpack8<BF16>(in[v * kThreads]);
+            u1[v] = unpack8<BF16>(own_elements(in[v * kThreads], p, v, s));
             if constexpr (CENTER) u1[v] = u1[v] + -st.x;
             u1[v] = u1[v] * st.y;
             const Vec8 wu = w[v] * u1[v];
-            Vec8 h = fma8(unpack8<BF16>(in[(VECS + v) * kThreads]), a.residual_scale, wu);
+            Vec8 h = fma8(unpack8<BF16>(own_elements(in[(VECS + v) * kThreads], p, v, s)), a.residual_scale, wu);
             if constexpr (CENTER) h = h + wb[v] + -st.z;
             u2[v] = h * rs2;
-            const Vec8 dy = unpack8<BF16>(in[(2 * VECS + v) * kThreads]);
+            const Vec8 dy = unpack8<BF16>(own_elements(in[(2 * VECS + v) * kThreads], p, v, s));
             const Vec8 q = g2[v] * dy;
-            D[v] = fma8(q, rs2, unpack8<BF16>(in[(3 * VECS + v) * kThreads]));
+            D[v] = fma8(q, rs2, unpack8<BF16>(own_elements(in[(3 * VECS + v) * kThreads], p, v, s)));
             dot8(t[0], q, u2[v]);
             dot8(t[1], wu, D[v]);
             dot8(t[2], wu, u2[v]);
@@ -231,17 +232,22 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
                 dot8(t[6], w[v], u2[v]);
                 sum8(t[7], wu);
             }
+        }
+        float k[CENTER ? 8 : 4];
+#pragma unroll
+        for (int i = 0; i < (CENTER ? 8 : 4); ++i) k[i] = t[i].x + t[i].y;
+        row_sum_begin<CENTER ? 8 : 4, TPR>(k, sums, half, cluster);
+        // While the row's other warps come to the barrier: what needs no sums.
+#pragma unroll
+        for (int v = 0; v < VECS; ++v) {
+            const Vec8 dy = unpack8<BF16>(own_elements(in[(2 * VECS + v) * kThreads], p, v, s));
             if (CENTER && a.a_dbeta2 >= 0) add8(sum_b2, v, s, dy);
             if (a.a_dgamma2 >= 0) add8(sum_g2, v, s, dy * u2[v]);
         }
         fetch(ahead, in);
         advance(ahead);
         stage = stage + 1 == a.depth ? 0 : stage + 1;
-
-        float k[CENTER ? 8 : 4];
-#pragma unroll
-        for (int i = 0; i < (CENTER ? 8 : 4); ++i) k[i] = t[i].x + t[i].y;
-        row_sum<CENTER ? 8 : 4, TPR>(k, sums, half, cluster, rank);
+        row_sum_end<CENTER ? 8 : 4, TPR>(k, sums, half, cluster, rank);
         const float c1 = rs2 * k[0] * inv_n;
         float c_0 = 0.0f, t0 = 0.0f, t1 = norm1 ? k[1] - c1 * k[2] : 0.0f;
         if constexpr (CENTER) {
@@ -306,7 +312,7 @@ struct Width {
 constexpr Width kWidths[] = {{32, 1}, {32, 2}, {96, 1}, {64, 2}, {160, 1}, {96, 2},
                              {128, 2}, {192, 2}, {256, 2}, {384, 2}, {512, 2}};
 
-inline int64_t ring_row(const JoinShape &s) { return 4ll * s.vecs * s.tpr * s.slots * 16; }
+inline int64_t ring_row(const JoinShape &s) { return (4ll * s.vecs + 1) * s.tpr * s.slots * 16; }
 inline int64_t sum_bytes(const JoinShape &s, int arrays) { return static_cast<int64_t>(arrays) * s.slots * s.cols * 4; }
 
 template <bool BF16, int MODE, bool CENTER>

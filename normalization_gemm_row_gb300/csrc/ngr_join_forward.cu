@@ -20,7 +20,7 @@ __host__ __device__ constexpr int forward_threads(int tpr) { return tpr > 256 ? 
 constexpr unsigned kWave = 4 * kJoinSms;   // CTAs that run at once
 
 template <bool BF16, int MODE, int TPR, int VECS>
-__global__ void __launch_bounds__(forward_threads(TPR), (MODE == kJoinAligned ? 1024 : 512) / forward_threads(TPR))
+__global__ void __launch_bounds__(forward_threads(TPR), (MODE == kJoinAligned ? 1024 : MODE == kJoinWindow && TPR <= 256 ? 768 : 512) / forward_threads(TPR))
     join_forward_kernel(const __grid_constant__ JoinArgs a)
 {
     constexpr int kSlots = forward_threads(TPR) / TPR;

@@ -150,8 +150,10 @@ __device__ __forceinline__ void dot8(float2 &s, const Vec8 &a, const Vec8 &b)
 // they are read and written (kJoin* modes).  Vector v of thread t is the
 // (v TPR + t)-th of the CTA's columns [c0, c1); in the window mode the
 // vectors are shifted back by `s` elements, the row's distance from the
-// 16-byte boundary before it, and those that reach over an end are read and
-// written by elements.  In the scalar mode element j of vector v is column
+// 16-byte boundary before it; those that reach over an end are read whole
+// (the aligned 16 bytes hold an element of the row, so they are the
+// caller's), what is not the row's is put to zero, and they are written by
+// elements.  In the scalar mode element j of vector v is column
 // c0 + (v 8 + j) TPR + t, so that neighbouring threads touch neighbouring
 // elements.
 template <int MODE, int TPR>
@@ -170,6 +172,12 @@ struct Place {
         if constexpr (MODE == kJoinAligned) return col(v, 0, s) < c1;
         const int c = col(v, j, s);
         return c >= c0 && c < c1;
+    }
+    // any of them
+    __device__ __forceinline__ bool some(int v, int s) const
+    {
+        const int c = col(v, 0, s);
+        return c < c1 && (MODE == kJoinAligned || c + 8 > c0);
     }
     // all 8 columns of the vector (one 16-byte access)
     __device__ __forceinline__ bool whole(int v, int s) const
@@ -195,13 +203,25 @@ __device__ __forceinline__ uint4 load_elements(const uint16_t *row, const P &p, 
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// A vector's elements with zeros where the thread has no column.
+template <int MODE, int TPR>
+__device__ __forceinline__ uint4 own_elements(const uint4 &d, const Place<MODE, TPR> &p, int v, int s)
+{
+    if (MODE != kJoinWindow || p.whole(v, s)) return d;
+    uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        w[i] &= (p.valid(v, 2 * i, s) ? 0xFFFFu : 0u) | (p.valid(v, 2 * i + 1, s) ? 0xFFFF0000u : 0u);
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // `row` is the address of the row's column 0.
 template <int MODE, int TPR>
 __device__ __forceinline__ uint4 load8(const uint16_t *row, const Place<MODE, TPR> &p, int v, int s)
 {
-    if (p.whole(v, s)) return *reinterpret_cast<const uint4 *>(row + p.col(v, 0, s));
-    if constexpr (MODE != kJoinAligned) return load_elements(row, p, v, s);
-    return make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (MODE == kJoinScalar) return load_elements(row, p, v, s);
+    if (!p.some(v, s)) return make_uint4(0u, 0u, 0u, 0u);
+    return own_elements(*reinterpret_cast<const uint4 *>(row + p.col(v, 0, s)), p, v, s);
 }
 
 template <int MODE, int TPR>
@@ -220,6 +240,34 @@ __device__ __forceinline__ void store8(uint16_t *row, const Place<MODE, TPR> &p,
     }
 }
 
+// 8 elements from any 2-byte aligned address: the one or two aligned 16-byte
+// words they lie in, shifted together; a word without any of the elements
+// [first, last) (counted from p) is not read.  The distance from the boundary
+// is the same for all threads of a row.
+__device__ __forceinline__ uint4 load_shifted(const uint16_t *p, int first, int last)
+{
+    const int d = static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 1) & 7u);
+    const uint4 *q = reinterpret_cast<const uint4 *>(p - d);
+    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+    const uint4 lo = first < 8 - d ? __ldg(q) : zero;
+    if (d == 0) return lo;
+    const uint4 hi = last > 8 - d ? __ldg(q + 1) : zero;
+    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+    if (d & 4) {
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    }
+    if (d & 2) {
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    }
+    if (d & 1) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // The same columns of a vector of the row's width (gamma, beta, a gate row):
 // read-only for the whole call, zero where the thread has no column.
 template <bool BF16, int MODE, int TPR>
@@ -229,6 +277,11 @@ __device__ __forceinline__ Vec8 param8(const uint16_t *b, const Place<MODE, TPR>
         return unpack8<BF16>(p.whole(v, s) ? __ldg(reinterpret_cast<const uint4 *>(b + p.col(v, 0, s)))
                                            : make_uint4(0u, 0u, 0u, 0u));
     } else {
+        if constexpr (MODE == kJoinWindow) {
+            if (!p.some(v, s)) return filled(0.0f);
+            const int c = p.col(v, 0, s);
+            return unpack8<BF16>(own_elements(load_shifted(b + c, max(p.c0 - c, 0), min(p.c1 - c, 8)), p, v, s));
+        }
         float f[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -277,8 +330,9 @@ struct RowSumSmem {
 // cluster's CTAs add up through shared memory.  The two halves of the
 // buffers take turns, so one barrier a call is enough.  All threads of the
 // CTA (of the cluster) call it together.
+// In two steps, between which a caller may do what needs no sums.
 template <int K, int TPR>
-__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank)
+__device__ __forceinline__ void row_sum_begin(float (&v)[K], RowSumSmem &s, int &half, int cluster)
 {
     static_assert(K == 1 || K == 4 || K == 8, "values");
     constexpr int kWarps = TPR / 32;
@@ -303,8 +357,15 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half,
         return;
     }
     half ^= 1;
+    if (lane % (32 / K) == 0) reinterpret_cast<float *>(s.warp[half][threadIdx.x >> 5])[lane / (32 / K)] = v[0];
+}
+
+template <int K, int TPR>
+__device__ __forceinline__ void row_sum_end(float (&v)[K], RowSumSmem &s, int half, int cluster, uint32_t rank)
+{
+    constexpr int kWarps = TPR / 32;
+    if (kWarps == 1 && cluster == 1) return;
     const int warp = threadIdx.x >> 5;
-    if (lane % (32 / K) == 0) reinterpret_cast<float *>(s.warp[half][warp])[lane / (32 / K)] = v[0];
     __syncthreads();
     const int first = warp / kWarps * kWarps;   // the row's warps
 #pragma unroll
@@ -339,6 +400,13 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half,
 #pragma unroll
             for (int k = 0; k < K; ++k) v[k] += s.peer[half][r][k];
     }
+}
+
+template <int K, int TPR>
+__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank)
+{
+    row_sum_begin<K, TPR>(v, s, half, cluster);
+    row_sum_end<K, TPR>(v, s, half, cluster, rank);
 }
 
 // ----------------------------------------------------------------- launching
