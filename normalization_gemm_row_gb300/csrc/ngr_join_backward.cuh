@@ -232,22 +232,17 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
                 dot8(t[6], w[v], u2[v]);
                 sum8(t[7], wu);
             }
-        }
-        float k[CENTER ? 8 : 4];
-#pragma unroll
-        for (int i = 0; i < (CENTER ? 8 : 4); ++i) k[i] = t[i].x + t[i].y;
-        row_sum_begin<CENTER ? 8 : 4, TPR>(k, sums, half, cluster);
-        // While the row's other warps come to the barrier: what needs no sums.
-#pragma unroll
-        for (int v = 0; v < VECS; ++v) {
-            const Vec8 dy = unpack8<BF16>(own_elements(in[(2 * VECS + v) * kThreads], p, v, s));
             if (CENTER && a.a_dbeta2 >= 0) add8(sum_b2, v, s, dy);
             if (a.a_dgamma2 >= 0) add8(sum_g2, v, s, dy * u2[v]);
         }
         fetch(ahead, in);
         advance(ahead);
         stage = stage + 1 == a.depth ? 0 : stage + 1;
-        row_sum_end<CENTER ? 8 : 4, TPR>(k, sums, half, cluster, rank);
+
+        float k[CENTER ? 8 : 4];
+#pragma unroll
+        for (int i = 0; i < (CENTER ? 8 : 4); ++i) k[i] = t[i].x + t[i].y;
+        row_sum<CENTER ? 8 : 4, TPR>(k, sums, half, cluster, rank);
         const float c1 = rs2 * k[0] * inv_n;
         float c_0 = 0.0f, t0 = 0.0f, t1 = norm1 ? k[1] - c1 * k[2] : 0.0f;
         if constexpr (CENTER) {

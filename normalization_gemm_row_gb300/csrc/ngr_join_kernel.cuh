@@ -330,9 +330,8 @@ struct RowSumSmem {
 // cluster's CTAs add up through shared memory.  The two halves of the
 // buffers take turns, so one barrier a call is enough.  All threads of the
 // CTA (of the cluster) call it together.
-// In two steps, between which a caller may do what needs no sums.
 template <int K, int TPR>
-__device__ __forceinline__ void row_sum_begin(float (&v)[K], RowSumSmem &s, int &half, int cluster)
+__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank)
 {
     static_assert(K == 1 || K == 4 || K == 8, "values");
     constexpr int kWarps = TPR / 32;
@@ -357,15 +356,8 @@ __device__ __forceinline__ void row_sum_begin(float (&v)[K], RowSumSmem &s, int 
         return;
     }
     half ^= 1;
-    if (lane % (32 / K) == 0) reinterpret_cast<float *>(s.warp[half][threadIdx.x >> 5])[lane / (32 / K)] = v[0];
-}
-
-template <int K, int TPR>
-__device__ __forceinline__ void row_sum_end(float (&v)[K], RowSumSmem &s, int half, int cluster, uint32_t rank)
-{
-    constexpr int kWarps = TPR / 32;
-    if (kWarps == 1 && cluster == 1) return;
     const int warp = threadIdx.x >> 5;
+    if (lane % (32 / K) == 0) reinterpret_cast<float *>(s.warp[half][warp])[lane / (32 / K)] = v[0];
     __syncthreads();
     const int first = warp / kWarps * kWarps;   // the row's warps
 #pragma unroll
@@ -400,13 +392,6 @@ __device__ __forceinline__ void row_sum_end(float (&v)[K], RowSumSmem &s, int ha
 #pragma unroll
             for (int k = 0; k < K; ++k) v[k] += s.peer[half][r][k];
     }
-}
-
-template <int K, int TPR>
-__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank)
-{
-    row_sum_begin<K, TPR>(v, s, half, cluster);
-    row_sum_end<K, TPR>(v, s, half, cluster, rank);
 }
 
 // ----------------------------------------------------------------- launching
