@@ -45,15 +45,17 @@ int tile_width(int64_t rows, int64_t cols)
 
 // Few output tiles of dx: the vocabulary is cut into ranges whose sums are
 // added afterwards.  The number of ranges that leaves the busiest pair the
-// least k blocks, a tile counted as kSplitCost k blocks more (its sums are
-// written and read again), at least 8 k blocks a range.
+// least k blocks, a tile counted as kSplitCost k blocks more (its epilogue
+// and first loads), and the sums' way to memory and back (8 bytes an element
+// of dx and range) as one k block for 2 MB; at least 8 k blocks a range.
 constexpr int64_t kSplitCost = 12;
-int64_t dx_splits(int64_t tiles, int64_t k_blocks)
+int64_t dx_splits(int64_t tiles, int64_t k_blocks, int64_t elements)
 {
     if (tiles >= 8 * kPairs) return 1;
     int64_t best = 1, least = 0;
     for (int64_t s = 1; s <= 32 && (s == 1 || k_blocks / s >= 8); ++s) {
-        const int64_t cost = (tiles * s + kPairs - 1) / kPairs * ((k_blocks + s - 1) / s + (s > 1 ? kSplitCost : 4));
+        const int64_t cost = (tiles * s + kPairs - 1) / kPairs * ((k_blocks + s - 1) / s + kSplitCost) +
+                             (s > 1 ? s * elements / 250000 : 0);
         if (least == 0 || cost < least) {
             least = cost;
             best = s;
@@ -97,7 +99,7 @@ CePlan ce_plan(bool backward, int64_t M, int64_t K, int64_t V)
         p.pieces = (V + p.piece - 1) / p.piece;
         p.row = take(static_cast<size_t>(rows) * sizeof(CeRow));
         p.dz = take(static_cast<size_t>(rows) * p.piece * 2);
-        p.splits = dx_splits(rows / kCeTile * ((K + kCeTile - 1) / kCeTile), p.piece / kBK);
+        p.splits = dx_splits(rows / kCeTile * ((K + kCeTile - 1) / kCeTile), p.piece / kBK, M * K);
         if (p.splits > 1 || p.pieces > 1)
             p.sums = take(static_cast<size_t>(p.splits) * M * K * sizeof(float));
     }

@@ -1,5 +1,5 @@
-// ngr_join_api.cu -- entry points of the block join (ngr_join.cu): argument
-// checks, workspace layout, how the backward pass cuts the rows.
+// ngr_join_api.cu -- entry points of the block join (ngr_join_forward.cu,
+// ngr_join_backward.cuh, ngr_join_reduce.cu): argument checks, workspace layout, how the backward pass cuts the rows.
 #include <algorithm>
 #include <cmath>
 #include <cstring>

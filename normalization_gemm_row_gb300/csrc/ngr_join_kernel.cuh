@@ -353,6 +353,9 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half,
         const float mine = v[0];
 #pragma unroll
         for (int k = 0; k < K; ++k) v[k] = __shfl_sync(0xffffffffu, mine, k * (32 / K));
+        // (shared memory that other lanes wrote before is seen after, as with
+        // the barrier of wider rows)
+        __syncwarp();
         return;
     }
     half ^= 1;
