@@ -17,10 +17,18 @@ namespace {
 
 // Threads of a CTA: 256 (four CTAs an SM), 512 for the widest rows.
 __host__ __device__ constexpr int forward_threads(int tpr) { return tpr > 256 ? tpr : 256; }
+// CTAs an SM.  The window mode's addresses want more registers than 64: with
+// a warp a row 85 are faster (16000 x 1151: 68 against 74 us), with wider rows
+// the fourth CTA is (8192 x 8191: 228 against 365 us).
+__host__ __device__ constexpr int forward_ctas(int mode, int tpr)
+{
+    const int threads = mode == kJoinScalar ? 512 : mode == kJoinWindow && tpr == 32 ? 768 : 1024;
+    return threads / forward_threads(tpr);
+}
 constexpr unsigned kWave = 4 * kJoinSms;   // CTAs that run at once
 
 template <bool BF16, int MODE, int TPR, int VECS>
-__global__ void __launch_bounds__(forward_threads(TPR), (MODE == kJoinAligned ? 1024 : MODE == kJoinWindow && TPR <= 256 ? 768 : 512) / forward_threads(TPR))
+__global__ void __launch_bounds__(forward_threads(TPR), forward_ctas(MODE, TPR))
     join_forward_kernel(const __grid_constant__ JoinArgs a)
 {
     constexpr int kSlots = forward_threads(TPR) / TPR;
