@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "ngr.h"
+#include "ngr_entry.h"
 #include "ngr_internal.h"
 #include "ngr_ptx.cuh"
 
@@ -301,7 +302,13 @@ EncodeTiledFn encode_fn()
 bool aligned2(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 1u) == 0; }
 
 bool map_2d(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t cols,
-            uint32_t box_rows, int64_t pitch)
+            uint32_t box_rows)
+{
+    return map_2d_pitch(m, ptr, bf16, rows, cols, box_rows, cols);
+}
+
+bool map_2d_pitch(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t cols, uint32_t box_rows,
+                  int64_t pitch)
 {
     EncodeTiledFn enc = encode_fn();
     if (!enc) {
@@ -309,7 +316,7 @@ bool map_2d(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t co
         return false;
     }
     cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch < 0 ? cols : pitch) * 2};
+    cuuint64_t strides[1] = {static_cast<cuuint64_t>(pitch) * 2};
     cuuint32_t box[2] = {static_cast<cuuint32_t>(kBK), box_rows};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2,

@@ -7,6 +7,7 @@
 // 128-byte lines whatever K is.  The copy moves 4 K bytes a token against the
 // 2 K V operations of one product.
 #include "ngr_ce.h"
+#include "ngr_entry.h"
 #include "ngr_internal.h"
 #include "ngr_ptx.cuh"
 

@@ -7,6 +7,7 @@
 
 #include "ngr.h"
 #include "ngr_ce.h"
+#include "ngr_entry.h"
 #include "ngr_internal.h"
 
 namespace ngr {
@@ -269,7 +270,7 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
         NGR_TIMED(launch_ce_gemm(kCeGrad, c.bf16, a, tiles_of(M, n, a.width), stream));
         if (dx) {
             a = ce_args(c);
-            if (!map_2d(&a.map_a, dz, c.bf16, rows, n, kBM, c.p.piece) ||
+            if (!map_2d_pitch(&a.map_a, dz, c.bf16, rows, n, kBM, c.p.piece) ||
                 !map_2d(&a.map_b, Wi, c.bf16, n, c.t.K8, kBK))
                 return NGR_ERR_CUDA;
             a.cols = static_cast<int>(K);
@@ -286,7 +287,7 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
         }
         if (dW) {
             a = ce_args(c);
-            if (!map_2d(&a.map_a, dz, c.bf16, rows, n, kBK, c.p.piece) ||
+            if (!map_2d_pitch(&a.map_a, dz, c.bf16, rows, n, kBK, c.p.piece) ||
                 !map_2d(&a.map_b, c.t.xc, c.bf16, up_to(M, 64), c.t.Kx, kBK))
                 return NGR_ERR_CUDA;
             a.rows = static_cast<int>(n);

@@ -35,6 +35,7 @@
 // commit to both; acc_full[a] the same at a tile's end; acc_empty[a] on the
 // leader, one arrival per epilogue warp of both CTAs.
 #include "ngr_ce.h"
+#include "ngr_ce_ptx.cuh"
 #include "ngr_gemm_kernel.cuh"
 
 namespace ngr {

@@ -151,26 +151,16 @@ constexpr int kMinKbPerSplitSingle = 16;
 // ngr_last_error).  Returns -7 (NGR_ERR_CUDA) for use in return statements.
 int record_cuda_error(const char *what, int code, const char *detail);
 
-// What the entry points outside ngr_api.cu share with those in it: the
-// current device's SM count (NGR_OK, or NGR_ERR_ARCH / NGR_ERR_CUDA), the
-// kernel timing (begin, then a pair around each launch), and the end of a
-// call (launch errors; with NGR_DEBUG the error word, `ws` may be null).
-int device_sms(int *sms);
-void call_begin();
-void kernel_begin(cudaStream_t stream);
-void kernel_end(cudaStream_t stream);
-int call_end(int rc, void *ws, cudaStream_t stream);
-
 // NGR_DEBUG set (and not "0"): every entry point synchronizes its stream
 // after launching and reports the device error word.
 bool debug_mode();
 // Bound on every in-kernel barrier wait: NGR_WAIT_TIMEOUT_MS, default 2 s.
 unsigned long long wait_timeout_ns();
 // Tensor maps (record the reason in ngr_last_error on failure):
-// row-major [rows, cols] 16-bit matrix (rows `pitch` elements apart, cols if
-// negative), box {64 columns, box_rows rows}, 128-byte swizzle;
+// row-major [rows, cols] 16-bit matrix, box {64 columns, box_rows rows},
+// 128-byte swizzle;
 bool map_2d(CUtensorMap *m, const void *ptr, bool bf16, int64_t rows, int64_t cols,
-            uint32_t box_rows, int64_t pitch = -1);
+            uint32_t box_rows);
 // FP32 gamma and beta as the two rows of a [2, K] matrix whose rows are
 // `row_stride` bytes apart, box {64 columns, 2 rows}, no swizzle.
 bool map_gb(CUtensorMap *m, const float *gamma_f, int64_t K, size_t row_stride);

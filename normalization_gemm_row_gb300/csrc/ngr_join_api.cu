@@ -5,6 +5,7 @@
 #include <cstring>
 
 #include "ngr.h"
+#include "ngr_entry.h"
 #include "ngr_internal.h"
 #include "ngr_join.h"
 
