@@ -16,6 +16,7 @@ every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 
@@ -203,6 +204,7 @@ def ngr_fused_norm_gate_residual_norm_backward(norm1, norm2, dy, dh, x, residual
         dgamma2, dbeta2, ws, ws_bytes, stream)
 
 
+@functools.lru_cache(maxsize=4096)      # a function of the sizes alone, asked for at every call
 def ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rows_per_gate, M, N) -> int:
     return int(lib().ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rows_per_gate, M, N))
 
@@ -220,6 +222,7 @@ def ngr_fused_linear_cross_entropy_backward(dloss, dlse, lse, x, W, target, logi
                                                          ws_bytes, stream)
 
 
+@functools.lru_cache(maxsize=4096)
 def ngr_linear_cross_entropy_workspace_bytes(backward, M, K, V) -> int:
     return int(lib().ngr_linear_cross_entropy_workspace_bytes(backward, M, K, V))
 
@@ -526,23 +529,27 @@ def fused_linear_residual_norm(x, W, gamma, norm: int = NORM_RMS, beta=None, bia
 
 def _uniform(x, *ts):
     """x is a 16-bit CUDA tensor, and the others (None left out) share its
-    type and device; all are contiguous.  Returns x's dtype code."""
-    dtype, device = x.dtype, x.device
+    type and device; all are contiguous.  Returns x's dtype code and the
+    addresses of the others (None for those left out)."""
+    dtype, index = x.dtype, x.get_device()
     code = _dtype_code(x)
-    if not x.is_cuda:
+    if index < 0:
         raise ValueError("all tensors must be CUDA tensors")
     if not x.is_contiguous():
         raise ValueError("all tensors must be contiguous")
+    at = [code]
     for t in ts:
         if t is None:
+            at.append(None)
             continue
         if t.dtype != dtype:
             raise TypeError("all tensors must share one dtype")
-        if t.device != device:
+        if t.get_device() != index:
             raise ValueError("all tensors must be on one CUDA device")
         if not t.is_contiguous():
             raise ValueError("all tensors must be contiguous")
-    return code
+        at.append(t.data_ptr())
+    return at
 
 
 def _tokens(x, what, *ts):
@@ -625,7 +632,8 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
     M, N, rpg, gamma1, beta1, gamma2, beta2 = _join_operands(
         x, gate, norm1, gamma1, beta1, norm2, gamma2, beta2)
     _tokens(x, "residual, h and out", residual, h, out)
-    code = _uniform(x, residual, gate, gamma1, beta1, gamma2, beta2, h, out)
+    code, p_res, p_gate, p_g1, p_b1, p_g2, p_b2, _, _ = _uniform(
+        x, residual, gate, gamma1, beta1, gamma2, beta2, h, out)
     if not _on_device(x):
         with torch.cuda.device(x.device):
             return fused_norm_gate_residual_norm(
@@ -639,10 +647,11 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
         out = torch.empty_like(x)
     st = torch.empty((M, 4), dtype=torch.float32, device=x.device) if return_stats else None
     rc = lib().ngr_fused_norm_gate_residual_norm(
-        norm1, norm2, _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1), _ptr(beta1),
-        _ptr(gamma2), _ptr(beta2), eps1, eps2, residual_scale, block_scale, M, N, code, _ptr(h),
-        _ptr(out), _ptr(st), _launch_stream(x, stream, h, out, st))
-    _raise(rc, "fused_norm_gate_residual_norm")
+        norm1, norm2, x.data_ptr(), p_res, p_gate, rpg, p_g1, p_b1, p_g2, p_b2, eps1, eps2,
+        residual_scale, block_scale, M, N, code, h.data_ptr(), _ptr(out), _ptr(st),
+        _launch_stream(x, stream, h, out, st))
+    if rc != 0:
+        raise NgrError(rc, "fused_norm_gate_residual_norm")
     return (h, out, st) if return_stats else (h, out)
 
 
@@ -659,7 +668,8 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     M, N, rpg, gamma1, beta1, gamma2, _ = _join_operands(
         x, gate, norm1, gamma1, beta1, norm2, gamma2, None)
     _tokens(x, "residual, dy and dh", residual, dy, dh)
-    code = _uniform(x, dy, dh, residual, gate, gamma1, beta1, gamma2)
+    code, p_dy, p_dh, p_res, p_gate, p_g1, p_b1, p_g2 = _uniform(
+        x, dy, dh, residual, gate, gamma1, beta1, gamma2)
     if (stats.dtype != torch.float32 or stats.numel() != 4 * M or stats.device != x.device
             or not stats.is_contiguous()):
         raise ValueError("stats must be the float32 [M, 4] of the forward call")
@@ -678,14 +688,15 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     db1 = like(beta1) if beta1 is not None else None
     dg2 = like(gamma2) if gamma2 is not None else None
     db2 = like(gamma2) if norm2 == NORM_LAYER else None
-    ws = _scratch(lib().ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rpg, M, N),
+    ws = _scratch(ngr_norm_gate_residual_norm_workspace_bytes(norm1, norm2, rpg, M, N),
                   x.device, workspace)
     rc = lib().ngr_fused_norm_gate_residual_norm_backward(
-        norm1, norm2, _ptr(dy), _ptr(dh), _ptr(x), _ptr(residual), _ptr(gate), rpg, _ptr(gamma1),
-        _ptr(beta1), _ptr(gamma2), _ptr(stats), residual_scale, block_scale, M, N, code, _ptr(dx),
-        _ptr(dr), _ptr(dg), _ptr(dg1), _ptr(db1), _ptr(dg2), _ptr(db2), _ptr(ws),
-        ws.numel() * ws.element_size(), _launch_stream(x, stream, dx, dr, dg, dg1, db1, dg2, db2, ws))
-    _raise(rc, "fused_norm_gate_residual_norm_backward")
+        norm1, norm2, p_dy, p_dh, x.data_ptr(), p_res, p_gate, rpg, p_g1, p_b1, p_g2,
+        stats.data_ptr(), residual_scale, block_scale, M, N, code, dx.data_ptr(), _ptr(dr), _ptr(dg),
+        _ptr(dg1), _ptr(db1), _ptr(dg2), _ptr(db2), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _launch_stream(x, stream, dx, dr, dg, dg1, db1, dg2, db2, ws))
+    if rc != 0:
+        raise NgrError(rc, "fused_norm_gate_residual_norm_backward")
     return {"dx": dx, "dresidual": dr, "dgate": dg, "dgamma1": dg1, "dbeta1": db1, "dgamma2": dg2,
             "dbeta2": db2}
 
@@ -699,7 +710,7 @@ def _ce_operands(x, W, target):
         raise TypeError("target must be int64")
     if target.shape != x.shape[:-1]:
         raise ValueError("target must have one entry per row of x")
-    code = _uniform(x, W)
+    code, _ = _uniform(x, W)
     if target.device != x.device or not target.is_contiguous():
         raise ValueError("target must be contiguous and on x's device")
     return target.numel(), K, W.shape[0], code
@@ -724,7 +735,7 @@ def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, st
             return fused_linear_cross_entropy(x, W, target, logit_scale, workspace, stream)
     loss = torch.empty(target.shape, dtype=torch.float32, device=x.device)
     lse = torch.empty_like(loss)
-    ws = _scratch(lib().ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
+    ws = _scratch(ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
     rc = lib().ngr_fused_linear_cross_entropy(
         _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V, code, _ptr(loss), _ptr(lse), _ptr(ws),
         ws.numel() * ws.element_size(), _launch_stream(x, stream, loss, lse, ws))
@@ -745,7 +756,7 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
                                                        need_dx, need_dW, workspace, stream)
     dx = torch.empty_like(x) if need_dx else None
     dW = torch.empty_like(W) if need_dW else None
-    ws = _scratch(lib().ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
+    ws = _scratch(ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
     rc = lib().ngr_fused_linear_cross_entropy_backward(
         _ptr(dloss), _ptr(dlse), _ptr(lse), _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
         code, _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(),
