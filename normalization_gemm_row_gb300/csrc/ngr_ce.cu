@@ -10,6 +10,7 @@
 #include "ngr_entry.h"
 #include "ngr_internal.h"
 #include "ngr_ptx.cuh"
+#include "ngr_shift.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -24,6 +25,29 @@ constexpr float kDzUnit = 8192.0f;   // dz's largest weight
 constexpr int kIndexThreads = 1024, kIndexEach = 8;
 constexpr int kGatherThreads = 128;
 constexpr int kFewTokens = kGatherThreads * kIndexEach;   // index and gather in one kernel up to this
+
+// W's rows of K elements (K % 8 != 0) as rows on 128-byte lines, zeros up to
+// the next multiple of 8: one 16-byte piece a thread, from the aligned words
+// it lies in.
+__global__ void __launch_bounds__(256) ce_pad_kernel(const uint16_t *__restrict__ src, uint4 *__restrict__ dst,
+                                                     int64_t rows, int K, int pitch_vecs)
+{
+    const int vecs = (K + 7) / 8;
+    const int64_t total = rows * vecs;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        const int64_t r = i / vecs;
+        const int v = static_cast<int>(i - r * vecs), left = K - 8 * v;
+        uint4 d = load_shifted(src + r * K + 8 * v, 0, left < 8 ? left : 8);
+        if (left < 8) {   // what follows belongs to the next row
+            uint32_t w[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] &= (2 * j < left ? 0xFFFFu : 0u) | (2 * j + 1 < left ? 0xFFFF0000u : 0u);
+            d = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        dst[r * pitch_vecs + v] = d;
+    }
+}
 
 // A prefix sum over the tokens [r0, r0 + THREADS x kIndexEach) gives each
 // counted token its place (their order kept) and the others theirs from the
@@ -280,7 +304,7 @@ __global__ void __launch_bounds__(ROWS == 1 ? 256 : 1024) ce_loss_kernel(
 // dx rows from the sums of the ranges of the vocabulary, in range order.
 template <bool BF16>
 __global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeTokens t,
-                                                    const float *__restrict__ sums, int64_t sums_rows, int splits)
+                                                    const float *__restrict__ sums, int64_t sums_pitch, int splits)
 {
     pdl_wait();
     const int count = t.info->count;
@@ -290,9 +314,10 @@ __global__ void __launch_bounds__(256) ce_dx_kernel(const __grid_constant__ CeTo
          i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
         const int64_t r = i / t.K;
         float v = 0.0f;
-        for (int k = 0; k < splits; ++k) v += sums[k * sums_rows * t.K + i];
+        const int64_t c = i - r * t.K;
+        for (int k = 0; k < splits; ++k) v += sums[(k * t.M + r) * sums_pitch + c];
         v *= down;
-        uint16_t *d = static_cast<uint16_t *>(t.dx) + t.index[r] * t.K + (i - r * t.K);
+        uint16_t *d = static_cast<uint16_t *>(t.dx) + t.index[r] * t.K + c;
         if constexpr (BF16) *d = __bfloat16_as_ushort(__float2bfloat16_rn(v));
         else *d = __half_as_ushort(__float2half_rn(v));
     }
@@ -320,6 +345,15 @@ int launch_after(const char *what, void (*kern)(P...), unsigned grid, unsigned t
 unsigned blocks(int64_t n, int64_t most) { return static_cast<unsigned>(n < 1 ? 1 : n < most ? n : most); }
 
 }  // namespace
+
+int launch_ce_pad(const void *W, void *dst, int64_t rows, int64_t K, int64_t pitch, cudaStream_t stream)
+{
+    ce_pad_kernel<<<blocks((rows * ((K + 7) / 8) + 255) / 256, 152 * 8), 256, 0, stream>>>(
+        static_cast<const uint16_t *>(W), static_cast<uint4 *>(dst), rows, static_cast<int>(K),
+        static_cast<int>(pitch / 8));
+    const cudaError_t e = cudaGetLastError();
+    return e == cudaSuccess ? 0 : record_cuda_error("cross entropy weight copy launch", e, cudaGetErrorString(e));
+}
 
 bool launch_ce_index_apart(const CeTokens &t) { return t.M > kFewTokens; }
 
@@ -355,12 +389,12 @@ int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, in
                         stream, t, part, part_pitch, parts, z_target, loss, lse);
 }
 
-int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_rows, int splits,
+int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_pitch, int splits,
                  cudaStream_t stream)
 {
     const unsigned grid = blocks((t.M * t.K + 255) / 256, 152 * 8);
     return launch_after("cross entropy dx sums launch", bf16 ? ce_dx_kernel<true> : ce_dx_kernel<false>, grid, 256u,
-                        stream, t, sums, sums_rows, splits);
+                        stream, t, sums, sums_pitch, splits);
 }
 
 }  // namespace ngr

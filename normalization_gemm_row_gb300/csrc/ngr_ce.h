@@ -56,8 +56,8 @@ struct alignas(128) CeGemmArgs {
     void *out;              // kCeGrad: dz [rows][pitch]; kCeDw: dW at v0; kCeDx: dx (finish)
     int64_t pitch;          // elements between rows of `out`
     int boxes;              // kCeDw: aligned rows, written as boxes (map_out)
-    float *sums;            // kCeDx: FP32 [splits][sums_rows][cols]
-    int64_t sums_rows;
+    float *sums;            // kCeDx: FP32 [splits][sums_rows][sums_pitch]
+    int64_t sums_rows, sums_pitch;
     int add;                // kCeDx: add to the sums of the pieces before
     int finish;             // kCeDx: this is the last piece and splits == 1: write dx itself
     const int *index;       // kCeDx (finish): a counted token's row of x
@@ -75,7 +75,7 @@ struct CeTokens {
     void *dx;               // [M, K] or null: rows of tokens that do not count are zeroed
     float logit_scale;
     int64_t M, K, V;
-    int64_t K8, Kx;         // K up to multiples of 8 (rows of W) and 64 (rows of xc)
+    int64_t K8, Kx;         // K up to multiples of 8 (what W's rows hold) and 64 (rows of xc)
     CeInfo *info;
     int *err;
     int *index;             // [M] counted tokens in order, the others behind them
@@ -84,6 +84,8 @@ struct CeTokens {
     void *xc;               // [M up to 64][Kx] the counted tokens' rows, zeros behind
 };
 
+// W's rows at `pitch` elements (a multiple of 8).
+int launch_ce_pad(const void *W, void *dst, int64_t rows, int64_t K, int64_t pitch, cudaStream_t stream);
 // The tokens' index and the gathered rows: two kernels, or for few tokens the
 // second alone.
 bool launch_ce_index_apart(const CeTokens &t);
@@ -91,7 +93,7 @@ int launch_ce_index(const CeTokens &t, cudaStream_t stream);
 int launch_ce_gather(const CeTokens &t, cudaStream_t stream);
 int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, int parts,
                    const float *z_target, float *loss, float *lse, cudaStream_t stream);
-int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_rows, int splits,
+int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_pitch, int splits,
                  cudaStream_t stream);
 int ce_clusters();          // resident CTA pairs of the product kernels
 

@@ -66,7 +66,8 @@ int64_t dx_splits(int64_t tiles, int64_t k_blocks, int64_t elements)
 }
 
 struct CePlan {
-    int64_t K8, Kx, piece, pieces, splits, parts;
+    int64_t K8, Kx, w_pitch, piece, pieces, splits, parts;
+    bool finish;
     size_t info, index, ctarget, xc, wp, row, part, z_target, dz, sums, total;
 };
 
@@ -86,7 +87,8 @@ CePlan ce_plan(bool backward, int64_t M, int64_t K, int64_t V)
     p.index = take(static_cast<size_t>(M) * 4);
     p.ctarget = take(static_cast<size_t>(M) * 4);
     p.xc = take(static_cast<size_t>(up_to(std::max<int64_t>(M, 1), 64)) * p.Kx * 2);
-    if (K % 8 != 0) p.wp = take(static_cast<size_t>(V) * p.K8 * 2);
+    p.w_pitch = K % 8 == 0 ? K : p.Kx;
+    if (K % 8 != 0) p.wp = take(static_cast<size_t>(V) * p.w_pitch * 2);
     if (!backward) {
         const int64_t w = tile_width(M, V);
         p.parts = (V + w - 1) / w * 2;
@@ -101,8 +103,11 @@ CePlan ce_plan(bool backward, int64_t M, int64_t K, int64_t V)
         p.row = take(static_cast<size_t>(rows) * sizeof(CeRow));
         p.dz = take(static_cast<size_t>(rows) * p.piece * 2);
         p.splits = dx_splits(rows / kCeTile * ((K + kCeTile - 1) / kCeTile), p.piece / kBK, M * K);
-        if (p.splits > 1 || p.pieces > 1)
-            p.sums = take(static_cast<size_t>(p.splits) * M * K * sizeof(float));
+        // dx itself is written by the last piece's product where its rows take
+        // 16-byte pieces and nothing is left to add.
+        p.finish = p.splits == 1 && K % 8 == 0;
+        if (!p.finish || p.pieces > 1)
+            p.sums = take(static_cast<size_t>(p.splits) * M * p.Kx * sizeof(float));
     }
     p.total = off;
     return p;
@@ -119,7 +124,7 @@ struct CeCall {
     CeTokens t;
     CePlan p;
     char *ws;
-    const void *W;   // rows of K8 elements
+    const void *W;   // rows of K8 elements, w_pitch apart
     bool bf16;
     cudaStream_t stream;
 };
@@ -155,7 +160,7 @@ int ce_begin(CeCall *c, bool backward, const void *x, const void *W, const int64
     t.index = reinterpret_cast<int *>(ws + c->p.index);
     t.ctarget = reinterpret_cast<int *>(ws + c->p.ctarget);
     t.xc = ws + c->p.xc;
-    if (K % 8 != 0) return launch_pad_rows(W, V, K, K, ws + c->p.wp, c->p.K8, sms, c->stream);
+    if (K % 8 != 0) return launch_ce_pad(W, ws + c->p.wp, V, K, c->p.w_pitch, c->stream);
     return NGR_OK;
 }
 
@@ -203,7 +208,7 @@ int ce_forward(const void *x, const void *W, const int64_t *target, float logit_
     CeGemmArgs a = ce_args(c);
     a.width = tile_width(M, V);
     if (!map_2d(&a.map_a, c.t.xc, c.bf16, up_to(M, 64), c.t.Kx, kBM) ||
-        !map_2d(&a.map_b, c.W, c.bf16, V, c.t.K8, static_cast<uint32_t>(a.width / 2)))
+        !map_2d_pitch(&a.map_b, c.W, c.bf16, V, c.t.K8, static_cast<uint32_t>(a.width / 2), c.p.w_pitch))
         return NGR_ERR_CUDA;
     a.cols = static_cast<int>(V);
     a.depth = static_cast<int>(c.t.K8);
@@ -255,11 +260,11 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
     float *sums = reinterpret_cast<float *>(c.ws + c.p.sums);
     for (int64_t i = 0; i < c.p.pieces; ++i) {
         const int64_t v0 = i * c.p.piece, n = std::min(c.p.piece, V - v0);
-        const char *Wi = static_cast<const char *>(c.W) + v0 * c.t.K8 * 2;
+        const char *Wi = static_cast<const char *>(c.W) + v0 * c.p.w_pitch * 2;
         CeGemmArgs a = ce_args(c);
         a.width = tile_width(M, n);
         if (!map_2d(&a.map_a, c.t.xc, c.bf16, up_to(M, 64), c.t.Kx, kBM) ||
-            !map_2d(&a.map_b, Wi, c.bf16, n, c.t.K8, static_cast<uint32_t>(a.width / 2)))
+            !map_2d_pitch(&a.map_b, Wi, c.bf16, n, c.t.K8, static_cast<uint32_t>(a.width / 2), c.p.w_pitch))
             return NGR_ERR_CUDA;
         a.cols = static_cast<int>(n);
         a.depth = static_cast<int>(c.t.K8);
@@ -271,15 +276,16 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
         if (dx) {
             a = ce_args(c);
             if (!map_2d_pitch(&a.map_a, dz, c.bf16, rows, n, kBM, c.p.piece) ||
-                !map_2d(&a.map_b, Wi, c.bf16, n, c.t.K8, kBK))
+                !map_2d_pitch(&a.map_b, Wi, c.bf16, n, c.t.K8, kBK, c.p.w_pitch))
                 return NGR_ERR_CUDA;
             a.cols = static_cast<int>(K);
             a.depth = static_cast<int>(n);
             a.splits = static_cast<int>(c.p.splits);
             a.sums = sums;
             a.sums_rows = M;
+            a.sums_pitch = c.p.Kx;
             a.add = i > 0;
-            a.finish = i == c.p.pieces - 1 && c.p.splits == 1;
+            a.finish = i == c.p.pieces - 1 && c.p.finish;
             a.out = dx;
             a.pitch = K;
             a.index = c.t.index;
@@ -300,8 +306,8 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
             NGR_TIMED(launch_ce_gemm(kCeDw, c.bf16, a, tiles_of(n, K), stream));
         }
     }
-    if (dx && c.p.splits > 1)
-        NGR_TIMED(launch_ce_dx(c.bf16, c.t, sums, M, static_cast<int>(c.p.splits), stream));
+    if (dx && !c.p.finish)
+        NGR_TIMED(launch_ce_dx(c.bf16, c.t, sums, c.p.Kx, static_cast<int>(c.p.splits), stream));
     return call_end(rc, workspace, stream);
 }
 

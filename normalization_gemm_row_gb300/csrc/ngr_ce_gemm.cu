@@ -116,13 +116,16 @@ __device__ __forceinline__ void store16(const float (&v)[kCePart], uint16_t *p, 
     }
 }
 
-// 128 values of each of a warp's 32 rows through the warp's own shared memory
-// to the box at (c, row0): whole lines to memory, where stores by rows from
-// 32 lanes write a sector of 32 lines each (dW of 33 tokens, 65536 x 8192:
-// 317 us so).  `box` is the warp's two 4 KB boxes in the 128-byte swizzle.
+// A warp's 32 rows of 128 values to the output at row0, column c, by way of
+// its own two 4 KB boxes of 64 columns in shared memory (the 128-byte
+// swizzle), so that whole lines go to memory: stores by rows from 32 lanes
+// write a sector of 32 lines each (dW of 33 tokens, 65536 x 8192: 317 us so,
+// 217 through the boxes).  With a tensor map one lane stores the boxes; where
+// the output's rows start at any element the warp writes row after row, two
+// elements a lane on 4-byte boundaries.
 template <bool BF16>
-__device__ __forceinline__ void store_boxes(const float (&v)[kCePart], uint8_t *box, const CUtensorMap *map,
-                                            int c, int row0, int lane, int cols, int rows)
+__device__ __forceinline__ void store_boxes(const float (&v)[kCePart], uint8_t *box, const CeGemmArgs &args, int c,
+                                            int row0, int lane)
 {
     if (lane == 0) tma_store_wait_read();   // the last tile's stores have read it
     __syncwarp();
@@ -134,14 +137,34 @@ __device__ __forceinline__ void store_boxes(const float (&v)[kCePart], uint8_t *
         *reinterpret_cast<uint4 *>(box + (i >> 3) * kCeOutBox + lane * 128 + (((i & 7) ^ (lane & 7)) << 4)) =
             make_uint4(o[0], o[1], o[2], o[3]);
     }
-    fence_proxy_async_smem();
+    if (args.boxes) fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-        if (row0 < rows) {
-            tma_store_2d(map, box, c, row0);
-            if (c + 64 < cols) tma_store_2d(map, box + kCeOutBox, c + 64, row0);
+    if (args.boxes) {
+        if (lane == 0) {
+            if (row0 < args.rows) {
+                tma_store_2d(&args.map_out, box, c, row0);
+                if (c + 64 < args.cols) tma_store_2d(&args.map_out, box + kCeOutBox, c + 64, row0);
+            }
+            tma_store_commit();
         }
-        tma_store_commit();
+        return;
+    }
+    const int n = min(kCePart, args.cols - c);
+#pragma unroll 1
+    for (int r = 0; r < 32 && row0 + r < args.rows; ++r) {
+        uint16_t *p = static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row0 + r) * args.pitch + c;
+        auto at = [&](int k) {
+            return *reinterpret_cast<const uint16_t *>(box + (k >> 6) * kCeOutBox + r * 128 +
+                                                       ((((k & 63) >> 3) ^ (r & 7)) << 4) + (k & 7) * 2);
+        };
+        const int odd = static_cast<int>(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+        if (odd && lane == 0) p[0] = at(0);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int k = odd + 2 * (32 * j + lane);
+            if (k + 1 < n) *reinterpret_cast<uint32_t *>(p + k) = at(k) | (static_cast<uint32_t>(at(k + 1)) << 16);
+            else if (k < n) p[k] = at(k);
+        }
     }
 }
 
@@ -430,23 +453,15 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
             } else if constexpr (MODE == kCeDw) {
 #pragma unroll
                 for (int j = 0; j < kCePart; ++j) v[j] *= down;
-                if (args.boxes)
-                    store_boxes<BF16>(v, out_box, &args.map_out, c0, row - lane, lane, args.cols, args.rows);
-                else if (row < args.rows)
-                    store16<BF16>(v, static_cast<uint16_t *>(args.out) + static_cast<int64_t>(row) * args.pitch + c0, cols);
+                store_boxes<BF16>(v, out_box, args, c0, row - lane, lane);
             } else if (row < count) {
-                float *s = args.sums + (units.split(u) * args.sums_rows + row) * static_cast<int64_t>(args.cols) + c0;
-                const bool sectors = (reinterpret_cast<uintptr_t>(s) & 31u) == 0;
+                // (rows of sums are padded: whole sectors always)
+                float *s = args.sums + (units.split(u) * args.sums_rows + row) * args.sums_pitch + c0;
 #pragma unroll
                 for (int c = 0; c < kCePart; c += 8) {
                     if (c >= cols || !args.add) break;
                     float o[8];
-                    if (c + 8 <= cols && sectors) {
-                        ld_global_v8(s + c, o);
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) o[i] = c + i < cols ? s[c + i] : 0.0f;
-                    }
+                    ld_global_v8(s + c, o);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) v[c + i] += o[i];
                 }
@@ -459,16 +474,10 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
 #pragma unroll
                     for (int c = 0; c < kCePart; c += 8) {
                         if (c >= cols) break;
-                        if (c + 8 <= cols && sectors) {
-                            uint32_t o[8];
+                        uint32_t o[8];
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[c + i]);
-                            st_global_v8(s + c, o);
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                if (c + i < cols) s[c + i] = v[c + i];
-                        }
+                        for (int i = 0; i < 8; ++i) o[i] = __float_as_uint(v[c + i]);
+                        st_global_v8(s + c, o);
                     }
                 }
             }
