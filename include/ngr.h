@@ -276,10 +276,9 @@ int ngr_fused_norm_gate_residual_norm_backward(
     const void *residual, const void *gate, int64_t rows_per_gate,
     const void *gamma1, const void *beta1, const void *gamma2,
     const float *stats, float residual_scale, float block_scale, int64_t M,
-    int64_t N, int dtype, void *dx,
-    void *dresidual, void *dgate, void *dgamma1, void *dbeta1, void *dgamma2,
-    void *dbeta2, void *workspace, size_t workspace_bytes,
-    ngr_stream_t stream);
+    int64_t N, int dtype, void *dx, void *dresidual, void *dgate,
+    void *dgamma1, void *dbeta1, void *dgamma2, void *dbeta2, void *workspace,
+    size_t workspace_bytes, ngr_stream_t stream);
 
 /* Bytes of workspace of the backward call above (0 for invalid sizes). */
 size_t ngr_norm_gate_residual_norm_workspace_bytes(int norm1, int norm2,
@@ -328,8 +327,9 @@ int ngr_fused_linear_cross_entropy_backward(
 
 /* Bytes of workspace of the two calls above (0 for invalid sizes): the
  * counted tokens' rows, and forward 16 bytes per token and tile of 128 to 256
- * vocabulary entries, backward dz of a piece of the vocabulary (256 MB, or 4096 entries
- * if that is more) and FP32 sums of dx where it is not made in one go. */
+ * vocabulary entries, backward dz of a piece of the vocabulary (256 MB, or
+ * 4096 entries if that is more) and FP32 sums of dx where it is not made in
+ * one go. */
 size_t ngr_linear_cross_entropy_workspace_bytes(int backward, int64_t M,
                                                 int64_t K, int64_t V);
 
@@ -417,7 +417,8 @@ int ngr_row_stats(int norm, const void *x, float eps, int64_t M, int64_t K,
 
 /* Synchronize `stream`, then return and clear the error word kept in
  * `workspace` (NGR_OK, NGR_ERR_TIMEOUT when a kernel's bounded wait ran
- * out, or NGR_ERR_ARG for a target outside the vocabulary).  NGR_ERR_CUDA if the synchronization itself fails. */
+ * out, or NGR_ERR_ARG for a target outside the vocabulary).  NGR_ERR_CUDA if
+ * the synchronization itself fails. */
 int ngr_workspace_error(void *workspace, ngr_stream_t stream);
 
 /* Launch one tiny kernel whose mbarrier wait can never complete, bounded by

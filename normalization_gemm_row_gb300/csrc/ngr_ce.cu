@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kGatherThreads) ce_index_gather_kernel(const _
 __device__ __forceinline__ void merge(float &m, float &s, float om, float os)
 {
     const float top = fmaxf(m, om);
-    const float base = top == -INFINITY ? 0.0f : top;
+    const float base = fabsf(top) == INFINITY ? 0.0f : top;   // (inf - inf is no number)
     s = s * exp2f(m - base) + os * exp2f(om - base);
     m = top;
 }

@@ -431,8 +431,8 @@ __global__ void __launch_bounds__(kCeThreads, 1) ce_gemm_kernel(const __grid_con
                     m[j & 3] = j < 4 ? v[j] : fmaxf(m[j & 3], v[j]);
                 }
                 const float top = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-                // (every logit -inf: their sum stays zero)
-                const float base = top == -INFINITY ? 0.0f : top;
+                // (every logit -inf: their sum stays zero; one +inf: inf, not NaN)
+                const float base = fabsf(top) == INFINITY ? 0.0f : top;
 #pragma unroll
                 for (int j = 0; j < kCePart; ++j) {
                     const float x = exp2_approx(v[j] - base);

@@ -1,5 +1,6 @@
 // ngr_join_api.cu -- entry points of the block join (ngr_join_forward.cu,
-// ngr_join_backward.cuh, ngr_join_reduce.cu): argument checks, workspace layout, how the backward pass cuts the rows.
+// ngr_join_backward.cuh, ngr_join_reduce.cu): argument checks, workspace
+// layout, how the backward pass cuts the rows.
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -203,8 +204,9 @@ size_t ngr_norm_gate_residual_norm_workspace_bytes(int norm1, int norm2, int64_t
 int ngr_fused_norm_gate_residual_norm_backward(
     int norm1, int norm2, const void *dy, const void *dh, const void *x, const void *residual,
     const void *gate, int64_t rows_per_gate, const void *gamma1, const void *beta1, const void *gamma2,
-    const float *stats, float residual_scale, float block_scale, int64_t M, int64_t N, int dtype, void *dx, void *dresidual, void *dgate, void *dgamma1, void *dbeta1, void *dgamma2,
-    void *dbeta2, void *workspace, size_t workspace_bytes, ngr_stream_t stream_)
+    const float *stats, float residual_scale, float block_scale, int64_t M, int64_t N, int dtype, void *dx,
+    void *dresidual, void *dgate, void *dgamma1, void *dbeta1, void *dgamma2, void *dbeta2, void *workspace,
+    size_t workspace_bytes, ngr_stream_t stream_)
 {
     cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
     // (beta2 has no part in the gradient: gamma2 stands in for it in the checks)

@@ -104,6 +104,32 @@ def test_large_logits():
         compare(d, "large logits")
 
 
+@pytest.mark.parametrize("dtype", list(DTYPES))
+def test_infinite_logits(dtype):
+    """An entry of W that overflowed: +inf or -inf in one logit of each token,
+    and what the formula makes of them.  A token with +inf has lse = loss =
+    inf and gives the other entries no gradient; where the formula has no
+    value (inf - inf) there is NaN, and nowhere else."""
+    d = R.case(70, 64, 600, DTYPES[dtype], seed=8, peaked=0.0)
+    d["x"][:, 0] = 1.0 - 2.0 * (torch.arange(70) % 2)
+    d["target"][d["target"] == 300] = 301
+    plain = {**d, "W": d["W"].clone()}
+    d["W"][300, 0] = float("inf")
+    plain["W"][300] = 0.0
+    got = run(d)
+    val, _ = R.reference(d, 1.0, d["dloss"])
+    up = torch.arange(70) % 2 == 0
+    assert torch.isinf(val["lse"][up]).all() and torch.isfinite(val["lse"][~up]).all()
+    for k in ("loss", "lse", "dx", "dW"):
+        a, b = got[k].double().cpu(), val[k]
+        assert torch.equal(torch.isnan(a), torch.isnan(b)) and torch.equal(torch.isinf(a), torch.isinf(b)), k
+    # the tolerance of the tokens with -inf: that of a logit of 0 there, which
+    # has no smaller sums
+    _, tol = R.reference(plain, 1.0, d["dloss"])
+    for k in ("loss", "lse"):
+        R.check(got[k].cpu()[~up], val[k][~up], tol[k][~up], k)
+
+
 def test_one_output_only():
     d = R.case(90, 128, 400, torch.float16, seed=5)
     full = run(d)
