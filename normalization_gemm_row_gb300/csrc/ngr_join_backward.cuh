@@ -37,13 +37,17 @@ __host__ __device__ constexpr int backward_ctas(int tpr, int vecs)
     return (vecs == 1 ? 768 : 512) / (tpr * backward_slots(tpr));
 }
 
+constexpr Width kWidths[] = {{32, 1}, {32, 2}, {96, 1}, {64, 2}, {160, 1}, {96, 2},
+                             {128, 2}, {192, 2}, {256, 2}, {384, 2}, {512, 2}};
+
 __device__ __forceinline__ void copy_async16(void *dst, const void *src)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
 }
 
 // CENTER: a LayerNorm on either side (8 sums a row, beta1); without one 3.
-template <bool BF16, int MODE, int TPR, int VECS, bool CENTER>
+// ONE: a CTA to a row (no cluster).
+template <bool BF16, int MODE, int TPR, int VECS, bool CENTER, bool ONE>
 __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, VECS))
     join_backward_kernel(const __grid_constant__ JoinArgs a)
 {
@@ -54,13 +58,14 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     float *const acc = reinterpret_cast<float *>(ring + a.depth * kStage);   // [arrays][slots][cols]
     __shared__ RowSumSmem sums;
     int half = 0;
-    const int cluster = a.shape.cluster;
+    const int cluster = ONE ? 1 : a.shape.cluster;
     const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0u;
     const int64_t cta = blockIdx.x / cluster;
     const int64_t n_ctas = gridDim.x / cluster;
     const int slot = threadIdx.x / TPR;
     const int c0 = static_cast<int>(rank) * a.shape.cols;
-    const Place<MODE, TPR> p(c0, min(a.N, c0 + a.shape.cols), threadIdx.x % TPR);
+    constexpr int kFull = ONE ? full_vectors(kWidths, TPR, VECS, MODE) : -1;
+    const Place<MODE, TPR, kFull> p(c0, min(a.N, c0 + a.shape.cols), threadIdx.x % TPR);
     const int ncols = p.c1 - p.c0;
     const float inv_n = 1.0f / static_cast<float>(a.N);
     const bool norm1 = a.norm1 != kNormNone, norm2 = a.norm2 != kNormNone;
@@ -300,13 +305,6 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     }
 }
 
-// Threads on a row and vectors a thread, by the vectors they hold.
-struct Width {
-    int tpr, vecs;
-};
-constexpr Width kWidths[] = {{32, 1}, {32, 2}, {96, 1}, {64, 2}, {160, 1}, {96, 2},
-                             {128, 2}, {192, 2}, {256, 2}, {384, 2}, {512, 2}};
-
 inline int64_t ring_row(const JoinShape &s) { return (4ll * s.vecs + 1) * s.tpr * s.slots * 16; }
 inline int64_t sum_bytes(const JoinShape &s, int arrays) { return static_cast<int64_t>(arrays) * s.slots * s.cols * 4; }
 
@@ -317,21 +315,25 @@ int run_mode(JoinArgs a, int ctas, cudaStream_t stream)
     const int64_t row = ring_row(a.shape), sums = sum_bytes(a.shape, a.arrays);
     a.depth = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, (kJoinSmem / a.shape.per_sm - 2048 - sums) / row)));
     const size_t smem = static_cast<size_t>(sums + a.depth * row);
-#define NGR_WIDTH(T, V)                           \
-    if (a.shape.tpr == T && a.shape.vecs == V)    \
-        return launch_join(join_backward_kernel<BF16, MODE, T, V, CENTER>, ctas, a.shape, smem, a, stream, "join gradient launch");
-    NGR_WIDTH(512, 2)
-    NGR_WIDTH(64, 2)
+#define NGR_WIDTH(T, V, ONE)                                                                                    \
+    if (a.shape.tpr == T && a.shape.vecs == V && (a.shape.cluster == 1) == ONE)                                 \
+        return launch_join(join_backward_kernel<BF16, MODE, T, V, CENTER, ONE>, ctas, a.shape, smem, a, stream, \
+                           "join gradient launch");
+    NGR_WIDTH(512, 2, true)
+    NGR_WIDTH(64, 2, true)
+    NGR_WIDTH(512, 2, false)
     if constexpr (MODE != kJoinScalar) {
-        NGR_WIDTH(32, 1)
-        NGR_WIDTH(32, 2)
-        NGR_WIDTH(96, 1)
-        NGR_WIDTH(160, 1)
-        NGR_WIDTH(96, 2)
-        NGR_WIDTH(128, 2)
-        NGR_WIDTH(192, 2)
-        NGR_WIDTH(256, 2)
-        NGR_WIDTH(384, 2)
+        NGR_WIDTH(32, 1, true)
+        NGR_WIDTH(32, 2, true)
+        NGR_WIDTH(96, 1, true)
+        NGR_WIDTH(160, 1, true)
+        NGR_WIDTH(96, 2, true)
+        NGR_WIDTH(128, 2, true)
+        NGR_WIDTH(192, 2, true)
+        NGR_WIDTH(256, 2, true)
+        NGR_WIDTH(384, 2, true)
+        NGR_WIDTH(256, 2, false)
+        NGR_WIDTH(384, 2, false)
     }
 #undef NGR_WIDTH
     return -9;

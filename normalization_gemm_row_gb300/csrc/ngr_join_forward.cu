@@ -25,20 +25,26 @@ __host__ __device__ constexpr int forward_ctas(int mode, int tpr)
     const int threads = mode == kJoinScalar ? 512 : mode == kJoinWindow && tpr == 32 ? 768 : 1024;
     return threads / forward_threads(tpr);
 }
+// A warp a row while five vectors a lane cover it (its sums need no barrier),
+// then three or four vectors a thread.
+constexpr Width kWidths[] = {{32, 1}, {32, 2}, {32, 3}, {32, 4}, {32, 5}, {64, 3}, {64, 4},
+                             {128, 3}, {128, 4}, {256, 3}, {256, 4}, {512, 3}, {512, 4}};
 constexpr unsigned kWave = 4 * kJoinSms;   // CTAs that run at once
 
-template <bool BF16, int MODE, int TPR, int VECS>
+// ONE: a CTA to a row (no cluster).
+template <bool BF16, int MODE, int TPR, int VECS, bool ONE>
 __global__ void __launch_bounds__(forward_threads(TPR), forward_ctas(MODE, TPR))
     join_forward_kernel(const __grid_constant__ JoinArgs a)
 {
     constexpr int kSlots = forward_threads(TPR) / TPR;
     __shared__ RowSumSmem sums;
     int half = 0;
-    const int cluster = a.shape.cluster;
+    const int cluster = ONE ? 1 : a.shape.cluster;
     const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0u;
     const int slot = threadIdx.x / TPR;
     const int c0 = static_cast<int>(rank) * a.shape.cols;
-    const Place<MODE, TPR> p(c0, min(a.N, c0 + a.shape.cols), threadIdx.x % TPR);
+    constexpr int kFull = ONE ? full_vectors(kWidths, TPR, VECS, MODE) : -1;
+    const Place<MODE, TPR, kFull> p(c0, min(a.N, c0 + a.shape.cols), threadIdx.x % TPR);
     const int64_t row = static_cast<int64_t>(blockIdx.x / cluster) * kSlots + slot;
     const bool active = kSlots == 1 || row < a.M;
     const int64_t off = active ? row * a.N : 0;
@@ -139,36 +145,30 @@ __global__ void __launch_bounds__(forward_threads(TPR), forward_ctas(MODE, TPR))
     if (a.stats && active && threadIdx.x % TPR == 0 && rank == 0) a.stats[row] = make_float4(mu1, rs1, mu2, rs2);
 }
 
-// Threads on a row and vectors a thread, by the vectors they hold: a warp a
-// row while five vectors a lane cover it (its sums need no barrier), then
-// three or four vectors a thread.
-struct Width {
-    int tpr, vecs;
-};
-constexpr Width kWidths[] = {{32, 1}, {32, 2}, {32, 3}, {32, 4}, {32, 5}, {64, 3}, {64, 4},
-                             {128, 3}, {128, 4}, {256, 3}, {256, 4}, {512, 3}, {512, 4}};
-
 template <bool BF16, int MODE>
 int run(const JoinArgs &a, cudaStream_t stream)
 {
     const int64_t ctas = (a.M + a.shape.slots - 1) / a.shape.slots;
-#define NGR_WIDTH(T, V)                           \
-    if (a.shape.tpr == T && a.shape.vecs == V)    \
-        return launch_join(join_forward_kernel<BF16, MODE, T, V>, ctas, a.shape, 0, a, stream, "join launch");
-    NGR_WIDTH(256, 4)
-    NGR_WIDTH(512, 4)
+#define NGR_WIDTH(T, V, ONE)                                                    \
+    if (a.shape.tpr == T && a.shape.vecs == V && (a.shape.cluster == 1) == ONE) \
+        return launch_join(join_forward_kernel<BF16, MODE, T, V, ONE>, ctas, a.shape, 0, a, stream, "join launch");
+    NGR_WIDTH(256, 4, true)
+    NGR_WIDTH(512, 4, true)
+    NGR_WIDTH(256, 4, false)
+    NGR_WIDTH(512, 4, false)
     if constexpr (MODE != kJoinScalar) {
-        NGR_WIDTH(32, 1)
-        NGR_WIDTH(32, 2)
-        NGR_WIDTH(32, 3)
-        NGR_WIDTH(32, 4)
-        NGR_WIDTH(32, 5)
-        NGR_WIDTH(64, 3)
-        NGR_WIDTH(64, 4)
-        NGR_WIDTH(128, 3)
-        NGR_WIDTH(128, 4)
-        NGR_WIDTH(256, 3)
-        NGR_WIDTH(512, 3)
+        NGR_WIDTH(32, 1, true)
+        NGR_WIDTH(32, 2, true)
+        NGR_WIDTH(32, 3, true)
+        NGR_WIDTH(32, 4, true)
+        NGR_WIDTH(32, 5, true)
+        NGR_WIDTH(64, 3, true)
+        NGR_WIDTH(64, 4, true)
+        NGR_WIDTH(128, 3, true)
+        NGR_WIDTH(128, 4, true)
+        NGR_WIDTH(256, 3, true)
+        NGR_WIDTH(512, 3, true)
+        NGR_WIDTH(512, 3, false)
     }
 #undef NGR_WIDTH
     return -9;

@@ -156,8 +156,11 @@ __device__ __forceinline__ void dot8(float2 &s, const Vec8 &a, const Vec8 &b)
 // caller's), what is not the row's is put to zero, and they are written by
 // elements.  In the scalar mode element j of vector v is column
 // c0 + (v 8 + j) TPR + t, so that neighbouring threads touch neighbouring
-// elements.
-template <int MODE, int TPR>
+// elements.  Where a CTA has whole rows, vectors from 1 on do not reach over
+// a row's start, nor the first FULL vectors over its end (see full_vectors),
+// and the tests for that fall away (8192 x 14337, LN/LN: 374 -> 273 us, the
+// gradient at 32768 x 2048 174 -> 142 us).  FULL -1: nothing is known.
+template <int MODE, int TPR, int FULL>
 struct Place {
     int c0, c1, first;   // first: the column of element 0 of vector 0 (unshifted)
     __device__ __forceinline__ Place(int c0_, int c1_, int t)
@@ -170,24 +173,28 @@ struct Place {
     }
     __device__ __forceinline__ bool valid(int v, int j, int s) const
     {
-        if constexpr (MODE == kJoinAligned) return col(v, 0, s) < c1;
+        if constexpr (MODE == kJoinAligned) return whole(v, s);
+        if (inner(v)) return true;
         const int c = col(v, j, s);
-        return c >= c0 && c < c1;
+        return (c >= c0 || (FULL >= 0 && v > 0)) && (c < c1 || v < FULL);
     }
     // any of them
     __device__ __forceinline__ bool some(int v, int s) const
     {
         const int c = col(v, 0, s);
-        return c < c1 && (MODE == kJoinAligned || c + 8 > c0);
+        return (c < c1 || v < FULL) && (MODE == kJoinAligned || c + 8 > c0 || (FULL >= 0 && v > 0));
     }
     // all 8 columns of the vector (one 16-byte access)
     __device__ __forceinline__ bool whole(int v, int s) const
     {
         if constexpr (MODE == kJoinScalar) return false;
-        if constexpr (MODE == kJoinAligned) return col(v, 0, s) < c1;
+        if (inner(v)) return true;
         const int c = col(v, 0, s);
-        return c >= c0 && c + 8 <= c1;
+        if constexpr (MODE == kJoinAligned) return c < c1;
+        return (c >= c0 || (FULL >= 0 && v > 0)) && (c + 8 <= c1 || v < FULL);
     }
+    // known to be whole
+    __device__ __forceinline__ static constexpr bool inner(int v) { return v < FULL && (MODE == kJoinAligned || v > 0); }
 };
 
 // The vector's elements one by one (zero where the thread has no column).
@@ -205,8 +212,8 @@ __device__ __forceinline__ uint4 load_elements(const uint16_t *row, const P &p, 
 }
 
 // A vector's elements with zeros where the thread has no column.
-template <int MODE, int TPR>
-__device__ __forceinline__ uint4 own_elements(const uint4 &d, const Place<MODE, TPR> &p, int v, int s)
+template <int MODE, int TPR, int FULL>
+__device__ __forceinline__ uint4 own_elements(const uint4 &d, const Place<MODE, TPR, FULL> &p, int v, int s)
 {
     if (MODE != kJoinWindow || p.whole(v, s)) return d;
     uint32_t w[4] = {d.x, d.y, d.z, d.w};
@@ -217,16 +224,16 @@ __device__ __forceinline__ uint4 own_elements(const uint4 &d, const Place<MODE, 
 }
 
 // `row` is the address of the row's column 0.
-template <int MODE, int TPR>
-__device__ __forceinline__ uint4 load8(const uint16_t *row, const Place<MODE, TPR> &p, int v, int s)
+template <int MODE, int TPR, int FULL>
+__device__ __forceinline__ uint4 load8(const uint16_t *row, const Place<MODE, TPR, FULL> &p, int v, int s)
 {
     if constexpr (MODE == kJoinScalar) return load_elements(row, p, v, s);
     if (!p.some(v, s)) return make_uint4(0u, 0u, 0u, 0u);
     return own_elements(*reinterpret_cast<const uint4 *>(row + p.col(v, 0, s)), p, v, s);
 }
 
-template <int MODE, int TPR>
-__device__ __forceinline__ void store8(uint16_t *row, const Place<MODE, TPR> &p, int v, int s, const uint4 &d)
+template <int MODE, int TPR, int FULL>
+__device__ __forceinline__ void store8(uint16_t *row, const Place<MODE, TPR, FULL> &p, int v, int s, const uint4 &d)
 {
     if (p.whole(v, s)) {
         *reinterpret_cast<uint4 *>(row + p.col(v, 0, s)) = d;
@@ -243,8 +250,8 @@ __device__ __forceinline__ void store8(uint16_t *row, const Place<MODE, TPR> &p,
 
 // The same columns of a vector of the row's width (gamma, beta, a gate row):
 // read-only for the whole call, zero where the thread has no column.
-template <bool BF16, int MODE, int TPR>
-__device__ __forceinline__ Vec8 param8(const uint16_t *b, const Place<MODE, TPR> &p, int v, int s)
+template <bool BF16, int MODE, int TPR, int FULL>
+__device__ __forceinline__ Vec8 param8(const uint16_t *b, const Place<MODE, TPR, FULL> &p, int v, int s)
 {
     if constexpr (MODE == kJoinAligned) {
         return unpack8<BF16>(p.whole(v, s) ? __ldg(reinterpret_cast<const uint4 *>(b + p.col(v, 0, s)))
@@ -253,7 +260,7 @@ __device__ __forceinline__ Vec8 param8(const uint16_t *b, const Place<MODE, TPR>
         if constexpr (MODE == kJoinWindow) {
             if (!p.some(v, s)) return filled(0.0f);
             const int c = p.col(v, 0, s);
-            return unpack8<BF16>(own_elements(load_shifted(b + c, max(p.c0 - c, 0), min(p.c1 - c, 8)), p, v, s));
+            return unpack8<BF16>(own_elements(load_shifted(b + c, p.inner(v) ? 0 : max(p.c0 - c, 0), p.inner(v) ? 8 : min(p.c1 - c, 8)), p, v, s));
         }
         float f[8];
 #pragma unroll
@@ -267,8 +274,8 @@ __device__ __forceinline__ Vec8 param8(const uint16_t *b, const Place<MODE, TPR>
 }
 
 // v with zeros where the thread has no column.
-template <int MODE, int TPR>
-__device__ __forceinline__ Vec8 masked(const Vec8 &a, const Place<MODE, TPR> &p, int v, int s)
+template <int MODE, int TPR, int FULL>
+__device__ __forceinline__ Vec8 masked(const Vec8 &a, const Place<MODE, TPR, FULL> &p, int v, int s)
 {
     if (MODE != kJoinScalar && p.whole(v, s)) return a;
     Vec8 f;
@@ -371,6 +378,23 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half,
 }
 
 // ----------------------------------------------------------------- launching
+// Threads on a row and vectors a thread; a kernel's widths are listed by the
+// vectors they hold, and a row takes the first that holds its own.
+struct Width {
+    int tpr, vecs;
+};
+// How many vectors of every thread surely end inside the row: it has more
+// vectors than the width before holds, the last of them in part (in the
+// window mode they are counted as for the worst shift, one too many).
+template <int N>
+constexpr int full_vectors(const Width (&widths)[N], int tpr, int vecs, int mode)
+{
+    if (mode == kJoinScalar) return -1;
+    for (int i = 0, before = 0; i < N; before = widths[i].tpr * widths[i].vecs, ++i)
+        if (widths[i].tpr == tpr && widths[i].vecs == vecs)
+            return (mode == kJoinWindow && before > 0 ? before - 1 : before) / tpr;
+    return -1;
+}
 // Vectors that cover the CTA's columns (one more where rows are shifted).
 inline int64_t join_vectors(const JoinShape &s, int mode) { return s.cols / 8 + (mode == kJoinWindow ? 1 : 0); }
 inline int64_t up8(int64_t v) { return (v + 7) / 8 * 8; }
