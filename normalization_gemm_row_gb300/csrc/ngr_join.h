@@ -49,10 +49,12 @@ struct JoinArgs {
     float eps1, eps2, residual_scale, block_scale;
     int shift;                                  // kJoinWindow: the arrays' offset in elements
     JoinShape shape;
-    // Backward: the rows are cut into items of item_rows rows that lie in
-    // one gate group each; group g has items [g * items_per_group, +items_per_group).
+    // Backward: the rows are cut into items whose rows lie in one gate group
+    // each; group g has items [g * items_per_group, +items_per_group).  Item i
+    // of a group takes every period-th row of a run of item_rows rows: run
+    // i / period, from its row i % period on.
     int64_t items, item_rows;
-    int items_per_group;
+    int items_per_group, period;
     // Column sums, -1 = not wanted: their places among the `arrays` sums a
     // CTA keeps in shared memory.  Over an item: p = sum u1 D, q = sum D
     // (D the gradient of h), written to item_p, item_q [items][N].  Over a

@@ -37,6 +37,9 @@ __host__ __device__ constexpr int backward_ctas(int tpr, int vecs)
     return (vecs == 1 ? 768 : 512) / (tpr * backward_slots(tpr));
 }
 
+// Floats of a row of sums (see `at`).
+__host__ __device__ constexpr int join_sum_cols(int cols, int mode) { return mode == kJoinWindow ? cols + 16 : cols; }
+
 constexpr Width kWidths[] = {{32, 1}, {32, 2}, {96, 1}, {64, 2}, {160, 1}, {96, 2},
                              {128, 2}, {192, 2}, {256, 2}, {384, 2}, {512, 2}};
 
@@ -72,7 +75,7 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     const bool ln1 = CENTER && a.norm1 == kNormLayer, ln2 = CENTER && a.norm2 == kNormLayer;
 
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-    const int cols = a.shape.cols, arr = kSlots * cols;
+    const int cols = a.shape.cols, sum_cols = join_sum_cols(cols, MODE), arr = kSlots * sum_cols;
     for (int i = threadIdx.x; i < a.arrays * arr; i += kThreads) acc[i] = 0.0f;
     // an array that the call does not have is zeros
     uint4 *const mine = ring + threadIdx.x;
@@ -82,10 +85,13 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
 
     // Where column c (from c0) of a sum lies, so that a warp's accesses fall
     // into different banks: aligned vectors as two planes of 16-byte halves,
-    // shifted ones as eight planes of elements.
+    // shifted ones as eight planes of elements, which have room for a vector's
+    // columns before c0 and behind the last (8192 x 5003: 182 -> 173 us against
+    // a test for every element).
+    const int plane = sum_cols >> 3;
     auto at = [&](int c) {
         if constexpr (MODE == kJoinAligned) return ((c >> 2) & 1) * (cols >> 1) + (c >> 3) * 4 + (c & 3);
-        if constexpr (MODE == kJoinWindow) return (c & 7) * (cols >> 3) + (c >> 3);
+        if constexpr (MODE == kJoinWindow) return (c & 7) * plane + (c >> 3) + 1;
         return c;
     };
     // sum `b` (of this slot) of vector v += d
@@ -99,6 +105,14 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
             const float2 y0 = __fadd2_rn(make_float2(y.x, y.y), d.p[2]), y1 = __fadd2_rn(make_float2(y.z, y.w), d.p[3]);
             *lo = make_float4(x0.x, x0.y, x1.x, x1.y);
             *hi = make_float4(y0.x, y0.y, y1.x, y1.y);
+        } else if constexpr (MODE == kJoinWindow) {
+            if (!p.some(v, s)) return;
+            b += threadIdx.x % TPR + v * TPR;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {   // at(col - c0)
+                const int e = j + 8 - s;
+                b[e * plane + (e >= 8 ? 1 - 8 * plane : 0)] += (j & 1) ? d.p[j >> 1].y : d.p[j >> 1].x;
+            }
         } else {
 #pragma unroll
             for (int j = 0; j < 8; ++j)
@@ -106,7 +120,7 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
                     b[at(p.col(v, j, s) - p.c0)] += (j & 1) ? d.p[j >> 1].y : d.p[j >> 1].x;
         }
     };
-    auto sum_of = [&](int k) { return acc + (k < 0 ? 0 : k) * arr + slot * cols; };
+    auto sum_of = [&](int k) { return acc + (k < 0 ? 0 : k) * arr + slot * sum_cols; };
     float *const sum_p = sum_of(a.a_p), *const sum_q = sum_of(a.a_q);
     float *const sum_g2 = sum_of(a.a_dgamma2), *const sum_b2 = sum_of(a.a_dbeta2);
     // The CTA's sum k over its slots, by columns, to `put`; then zero.
@@ -115,13 +129,14 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
         for (int c = threadIdx.x; c < ncols; c += kThreads) {
             float t = 0.0f;
             for (int q = 0; q < kSlots; ++q) {
-                t += b[q * cols + at(c)];
-                b[q * cols + at(c)] = 0.0f;
+                t += b[q * sum_cols + at(c)];
+                b[q * sum_cols + at(c)] = 0.0f;
             }
             put(p.c0 + c, t);
         }
     };
 
+    const int period = MODE == kJoinWindow ? a.period : 1;
     // The CTA's way through the rows of its items: one cursor for the rows it
     // works on, one for those it fetches.
     struct Cursor {
@@ -132,12 +147,14 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
         c.group = c.item / a.items_per_group;
         const int64_t g0 = c.group * a.rows_per_gate;
         const int64_t g1 = g0 + a.rows_per_gate < a.M ? g0 + a.rows_per_gate : a.M;
-        c.base = g0 + (c.item - c.group * a.items_per_group) * a.item_rows;
+        const int64_t i = c.item - c.group * a.items_per_group, run = MODE == kJoinWindow ? i / a.period : i;
+        c.base = g0 + run * a.item_rows;
         c.r1 = c.base + a.item_rows < g1 ? c.base + a.item_rows : g1;
+        if (MODE == kJoinWindow) c.base += i - run * a.period;
     };
     // the next rows of this item, or the first of the CTA's next item
     auto advance = [&](Cursor &c) {
-        c.base += kSlots;
+        c.base += kSlots * period;
         if (c.base >= c.r1) {
             c.item += n_ctas;
             open(c);
@@ -145,7 +162,7 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     };
     // The cursor's row into stage `st` of the ring.
     auto fetch = [&](const Cursor &c, uint4 *st) {
-        const int64_t row = c.base + slot;
+        const int64_t row = c.base + slot * period;
         if (c.item < a.items && row < c.r1) {
             const int s = row_shift<MODE>(a, row);
             const int64_t off = row * a.N;
@@ -175,8 +192,8 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     open(now);
     open(ahead);
     // w = s gate gamma1, wb = s gate beta1, g2 = gamma2 at this thread's
-    // columns; they hold for an item (for a row in the window mode, where
-    // the columns move with the row).
+    // columns.  They hold for an item; in the window mode the columns move
+    // with the row, so there as long as the rows have one shift.
     Vec8 w[VECS], wb[CENTER ? VECS : 1], g2[VECS];
     auto params = [&](int s) {
 #pragma unroll
@@ -192,12 +209,11 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
         fetch(ahead, mine + i * kStage);
         advance(ahead);
     }
-    if constexpr (MODE != kJoinWindow) {
-        if (now.item < a.items) params(0);
-    }
+    if (MODE != kJoinWindow && now.item < a.items) params(0);
+    int shift = -1;   // kJoinWindow: the parameters' (-1: of another item)
     int stage = 0;
     while (now.item < a.items) {
-        const int64_t row = now.base + slot;
+        const int64_t row = now.base + slot * period;
         const bool active = row < now.r1;
         const int64_t off = row * a.N;
         const int s = row_shift<MODE>(a, row);
@@ -209,7 +225,10 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
         uint4 *const in = mine + stage * kStage;
         const float4 st = *reinterpret_cast<const float4 *>(in + 4 * VECS * kThreads);
         const float rs2 = norm2 ? st.w : 0.0f;
-        if constexpr (MODE == kJoinWindow) params(s);
+        if (MODE == kJoinWindow && s != shift) {
+            params(s);
+            shift = s;
+        }
 
         Vec8 u1[VECS], u2[VECS], D[VECS];
         float2 t[8];
@@ -289,9 +308,8 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
                 if (a.a_p >= 0) flush(a.a_p, [&](int c, float f) { a.item_p[item * a.N + c] = f; });
                 if (a.a_q >= 0) flush(a.a_q, [&](int c, float f) { a.item_q[item * a.N + c] = f; });
             }
-            if constexpr (MODE != kJoinWindow) {
-                if (now.item < a.items) params(0);
-            }
+            if (MODE != kJoinWindow && now.item < a.items) params(0);
+            shift = -1;
             __syncthreads();
         }
     }
@@ -306,13 +324,16 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
 }
 
 inline int64_t ring_row(const JoinShape &s) { return (4ll * s.vecs + 1) * s.tpr * s.slots * 16; }
-inline int64_t sum_bytes(const JoinShape &s, int arrays) { return static_cast<int64_t>(arrays) * s.slots * s.cols * 4; }
+inline int64_t sum_bytes(const JoinShape &s, int arrays, int mode)
+{
+    return static_cast<int64_t>(arrays) * s.slots * join_sum_cols(s.cols, mode) * 4;
+}
 
 template <bool BF16, int MODE, bool CENTER>
 int run_mode(JoinArgs a, int ctas, cudaStream_t stream)
 {
     // as deep a ring as the SM's shared memory has room for beside the sums
-    const int64_t row = ring_row(a.shape), sums = sum_bytes(a.shape, a.arrays);
+    const int64_t row = ring_row(a.shape), sums = sum_bytes(a.shape, a.arrays, MODE);
     a.depth = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(3, (kJoinSmem / a.shape.per_sm - 2048 - sums) / row)));
     const size_t smem = static_cast<size_t>(sums + a.depth * row);
 #define NGR_WIDTH(T, V, ONE)                                                                                    \

@@ -96,7 +96,7 @@ JoinShape join_backward_shape(int64_t N, int mode, int arrays)
         s.slots = backward_slots(s.tpr);
         // As many CTAs as the SM has registers for, and shared memory for
         // their sums and a row each.
-        const int64_t bytes = sum_bytes(s, arrays) + ring_row(s) + 2048;
+        const int64_t bytes = sum_bytes(s, arrays, mode) + ring_row(s) + 2048;
         s.per_sm = static_cast<int>(std::min<int64_t>(backward_ctas(s.tpr, s.vecs), kJoinSmem / bytes));
         if (s.per_sm >= 1) return s;
     }

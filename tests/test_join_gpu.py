@@ -84,6 +84,16 @@ def test_gate_groups(M, gates):
     compare(d, LAYER, RMS, f"{M} rows, {gates} gates")
 
 
+@pytest.mark.parametrize("M,N,gates", [(1400, 1001, 1), (4000, 131, 2), (1300, 2050, 0), (2403, 517, 3), (1801, 36, 1),
+                                       (900, 5003, 1), (700, 20004, 0)])
+def test_many_rows_that_are_not_aligned(M, N, gates):
+    """The gradient's CTAs take every 8th, 4th or 2nd row: rows that start
+    alike."""
+    for norm1, norm2, dtype in ((LAYER, LAYER, torch.float16), (RMS, RMS, torch.bfloat16)):
+        d = R.case(M, N, norm1, norm2, gates, dtype, seed=M + N)
+        compare(d, norm1, norm2, f"{M}x{N}", a=0.75)
+
+
 def test_ragged_last_group():
     """M need not be a multiple of rows_per_gate at the C entry."""
     M, N, rpg = 10, 40, 4
