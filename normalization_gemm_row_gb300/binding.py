@@ -542,7 +542,7 @@ def _uniform(x, *ts):
         if t is None:
             at.append(None)
             continue
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise TypeError("all tensors must share one dtype")
         if t.get_device() != index:
             raise ValueError("all tensors must be on one CUDA device")
@@ -564,11 +564,13 @@ def _tokens(x, what, *ts):
 # stream object for it first, a tenth of a short call's host time.
 _current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
                                  lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The current device, CUDA being up (torch.cuda.current_device asks that first).
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on_device(x):
     """Whether x's device is the current one (the library launches there)."""
-    return x.get_device() == torch.cuda.current_device()
+    return x.get_device() == _current_device()
 
 
 def _launch_stream(x, stream, *tensors):
