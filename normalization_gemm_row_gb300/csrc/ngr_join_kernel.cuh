@@ -309,9 +309,11 @@ struct RowSumSmem {
 // about K + 5 - log2 K shuffles and not 5 K; then the row's warps and the
 // cluster's CTAs add up through shared memory.  The two halves of the
 // buffers take turns, so one barrier a call is enough.  All threads of the
-// CTA (of the cluster) call it together.
-template <int K, int TPR>
-__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank)
+// CTA (of the cluster) call it together.  `barrier` stands between the warps'
+// writes and reads.
+template <int K, int TPR, typename Barrier>
+__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank,
+                                        Barrier barrier)
 {
     static_assert(K == 1 || K == 4 || K == 8, "values");
     constexpr int kWarps = TPR / 32;
@@ -341,7 +343,7 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half,
     half ^= 1;
     const int warp = threadIdx.x >> 5;
     if (lane % (32 / K) == 0) reinterpret_cast<float *>(s.warp[half][warp])[lane / (32 / K)] = v[0];
-    __syncthreads();
+    barrier();
     const int first = warp / kWarps * kWarps;   // the row's warps
 #pragma unroll
     for (int k = 0; k < K; ++k) v[k] = 0.0f;
@@ -375,6 +377,12 @@ __device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half,
 #pragma unroll
             for (int k = 0; k < K; ++k) v[k] += s.peer[half][r][k];
     }
+}
+
+template <int K, int TPR>
+__device__ __forceinline__ void row_sum(float (&v)[K], RowSumSmem &s, int &half, int cluster, uint32_t rank)
+{
+    row_sum<K, TPR>(v, s, half, cluster, rank, [] { __syncthreads(); });
 }
 
 // ----------------------------------------------------------------- launching
