@@ -162,11 +162,10 @@ int launch_join_reduce(bool bf16, const JoinReduce &r, cudaStream_t stream)
 {
     if (!r.dgamma1 && !r.dbeta1 && !r.dgamma2 && !r.dbeta2 && !r.dgate) return 0;
     const int64_t outs = 4 + (r.dgate ? r.groups : 0);
-    // Four columns a thread where that leaves a CTA for every SM: the gradient
-    // at 8192 x 8192 154.3 -> 151.4 us, but at 16000 x 1152 56.5 -> 62.7.
-    const int64_t wanted = (r.dgamma1 != nullptr) + (r.dbeta1 != nullptr) + (r.dgamma2 != nullptr) +
-                           (r.dbeta2 != nullptr) + (r.dgate ? r.groups : 0);
-    const bool wide = r.N % 4 == 0 && r.N / (4 * kReduceCols) * wanted >= kJoinSms;
+    // Four columns a thread in rows so wide that four outputs have a CTA for
+    // every SM: the gradient at 8192 x 8192 154.3 -> 151.4 us, but at 32768 x
+    // 2048 141.6 -> 142.9 and at 16000 x 1152 56.5 -> 62.7.
+    const bool wide = r.N % 4 == 0 && r.N / (4 * kReduceCols) * 4 >= kJoinSms;
     const cudaError_t e = wide ? reduce<4>(bf16, r, outs, stream) : reduce<1>(bf16, r, outs, stream);
     return e == cudaSuccess ? 0 : record_cuda_error("join sums launch", e, cudaGetErrorString(e));
 }

@@ -84,6 +84,13 @@ def test_gate_groups(M, gates):
     compare(d, LAYER, RMS, f"{M} rows, {gates} gates")
 
 
+@pytest.mark.parametrize("M,N,gates", [(640, 4900, 16), (160, 8200, 10), (300, 10252, 1)])
+def test_last_sums_by_four_columns(M, N, gates):
+    for norm1, dtype in ((LAYER, torch.float16), (NONE, torch.bfloat16)):
+        d = R.case(M, N, norm1, LAYER, gates, dtype, seed=M + N)
+        compare(d, norm1, LAYER, f"{M}x{N}, {gates} gates", s=1.5)
+
+
 @pytest.mark.parametrize("M,N,gates", [(1400, 1001, 1), (4000, 131, 2), (1300, 2050, 0), (2403, 517, 3), (1801, 36, 1),
                                        (900, 5003, 1), (700, 20004, 0)])
 def test_many_rows_that_are_not_aligned(M, N, gates):
