@@ -17,13 +17,11 @@ namespace {
 
 // Threads of a CTA: 256 (four CTAs an SM), 512 for the widest rows.
 __host__ __device__ constexpr int forward_threads(int tpr) { return tpr > 256 ? tpr : 256; }
-// CTAs an SM.  The window mode's addresses want more registers than 64: with
-// a warp a row 85 are faster (16000 x 1151: 68 against 74 us), with wider rows
-// the fourth CTA is (8192 x 8191: 228 against 365 us).
+// CTAs an SM: three of the window mode take 398 us against 239 at 8192 x 8191,
+// LN/LN.
 __host__ __device__ constexpr int forward_ctas(int mode, int tpr)
 {
-    const int threads = mode == kJoinScalar ? 512 : mode == kJoinWindow && tpr == 32 ? 768 : 1024;
-    return threads / forward_threads(tpr);
+    return (mode == kJoinScalar ? 512 : 1024) / forward_threads(tpr);
 }
 // A warp a row while five vectors a lane cover it (its sums need no barrier),
 // then three or four vectors a thread.
