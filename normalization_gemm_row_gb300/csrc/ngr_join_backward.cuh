@@ -65,7 +65,8 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     // warp's arrival at their barrier and its wait: 32768 x 2048 198 -> 176 us,
     // 8192 x 5000 146 -> 133.  (With one vector a thread 16000 x 1152 took 72
     // against 69 us, and RMSNorm alone 5 % longer: fewer instructions to put
-    // there, and the next rows asked for later.)
+    // there, and the next rows asked for later.  In the window mode a column's
+    // thread changes with the shift, and the barrier orders its sums.)
     constexpr bool kArrive = CENTER && ONE && TPR > 32 && VECS > 1 && MODE == kJoinAligned;
     __shared__ uint64_t given;
     uint32_t given_phase = 0, tries = 1u << 20;
