@@ -10,7 +10,8 @@
 namespace ngr {
 
 constexpr int kJoinThreads = 512;      // threads per CTA at most
-constexpr int kJoinMaxCluster = 8;     // CTAs that share one row at most
+constexpr int kJoinMaxCluster = 16;    // CTAs that share one row at most
+constexpr int kJoinPortableCluster = 8;   // a larger cluster has to be asked for
 constexpr int64_t kJoinMaxN = 65536;   // widest row
 constexpr int64_t kJoinSmem = 224 * 1024;   // shared memory of an SM for its CTAs' rings and sums
 constexpr int kJoinForwardCols = 16384;   // columns a CTA takes at most: 512 threads x 4 vectors

@@ -417,6 +417,11 @@ int launch_join(K kern, int64_t ctas, const JoinShape &sh, size_t smem, const Jo
         if (e != cudaSuccess)
             return record_cuda_error("cudaFuncSetAttribute(max dynamic smem)", e, cudaGetErrorString(e));
     }
+    if (sh.cluster > kJoinPortableCluster) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess)
+            return record_cuda_error("cudaFuncSetAttribute(cluster size)", e, cudaGetErrorString(e));
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(ctas * sh.cluster));
     cfg.blockDim = dim3(static_cast<unsigned>(sh.tpr * sh.slots));

@@ -117,6 +117,10 @@ cudaError_t reduce(bool bf16, const JoinReduce &r, int64_t outs, cudaStream_t st
 
 }  // namespace
 
+// The row's columns over as few CTAs as hold them and their sums.  Clusters of
+// 8 hold every row up to 65536 columns but for two kinds that are wider than
+// 60000: shifted rows, which need a vector more than 8 CTAs have, and rows
+// with five sums, which need more shared memory; those take 16 CTAs.
 JoinShape join_backward_shape(int64_t N, int mode, int arrays)
 {
     JoinShape s;
