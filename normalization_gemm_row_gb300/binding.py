@@ -568,25 +568,38 @@ _current_stream_handle = getattr(torch._C, "_cuda_getCurrentRawStream",
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _on_device(x):
-    """Whether x's device is the current one (the library launches there)."""
-    return x.get_device() == _current_device()
+def _here(x, stream):
+    """Whether x's device is the current one, and ``stream`` its current
+    stream (which None stands for): the library launches there."""
+    index = x.get_device()
+    return index == _current_device() and (stream is None or _stream(stream) == _current_stream_handle(index))
 
 
-def _launch_stream(x, stream, *tensors):
-    """The stream handle to launch on (by default the current one of x's
-    device).  The tensors that were allocated for the call are kept from
-    reuse until a stream other than the current one is done with them."""
-    current = _current_stream_handle(x.get_device())
-    if stream is None:
-        return current
-    handle = _stream(stream)
-    if handle != current:
-        s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(handle)
-        for t in tensors:
-            if t is not None:
-                t.record_stream(s)
-    return handle
+def _there(call, x, stream, *args):
+    """call(*args, stream) with x's device current, and then with ``stream``
+    current: what the call allocates is that stream's memory and not a block
+    that work under way on the caller's stream still uses.  The caller's
+    tensors and the results are kept from reuse until both streams are done
+    with them."""
+    if x.get_device() != _current_device():
+        with torch.cuda.device(x.device):
+            return call(*args, stream)
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)
+        stream = (torch.cuda.ExternalStream(handle, device=x.device) if handle else
+                  torch.cuda.default_stream(x.device))
+    if stream.device != x.device:
+        raise ValueError("the stream must be on the tensors' device")
+    outer = torch.cuda.current_stream(x.device)
+    for t in args:
+        if torch.is_tensor(t):
+            t.record_stream(stream)
+    with torch.cuda.stream(stream):
+        results = call(*args, stream)
+    for t in results.values() if isinstance(results, dict) else results:
+        if t is not None:
+            t.record_stream(outer)
+    return results
 
 
 def _scratch(nbytes, device, workspace):
@@ -636,11 +649,10 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
     _tokens(x, "residual, h and out", residual, h, out)
     code, p_res, p_gate, p_g1, p_b1, p_g2, p_b2, _, _ = _uniform(
         x, residual, gate, gamma1, beta1, gamma2, beta2, h, out)
-    if not _on_device(x):
-        with torch.cuda.device(x.device):
-            return fused_norm_gate_residual_norm(
-                x, residual, gate, norm1, gamma1, beta1, eps1, norm2, gamma2, beta2, eps2,
-                residual_scale, block_scale, h, out, return_stats, stream)
+    if not _here(x, stream):
+        return _there(fused_norm_gate_residual_norm, x, stream, x, residual, gate, norm1, gamma1, beta1,
+                      eps1, norm2, gamma2, beta2, eps2, residual_scale, block_scale, h, out,
+                      return_stats)
     if h is None:
         h = torch.empty_like(x)
     if norm2 == NORM_NONE:
@@ -651,7 +663,7 @@ def fused_norm_gate_residual_norm(x, residual=None, gate=None, norm1: int = NORM
     rc = lib().ngr_fused_norm_gate_residual_norm(
         norm1, norm2, x.data_ptr(), p_res, p_gate, rpg, p_g1, p_b1, p_g2, p_b2, eps1, eps2,
         residual_scale, block_scale, M, N, code, h.data_ptr(), _ptr(out), _ptr(st),
-        _launch_stream(x, stream, h, out, st))
+        _current_stream_handle(x.get_device()))
     if rc != 0:
         raise NgrError(rc, "fused_norm_gate_residual_norm")
     return (h, out, st) if return_stats else (h, out)
@@ -675,11 +687,10 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
     if (stats.dtype != torch.float32 or stats.numel() != 4 * M or stats.device != x.device
             or not stats.is_contiguous()):
         raise ValueError("stats must be the float32 [M, 4] of the forward call")
-    if not _on_device(x):
-        with torch.cuda.device(x.device):
-            return fused_norm_gate_residual_norm_backward(
-                dy, dh, x, residual, stats, gate, norm1, gamma1, beta1, eps1, norm2, gamma2, beta2,
-                eps2, residual_scale, block_scale, workspace, stream)
+    if not _here(x, stream):
+        return _there(fused_norm_gate_residual_norm_backward, x, stream, dy, dh, x, residual, stats, gate,
+                      norm1, gamma1, beta1, eps1, norm2, gamma2, beta2, eps2, residual_scale,
+                      block_scale, workspace)
     like = torch.empty_like
     dx = like(x)
     dr = like(residual) if residual is not None else None
@@ -696,7 +707,7 @@ def fused_norm_gate_residual_norm_backward(dy, dh, x, residual, stats, gate=None
         norm1, norm2, p_dy, p_dh, x.data_ptr(), p_res, p_gate, rpg, p_g1, p_b1, p_g2,
         stats.data_ptr(), residual_scale, block_scale, M, N, code, dx.data_ptr(), _ptr(dr), _ptr(dg),
         _ptr(dg1), _ptr(db1), _ptr(dg2), _ptr(db2), ws.data_ptr(), ws.numel() * ws.element_size(),
-        _launch_stream(x, stream, dx, dr, dg, dg1, db1, dg2, db2, ws))
+        _current_stream_handle(x.get_device()))
     if rc != 0:
         raise NgrError(rc, "fused_norm_gate_residual_norm_backward")
     return {"dx": dx, "dresidual": dr, "dgate": dg, "dgamma1": dg1, "dbeta1": db1, "dgamma2": dg2,
@@ -732,15 +743,14 @@ def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, st
     negative; x [..., K], W [V, K], target [...] int64.  The logits are not
     kept."""
     M, K, V, code = _ce_operands(x, W, target)
-    if not _on_device(x):
-        with torch.cuda.device(x.device):
-            return fused_linear_cross_entropy(x, W, target, logit_scale, workspace, stream)
+    if not _here(x, stream):
+        return _there(fused_linear_cross_entropy, x, stream, x, W, target, logit_scale, workspace)
     loss = torch.empty(target.shape, dtype=torch.float32, device=x.device)
     lse = torch.empty_like(loss)
     ws = _scratch(ngr_linear_cross_entropy_workspace_bytes(0, M, K, V), x.device, workspace)
     rc = lib().ngr_fused_linear_cross_entropy(
         _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V, code, _ptr(loss), _ptr(lse), _ptr(ws),
-        ws.numel() * ws.element_size(), _launch_stream(x, stream, loss, lse, ws))
+        ws.numel() * ws.element_size(), _current_stream_handle(x.get_device()))
     _raise(rc, "fused_linear_cross_entropy")
     return loss, lse
 
@@ -752,17 +762,16 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
     either output is None when not needed."""
     M, K, V, code = _ce_operands(x, W, target)
     _row_vectors(M, x.device, dloss, dlse, lse)
-    if not _on_device(x):
-        with torch.cuda.device(x.device):
-            return fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale, dlse,
-                                                       need_dx, need_dW, workspace, stream)
+    if not _here(x, stream):
+        return _there(fused_linear_cross_entropy_backward, x, stream, dloss, lse, x, W, target, logit_scale,
+                      dlse, need_dx, need_dW, workspace)
     dx = torch.empty_like(x) if need_dx else None
     dW = torch.empty_like(W) if need_dW else None
     ws = _scratch(ngr_linear_cross_entropy_workspace_bytes(1, M, K, V), x.device, workspace)
     rc = lib().ngr_fused_linear_cross_entropy_backward(
         _ptr(dloss), _ptr(dlse), _ptr(lse), _ptr(x), _ptr(W), _ptr(target), logit_scale, M, K, V,
         code, _ptr(dx), _ptr(dW), _ptr(ws), ws.numel() * ws.element_size(),
-        _launch_stream(x, stream, dx, dW, ws))
+        _current_stream_handle(x.get_device()))
     _raise(rc, "fused_linear_cross_entropy_backward")
     return dx, dW
 
