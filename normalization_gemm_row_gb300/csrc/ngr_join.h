@@ -45,6 +45,7 @@ struct JoinArgs {
     void *dx, *dresidual, *dgate;               // backward outputs
     float4 *stats;                              // [M] (mu1, rstd1, mu2, rstd2)
     int *err;                                   // backward: the workspace's error word, cleared
+    unsigned long long timeout_ns;              // backward: of a wait for the row's warps
     int64_t M, rows_per_gate;
     int N, norm1, norm2;
     float eps1, eps2, residual_scale, block_scale;

@@ -266,6 +266,7 @@ int ngr_fused_norm_gate_residual_norm_backward(
     a.dgate = dgate;
     a.stats = const_cast<float4 *>(reinterpret_cast<const float4 *>(stats));
     a.err = reinterpret_cast<int *>(ws);
+    a.timeout_ns = wait_timeout_ns();
     a.shape = p.shape;
     a.items = p.items;
     a.item_rows = p.item_rows;
@@ -314,7 +315,7 @@ int ngr_fused_norm_gate_residual_norm_backward(
         rc = launch_join_reduce(bf16, r, stream);
         kernel_end(stream);
     }
-    return call_end(rc, nullptr, stream);
+    return call_end(rc, workspace, stream);
 }
 
 }  // extern "C"

@@ -69,7 +69,8 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
     // thread changes with the shift, and the barrier orders its sums.)
     constexpr bool kArrive = CENTER && ONE && TPR > 32 && VECS > 1 && MODE == kJoinAligned;
     __shared__ uint64_t given;
-    uint32_t given_phase = 0, tries = 1u << 20;
+    uint32_t given_phase = 0;
+    bool waits = true;
     const int cluster = ONE ? 1 : a.shape.cluster;
     const uint32_t rank = cluster > 1 ? cluster_ctarank() : 0u;
     const int64_t cta = blockIdx.x / cluster;
@@ -298,11 +299,18 @@ __global__ void __launch_bounds__(TPR * backward_slots(TPR), backward_ctas(TPR, 
                 fetch(ahead, in);
                 advance(ahead);
                 stage = stage + 1 == a.depth ? 0 : stage + 1;
-                uint32_t left = tries;
-                while (!mbar_try_wait(&given, given_phase) && --left > 0) {}
-                if (left == 0) {   // reported; the waits to come are short
-                    atomicExch(a.err, kDevErrTimeout);
-                    tries = 1;
+                // A wait that runs out is reported, and those to come try once.
+                // (Here and not by the shared bounded wait: its call in this
+                // loop, registers saved around it, took 32768 x 2048 from 177 to
+                // 191 us.)
+                uint64_t since = 0;
+                for (uint32_t it = 1; !mbar_try_wait(&given, given_phase) && waits; ++it) {
+                    if ((it & 63u) != 0) continue;
+                    if (since == 0) since = global_timer_ns();
+                    if (global_timer_ns() - since > a.timeout_ns) {
+                        atomicExch(a.err, kDevErrTimeout);
+                        waits = false;
+                    }
                 }
                 given_phase ^= 1u;
             });
