@@ -130,7 +130,7 @@ struct CeCall {
 };
 
 // What forward and backward have in common: checks of the workspace, the
-// tokens' index, their rows, W with rows of a 16-byte pitch.
+// tokens' arguments, W with rows of a 16-byte pitch (a call's first launch).
 int ce_begin(CeCall *c, bool backward, const void *x, const void *W, const int64_t *target, float logit_scale,
              int64_t M, int64_t K, int64_t V, int dtype, void *workspace, size_t workspace_bytes)
 {
@@ -160,8 +160,12 @@ int ce_begin(CeCall *c, bool backward, const void *x, const void *W, const int64
     t.index = reinterpret_cast<int *>(ws + c->p.index);
     t.ctarget = reinterpret_cast<int *>(ws + c->p.ctarget);
     t.xc = ws + c->p.xc;
-    if (K % 8 != 0) return launch_ce_pad(W, ws + c->p.wp, V, K, c->p.w_pitch, c->stream);
-    return NGR_OK;
+    call_begin();
+    if (K % 8 == 0) return NGR_OK;
+    kernel_begin(c->stream);
+    const int pad = launch_ce_pad(W, ws + c->p.wp, V, K, c->p.w_pitch, c->stream);
+    kernel_end(c->stream);
+    return pad == NGR_OK ? NGR_OK : call_end(pad, nullptr, c->stream);
 }
 
 CeGemmArgs ce_args(const CeCall &c)
@@ -216,7 +220,6 @@ int ce_forward(const void *x, const void *W, const int64_t *target, float logit_
     a.part = reinterpret_cast<float2 *>(c.ws + c.p.part);
     a.part_pitch = M;
     a.z_target = reinterpret_cast<float *>(c.ws + c.p.z_target);
-    call_begin();
     if (launch_ce_index_apart(c.t)) NGR_TIMED(launch_ce_index(c.t, stream));
     NGR_TIMED(launch_ce_gather(c.t, stream));
     NGR_TIMED(launch_ce_gemm(kCeLse, c.bf16, a, tiles_of(M, V, a.width), stream));
@@ -252,7 +255,6 @@ int ce_backward(const float *dloss, const float *dlse, const float *lse, const v
     rc = ce_begin(&c, true, x, W, target, logit_scale, M, K, V, dtype, workspace, workspace_bytes);
     if (rc != NGR_OK) return rc;
     c.t.row = reinterpret_cast<CeRow *>(c.ws + c.p.row);
-    call_begin();
     if (launch_ce_index_apart(c.t)) NGR_TIMED(launch_ce_index(c.t, stream));
     NGR_TIMED(launch_ce_gather(c.t, stream));
     const int64_t rows = up_to(M, kCeTile);
