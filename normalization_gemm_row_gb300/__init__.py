@@ -10,7 +10,7 @@ generator used by tests and benchmarks.
 from ._build import build, LIB_PATH  # noqa: F401
 from .binding import (  # noqa: F401
     ACT_GELU, ACT_NONE, ACT_RELU, ACT_SILU, NORM_LAYER, NORM_NONE, NORM_RMS,
-    NgrError, ffn_linear_silu_linear, fold_prepare, fused_layernorm_linear,
+    NgrError, check_workspace, ffn_linear_silu_linear, fold_prepare, fused_layernorm_linear,
     fused_linear_cross_entropy, fused_linear_cross_entropy_backward,
     fused_linear_residual_norm, fused_linear_silu, fused_mlp, fused_mlp_swiglu,
     fused_norm_gate_residual_norm, fused_norm_gate_residual_norm_backward,

@@ -609,6 +609,17 @@ def _scratch(nbytes, device, workspace):
     return _workspace(nbytes, device, workspace)
 
 
+def check_workspace(workspace, stream=None):
+    """Wait for ``stream`` (by default the current one of the workspace's
+    device) and raise NgrError if a kernel of the last call with this
+    workspace reported an error: a target outside the vocabulary, or a wait
+    that ran out.  The report is cleared."""
+    if not workspace.is_cuda:
+        raise ValueError("the workspace must be a CUDA tensor")
+    handle = _stream(stream) if stream is not None else _current_stream_handle(workspace.get_device())
+    _raise(ngr_workspace_error(workspace.data_ptr(), handle), "check_workspace")
+
+
 def _join_operands(x, gate, norm1, gamma1, beta1, norm2, gamma2, beta2):
     """(M, N, rows_per_gate, gamma1, beta1, gamma2, beta2), the vectors that
     the norms do not use as None."""
@@ -741,7 +752,9 @@ def fused_linear_cross_entropy(x, W, target, logit_scale=1.0, workspace=None, st
     """(loss, lse), float32 of target's shape: z = logit_scale x . W^T,
     lse = log sum exp z, loss = lse - z[target], both 0 where target is
     negative; x [..., K], W [V, K], target [...] int64.  The logits are not
-    kept."""
+    kept.  A target of V or more is an error that only the GPU sees: its token
+    does not count, and the call's workspace records it.  To learn of it pass
+    a ``workspace`` and ask ``check_workspace``, or set NGR_DEBUG=1."""
     M, K, V, code = _ce_operands(x, W, target)
     if not _here(x, stream):
         return _there(fused_linear_cross_entropy, x, stream, x, W, target, logit_scale, workspace)
@@ -759,7 +772,8 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
                                         need_dx=True, need_dW=True, workspace=None, stream=None):
     """(dx, dW) of ``fused_linear_cross_entropy`` from the gradients of its
     loss (``dloss``) and, if given, of its lse (``dlse``), float32 per token;
-    either output is None when not needed."""
+    either output is None when not needed.  Targets of V or more as in the
+    forward call."""
     M, K, V, code = _ce_operands(x, W, target)
     _row_vectors(M, x.device, dloss, dlse, lse)
     if not _here(x, stream):
