@@ -36,7 +36,10 @@
 // leader, one arrival per epilogue warp of both CTAs.
 #include "ngr_ce.h"
 #include "ngr_ce_ptx.cuh"
+#include "ngr_entry.h"
 #include "ngr_gemm_kernel.cuh"
+
+#include <cstdio>
 
 namespace ngr {
 
@@ -552,6 +555,10 @@ int launch_ce_gemm(int mode, bool bf16, const CeGemmArgs &a, int64_t units, cuda
     if (clusters == 0) clusters = ce_clusters();
     const int64_t most = clusters > 0 ? clusters : 64;
     const int grid = 2 * static_cast<int>(units < most ? units : most);
+    if (trace_mode())
+        std::fprintf(stderr, "ngr: cross entropy %s: %d columns, width=%d splits=%d grid=%d\n",
+                     mode == kCeLse ? "z" : mode == kCeGrad ? "dz" : mode == kCeDx ? "dx" : "dW", a.cols, a.width,
+                     a.splits, grid);
 #define NGR_CE(M_)      \
     case M_: return bf16 ? run<M_, true>(a, grid, stream) : run<M_, false>(a, grid, stream);
     switch (mode) {

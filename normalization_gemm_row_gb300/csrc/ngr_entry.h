@@ -15,6 +15,9 @@ enum : int { kDevErrTarget = 2 };
 // The current device's SM count: NGR_OK, NGR_ERR_ARCH or NGR_ERR_CUDA.
 int device_sms(int *sms);
 
+// NGR_TRACE: every call prints the kernel variant it chose to stderr.
+bool trace_mode();
+
 // The kernel timing (ngr_kernel_timing_start): the call's begin, a pair
 // around each launch; then the call's end, which reports launch errors and,
 // with NGR_DEBUG, the error word (`ws` may be null).

@@ -3,6 +3,7 @@
 // layout, how the backward pass cuts the rows.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <cstring>
 
 #include "ngr.h"
@@ -153,6 +154,15 @@ JoinArgs join_args(const void *x, const void *residual, const void *gate, int64_
     return a;
 }
 
+void trace(const char *what, int mode, const JoinArgs &a, int64_t ctas)
+{
+    if (!trace_mode()) return;
+    std::fprintf(stderr, "ngr: %s M=%lld N=%d norms=%d,%d %s cluster=%d cols=%d threads=%d x %d vecs=%d grid=%lld\n", what,
+                 static_cast<long long>(a.M), a.N, a.norm1, a.norm2,
+                 mode == kJoinAligned ? "aligned" : mode == kJoinWindow ? "shifted" : "by elements", a.shape.cluster,
+                 a.shape.cols, a.shape.slots, a.shape.tpr, a.shape.vecs, static_cast<long long>(ctas * a.shape.cluster));
+}
+
 int zero_vector(void *p, int64_t n, cudaStream_t stream)
 {
     if (!p) return NGR_OK;
@@ -196,6 +206,7 @@ int ngr_fused_norm_gate_residual_norm(int norm1, int norm2, const void *x, const
     rc = device_sms(&sms);
     if (rc != NGR_OK) return rc;
     a.shape = join_forward_shape(N, mode);
+    trace("block join", mode, a, (M + a.shape.slots - 1) / a.shape.slots);
     call_begin();
     kernel_begin(stream);
     rc = launch_join_forward(dtype == NGR_BF16, mode, a, stream);
@@ -306,6 +317,7 @@ int ngr_fused_norm_gate_residual_norm_backward(
     r.fold_gate = p.fold_gate;
 
     const bool bf16 = dtype == NGR_BF16;
+    trace("block join gradient", mode, a, p.ctas);
     call_begin();
     kernel_begin(stream);
     rc = launch_join_backward(bf16, mode, a, p.ctas, stream);
