@@ -246,8 +246,9 @@ int ngr_fused_linear_residual_norm(int norm, const void *x, const void *W,
  * where a norm has none); it is 16-byte aligned.  Statistics and all
  * arithmetic are FP32; h and y are rounded once, y from the unrounded h.
  * Any N up to 65536; pointers need 2-byte alignment (16-byte aligned ones
- * with N % 8 == 0 take the vectorized kernel).  h or y may be the memory of
- * x or residual.  Needs no workspace. */
+ * with N % 8 == 0 take the vectorized kernel).  h and y may each be the
+ * memory of x or residual, but not both the same (NGR_ERR_ARG).  Needs no
+ * workspace. */
 int ngr_fused_norm_gate_residual_norm(int norm1, int norm2, const void *x,
                                       const void *residual, const void *gate,
                                       int64_t rows_per_gate,
@@ -266,9 +267,9 @@ int ngr_fused_norm_gate_residual_norm(int norm1, int norm2, const void *x,
  *   dx, dresidual [M, N], dgate [G, N] (summed over each gate row's tokens),
  *   dgamma1, dbeta1, dgamma2, dbeta2 [N] (summed over the tokens),
  * all in `dtype`; the sums are FP32, taken in a fixed order (the same call
- * gives the same bits).  Any output but dx may be NULL (not wanted).  dx or
- * dresidual may be the memory of dy, dh, x or residual.  M == 0 zeroes the
- * vectors.  The workspace (256-byte aligned) holds the partial sums:
+ * gives the same bits).  Any output but dx may be NULL (not wanted).  dx and
+ * dresidual may each be the memory of dy, dh, x or residual, but not both the
+ * same (NGR_ERR_ARG).  M == 0 zeroes the vectors.  The workspace (256-byte aligned) holds the partial sums:
  * ngr_norm_gate_residual_norm_workspace_bytes, with rows_per_gate = 0 for no
  * gate. */
 int ngr_fused_norm_gate_residual_norm_backward(

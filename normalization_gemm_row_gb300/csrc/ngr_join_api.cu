@@ -202,6 +202,7 @@ int ngr_fused_norm_gate_residual_norm(int norm1, int norm2, const void *x, const
     int mode = 0;
     rc = join_alignment({x, residual, h, a.y}, {gate, a.gamma1, a.beta1, a.gamma2, a.beta2}, N, &mode, &a.shift);
     if (rc != NGR_OK) return rc;
+    if (a.y == h) return NGR_ERR_ARG;
     int sms = 0;
     rc = device_sms(&sms);
     if (rc != NGR_OK) return rc;
@@ -260,6 +261,7 @@ int ngr_fused_norm_gate_residual_norm_backward(
     const JoinPlan p = join_plan(mode, M, N, gate ? rows_per_gate : 0, norm1, norm2);
     if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
+    if (M > 0 && dresidual == dx) return NGR_ERR_ARG;
     int sms = 0;
     rc = device_sms(&sms);
     if (rc != NGR_OK) return rc;
