@@ -95,6 +95,5 @@ int launch_ce_loss(const CeTokens &t, const float2 *part, int64_t part_pitch, in
                    const float *z_target, float *loss, float *lse, cudaStream_t stream);
 int launch_ce_dx(bool bf16, const CeTokens &t, const float *sums, int64_t sums_pitch, int splits,
                  cudaStream_t stream);
-int ce_clusters();          // resident CTA pairs of the product kernels
 
 }  // namespace ngr

@@ -526,8 +526,7 @@ int run(const CeGemmArgs &a, int grid, cudaStream_t stream)
     return e == cudaSuccess ? 0 : record_cuda_error("cudaLaunchKernelEx (cross entropy)", e, cudaGetErrorString(e));
 }
 
-}  // namespace
-
+// Resident CTA pairs of the product kernels.
 int ce_clusters()
 {
     auto kern = ce_gemm_kernel<kCeLse, true>;
@@ -546,6 +545,8 @@ int ce_clusters()
     int n = 0;
     return cudaOccupancyMaxActiveClusters(&n, kern, &cfg) == cudaSuccess ? n : 0;
 }
+
+}  // namespace
 
 int launch_ce_gemm(int mode, bool bf16, const CeGemmArgs &a, int64_t units, cudaStream_t stream)
 {

@@ -40,6 +40,11 @@ __host__ __device__ constexpr int backward_ctas(int tpr, int vecs)
 // Floats of a row of sums (see `at`).
 __host__ __device__ constexpr int join_sum_cols(int cols, int mode) { return mode == kJoinWindow ? cols + 16 : cols; }
 
+// Two vectors a thread, but one at 96 and 160 threads, where the SM holds half
+// as many threads again (two vectors measured beside them: 16000 x 1152 LN/LN
+// with 16 gate rows 69.8 us against 73.2 and 32000 x 768 RMS/RMS 62.8 against
+// 63.8; the other norms the other way round, 56.4 against 52.7 and 89.0
+// against 81.5).
 constexpr Width kWidths[] = {{32, 1}, {32, 2}, {96, 1}, {64, 2}, {160, 1}, {96, 2},
                              {128, 2}, {192, 2}, {256, 2}, {384, 2}, {512, 2}};
 
@@ -403,8 +408,9 @@ int run_mode(JoinArgs a, int ctas, cudaStream_t stream)
         NGR_WIDTH(192, 2, true)
         NGR_WIDTH(256, 2, true)
         NGR_WIDTH(384, 2, true)
-        NGR_WIDTH(256, 2, false)
         NGR_WIDTH(384, 2, false)
+        // (five sums alone cut a row into CTAs of fewer than 4097 columns)
+        if constexpr (CENTER) NGR_WIDTH(256, 2, false)
     }
 #undef NGR_WIDTH
     return -9;

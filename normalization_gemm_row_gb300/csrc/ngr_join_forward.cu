@@ -150,9 +150,9 @@ int run(const JoinArgs &a, cudaStream_t stream)
 #define NGR_WIDTH(T, V, ONE)                                                    \
     if (a.shape.tpr == T && a.shape.vecs == V && (a.shape.cluster == 1) == ONE) \
         return launch_join(join_forward_kernel<BF16, MODE, T, V, ONE>, ctas, a.shape, 0, a, stream, "join launch");
+    // (a CTA of a cluster has more than 8192 columns)
     NGR_WIDTH(256, 4, true)
     NGR_WIDTH(512, 4, true)
-    NGR_WIDTH(256, 4, false)
     NGR_WIDTH(512, 4, false)
     if constexpr (MODE != kJoinScalar) {
         NGR_WIDTH(32, 1, true)

@@ -62,3 +62,25 @@ def test_widest_rows_are_sized():
     for N in (61313, 61440, 61448, 65472, 65473, 65535, 65536):
         for rows_per_gate in (0, 1, 3, 16):
             assert f(1, 1, rows_per_gate, 48, N) > 256
+
+
+def test_every_compiled_width_is_taken(shapes):
+    """(threads on a row, vectors a thread, whether a CTA has whole rows):
+    what the launches list, and nothing that no width leads to."""
+    one = [(32, 1), (32, 2), (96, 1), (64, 2), (160, 1), (96, 2), (128, 2), (192, 2), (256, 2), (384, 2), (512, 2)]
+    for mode in (ALIGNED, WINDOW, SCALAR):
+        widths = range(8, MAX_N + 1, 8) if mode == ALIGNED else range(1, MAX_N + 1, 3)
+        taken = lambda f: {(s.tpr, s.vecs, s.cluster == 1) for s in map(f, widths)}
+        got = taken(lambda n: shapes[0](n, mode))
+        want = {(512, 4, True), (512, 4, False), (256, 4, True)}
+        if mode != SCALAR:
+            want |= {(32, v, True) for v in range(1, 6)} | {(t, v, True) for t in (64, 128) for v in (3, 4)}
+            want |= {(256, 3, True), (512, 3, True), (512, 3, False)}
+        assert got == want
+        # without a LayerNorm three sums at most, with one five
+        for most in (3, 5):
+            got = set().union(*(taken(lambda n: shapes[1](n, mode, k)) for k in range(most + 1)))
+            want = {(64, 2, True), (512, 2, True), (512, 2, False)}
+            if mode != SCALAR:
+                want |= {(*w, True) for w in one} | {(384, 2, False)} | ({(256, 2, False)} if most == 5 else set())
+            assert got == want, (mode, most)
