@@ -52,8 +52,8 @@ __global__ void __launch_bounds__(256) ce_pad_kernel(const uint16_t *__restrict_
 // A prefix sum over the tokens [r0, r0 + THREADS x kIndexEach) gives each
 // counted token its place (their order kept) and the others theirs from the
 // end: put(place, token, target or -1).  `base` counts the tokens of the
-// rounds before and is carried on; `top` takes the largest weight of this
-// thread's tokens; *bad is set by a target outside the vocabulary.
+// rounds before and is carried on; `top` takes the largest finite weight of
+// this thread's tokens; *bad is set by a target outside the vocabulary.
 template <int THREADS, typename Put>
 __device__ __forceinline__ void place_tokens(const CeTokens &t, int64_t r0, int64_t &base, float &top, int *bad,
                                              int *warp_sum, Put put)
@@ -94,7 +94,9 @@ __device__ __forceinline__ void place_tokens(const CeTokens &t, int64_t r0, int6
             ++at;
             if (t.lse) {
                 const float g = t.dloss ? t.dloss[i] : 0.0f, l = t.dlse ? t.dlse[i] : 0.0f;
-                top = fmaxf(top, fmaxf(fabsf(g), fabsf(g + l)));
+                const float w = fmaxf(fabsf(g), fabsf(g + l));
+                // (an infinite weight is no unit for the others')
+                if (w < INFINITY) top = fmaxf(top, w);
             }
         } else {
             put(t.M - 1 - (i - at), static_cast<int>(i), -1);
@@ -114,7 +116,7 @@ __device__ __forceinline__ CeInfo tokens_info(const CeTokens &t, int64_t count, 
     __syncthreads();
     for (int w = 0; w < THREADS / 32; ++w) top = fmaxf(top, warp_max[w]);
     top *= fabsf(t.logit_scale);
-    // (no weight, or one that is not finite: unscaled)
+    // (no weight, or one at the ends of FP32's range: unscaled)
     if (!(top >= 1.0e-30f && top <= 1.0e38f)) top = kDzUnit;
     CeInfo info;
     info.count = static_cast<int>(count);
