@@ -314,8 +314,8 @@ int ngr_fused_linear_cross_entropy(const void *x, const void *W,
  * (dlse gives the gradient of a penalty on lse.)  Tokens that do not count
  * have dx = 0 and add nothing to dW.  The logits are computed again a piece
  * of the vocabulary at a time; dz of one piece is held in the workspace,
- * rounded to `dtype` in units of the largest weight (which keeps it inside
- * fp16's range); the products accumulate in FP32 and dx and dW are rounded
+ * rounded to `dtype` in units of the largest finite weight (which keeps it
+ * inside fp16's range); the products accumulate in FP32 and dx and dW are rounded
  * once.  The order of every sum is fixed (the same call gives the same
  * bits).  dx or dW may be NULL (not wanted).  M == 0 zeroes dW.  Alignment
  * as in the forward call, dx and dW 2 bytes.  Workspace:

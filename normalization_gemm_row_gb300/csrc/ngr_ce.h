@@ -16,7 +16,7 @@ enum { kCeLse = 0, kCeGrad = 1, kCeDx = 2, kCeDw = 3 };
 constexpr int kCeTile = 256;      // rows, and columns at most, of a CTA pair's output tile
 
 // What the kernels of a call learn of its tokens (device memory): `count`
-// tokens have a target, and `weight` is the largest size of a gradient
+// tokens have a target, and `weight` is the largest finite size of a gradient
 // weight logit_scale dloss or logit_scale (dloss + dlse).  dz is held in 16
 // bits as a multiple of weight / 2^13: it neither overflows nor loses small
 // probabilities among fp16's subnormals, and where all tokens weigh the same
