@@ -592,7 +592,7 @@ def _there(call, x, stream, *args):
         raise ValueError("the stream must be on the tensors' device")
     outer = torch.cuda.current_stream(x.device)
     for t in args:
-        if torch.is_tensor(t):
+        if torch.is_tensor(t) and t.is_cuda:
             t.record_stream(stream)
     with torch.cuda.stream(stream):
         results = call(*args, stream)

@@ -54,7 +54,7 @@ def test_every_width_has_its_ctas(shapes, mode):
             cols = s.cols + 16 if mode == WINDOW else s.cols
             row = (4 * s.vecs + 1) * s.tpr * s.slots * 16
             # (2 KB a CTA for the sums over a row, 1 KB that the device takes)
-            assert s.per_sm * (sums * s.slots * cols * 4 + row + 3072) <= 228 * 1024, (N, sums)
+            assert s.per_sm * (sums * s.slots * cols * 4 + row + 3 * 1024) <= 228 * 1024, (N, sums)
 
 
 def test_widest_rows_are_sized():

@@ -145,3 +145,17 @@ def test_another_stream_within_a_capture(data, call):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert torch.equal(a, b)
+
+
+def test_refusals_are_the_same_on_another_stream():
+    c = ce_data()
+    side = torch.cuda.Stream()
+    for stream in (None, side):
+        for workspace in (torch.empty(1 << 24, dtype=torch.uint8), torch.empty(256, dtype=torch.uint8, device="cuda")):
+            with pytest.raises(ValueError, match="workspace"):
+                ngr.fused_linear_cross_entropy(c["x"], c["W"], c["target"], workspace=workspace, stream=stream)
+        with pytest.raises(ValueError, match="one entry"):
+            ngr.fused_linear_cross_entropy(c["x"], c["W"], c["target"][:-1], stream=stream)
+        with pytest.raises(ngr.NgrError):
+            ngr.fused_linear_cross_entropy(c["x"], c["W"], c["target"], logit_scale=float("nan"), stream=stream)
+        assert torch.cuda.current_stream() == torch.cuda.default_stream()
