@@ -334,6 +334,128 @@ int ngr_fused_linear_cross_entropy_backward(
 size_t ngr_linear_cross_entropy_workspace_bytes(int backward, int64_t M,
                                                 int64_t K, int64_t V);
 
+/* A paged cache of keys and values.  k and v are [pages, page_size, G, D]
+ * device arrays (G key heads of D elements) by their strides in elements, the
+ * last dimension contiguous: any order of the others in memory, k and v as
+ * parts of one array, and rows wider than G D are all strides.  `table` is
+ * the block table, int32 [table_rows, table_stride] on the device: token j of
+ * the sequence in row b lies in page table[b][j / page_size], slot j %
+ * page_size; a row's first table_pages entries count, and only those that the
+ * sequence's tokens need are looked at.  A cache without pages, [B, S, G, D],
+ * is pages = B of page_size = S with the table 0, 1, ..., B - 1.
+ * (The pages name keeping the cache in segments that attention reads piece by
+ * piece: [OPS], KV-cache-aware incremental attention.) */
+typedef struct {
+    void *k, *v;
+    int64_t pages, page_size;
+    int64_t k_page_stride, k_token_stride, k_head_stride;
+    int64_t v_page_stride, v_token_stride, v_head_stride;
+    const int32_t *table;
+    int64_t table_rows, table_pages, table_stride;
+} ngr_kv_cache;
+
+/* New tokens' keys and values into a paged cache, keys and queries rotated by
+ * their position on the way: between the QKV product and the attention of a
+ * decode step (T = B tokens) or of a prompt (T = all its tokens).
+ *   angle = positions[t] inv_freq[i], i < rot / 2
+ *   (a, b) -> (a cos - b sin, a sin + b cos) for the pairs of dimensions
+ *   (i, i + rot / 2), or (2 i, 2 i + 1) if `interleaved`; the dimensions from
+ *   rot on stay (rot even, 0 for no rotation: inv_freq may be NULL then);
+ *   q_out[t] = rotated q[t];  the cache's slot of (row, positions[t]) takes
+ *   the rotated k[t] and v[t] as it is.
+ * q, q_out are [T, H, D], k, v [T, G, D] by their token and head strides in
+ * elements (parts of one QKV row, say); q_out may be q itself with q's strides.
+ * q may be NULL (H and q_out are not looked at).  rows[t] is the token's row
+ * of the block table (NULL: row t).  A token with a negative position is left
+ * out: nothing of it is written.  A token whose row, position or page is not
+ * there is left out too, and the workspace's error word reports NGR_ERR_ARG.
+ * Two tokens of one call in one slot: one of them is kept, in each piece of
+ * its row either.  Angles are reduced exactly (2^-64 of a turn a position),
+ * the rotation is FP32 and rounded once.  inv_freq is FP32 [rot / 2],
+ * positions and rows are int32 [T].  D up to 256; any alignment (16-byte
+ * aligned heads, rows and pages take 16-byte accesses).  The workspace
+ * (256-byte aligned) holds only the error word; it may be NULL, and nothing
+ * is reported then. */
+#define NGR_ROPE_APPEND_KV_WORKSPACE 256
+int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
+                             int64_t q_head_stride, const void *k,
+                             int64_t k_token_stride, int64_t k_head_stride,
+                             const void *v, int64_t v_token_stride,
+                             int64_t v_head_stride, const ngr_kv_cache *cache,
+                             const int32_t *positions, const int32_t *rows,
+                             const float *inv_freq, int64_t rot,
+                             int interleaved, int64_t T, int64_t H, int64_t G,
+                             int64_t D, int dtype, void *q_out,
+                             int64_t q_out_token_stride,
+                             int64_t q_out_head_stride, void *workspace,
+                             size_t workspace_bytes, ngr_stream_t stream);
+
+/* Attention of one new token for each of B sequences over a paged cache:
+ *   s_j = scale q[b, h] . k_j,  lse = log sum_j exp s_j,
+ *   out[b, h] = sum_j exp(s_j - lse) v_j
+ * over the lengths[b] tokens of table row b (the new token's own among them,
+ * if it was appended), or the last `window` of them (0: all).  Query head h
+ * uses key head h / (H / G); H is a multiple of G.  q is [B, H, D] by its row
+ * and head strides in elements, out [B, H, D] dense, lse FP32 [B, H] or NULL
+ * (it joins results over parts of a context).  lengths[b] = 0 gives out = 0
+ * and lse = -inf, and so do scores that are all -inf; a negative length is a row that is not in use, whose out
+ * and lse are left as they were.  A length beyond table_pages page_size counts
+ * as that, a page that is not there as if its tokens were not, and either is
+ * reported by the workspace's error word as NGR_ERR_ARG.  What the cache holds
+ * beside the sequences' tokens is not looked at (it may be NaN).  Scores,
+ * softmax and sums are FP32, the softmax weights are rounded to `dtype` for
+ * their product with v; the order of every sum follows from the lengths alone
+ * (the same call gives the same bits).  D is a multiple of 8 up to 256, every
+ * pointer but lengths, lse and the table 16-byte aligned and every stride a
+ * multiple of 8 elements.  Workspace (256-byte aligned):
+ * ngr_paged_attention_workspace_bytes, with capacity = table_pages page_size.
+ * The lengths stay on the device, so a captured call follows them. */
+int ngr_fused_paged_attention(const void *q, int64_t q_row_stride,
+                              int64_t q_head_stride, const ngr_kv_cache *cache,
+                              const int32_t *lengths, float scale,
+                              int64_t window, int64_t B, int64_t H, int64_t G,
+                              int64_t D, int dtype, void *out, float *lse,
+                              void *workspace, size_t workspace_bytes,
+                              ngr_stream_t stream);
+
+/* Bytes of workspace of the call above (0 for invalid sizes). */
+size_t ngr_paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t G,
+                                           int64_t D, int64_t capacity,
+                                           int64_t window);
+
+/* A mixture-of-experts layer with SwiGLU experts for a few tokens (decode;
+ * M <= NGR_MOE_MAX_M), its norm and router included:
+ *   a = norm(x),  p = softmax(a . Wr^T) over the E experts,
+ *   the top_k largest p of a token (equal ones: the lowest expert first),
+ *   divided by their sum if `renormalize`,
+ *   y = sum over them of p (SiLU(a . Wg[e]^T) * (a . Wu[e]^T)) . Wd[e]^T.
+ * x and y are [M, K], Wr [E, K], Wg and Wu [E, F, K], Wd [E, K, F]; norm,
+ * gamma, beta and eps as in ngr_fused_norm_swiglu.  The choice is returned in
+ * experts (int32 [M, top_k], largest first) and weights (FP32 [M, top_k]) when
+ * they are not NULL.  The router works in FP32 throughout; the experts'
+ * products take a, and p times the gated product, rounded to `dtype`, and
+ * accumulate in FP32; y is rounded once.  Only chosen experts' weights are
+ * read, each once.  A token whose router's logits hold a NaN has y = NaN.
+ * Any K and F up to NGR_MOE_MAX_WIDTH, any 2-byte alignment (16-byte aligned
+ * weights with K, F multiples of 8 take 16-byte loads).  y may be x's memory.
+ * Sums have a fixed order.  Workspace (256-byte aligned):
+ * ngr_moe_swiglu_workspace_bytes. */
+#define NGR_MOE_MAX_M 32
+#define NGR_MOE_MAX_EXPERTS 1024
+#define NGR_MOE_MAX_TOP_K 32
+#define NGR_MOE_MAX_WIDTH 1048576
+int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma,
+                         const void *beta, const void *Wr, const void *Wg,
+                         const void *Wu, const void *Wd, float eps,
+                         int64_t top_k, int renormalize, int64_t M, int64_t K,
+                         int64_t F, int64_t E, int dtype, void *y,
+                         int32_t *experts, float *weights, void *workspace,
+                         size_t workspace_bytes, ngr_stream_t stream);
+
+/* Bytes of workspace of the call above (0 for invalid sizes). */
+size_t ngr_moe_swiglu_workspace_bytes(int64_t M, int64_t K, int64_t F,
+                                      int64_t E, int64_t top_k);
+
 /* Inference-mode weight fold, step 1 of 2 ([LNF] §6.2: with gamma and beta
  * fixed, gamma is folded into the matmul weight once, ahead of the calls).
  * norm: 1 = LayerNorm, 2 = RMSNorm (beta ignored, may be NULL).  With K8,
@@ -418,8 +540,9 @@ int ngr_row_stats(int norm, const void *x, float eps, int64_t M, int64_t K,
 
 /* Synchronize `stream`, then return and clear the error word kept in
  * `workspace` (NGR_OK, NGR_ERR_TIMEOUT when a kernel's bounded wait ran
- * out, or NGR_ERR_ARG for a target outside the vocabulary).  NGR_ERR_CUDA if
- * the synchronization itself fails. */
+ * out, or NGR_ERR_ARG for a target outside the vocabulary or a page, position
+ * or table row that is not there).  NGR_ERR_CUDA if the synchronization itself
+ * fails. */
 int ngr_workspace_error(void *workspace, ngr_stream_t stream);
 
 /* Launch one tiny kernel whose mbarrier wait can never complete, bounded by

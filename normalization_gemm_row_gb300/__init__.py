@@ -14,5 +14,5 @@ from .binding import (  # noqa: F401
     fused_linear_cross_entropy, fused_linear_cross_entropy_backward,
     fused_linear_residual_norm, fused_linear_silu, fused_mlp, fused_mlp_swiglu,
     fused_norm_gate_residual_norm, fused_norm_gate_residual_norm_backward,
-    fused_norm_linear_act, fused_norm_linear_folded, fused_norm_swiglu,
-    fused_rmsnorm_linear, row_stats)
+    fused_moe_swiglu, fused_norm_linear_act, fused_norm_linear_folded, fused_norm_swiglu,
+    fused_paged_attention, fused_rmsnorm_linear, fused_rope_append_kv, row_stats)

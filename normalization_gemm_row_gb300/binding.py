@@ -34,6 +34,17 @@ STATUS = {0: "NGR_OK", -1: "NGR_ERR_NULL", -2: "NGR_ERR_SHAPE",
           -6: "NGR_ERR_ARCH", -7: "NGR_ERR_CUDA", -8: "NGR_ERR_TIMEOUT",
           -9: "NGR_ERR_ARG"}
 
+
+
+class KvCache(ctypes.Structure):
+    """ngr_kv_cache: a paged cache by its addresses, sizes and strides."""
+    _fields_ = ([("k", ctypes.c_void_p), ("v", ctypes.c_void_p)] +
+                [(n, ctypes.c_int64) for n in ("pages", "page_size", "k_page_stride", "k_token_stride", "k_head_stride",
+                                               "v_page_stride", "v_token_stride", "v_head_stride")] +
+                [("table", ctypes.c_void_p)] +
+                [(n, ctypes.c_int64) for n in ("table_rows", "table_pages", "table_stride")])
+
+
 # Every symbol include/ngr.h declares, with (restype, argtypes).
 _P, _I64, _I, _F, _SZ, _U32 = (ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
                                ctypes.c_float, ctypes.c_size_t, ctypes.c_uint32)
@@ -59,6 +70,15 @@ SIGNATURES = {
     "ngr_fused_linear_cross_entropy_backward": (
         _I, [_P, _P, _P, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
     "ngr_linear_cross_entropy_workspace_bytes": (_SZ, [_I, _I64, _I64, _I64]),
+    "ngr_fused_rope_append_kv": (
+        _I, [_P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _P, _P, _P, _I64, _I, _I64, _I64, _I64, _I64, _I,
+             _P, _I64, _I64, _P, _SZ, _P]),
+    "ngr_fused_paged_attention": (
+        _I, [_P, _I64, _I64, _P, _P, _F, _I64, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _SZ, _P]),
+    "ngr_paged_attention_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64, _I64]),
+    "ngr_fused_moe_swiglu": (
+        _I, [_I, _P, _P, _P, _P, _P, _P, _P, _F, _I64, _I, _I64, _I64, _I64, _I64, _I, _P, _P, _P, _P, _SZ, _P]),
+    "ngr_moe_swiglu_workspace_bytes": (_SZ, [_I64, _I64, _I64, _I64, _I64]),
     "ngr_row_stats": (_I, [_I, _P, _F, _I64, _I64, _I, _P, _P]),
     "ngr_fold_prepare": (_I, [_I, _P, _P, _P, _P, _I64, _I64, _I, _P, _P, _P]),
     "ngr_fused_norm_linear_folded": (_I, [_I, _P, _P, _P, _F, _I64, _I64, _I64, _I, _P, _P, _SZ, _P]),
@@ -225,6 +245,42 @@ def ngr_fused_linear_cross_entropy_backward(dloss, dlse, lse, x, W, target, logi
 @functools.lru_cache(maxsize=4096)
 def ngr_linear_cross_entropy_workspace_bytes(backward, M, K, V) -> int:
     return int(lib().ngr_linear_cross_entropy_workspace_bytes(backward, M, K, V))
+
+
+def ngr_fused_rope_append_kv(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, cache, positions, rows,
+                             inv_freq, rot, interleaved, T, H, G, D, dtype, q_out, q_out_token, q_out_head, ws,
+                             ws_bytes, stream) -> int:
+    """``cache``: a KvCache, or None."""
+    return lib().ngr_fused_rope_append_kv(q, q_token, q_head, k, k_token, k_head, v, v_token, v_head, _ref(cache),
+                                          positions, rows, inv_freq, rot, interleaved, T, H, G, D, dtype, q_out,
+                                          q_out_token, q_out_head, ws, ws_bytes, stream)
+
+
+def ngr_fused_paged_attention(q, q_row, q_head, cache, lengths, scale, window, B, H, G, D, dtype, out, lse, ws,
+                              ws_bytes, stream) -> int:
+    """``cache``: a KvCache, or None."""
+    return lib().ngr_fused_paged_attention(q, q_row, q_head, _ref(cache), lengths, scale, window, B, H, G, D, dtype,
+                                           out, lse, ws, ws_bytes, stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def ngr_paged_attention_workspace_bytes(B, H, G, D, capacity, window) -> int:
+    return int(lib().ngr_paged_attention_workspace_bytes(B, H, G, D, capacity, window))
+
+
+def ngr_fused_moe_swiglu(norm, x, gamma, beta, Wr, Wg, Wu, Wd, eps, top_k, renormalize, M, K, F, E, dtype, y, experts,
+                         weights, ws, ws_bytes, stream) -> int:
+    return lib().ngr_fused_moe_swiglu(norm, x, gamma, beta, Wr, Wg, Wu, Wd, eps, top_k, renormalize, M, K, F, E, dtype,
+                                      y, experts, weights, ws, ws_bytes, stream)
+
+
+@functools.lru_cache(maxsize=4096)
+def ngr_moe_swiglu_workspace_bytes(M, K, F, E, top_k) -> int:
+    return int(lib().ngr_moe_swiglu_workspace_bytes(M, K, F, E, top_k))
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.addressof(struct)
 
 
 def ngr_row_stats(norm, x, eps, M, K, dtype, stats, stream) -> int:
@@ -788,6 +844,228 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
         _current_stream_handle(x.get_device()))
     _raise(rc, "fused_linear_cross_entropy_backward")
     return dx, dW
+
+
+def _kv_cache(x, k_cache, v_cache, block_table):
+    """(KvCache, G, D) of caches [pages, page_size, G, D] and a block table
+    [rows, pages a row], of x's type and device."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError("the caches must be [pages, page_size, heads, dim] and alike")
+    if k_cache.dtype is not x.dtype or v_cache.dtype is not x.dtype:
+        raise TypeError("all tensors must share one dtype")
+    if block_table.dtype is not torch.int32:
+        raise TypeError("block_table must be int32")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [rows, pages a row]")
+    index = x.get_device()
+    if index < 0:
+        raise ValueError("all tensors must be CUDA tensors")
+    if k_cache.get_device() != index or v_cache.get_device() != index or block_table.get_device() != index:
+        raise ValueError("all tensors must be on one CUDA device")
+    pages, size, G, D = k_cache.shape
+    kp, kt, kh, kd = k_cache.stride()
+    vp, vt, vh, vd = v_cache.stride()
+    rows, width = block_table.shape
+    step, one = block_table.stride()
+    if (D > 1 and (kd != 1 or vd != 1)) or (width > 1 and one != 1):
+        raise ValueError("the last dimension of the caches and of block_table must be contiguous")
+    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, kp, kt, kh, vp, vt, vh,
+                   block_table.data_ptr(), rows, width, step), G, D
+
+
+def _int32(what, device_index, n, *ts):
+    """The others (None left out) are contiguous int32 vectors of n entries."""
+    for t in ts:
+        if t is None:
+            continue
+        if t.dtype is not torch.int32:
+            raise TypeError(f"{what} must be int32")
+        if t.dim() != 1 or t.shape[0] != n or t.get_device() != device_index or not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous on the tensors' device, with one entry per token")
+
+
+def _heads_last(what, x, t, tokens, heads, dim):
+    """t's token and head strides, t [tokens, heads, dim] of x's type and device."""
+    if t.dtype is not x.dtype:
+        raise TypeError("all tensors must share one dtype")
+    if t.get_device() != x.get_device():
+        raise ValueError("all tensors must be on one CUDA device")
+    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+        raise ValueError(f"{what} must be [tokens, heads, dim], with the caches' dim (and heads, for k and v)")
+    a, b, c = t.stride()
+    if dim > 1 and c != 1:
+        raise ValueError(f"{what} must have contiguous heads")
+    return a, b
+
+
+def fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows=None, inv_freq=None,
+                         interleaved=False, q_out=None, workspace=None, stream=None):
+    """Rotate q [T, H, D] and k [T, G, D] by their ``positions`` [T] int32 and
+    put k and v [T, G, D] into the paged cache; returns the rotated q (None
+    without q), in ``q_out`` when given (which may be q).
+
+    k_cache, v_cache [pages, page_size, G, D] and block_table [rows, pages a
+    row] int32 may have any strides with a contiguous last dimension, q, k and
+    v any token and head strides (slices of one QKV product's output).  Token
+    t goes to the sequence in row ``rows[t]`` (int32; by default t) of the
+    table.  inv_freq, float32 [rot / 2], gives the angles (None: no rotation);
+    the first rot dimensions are turned in pairs (i, i + rot / 2), or (2i, 2i +
+    1) with ``interleaved``.  A token with a negative position is left out,
+    its row of q_out and its slot included.  One whose row, position or page
+    is not there is left out as well; only the GPU sees it: to learn of it
+    pass a ``workspace`` (256 bytes) and ask ``check_workspace``, or set
+    NGR_DEBUG=1."""
+    code = _dtype_code(k)
+    cache, G, D = _kv_cache(k, k_cache, v_cache, block_table)
+    T = k.shape[0]
+    index = k.get_device()
+    kt, kh = _heads_last("k", k, k, T, G, D)
+    vt, vh = _heads_last("v", k, v, T, G, D)
+    H = qt = qh = ot = oh = 0
+    if q is not None:
+        qt, qh = _heads_last("q", k, q, T, None, D)
+        H = q.shape[1]
+        if q_out is not None:
+            ot, oh = _heads_last("q_out", k, q_out, T, H, D)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _int32("positions and rows", index, T, positions, rows)
+    rot = 0
+    if inv_freq is not None:
+        if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != index
+                or not inv_freq.is_contiguous()):
+            raise ValueError("inv_freq must be a contiguous float32 vector on the tensors' device")
+        rot = 2 * inv_freq.shape[0]
+    if not _here(k, stream):
+        got = _there(_append_there, k, stream, q, k, v, k_cache, v_cache, block_table, positions, rows, inv_freq,
+                     interleaved, q_out, workspace)
+        return got[0]
+    if q is not None and q_out is None:
+        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        ot, oh = H * D, D
+    if workspace is not None or _debug():
+        workspace = _scratch(256, k.device, workspace)
+    rc = lib().ngr_fused_rope_append_kv(
+        _ptr(q), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ctypes.addressof(cache), positions.data_ptr(),
+        _ptr(rows), _ptr(inv_freq), rot, 1 if interleaved else 0, T, H, G, D, code, _ptr(q_out), ot, oh,
+        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _current_stream_handle(index))
+    if rc != 0:
+        raise NgrError(rc, "fused_rope_append_kv")
+    return q_out
+
+
+def _append_there(q, k, v, k_cache, v_cache, block_table, positions, rows, inv_freq, interleaved, q_out, workspace,
+                  stream):
+    return (fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows, inv_freq, interleaved, q_out,
+                                 workspace, stream),)
+
+
+def _debug():
+    """NGR_DEBUG: calls report what their kernels found."""
+    return os.environ.get("NGR_DEBUG", "0") not in ("", "0")
+
+
+def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None, window=0, out=None,
+                          return_lse=False, lse=None, workspace=None, stream=None):
+    """Attention of one new token for each sequence, q [B, H, D], over the
+    first ``lengths[b]`` (int32 [B]) tokens of row b of the block table, or
+    the last ``window`` of them (0: all): [B, H, D], or with ``return_lse``
+    (out, lse), lse float32 [B, H] the log of the sum of the exponentials of
+    the scores.  scale is 1 / sqrt(D) by default.  The caches and the table
+    as in ``fused_rope_append_kv``, at 16-byte steps; D a multiple of 8 up to
+    256; H a multiple of the caches' heads.
+
+    A length of 0 gives 0 and -inf; a row with a negative length is left as it
+    was (in ``out`` and ``lse`` when given).  A length beyond the table, or a
+    page that is not there, is seen by the GPU alone, which leaves those tokens
+    out: pass a ``workspace`` and ask ``check_workspace``, or set NGR_DEBUG=1."""
+    code = _dtype_code(q)
+    cache, G, D = _kv_cache(q, k_cache, v_cache, block_table)
+    B = q.shape[0]
+    index = q.get_device()
+    qr, qh = _heads_last("q", q, q, B, None, D)
+    H = q.shape[1]
+    _int32("lengths", index, B, lengths)
+    if out is not None and (out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != index
+                            or not out.is_contiguous()):
+        raise ValueError("out must be contiguous, with q's shape, type and device")
+    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.get_device() != index
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be contiguous float32 [B, H] on q's device")
+    if not _here(q, stream):
+        got = _there(_attend_there, q, stream, q, k_cache, v_cache, block_table, lengths, scale, window, out,
+                     return_lse, lse, workspace)
+        return got if return_lse else got[0]
+    if scale is None:
+        scale = D ** -0.5
+    if out is None:
+        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
+    if lse is None and return_lse:
+        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    ws = _scratch(ngr_paged_attention_workspace_bytes(B, H, G, D, cache.table_pages * cache.page_size, window),
+                  q.device, workspace)
+    rc = lib().ngr_fused_paged_attention(
+        q.data_ptr(), qr, qh, ctypes.addressof(cache), lengths.data_ptr(), scale, window, B, H, G, D, code,
+        out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel() * ws.element_size(), _current_stream_handle(index))
+    if rc != 0:
+        raise NgrError(rc, "fused_paged_attention")
+    return (out, lse) if return_lse else out
+
+
+def _attend_there(q, k_cache, v_cache, block_table, lengths, scale, window, out, return_lse, lse, workspace, stream):
+    got = fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale, window, out, return_lse, lse,
+                                workspace, stream)
+    return got if return_lse else (got,)
+
+
+def fused_moe_swiglu(x, Wr, Wg, Wu, Wd, top_k, norm: int = NORM_NONE, gamma=None, beta=None, eps=1e-5,
+                     renormalize=True, out=None, return_routing=False, workspace=None, stream=None):
+    """A mixture-of-experts layer with SwiGLU experts for at most 32 tokens:
+    a = norm(x), the ``top_k`` largest of p = softmax(a . Wr^T) (over their
+    sum with ``renormalize``), y = sum p (SiLU(a . Wg[e]^T) * (a . Wu[e]^T)) .
+    Wd[e]^T; x [..., K], Wr [E, K], Wg and Wu [E, F, K], Wd [E, K, F].  With
+    ``return_routing`` (y, experts, weights), int32 and float32 [..., top_k],
+    the largest first.  ``out`` may be x."""
+    K = x.shape[-1]
+    M = x.numel() // K if K else 0
+    if Wr.dim() != 2 or Wg.dim() != 3:
+        raise ValueError("Wr must be [E, K], Wg and Wu [E, F, K], Wd [E, K, F]")
+    E, F = Wr.shape[0], Wg.shape[1]
+    if Wr.shape[1] != K or Wg.shape != (E, F, K) or Wu.shape != (E, F, K) or Wd.shape != (E, K, F):
+        raise ValueError("Wr must be [E, K], Wg and Wu [E, F, K], Wd [E, K, F]")
+    if norm != NORM_LAYER:
+        beta = None
+        if norm == NORM_NONE:
+            gamma = None
+    for t in (gamma, beta):
+        if t is not None and t.numel() != K:
+            raise ValueError("gamma and beta must have one element per column")
+    _tokens(x, "out", out)
+    code, p_r, p_g, p_u, p_d, p_gamma, p_beta, _ = _uniform(x, Wr, Wg, Wu, Wd, gamma, beta, out)
+    if not _here(x, stream):
+        got = _there(_moe_there, x, stream, x, Wr, Wg, Wu, Wd, top_k, norm, gamma, beta, eps, renormalize, out,
+                     return_routing, workspace)
+        return got if return_routing else got[0]
+    y = out if out is not None else torch.empty_like(x)
+    experts = weights = None
+    if return_routing:
+        experts = torch.empty((*x.shape[:-1], top_k), dtype=torch.int32, device=x.device)
+        weights = torch.empty((*x.shape[:-1], top_k), dtype=torch.float32, device=x.device)
+    ws = _scratch(ngr_moe_swiglu_workspace_bytes(M, K, F, E, top_k), x.device, workspace)
+    rc = lib().ngr_fused_moe_swiglu(
+        norm, x.data_ptr(), p_gamma, p_beta, p_r, p_g, p_u, p_d, eps, top_k, 1 if renormalize else 0, M, K, F, E, code,
+        y.data_ptr(), _ptr(experts), _ptr(weights), ws.data_ptr(), ws.numel() * ws.element_size(),
+        _current_stream_handle(x.get_device()))
+    if rc != 0:
+        raise NgrError(rc, "fused_moe_swiglu")
+    return (y, experts, weights) if return_routing else y
+
+
+def _moe_there(x, Wr, Wg, Wu, Wd, top_k, norm, gamma, beta, eps, renormalize, out, return_routing, workspace, stream):
+    got = fused_moe_swiglu(x, Wr, Wg, Wu, Wd, top_k, norm, gamma, beta, eps, renormalize, out, return_routing,
+                           workspace, stream)
+    return got if return_routing else (got,)
 
 
 def fold_prepare(norm: int, gamma, beta, W, bias=None, stream=None):

@@ -1316,7 +1316,7 @@ int ngr_workspace_error(void *workspace, ngr_stream_t stream)
     if (cudaMemcpy(&v, workspace, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
         return NGR_ERR_CUDA;
     if (v != 0 && cudaMemset(workspace, 0, sizeof(int)) != cudaSuccess) return NGR_ERR_CUDA;
-    return v == 0 ? NGR_OK : v == kDevErrTarget ? NGR_ERR_ARG : NGR_ERR_TIMEOUT;
+    return v == 0 ? NGR_OK : v == kDevErrTarget || v == kDevErrPage ? NGR_ERR_ARG : NGR_ERR_TIMEOUT;
 }
 
 int ngr_debug_bounded_wait(void *workspace, uint32_t timeout_us, ngr_stream_t stream_)

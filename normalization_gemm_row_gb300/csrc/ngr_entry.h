@@ -8,9 +8,10 @@
 
 namespace ngr {
 
-// A value of the device error word beside kDevErrTimeout: a target outside
-// the vocabulary (reported as NGR_ERR_ARG).
-enum : int { kDevErrTarget = 2 };
+// Values of the device error word beside kDevErrTimeout, reported as
+// NGR_ERR_ARG: a target outside the vocabulary; a page, position or row of a
+// block table that is not there.
+enum : int { kDevErrTarget = 2, kDevErrPage = 3 };
 
 // The current device's SM count: NGR_OK, NGR_ERR_ARCH or NGR_ERR_CUDA.
 int device_sms(int *sms);

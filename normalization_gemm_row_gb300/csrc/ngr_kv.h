@@ -1,0 +1,82 @@
+// ngr_kv.h -- argument blocks of the paged key-value cache's kernels: the
+// rotated append (ngr_append.cu) and the attention of one new token
+// (ngr_attend.cu).  Not installed.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+namespace ngr {
+
+// The caches [pages, page_size, heads, dim] by their strides in elements, and
+// the block table [rows, table_stride] whose rows' first table_pages entries
+// are pages.
+struct KvView {
+    void *k, *v;
+    int64_t k_page, k_token, k_head, v_page, v_token, v_head;
+    const int *table;
+    int64_t table_stride;
+    int64_t capacity;     // tokens that a row of the table has room for
+    int pages, page_size, rows;
+};
+
+struct AppendArgs {
+    KvView kv;
+    const void *q, *k, *v;    // q may be null
+    void *q_out;
+    int64_t q_token, q_head, k_token, k_head, v_token, v_head, qo_token, qo_head;
+    const int *positions, *rows;   // rows null: token t's is t
+    const float *inv_freq;
+    int *err;                 // null: nothing is reported
+    int T, H, G, D, rot;
+    int blocks_per_token;
+};
+constexpr int kAppendThreads = 256;
+// vec: elements that one access moves (8, 4, 2 or 1).
+int launch_append(bool bf16, int vec, bool interleaved, const AppendArgs &a, cudaStream_t stream);
+// Units (thread's work) of one token, of which a block takes kAppendThreads.
+int64_t append_units(int vec, bool interleaved, int64_t H, int64_t G, int64_t D, int64_t rot);
+
+constexpr int kAttendMaxDim = 256;
+constexpr int kAttendRows = 16;    // query heads of one key head that a warp takes at once
+constexpr int kAttendTile = 16;    // tokens a warp takes at once
+constexpr int kAttendSms = 152;    // sizing must not ask a device
+
+// An item whose tokens several workers (warps) share.  Each leaves its part
+// of it, [part_rows] (maximum, sum) and [part_rows][dim padded] sums in FP32:
+// in the second of a worker's two places if the part begins the item.
+struct AttendJob {
+    int first, last;     // the workers; first < 0: no job
+    int row, item;       // sequence, (key head, block of query heads)
+};
+
+struct AttendArgs {
+    KvView kv;
+    const void *q;
+    int64_t q_row, q_head;
+    const int *lengths;
+    void *out;                // [B, H, D]
+    float *lse;               // [B, H] or null
+    float scale2;             // softmax scale x log2 e
+    int window;               // 0: none
+    int B, H, G, D;
+    int group, blocks;        // query heads of a key head; blocks of kAttendRows of them
+    int workers, min_share;
+    int part_rows;            // query heads in a part: at most kAttendRows
+    int slots;                // jobs: one an item, or one a worker if there are fewer
+    bool slot_by_item;
+    float2 *part_ml;          // [workers][2][rows]
+    float *part_o;            // [workers][2][rows][dim padded]
+    AttendJob *jobs;
+    int *flags;               // [workers]
+    int *err;
+};
+
+// The padded head dimension (64, 128 or 256) and the warps of a CTA for it.
+inline int attend_dim(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
+inline int attend_warps(int dim) { return dim == 256 ? 4 : 8; }
+int launch_attend(bool bf16, const AttendArgs &a, cudaStream_t stream);
+int launch_attend_join(bool bf16, const AttendArgs &a, cudaStream_t stream);
+
+}  // namespace ngr

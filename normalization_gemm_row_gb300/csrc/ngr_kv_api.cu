@@ -1,0 +1,292 @@
+// ngr_kv_api.cu -- entry points of the paged key-value cache (ngr_append.cu,
+// ngr_attend.cu): argument checks, workspace layout, how many workers.
+#include <algorithm>
+#include <cmath>
+#include <cstdio>
+#include <cstring>
+
+#include "ngr.h"
+#include "ngr_entry.h"
+#include "ngr_internal.h"
+#include "ngr_kv.h"
+
+namespace ngr {
+
+namespace {
+
+constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
+// Fewer tiles than this are not worth a worker of their own.
+constexpr int64_t kMinShare = 2;
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+// The step of a dimension that may have one entry (any step means the same).
+int64_t step(int64_t stride, int64_t entries) { return entries > 1 ? stride : 0; }
+
+int kv_view(const ngr_kv_cache *c, int64_t G, KvView *v)
+{
+    if (!c || !c->k || !c->v || !c->table) return NGR_ERR_NULL;
+    if (c->pages <= 0 || c->pages > kMax31 || c->page_size <= 0 || c->page_size > kMax31 || c->table_rows <= 0 ||
+        c->table_rows > kMax31 || c->table_pages <= 0 || c->table_pages > kMax31)
+        return NGR_ERR_SHAPE;
+    if (!aligned(c->table, 4) || !aligned(c->k, 2) || !aligned(c->v, 2)) return NGR_ERR_ALIGN;
+    // (rows of the table may be a view of wider ones; tokens may be in any order in memory)
+    if ((c->table_rows > 1 && c->table_stride < c->table_pages) || c->k_page_stride < 0 || c->k_token_stride < 0 ||
+        c->k_head_stride < 0 || c->v_page_stride < 0 || c->v_token_stride < 0 || c->v_head_stride < 0)
+        return NGR_ERR_ARG;
+    v->k = c->k;
+    v->v = c->v;
+    v->k_page = step(c->k_page_stride, c->pages);
+    v->k_token = step(c->k_token_stride, c->page_size);
+    v->k_head = step(c->k_head_stride, G);
+    v->v_page = step(c->v_page_stride, c->pages);
+    v->v_token = step(c->v_token_stride, c->page_size);
+    v->v_head = step(c->v_head_stride, G);
+    v->table = c->table;
+    v->table_stride = c->table_stride;
+    v->capacity = c->table_pages * c->page_size;
+    v->pages = static_cast<int>(c->pages);
+    v->page_size = static_cast<int>(c->page_size);
+    v->rows = static_cast<int>(c->table_rows);
+    return NGR_OK;
+}
+
+// Elements that every address of these strides is a multiple of: 8, 4, 2 or 1.
+int granule(std::initializer_list<const void *> bases, std::initializer_list<int64_t> steps)
+{
+    int64_t bits = 8;
+    for (const void *p : bases) bits |= static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) >> 1);
+    for (int64_t s : steps) bits |= s;
+    return static_cast<int>(bits & -bits);
+}
+
+struct AttendPlan {
+    int64_t workers, slots, part_rows, blocks, items;
+    size_t flags, jobs, ml, o, total;
+};
+
+// The workers that the longest sequences the table has room for keep busy,
+// up to every warp of the device.
+AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capacity, int64_t window)
+{
+    AttendPlan p;
+    std::memset(&p, 0, sizeof(p));
+    const int dim = attend_dim(D), warps = attend_warps(dim);
+    const int64_t group = H / G, longest = window > 0 ? std::min(window, capacity) : capacity;
+    p.blocks = (group + kAttendRows - 1) / kAttendRows;
+    p.items = B * G * p.blocks;
+    p.part_rows = std::min<int64_t>(group, kAttendRows);
+    const int64_t tiles = (longest + kAttendTile - 1) / kAttendTile;
+    const double all = static_cast<double>(p.items) * static_cast<double>(tiles);
+    const int64_t ctas = all >= static_cast<double>(kAttendSms * kMinShare)
+                             ? kAttendSms
+                             : std::max<int64_t>(1, (p.items * tiles + kMinShare - 1) / kMinShare);
+    p.workers = ctas * warps;
+    p.slots = std::min(p.items, p.workers);
+    size_t off = 256;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) & ~static_cast<size_t>(255);
+        return at;
+    };
+    p.flags = take(static_cast<size_t>(p.workers) * sizeof(int));
+    p.jobs = take(static_cast<size_t>(p.slots) * sizeof(AttendJob));
+    p.ml = take(static_cast<size_t>(p.workers) * 2 * p.part_rows * sizeof(float2));
+    p.o = take(static_cast<size_t>(p.workers) * 2 * p.part_rows * dim * sizeof(float));
+    p.total = off;
+    return p;
+}
+
+int heads(int64_t H, int64_t G, int64_t D, bool queries)
+{
+    if (G <= 0 || D <= 0 || D > kAttendMaxDim || G > kMax31) return NGR_ERR_SHAPE;
+    if (queries && (H <= 0 || H > kMax31 || H % G != 0)) return NGR_ERR_SHAPE;
+    return NGR_OK;
+}
+
+int attend_sizes(int64_t B, int64_t H, int64_t G, int64_t D)
+{
+    const int rc = heads(H, G, D, true);
+    if (rc != NGR_OK) return rc;
+    if (D % 8 != 0 || B < 0 || B > kMax31 || (B > 0 && H > kMax31 / B)) return NGR_ERR_SHAPE;
+    return NGR_OK;
+}
+
+}  // namespace
+
+}  // namespace ngr
+
+using namespace ngr;
+
+extern "C" {
+
+int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride, int64_t q_head_stride, const void *k,
+                             int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                             int64_t v_head_stride, const ngr_kv_cache *cache, const int32_t *positions,
+                             const int32_t *rows, const float *inv_freq, int64_t rot, int interleaved, int64_t T,
+                             int64_t H, int64_t G, int64_t D, int dtype, void *q_out, int64_t q_out_token_stride,
+                             int64_t q_out_head_stride, void *workspace, size_t workspace_bytes, ngr_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (dtype != NGR_F16 && dtype != NGR_BF16) return NGR_ERR_DTYPE;
+    int rc = heads(H, G, D, false);
+    if (rc != NGR_OK) return rc;
+    if (T < 0 || T > kMax31 || (q && (H <= 0 || H > kMax31))) return NGR_ERR_SHAPE;
+    if (rot < 0 || rot > D || rot % 2 != 0) return NGR_ERR_ARG;
+    if (workspace && workspace_bytes < NGR_ROPE_APPEND_KV_WORKSPACE) return NGR_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
+    if (T == 0) return NGR_OK;
+    if (!k || !v || !positions || (rot > 0 && !inv_freq) || (q && !q_out)) return NGR_ERR_NULL;
+    AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    rc = kv_view(cache, G, &a.kv);
+    if (rc != NGR_OK) return rc;
+    if (!rows && cache->table_rows < T) return NGR_ERR_SHAPE;
+    if (!aligned(positions, 4) || !aligned(rows, 4) || !aligned(inv_freq, 4)) return NGR_ERR_ALIGN;
+    if (!aligned(q, 2) || !aligned(k, 2) || !aligned(v, 2) || !aligned(q_out, 2)) return NGR_ERR_ALIGN;
+    if (!q) {
+        H = 0;
+        q_out = nullptr;
+    }
+    q_token_stride = step(q_token_stride, q ? T : 0);
+    q_head_stride = step(q_head_stride, H);
+    q_out_token_stride = step(q_out_token_stride, q ? T : 0);
+    q_out_head_stride = step(q_out_head_stride, H);
+    k_token_stride = step(k_token_stride, T);
+    k_head_stride = step(k_head_stride, G);
+    v_token_stride = step(v_token_stride, T);
+    v_head_stride = step(v_head_stride, G);
+    if (q_token_stride < 0 || q_head_stride < 0 || k_token_stride < 0 || k_head_stride < 0 || v_token_stride < 0 ||
+        v_head_stride < 0 || q_out_token_stride < 0 || q_out_head_stride < 0)
+        return NGR_ERR_ARG;
+    // what is written has a place of its own for every element
+    const KvView &kv = a.kv;
+    if ((q && T > 1 && q_out_token_stride == 0) || (H > 1 && q_out_head_stride < D) ||
+        (G > 1 && (kv.k_head < D || kv.v_head < D)) || (kv.page_size > 1 && (kv.k_token < D || kv.v_token < D)) ||
+        (kv.pages > 1 && (kv.k_page < D || kv.v_page < D)))
+        return NGR_ERR_ARG;
+    // q_out in q's memory: the same elements in the same places
+    if (q && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
+        return NGR_ERR_ARG;
+    int vec = granule({q, k, v, q_out, a.kv.k, a.kv.v},
+                      {D, q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
+                       q_out_token_stride, q_out_head_stride, a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv.v_page,
+                       a.kv.v_token, a.kv.v_head});
+    vec = std::min(vec, granule({}, {interleaved ? rot : rot / 2, interleaved ? 0 : rot}));
+    int sms = 0;
+    rc = device_sms(&sms);
+    if (rc != NGR_OK) return rc;
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_out = q_out;
+    a.q_token = q_token_stride;
+    a.q_head = q_head_stride;
+    a.k_token = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_token = v_token_stride;
+    a.v_head = v_head_stride;
+    a.qo_token = q_out_token_stride;
+    a.qo_head = q_out_head_stride;
+    a.positions = positions;
+    a.rows = rows;
+    a.inv_freq = inv_freq;
+    a.err = static_cast<int *>(workspace);
+    a.T = static_cast<int>(T);
+    a.H = static_cast<int>(H);
+    a.G = static_cast<int>(G);
+    a.D = static_cast<int>(D);
+    a.rot = static_cast<int>(rot);
+    const int64_t units = append_units(vec, interleaved != 0, H, G, D, rot);
+    const int64_t blocks = (units + kAppendThreads - 1) / kAppendThreads;
+    if (units > kMax31 - kAppendThreads || blocks > (kMax31 - 1) / T) return NGR_ERR_SHAPE;
+    a.blocks_per_token = static_cast<int>(blocks);
+    if (trace_mode())
+        std::fprintf(stderr, "ngr: rotated append T=%d H=%d G=%d D=%d rot=%d%s page=%d elements at once=%d blocks a token=%d\n",
+                     a.T, a.H, a.G, a.D, a.rot, interleaved ? " interleaved" : "", a.kv.page_size, vec, a.blocks_per_token);
+    call_begin();
+    kernel_begin(stream);
+    rc = launch_append(dtype == NGR_BF16, vec, interleaved != 0, a, stream);
+    kernel_end(stream);
+    return call_end(rc, workspace, stream);
+}
+
+size_t ngr_paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capacity,
+                                           int64_t window)
+{
+    if (attend_sizes(B, H, G, D) != NGR_OK || capacity <= 0 || window < 0) return 0;
+    return attend_plan(B, H, G, D, std::min(capacity, kMax31), window).total;
+}
+
+int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_head_stride, const ngr_kv_cache *cache,
+                              const int32_t *lengths, float scale, int64_t window, int64_t B, int64_t H, int64_t G,
+                              int64_t D, int dtype, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                              ngr_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (dtype != NGR_F16 && dtype != NGR_BF16) return NGR_ERR_DTYPE;
+    int rc = attend_sizes(B, H, G, D);
+    if (rc != NGR_OK) return rc;
+    if (!std::isfinite(scale) || window < 0) return NGR_ERR_ARG;
+    if (B == 0) return NGR_OK;
+    if (!q || !lengths || !out) return NGR_ERR_NULL;
+    AttendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    rc = kv_view(cache, G, &a.kv);
+    if (rc != NGR_OK) return rc;
+    if (cache->table_rows < B) return NGR_ERR_SHAPE;
+    q_row_stride = step(q_row_stride, B);
+    q_head_stride = step(q_head_stride, H);
+    if (q_row_stride < 0 || q_head_stride < 0) return NGR_ERR_ARG;
+    if (!aligned(lengths, 4) || !aligned(lse, 4) || !aligned(out, 16) ||
+        granule({q, a.kv.k, a.kv.v}, {q_row_stride, q_head_stride, a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv.v_page,
+                                      a.kv.v_token, a.kv.v_head}) != 8)
+        return NGR_ERR_ALIGN;
+    const AttendPlan p = attend_plan(B, H, G, D, std::min(a.kv.capacity, kMax31), window);
+    if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
+    int sms = 0;
+    rc = device_sms(&sms);
+    if (rc != NGR_OK) return rc;
+    char *ws = static_cast<char *>(workspace);
+    a.q = q;
+    a.q_row = q_row_stride;
+    a.q_head = q_head_stride;
+    a.lengths = lengths;
+    a.out = out;
+    a.lse = lse;
+    a.scale2 = scale * 1.4426950408889634f;
+    a.window = static_cast<int>(std::min(window, kMax31));
+    a.B = static_cast<int>(B);
+    a.H = static_cast<int>(H);
+    a.G = static_cast<int>(G);
+    a.D = static_cast<int>(D);
+    a.group = static_cast<int>(H / G);
+    a.blocks = static_cast<int>(p.blocks);
+    a.workers = static_cast<int>(p.workers);
+    a.min_share = static_cast<int>(kMinShare);
+    a.part_rows = static_cast<int>(p.part_rows);
+    a.slots = static_cast<int>(p.slots);
+    a.slot_by_item = p.items <= p.workers;
+    a.flags = reinterpret_cast<int *>(ws + p.flags);
+    a.jobs = reinterpret_cast<AttendJob *>(ws + p.jobs);
+    a.part_ml = reinterpret_cast<float2 *>(ws + p.ml);
+    a.part_o = reinterpret_cast<float *>(ws + p.o);
+    a.err = reinterpret_cast<int *>(ws);
+    if (trace_mode())
+        std::fprintf(stderr, "ngr: paged attention B=%d H=%d G=%d D=%d page=%d window=%d dim=%d workers=%d jobs=%d\n", a.B, a.H,
+                     a.G, a.D, a.kv.page_size, a.window, attend_dim(D), a.workers, a.slots);
+    const bool bf16 = dtype == NGR_BF16;
+    call_begin();
+    kernel_begin(stream);
+    rc = launch_attend(bf16, a, stream);
+    kernel_end(stream);
+    if (rc == NGR_OK) {
+        kernel_begin(stream);
+        rc = launch_attend_join(bf16, a, stream);
+        kernel_end(stream);
+    }
+    return call_end(rc, workspace, stream);
+}
+
+}  // extern "C"

@@ -1,0 +1,86 @@
+// ngr_mma.cuh -- inline-PTX wrappers of the warp-wide matrix instructions and
+// the 16-byte asynchronous copies that the decode step's kernels use.
+//
+// Those kernels have 1 to 16 rows on one side of their products and stream
+// the other side from memory once: 2 to 16 operations a byte, where
+// tcgen05.mma's 128-row tiles would be mostly padding.  mma.sync's 16 x 8 x 16
+// pieces take their operands from registers and need no tensor memory.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <cstdint>
+
+namespace ngr {
+
+// d += a b, 16 x 8 x 16.  With g = lane / 4, t = lane % 4: a0..a3 hold rows
+// (g, g + 8, g, g + 8) at k (2t, 2t, 2t + 8, 2t + 8) and the next; b0, b1
+// column g at k 2t and 2t + 8 and the next; d0, d1 row g, d2, d3 row g + 8 at
+// columns 2t, 2t + 1.
+template <bool BF16>
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Four 8 x 8 matrices of 16-bit elements from shared memory; lane i gives the
+// address of row i % 8 of matrix i / 8.  `_t`: each transposed.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t saddr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t saddr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(saddr)
+                 : "memory");
+}
+
+// 16 bytes to shared memory behind the thread's back; zeros where !there
+// (nothing is read then).
+__device__ __forceinline__ void cp_async16(uint32_t saddr, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// Until at most N of the thread's groups are under way.
+template <int N>
+__device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Two values rounded to the 16-bit type, the first in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    if (BF16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <bool BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t v)
+{
+    if (BF16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xFFFF0000u));
+    return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+}
+
+}  // namespace ngr

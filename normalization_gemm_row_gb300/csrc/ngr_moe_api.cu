@@ -1,0 +1,157 @@
+// ngr_moe_api.cu -- entry point of the mixture-of-experts layer for a few
+// tokens (ngr_moe.cu): argument checks, workspace layout, launch sizes.
+#include <algorithm>
+#include <cstdio>
+#include <cstring>
+
+#include "ngr.h"
+#include "ngr_entry.h"
+#include "ngr_internal.h"
+#include "ngr_moe.h"
+
+namespace ngr {
+
+namespace {
+
+constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
+
+static_assert(NGR_MOE_MAX_M == kMoeMaxTokens && NGR_MOE_MAX_EXPERTS == kMoeMaxExperts && NGR_MOE_MAX_TOP_K == kMoeMaxTopK,
+              "ngr.h and the kernels agree");
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
+
+int moe_sizes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
+{
+    if (M < 0 || M > NGR_MOE_MAX_M || K <= 0 || K > NGR_MOE_MAX_WIDTH || F <= 0 || F > NGR_MOE_MAX_WIDTH || E <= 0 || E > NGR_MOE_MAX_EXPERTS ||
+        top_k <= 0 || top_k > E || top_k > NGR_MOE_MAX_TOP_K)
+        return NGR_ERR_SHAPE;
+    return NGR_OK;
+}
+
+struct MoePlan {
+    size_t ids, w, a, h, total;
+    int64_t Kp, Fp;
+};
+
+MoePlan moe_plan(int64_t M, int64_t K, int64_t F, int64_t top_k)
+{
+    MoePlan p;
+    p.Kp = up_to(K, 64);
+    p.Fp = up_to(F, 64);
+    size_t off = 256;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off += (bytes + 255) & ~static_cast<size_t>(255);
+        return at;
+    };
+    p.ids = take(static_cast<size_t>(M * top_k) * sizeof(int));
+    p.w = take(static_cast<size_t>(M * top_k) * sizeof(float));
+    p.a = take(static_cast<size_t>(M * p.Kp) * 2);
+    p.h = take(static_cast<size_t>(M * top_k * p.Fp) * 2);
+    p.total = off;
+    return p;
+}
+
+// CTAs that share 16 rows of y: as many (1, 2, 4, 8) as fill the SMs twice
+// over, each with eight steps a warp at least where all choose apart.
+int down_splits(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
+{
+    const int64_t tiles = (K + 15) / 16, steps = std::min(E, M * top_k) * ((F + 63) / 64);
+    int s = 1;
+    while (s < 8 && tiles * s < 2 * kMoeSms && steps / (2 * s * (kMoeThreads / 32)) >= 4) s *= 2;
+    return s;
+}
+
+}  // namespace
+
+}  // namespace ngr
+
+using namespace ngr;
+
+extern "C" {
+
+size_t ngr_moe_swiglu_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
+{
+    if (moe_sizes(M, K, F, E, top_k) != NGR_OK) return 0;
+    return moe_plan(M, K, F, top_k).total;
+}
+
+int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void *beta, const void *Wr, const void *Wg,
+                         const void *Wu, const void *Wd, float eps, int64_t top_k, int renormalize, int64_t M, int64_t K,
+                         int64_t F, int64_t E, int dtype, void *y, int32_t *experts, float *weights, void *workspace,
+                         size_t workspace_bytes, ngr_stream_t stream_)
+{
+    cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+    if (dtype != NGR_F16 && dtype != NGR_BF16) return NGR_ERR_DTYPE;
+    if (norm != NGR_NORM_NONE && norm != NGR_NORM_LAYER && norm != NGR_NORM_RMS) return NGR_ERR_ARG;
+    int rc = moe_sizes(M, K, F, E, top_k);
+    if (rc != NGR_OK) return rc;
+    if (norm != NGR_NORM_NONE && !(eps >= 0.0f)) return NGR_ERR_ARG;
+    if (M == 0) return NGR_OK;
+    if (!x || !Wr || !Wg || !Wu || !Wd || !y || (norm != NGR_NORM_NONE && !gamma) || (norm == NGR_NORM_LAYER && !beta))
+        return NGR_ERR_NULL;
+    for (const void *p : {x, gamma, beta, Wr, Wg, Wu, Wd, static_cast<const void *>(y)})
+        if (!aligned(p, 2)) return NGR_ERR_ALIGN;
+    if (!aligned(experts, 4) || !aligned(weights, 4)) return NGR_ERR_ALIGN;
+    const MoePlan p = moe_plan(M, K, F, top_k);
+    if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
+    if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
+    int sms = 0;
+    rc = device_sms(&sms);
+    if (rc != NGR_OK) return rc;
+    char *ws = static_cast<char *>(workspace);
+    MoeArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.gamma = gamma;
+    a.beta = beta;
+    a.Wr = Wr;
+    a.Wg = Wg;
+    a.Wu = Wu;
+    a.Wd = Wd;
+    a.y = y;
+    a.experts = experts;
+    a.weights = weights;
+    a.ids = reinterpret_cast<int *>(ws + p.ids);
+    a.w = reinterpret_cast<float *>(ws + p.w);
+    a.a = ws + p.a;
+    a.h = ws + p.h;
+    a.err = reinterpret_cast<int *>(ws);
+    a.norm = norm;
+    a.M = static_cast<int>(M);
+    a.K = static_cast<int>(K);
+    a.F = static_cast<int>(F);
+    a.E = static_cast<int>(E);
+    a.top_k = static_cast<int>(top_k);
+    a.renormalize = renormalize != 0;
+    a.Kp = static_cast<int>(p.Kp);
+    a.Fp = static_cast<int>(p.Fp);
+    a.eps = eps;
+    a.cluster = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;   // an expert a warp, up to 64
+    a.splits = down_splits(M, K, F, E, top_k);
+    const bool bf16 = dtype == NGR_BF16;
+    const bool vec_r = K % 8 == 0 && aligned(Wr, 16), vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
+    const bool vec_f = F % 8 == 0 && aligned(Wd, 16);
+    if (trace_mode())
+        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d router=%d CTAs a token, down=%d CTAs for 16 rows%s%s\n",
+                     a.M, a.K, a.F, a.E, a.top_k, norm, a.cluster, a.splits, vec_k ? "" : ", gate and up shifted",
+                     vec_f ? "" : ", down shifted");
+    call_begin();
+    kernel_begin(stream);
+    rc = launch_moe_router(bf16, vec_r, a, stream);
+    kernel_end(stream);
+    if (rc == NGR_OK) {
+        kernel_begin(stream);
+        rc = launch_moe_up(bf16, vec_k, a, stream);
+        kernel_end(stream);
+    }
+    if (rc == NGR_OK) {
+        kernel_begin(stream);
+        rc = launch_moe_down(bf16, vec_f, a, stream);
+        kernel_end(stream);
+    }
+    return call_end(rc, workspace, stream);
+}
+
+}  // extern "C"
