@@ -12,7 +12,17 @@ constexpr int kMoeMaxTokens = 32;     // one bit of a word each
 constexpr int kMoeMaxExperts = 1024;  // 32 logits a lane
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeThreads = 256;
-constexpr int kMoeSms = 152;          // sizing must not ask a device
+// Both product kernels run kMoeCtas CTAs, two for each of a GB300's SMs
+// (sizing must not ask a device); their warps are the workers.
+constexpr int kMoeCtas = 2 * 152;
+constexpr int kMoeWorkers = kMoeCtas * (kMoeThreads / 32);
+// Tokens of one matrix instruction: each has two of its 8 columns, its row
+// rounded to the 16-bit type and what that rounding left out.
+constexpr int kMoeGroup = 4;
+constexpr int kMoeMinShare = 4;       // steps of a worker at least
+
+// Groups that a kernel for M tokens has room for: 1, 2, 4 or 8.
+__host__ __device__ constexpr int moe_groups(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : M <= 16 ? 4 : 8; }
 
 struct MoeArgs {
     const void *x, *gamma, *beta;     // [M, K], [K]
@@ -22,19 +32,24 @@ struct MoeArgs {
     float *weights;
     int *ids;                         // [M, top_k]: the workspace's
     float *w;
-    void *a;                          // [M, Kp] normalized rows, zeros up to Kp
-    void *h;                          // [M top_k, Fp] weight x SiLU(gate) x up, zeros up to a multiple of 8
+    void *a;                          // [M, 2, Kp] normalized rows in two parts, zeros up to a multiple of 8
+    void *h;                          // [M top_k, 2, Fp] weight x SiLU(gate) x up in two parts, likewise
+    // A worker's parts of the units that it shares, the second place for the
+    // unit that begins with it: up [workers][2][groups][32 lanes][gate, up],
+    // down [workers][2][tokens][16 rows], FP32.
+    float *part_up, *part_down;
+    int *count_up, *count_down;       // [workers], zeroed by the router
     int *err;
     int norm, M, K, F, E, top_k, renormalize;
     int Kp, Fp;                       // pitches, multiples of 64
     int cluster;                      // CTAs that share a token's router row
-    int splits;                       // CTAs (a cluster) that share 16 rows of y
     float eps;
 };
 
-// vec_k, vec_f: rows of K (of F) elements start on 16-byte boundaries.
-int launch_moe_router(bool bf16, bool vec_k, const MoeArgs &a, cudaStream_t stream);
-int launch_moe_up(bool bf16, bool vec_k, const MoeArgs &a, cudaStream_t stream);
-int launch_moe_down(bool bf16, bool vec_f, const MoeArgs &a, cudaStream_t stream);
+// vec: rows of K (of F) elements start on 16-byte boundaries (router: x,
+// gamma, beta and Wr).
+int launch_moe_router(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream);
+int launch_moe_up(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream);
+int launch_moe_down(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream);
 
 }  // namespace ngr

@@ -30,7 +30,7 @@ int moe_sizes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
 }
 
 struct MoePlan {
-    size_t ids, w, a, h, total;
+    size_t ids, w, a, h, part_up, part_down, count_up, count_down, total;
     int64_t Kp, Fp;
 };
 
@@ -40,27 +40,22 @@ MoePlan moe_plan(int64_t M, int64_t K, int64_t F, int64_t top_k)
     p.Kp = up_to(K, 64);
     p.Fp = up_to(F, 64);
     size_t off = 256;
-    auto take = [&](size_t bytes) {
+    auto take = [&](int64_t bytes) {
         const size_t at = off;
-        off += (bytes + 255) & ~static_cast<size_t>(255);
+        off += (static_cast<size_t>(bytes) + 255) & ~static_cast<size_t>(255);
         return at;
     };
-    p.ids = take(static_cast<size_t>(M * top_k) * sizeof(int));
-    p.w = take(static_cast<size_t>(M * top_k) * sizeof(float));
-    p.a = take(static_cast<size_t>(M * p.Kp) * 2);
-    p.h = take(static_cast<size_t>(M * top_k * p.Fp) * 2);
+    const int64_t groups = moe_groups(M);
+    p.ids = take(M * top_k * 4);
+    p.w = take(M * top_k * 4);
+    p.a = take(M * 2 * p.Kp * 2);
+    p.h = take(M * top_k * 2 * p.Fp * 2);
+    p.part_up = take(static_cast<int64_t>(kMoeWorkers) * 2 * groups * 32 * 8);
+    p.part_down = take(static_cast<int64_t>(kMoeWorkers) * 2 * groups * kMoeGroup * 16 * 4);
+    p.count_up = take(kMoeWorkers * 4);
+    p.count_down = take(kMoeWorkers * 4);
     p.total = off;
     return p;
-}
-
-// CTAs that share 16 rows of y: as many (1, 2, 4, 8) as fill the SMs twice
-// over, each with eight steps a warp at least where all choose apart.
-int down_splits(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
-{
-    const int64_t tiles = (K + 15) / 16, steps = std::min(E, M * top_k) * ((F + 63) / 64);
-    int s = 1;
-    while (s < 8 && tiles * s < 2 * kMoeSms && steps / (2 * s * (kMoeThreads / 32)) >= 4) s *= 2;
-    return s;
 }
 
 }  // namespace
@@ -104,8 +99,8 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     MoeArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = x;
-    a.gamma = gamma;
-    a.beta = beta;
+    a.gamma = norm != NGR_NORM_NONE ? gamma : nullptr;
+    a.beta = norm == NGR_NORM_LAYER ? beta : nullptr;
     a.Wr = Wr;
     a.Wg = Wg;
     a.Wu = Wu;
@@ -117,6 +112,10 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.w = reinterpret_cast<float *>(ws + p.w);
     a.a = ws + p.a;
     a.h = ws + p.h;
+    a.part_up = reinterpret_cast<float *>(ws + p.part_up);
+    a.part_down = reinterpret_cast<float *>(ws + p.part_down);
+    a.count_up = reinterpret_cast<int *>(ws + p.count_up);
+    a.count_down = reinterpret_cast<int *>(ws + p.count_down);
     a.err = reinterpret_cast<int *>(ws);
     a.norm = norm;
     a.M = static_cast<int>(M);
@@ -129,13 +128,13 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.Fp = static_cast<int>(p.Fp);
     a.eps = eps;
     a.cluster = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;   // an expert a warp, up to 64
-    a.splits = down_splits(M, K, F, E, top_k);
     const bool bf16 = dtype == NGR_BF16;
-    const bool vec_r = K % 8 == 0 && aligned(Wr, 16), vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
+    const bool vec_r = K % 8 == 0 && aligned(Wr, 16) && aligned(x, 16) && aligned(a.gamma, 16) && aligned(a.beta, 16);
+    const bool vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
     const bool vec_f = F % 8 == 0 && aligned(Wd, 16);
     if (trace_mode())
-        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d router=%d CTAs a token, down=%d CTAs for 16 rows%s%s\n",
-                     a.M, a.K, a.F, a.E, a.top_k, norm, a.cluster, a.splits, vec_k ? "" : ", gate and up shifted",
+        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d router=%d CTAs a token%s%s\n",
+                     a.M, a.K, a.F, a.E, a.top_k, norm, a.cluster, vec_k ? "" : ", gate and up shifted",
                      vec_f ? "" : ", down shifted");
     call_begin();
     kernel_begin(stream);
