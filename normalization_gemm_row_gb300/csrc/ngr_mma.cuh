@@ -57,6 +57,12 @@ __device__ __forceinline__ void cp_async16(uint32_t saddr, const void *src, bool
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+// The same for a stream whose next bytes are wanted soon: L2 fetches 256.
+__device__ __forceinline__ void cp_async16_ahead(uint32_t saddr, const void *src, bool there)
+{
+    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "r"(there ? 16 : 0)
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 // Until at most N of the thread's groups are under way.
 template <int N>

@@ -98,9 +98,10 @@ __device__ __forceinline__ float block_sum(float v, float *red)
 }
 
 // ---------------------------------------------------------------- router
-// A cluster for a token.  Its CTAs share the experts, each with the token's
-// normalized row in FP32, a piece at a time; the first CTA gathers the logits
-// and chooses.
+// A cluster of kMoeRouterCtas for a token.  Its CTAs share the experts, each
+// with the token's normalized row in FP32, a piece at a time; the first CTA
+// gathers the logits and chooses.  Bound by the latency of what it does one
+// after the other: row, statistics, logits, choice.
 constexpr int kRouterPiece = 8192;
 constexpr int kRouterPitch = kRouterPiece / 8 + 1;
 
@@ -117,57 +118,96 @@ __global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_co
     // column k of a piece at [k % 8][k / 8]: a lane's 8 columns lie in 8 rows
     __shared__ float row[8 * kRouterPitch];
     __shared__ float logit[kMoeMaxExperts];
-    __shared__ float mine[kMoeMaxExperts / 8];     // of experts i cluster + rank
+    __shared__ float mine[kMoeMaxExperts / kMoeRouterCtas][kWarps];     // parts of the CTA's experts' logits
     __shared__ float red[kWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
-    const int m = static_cast<int>(blockIdx.x) / a.cluster;
+    const int m = static_cast<int>(blockIdx.x) / kMoeRouterCtas;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *x = static_cast<const uint16_t *>(a.x) + static_cast<int64_t>(m) * a.K;
     const uint16_t *gamma = static_cast<const uint16_t *>(a.gamma), *beta = static_cast<const uint16_t *>(a.beta);
     pdl_launch_dependents();
     cluster.barrier_arrive();      // (waited for before the first one's memory is written: it has to have started)
+    // The CTA's experts rank, rank + 8, ...: a warp takes one, or a part of
+    // one's row where they are fewer than the warps.
+    const int experts = rank < a.E ? (a.E - rank + kMoeRouterCtas - 1) / kMoeRouterCtas : 0;
+    const int split = experts >= 8 ? 1 : experts >= 4 ? 2 : experts >= 2 ? 4 : 8;
+    // What is read last is on its way to L2 first.
+    for (int i = warp / split; i < experts; i += kWarps / split) {
+        const char *wr = static_cast<const char *>(a.Wr) + (static_cast<int64_t>(i) * kMoeRouterCtas + rank) * a.K * 2;
+        for (int at = (warp % split * 32 + lane) * 128; at < a.K * 2; at += split * 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(wr + at));
+    }
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-    for (int i = static_cast<int>(blockIdx.x) * kMoeThreads + threadIdx.x; i < kMoeWorkers;
+    for (int i = static_cast<int>(blockIdx.x) * kMoeThreads + threadIdx.x; i < kMoeCounters;
          i += static_cast<int>(gridDim.x) * kMoeThreads)
-        a.count_up[i] = a.count_down[i] = 0;
+        a.counters[i] = 0;
 
-    float mean = 0.0f, scale = 1.0f;
-    if (a.norm != kNormNone) {
+    uint4 held[kRouterPiece / 8 / kMoeThreads];      // the row, if it is no longer than a piece
+    uint4 held_gamma[kRouterPiece / 8 / kMoeThreads];
+    const bool short_row = a.K <= kRouterPiece;
+    if (short_row && a.norm != kNormNone) {
+#pragma unroll
+        for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i)
+            held_gamma[i] = row8<VEC>(gamma, (i * kMoeThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
+    }
+    if (short_row) {
+#pragma unroll
+        for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i)
+            held[i] = row8<VEC>(x, (i * kMoeThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
+    }
+    // f(values, column) over the row, 8 columns a thread at a time
+    auto over_row = [&](auto f) {
         float v[8];
-        if (a.norm == kNormLayer) {
-            float s = 0.0f;
+        if (short_row) {
+#pragma unroll
+            for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i) {
+                const int k = (i * kMoeThreads + static_cast<int>(threadIdx.x)) * 8;
+                if (k >= a.K) break;
+                unpack8<BF16>(held[i], v);
+                f(v, k);
+            }
+        } else {
 #pragma unroll 4
             for (int k = threadIdx.x * 8; k < a.K; k += kMoeThreads * 8) {
                 unpack8<BF16>(row8<VEC>(x, k, a.K), v);
+                f(v, k);
+            }
+        }
+    };
+    float mean = 0.0f, scale = 1.0f;
+    if (a.norm != kNormNone) {
+        if (a.norm == kNormLayer) {
+            float s = 0.0f;
+            over_row([&](const float (&v)[8], int) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s += v[j];
-            }
+            });
             mean = block_sum(s, red) / a.K;
         }
         float s = 0.0f;
-#pragma unroll 4
-        for (int k = threadIdx.x * 8; k < a.K; k += kMoeThreads * 8) {
-            unpack8<BF16>(row8<VEC>(x, k, a.K), v);
+        over_row([&](const float (&v)[8], int k) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float c = k + j < a.K ? v[j] - mean : 0.0f;
                 s = fmaf(c, c, s);
             }
-        }
+        });
         scale = 1.0f / sqrtf(block_sum(s, red) / a.K + a.eps);
     }
-    for (int i = threadIdx.x; i < kMoeMaxExperts / 8; i += kMoeThreads) mine[i] = 0.0f;
+    for (int i = threadIdx.x; i < kMoeMaxExperts / kMoeRouterCtas * kWarps; i += kMoeThreads) mine[i / kWarps][i % kWarps] = 0.0f;
     for (int k0 = 0; k0 < a.K; k0 += kRouterPiece) {
         const int n = min(kRouterPiece, a.K - k0);
         __syncthreads();
-        for (int c = threadIdx.x; c * 8 < n; c += kMoeThreads) {
-            const int k = k0 + c * 8;
+#pragma unroll
+        for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i) {
+            const int c = i * kMoeThreads + static_cast<int>(threadIdx.x), k = k0 + c * 8;
+            if (c * 8 >= n) break;
             float v[8];
-            unpack8<BF16>(row8<VEC>(x, k, a.K), v);
+            unpack8<BF16>(short_row ? held[i] : row8<VEC>(x, k, a.K), v);
             if (a.norm != kNormNone) {
                 float g[8];
-                unpack8<BF16>(row8<VEC>(gamma, k, a.K), g);
+                unpack8<BF16>(short_row ? held_gamma[i] : row8<VEC>(gamma, k, a.K), g);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = k + j < a.K ? (v[j] - mean) * scale * g[j] : 0.0f;
                 if (a.norm == kNormLayer) {
@@ -187,12 +227,11 @@ __global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_co
             }
         }
         __syncthreads();
-        for (int i = warp; i * a.cluster + rank < a.E; i += kWarps) {
-            const int e = i * a.cluster + rank;
+        for (int i = warp / split; i < experts; i += kWarps / split) {
             float z = 0.0f;
-            const uint16_t *wr = static_cast<const uint16_t *>(a.Wr) + static_cast<int64_t>(e) * a.K;
+            const uint16_t *wr = static_cast<const uint16_t *>(a.Wr) + (static_cast<int64_t>(i) * kMoeRouterCtas + rank) * a.K;
 #pragma unroll 8
-            for (int c = lane; c * 8 < n; c += 32) {
+            for (int c = warp % split * 32 + lane; c * 8 < n; c += split * 32) {
                 float w[8];
                 unpack8<BF16>(row8<VEC>(wr, k0 + c * 8, a.K), w);
 #pragma unroll
@@ -200,13 +239,18 @@ __global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_co
             }
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            if (lane == 0) mine[i] += z;
+            if (lane == 0) mine[i][warp % split] += z;
         }
     }
     cluster.barrier_wait();
     float *logits = cluster.map_shared_rank(logit, 0);
     __syncthreads();
-    for (int i = threadIdx.x; i * a.cluster + rank < a.E; i += kMoeThreads) logits[i * a.cluster + rank] = mine[i];
+    for (int i = threadIdx.x; i < experts; i += kMoeThreads) {
+        float z = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) z += mine[i][w];
+        logits[i * kMoeRouterCtas + rank] = z;
+    }
     cluster.sync();
     if (rank != 0 || warp != 0) return;
 
@@ -256,72 +300,125 @@ __global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_co
 
 // -------------------------------------------------------------- products
 // The experts that somebody chose, in order, for every CTA in its shared
-// memory.  The rows of h stand by expert and then by token.
+// memory; one that more than kMoeEntry tokens chose stands there once for
+// each kMoeEntry of them, and its weights' second reader finds them in L2 (it
+// runs at the same time).  So every step costs the same, whatever the choice:
+// with all of an expert's tokens in one entry the runs with the busiest
+// experts kept the others waiting (down at 32 tokens, 32 experts of 4096 x
+// 1536: a third of the warps' time).  The rows of h stand by expert and then
+// by token.
 struct Chosen {
-    uint16_t expert[kMoeMaxExperts], base[kMoeMaxExperts + 2];
+    uint16_t expert[kMoeMaxEntries], base[kMoeMaxEntries];
+    uint8_t tokens[kMoeMaxEntries];
     uint8_t token[kMoeMaxTokens * kMoeMaxTopK];        // of a row of h
     int count;
 };
-// `tokens`: room for kMoeMaxExperts words.
-__device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, uint32_t *tokens)
+struct ChosenScratch {
+    uint32_t tokens[kMoeMaxExperts];                   // bits
+    uint16_t base[kMoeMaxExperts];                     // by expert
+};
+// `p`, if not null, takes the weight of each row of h.
+template <int THREADS>
+__device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenScratch &x, float *p)
 {
     const int lane = threadIdx.x & 31, all = a.M * a.top_k;
-    for (int e = threadIdx.x; e < a.E; e += kMoeThreads) tokens[e] = 0u;
+    for (int e = threadIdx.x; e < a.E; e += THREADS) x.tokens[e] = 0u;
     __syncthreads();
-    for (int i = threadIdx.x; i < all; i += kMoeThreads) atomicOr(&tokens[a.ids[i]], 1u << (i / a.top_k));
+    for (int i = threadIdx.x; i < all; i += THREADS) atomicOr(&x.tokens[__ldcg(a.ids + i)], 1u << (i / a.top_k));
     __syncthreads();
     if (threadIdx.x < 32) {
         int n = 0, rows = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const uint32_t t = e0 + lane < a.E ? tokens[e0 + lane] : 0u;
-            const uint32_t some = __ballot_sync(0xffffffffu, t != 0u);
-            if (some == 0u) continue;
-            const int mine = __popc(t);
-            int incl = mine;
+            const uint32_t t = e0 + lane < a.E ? x.tokens[e0 + lane] : 0u;
+            if (__ballot_sync(0xffffffffu, t != 0u) == 0u) continue;
+            const int mine = __popc(t), entries = (mine + kMoeEntry - 1) / kMoeEntry;
+            int incl = mine | entries << 16;      // both sums at once
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, incl, o);
                 if (lane >= o) incl += v;
             }
             if (t != 0u) {
-                const int at = n + __popc(some & ((1u << lane) - 1u));
-                int r = rows + incl - mine;
-                c.expert[at] = static_cast<uint16_t>(e0 + lane);
-                c.base[at] = static_cast<uint16_t>(r);
-                for (uint32_t left = t; left; left &= left - 1u) c.token[r++] = static_cast<uint8_t>(__ffs(left) - 1);
+                int at = n + (incl >> 16) - entries, r = rows + (incl & 0xFFFF) - mine, left = mine;
+                x.base[e0 + lane] = static_cast<uint16_t>(r);
+                for (int i = 0; i < entries; ++i, ++at, left -= kMoeEntry) {
+                    c.expert[at] = static_cast<uint16_t>(e0 + lane);
+                    c.base[at] = static_cast<uint16_t>(r + i * kMoeEntry);
+                    c.tokens[at] = static_cast<uint8_t>(min(left, kMoeEntry));
+                }
+                for (uint32_t bits = t; bits; bits &= bits - 1u) c.token[r++] = static_cast<uint8_t>(__ffs(bits) - 1);
             }
-            n += __popc(some);
-            rows += __shfl_sync(0xffffffffu, incl, 31);
+            const int sums = __shfl_sync(0xffffffffu, incl, 31);
+            n += sums >> 16;
+            rows += sums & 0xFFFF;
         }
-        if (lane == 0) {
-            c.count = n;
-            c.base[n] = static_cast<uint16_t>(all);
+        if (lane == 0) c.count = n;
+    }
+    __syncthreads();
+    if (p) {
+        for (int i = threadIdx.x; i < all; i += THREADS) {
+            const int e = __ldcg(a.ids + i), m = i / a.top_k;
+            p[x.base[e] + __popc(x.tokens[e] & ((1u << m) - 1u))] = __ldcg(a.w + i);
         }
     }
     __syncthreads();
 }
 
-// A stage of a worker's ring: a step's 16 weight rows of 128 bytes, or of the
-// nine 16-byte words that they lie in where rows are off the boundary, and
-// the first group's 8 token rows of 128 bytes.
-template <bool VEC>
-struct Stage {
-    static constexpr int kPitch = VEC ? 128 : 144;
-    static constexpr int kTokens = 16 * kPitch;
-    static constexpr int kBytes = kTokens + 8 * 128;
+// How one kernel is laid out, with room for NT groups of tokens in an entry:
+// 1 if the call has no more tokens, else 2.
+template <bool DOWN, bool VEC, int NT>
+struct Layout {
+    static constexpr int kStages = NT == 1 ? 4 : 3;
+    // A stage: a step's 16 weight rows of 128 bytes, or of the nine 16-byte
+    // words that they lie in where rows are off the boundary, and 8 token
+    // rows of 128 bytes a group.
+    static constexpr int kGroups = NT;
+    static constexpr int kPitch = VEC ? 128 : 144, kCopies = VEC ? 4 : 5;
+    static constexpr int kTokens = 16 * kPitch, kStage = kTokens + NT * 1024;
+    // DOWN: the tokens' sums of the 16 rows under way, [token][17]
+    static constexpr int kMost = NT == 1 ? kMoeGroup : kMoeMaxTokens;
+    static constexpr int kSums = DOWN ? kMost * 17 * 4 : 0;
+    static constexpr int kWarp = kStages * kStage + kSums;
+    // Two CTAs have to fit into an SM's shared memory.
+    static constexpr int kWarps = DOWN && NT == 2 ? 7 : 8, kThreads = 32 * kWarps, kWorkers = kMoeCtas * kWarps;
+    static constexpr int kWeights = DOWN ? 0 : kMost * kMoeMaxTopK * 4;
+    static constexpr int kBytes = kWarps * kWarp + kWeights;
+    static_assert(kWarps * kWarp >= static_cast<int>(sizeof(ChosenScratch)), "the rings hold it first");
+    static_assert(2 * (kBytes + static_cast<int>(sizeof(Chosen)) + 1024) <= 228 * 1024, "two CTAs an SM");
+    static_assert(kWorkers <= kMoeWorkers, "places of the parts");
 };
 
-// Where a segment (the steps over one expert's 16 rows) has its operands.
-// Rows 0 to 7 start at r0, rows 8 to 15 at r1, `pitch` elements apart, n0 and
-// n1 of each are there; the tokens' rows are those of `tokens` rows from
-// `base` on, of h, or of a through the list.
+// A segment: the steps over one expert's 16 rows.  DOWN: by 16 rows of Wd,
+// then by expert; else by expert, then by 8 rows of Wg and of Wu.
 struct Segment {
-    const uint16_t *r0, *r1;
-    int n0, n1;
-    int base, tokens, expert;
+    int tile, i;
+    int base, tokens;      // its rows of h
 };
+template <bool DOWN>
+__device__ __forceinline__ void tokens_of(const Chosen &c, Segment &s)
+{
+    s.base = c.base[s.i];
+    s.tokens = c.tokens[s.i];
+}
+// The next one: false behind the last.
+template <bool DOWN>
+__device__ __forceinline__ bool next(const Chosen &c, Segment &s, int tiles)
+{
+    if (DOWN) {
+        if (++s.i == c.count) {
+            s.i = 0;
+            if (++s.tile == tiles) return false;
+        }
+    } else if (++s.tile == tiles) {
+        s.tile = 0;
+        if (++s.i == c.count) return false;
+    }
+    tokens_of<DOWN>(c, s);
+    return true;
+}
 
-// The row (of a or h) of a token's part: column `col` of group j.
+// The row (of a or h) of a token's part: column `col` of group j; null if
+// there is none.
 template <bool DOWN>
 __device__ __forceinline__ const uint16_t *token_row(const MoeArgs &a, const Chosen &c, const Segment &s, int j, int col)
 {
@@ -331,68 +428,94 @@ __device__ __forceinline__ const uint16_t *token_row(const MoeArgs &a, const Cho
     return static_cast<const uint16_t *>(a.a) + (static_cast<int64_t>(c.token[s.base + r]) * 2 + (col & 1)) * a.Kp;
 }
 
+// A weight's 16 rows of the segment: the q-th of the first or second 8.
 template <bool DOWN>
-__device__ __forceinline__ Segment segment(const MoeArgs &a, const Chosen &c, int64_t index)
+__device__ __forceinline__ const uint16_t *weight_row(const MoeArgs &a, const Chosen &c, const Segment &s, int half, int q)
 {
-    Segment s;
-    if (DOWN) {      // by 16 rows of Wd, then by expert
-        const int tile = static_cast<int>(index / c.count), i = static_cast<int>(index - static_cast<int64_t>(tile) * c.count);
-        s.expert = i;
-        s.r0 = static_cast<const uint16_t *>(a.Wd) + (static_cast<int64_t>(c.expert[i]) * a.K + tile * 16) * a.F;
-        s.r1 = s.r0 + static_cast<int64_t>(8) * a.F;
-        s.n0 = a.K - tile * 16;
-        s.n1 = s.n0 - 8;
-    } else {         // by expert, then by 8 rows of Wg and of Wu
-        const int tiles = (a.F + 7) / 8;
-        const int i = static_cast<int>(index / tiles), tile = static_cast<int>(index - static_cast<int64_t>(i) * tiles);
-        const int64_t at = (static_cast<int64_t>(c.expert[i]) * a.F + tile * 8) * a.K;
-        s.expert = i;
-        s.r0 = static_cast<const uint16_t *>(a.Wg) + at;
-        s.r1 = static_cast<const uint16_t *>(a.Wu) + at;
-        s.n0 = s.n1 = a.F - tile * 8;
-    }
-    s.base = c.base[s.expert];
-    s.tokens = c.base[s.expert + 1] - s.base;
-    return s;
+    const int64_t e = c.expert[s.i];
+    if (DOWN) return static_cast<const uint16_t *>(a.Wd) + (e * a.K + s.tile * 16 + half * 8 + q) * a.F;
+    return static_cast<const uint16_t *>(half ? a.Wu : a.Wg) + (e * a.F + s.tile * 8 + q) * a.K;
+}
+template <bool DOWN>
+__device__ __forceinline__ bool weight_there(const MoeArgs &a, const Segment &s, int half, int q)
+{
+    return DOWN ? s.tile * 16 + half * 8 + q < a.K : s.tile * 8 + q < a.F;
 }
 
-// The copies of one step, columns [k, k + 64) of n.
-template <bool DOWN, bool VEC>
-__device__ __forceinline__ void fetch(const MoeArgs &a, const Chosen &c, const Segment &s, int k, uint32_t stage, int lane)
+// A lane's copies of a segment's steps: 16 bytes from `from`, 128 further a
+// step, for the first `steps` of them (then zeros).
+template <typename L>
+struct Copies {
+    const uint16_t *from[L::kCopies], *token[2 * L::kGroups];
+    int steps[L::kCopies], token_steps[2 * L::kGroups];
+
+    template <bool VEC>
+    __device__ __forceinline__ void weights(int step, uint32_t stage, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < L::kCopies; ++i) {
+            if (VEC) {
+                const int r = i * 4 + (lane >> 3);
+                cp_async16_ahead(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4), from[i], step < steps[i]);
+            } else if (i * 32 + lane < 144) {
+                cp_async16_ahead(stage + (i * 32 + lane) * 16, from[i], step < steps[i]);
+            }
+        }
+        skip_weights();
+    }
+    __device__ __forceinline__ void tokens(int step, uint32_t stage, int lane)
+    {
+#pragma unroll
+        for (int i = 0; i < 2 * L::kGroups; ++i) {
+            const int col = (i & 1) * 4 + (lane >> 3);
+            cp_async16(stage + L::kTokens + (i >> 1) * 1024 + col * 128 + (((lane & 7) ^ col) << 4), token[i],
+                       step < token_steps[i]);
+            token[i] += 64;
+        }
+    }
+    __device__ __forceinline__ void skip_weights()
+    {
+#pragma unroll
+        for (int i = 0; i < L::kCopies; ++i) from[i] += 64;
+    }
+    __device__ __forceinline__ void skip(int steps)
+    {
+#pragma unroll
+        for (int i = 0; i < L::kCopies; ++i) from[i] += steps * 64;
+#pragma unroll
+        for (int i = 0; i < 2 * L::kGroups; ++i) token[i] += steps * 64;
+    }
+};
+template <bool DOWN, bool VEC, typename L>
+__device__ __forceinline__ void plan_copies(const MoeArgs &a, const Chosen &c, const Segment &s, Copies<L> &p, int lane)
 {
     const int n = DOWN ? a.F : a.K;
-    if (VEC) {
-        const int col = lane & 7, at = k + col * 8;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = i * 4 + (lane >> 3), q = r & 7;
-            const uint16_t *row = r < 8 ? s.r0 : s.r1;
-            const bool there = at < n && q < (r < 8 ? s.n0 : s.n1);
-            cp_async16(stage + r * 128 + ((col ^ q) << 4), there ? row + static_cast<int64_t>(q) * n + at : row, there);
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            const int w = i * 32 + lane, r = w / 9, col = w - r * 9, q = r & 7;
-            if (r >= 16) continue;
-            // the aligned word `col` after the one that column k lies in:
-            // there if it holds any of the columns up to n
-            const uint16_t *p = (r < 8 ? s.r0 : s.r1) + static_cast<int64_t>(q) * n + k;
-            const int d = static_cast<int>((reinterpret_cast<uintptr_t>(p) >> 1) & 7u);
-            const bool there = k + col * 8 - d < n && (col < 8 || d > 0) && q < (r < 8 ? s.n0 : s.n1);
-            cp_async16(stage + r * 144 + col * 16, there ? static_cast<const void *>(p - d + col * 8) : a.h, there);
+    for (int i = 0; i < L::kCopies; ++i) {
+        if (VEC) {
+            const int r = i * 4 + (lane >> 3), col = (lane & 7) * 8;
+            const bool there = weight_there<DOWN>(a, s, r >> 3, r & 7);
+            p.from[i] = weight_row<DOWN>(a, c, s, there ? r >> 3 : 0, there ? r & 7 : 0) + col;
+            p.steps[i] = there ? (n - col + 63) >> 6 : 0;
+        } else {
+            // word `col` after the aligned one that the row's start lies in:
+            // there as long as it holds any column below n
+            const int w = i * 32 + lane, r = w / 9, col = w - r * 9;
+            const bool there = r < 16 && weight_there<DOWN>(a, s, r >> 3, r & 7);
+            const uint16_t *row = weight_row<DOWN>(a, c, s, there ? r >> 3 : 0, there ? r & 7 : 0);
+            const int d = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 1) & 7u);
+            p.from[i] = row - d + col * 8;
+            p.steps[i] = there && (col < 8 || d > 0) ? (n - col * 8 + d + 63) >> 6 : 0;
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int col = i * 4 + (lane >> 3), at = k + (lane & 7) * 8;
-        const uint16_t *row = token_row<DOWN>(a, c, s, 0, col);
-        const bool there = row && at < n;
-        cp_async16(stage + Stage<VEC>::kTokens + col * 128 + (((lane & 7) ^ col) << 4),
-                   there ? static_cast<const void *>(row + at) : a.h, there);
+    for (int i = 0; i < 2 * L::kGroups; ++i) {
+        const uint16_t *row = token_row<DOWN>(a, c, s, i >> 1, (i & 1) * 4 + (lane >> 3));
+        const int col = (lane & 7) * 8;
+        p.token[i] = (row ? row : static_cast<const uint16_t *>(a.h)) + col;
+        p.token_steps[i] = row ? (n - col + 63) >> 6 : 0;
     }
 }
-
 // A 32-bit operand word of a row off the 16-byte boundary: columns e, e + 1 of
 // the stage's row whose first word starts `d` elements before column 0.
 __device__ __forceinline__ uint32_t pair_at(uint32_t row, int d, int e)
@@ -406,23 +529,20 @@ __device__ __forceinline__ uint32_t pair_at(uint32_t row, int d, int e)
     return __funnelshift_r(lo, hi, 16);
 }
 
-// The products of one step.
+// The products of one step, `left` columns from the row's end.  d0, d1: how
+// far rows g and g + 8 start from the boundary.
 template <bool BF16, bool DOWN, bool VEC, int NT>
-__device__ __forceinline__ void take(float (&acc)[NT][4], const MoeArgs &a, const Chosen &c, const Segment &s, int k,
-                                     uint32_t stage, int lane)
+__device__ __forceinline__ void take(float (&acc)[NT][4], int tokens, int left, int d0, int d1, uint32_t stage, int lane)
 {
-    const int g = lane >> 2, t = lane & 3, n = DOWN ? a.F : a.K;
+    using L = Layout<DOWN, VEC, NT>;
+    const int g = lane >> 2, t = lane & 3;
     uint32_t w[4][4];      // the weights' operands of four contractions of 16
     if (VEC) {
         const int r = ((lane >> 3) & 1) * 8 + (lane & 7), half = lane >> 4;
 #pragma unroll
         for (int i = 0; i < 4; ++i) ldmatrix4(w[i], stage + r * 128 + (((2 * i + half) ^ (r & 7)) << 4));
     } else {
-        const uint16_t *p0 = s.r0 + static_cast<int64_t>(g) * n + k, *p1 = s.r1 + static_cast<int64_t>(g) * n + k;
-        const int d0 = static_cast<int>((reinterpret_cast<uintptr_t>(p0) >> 1) & 7u);
-        const int d1 = static_cast<int>((reinterpret_cast<uintptr_t>(p1) >> 1) & 7u);
         const uint32_t row0 = stage + g * 144, row1 = stage + (g + 8) * 144;
-        const int left = n - k;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -434,32 +554,18 @@ __device__ __forceinline__ void take(float (&acc)[NT][4], const MoeArgs &a, cons
                 w[i][2 * h + 1] = pair_at(row1, d1, e) & keep;
             }
     }
-    {
+#pragma unroll
+    for (int j = 0; j < L::kGroups; ++j) {
+        if (j > 0 && j * kMoeGroup >= tokens) break;
         const int col = lane & 7, quarter = lane >> 3;
+        const uint32_t row = stage + L::kTokens + j * 1024 + col * 128;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             uint32_t b[4];
-            ldmatrix4(b, stage + Stage<VEC>::kTokens + col * 128 + (((4 * i + quarter) ^ col) << 4));
-            mma_16816<BF16>(acc[0], w[2 * i][0], w[2 * i][1], w[2 * i][2], w[2 * i][3], b[0], b[1]);
-            mma_16816<BF16>(acc[0], w[2 * i + 1][0], w[2 * i + 1][1], w[2 * i + 1][2], w[2 * i + 1][3], b[2], b[3]);
+            ldmatrix4(b, row + (((4 * i + quarter) ^ col) << 4));
+            mma_16816<BF16>(acc[j], w[2 * i][0], w[2 * i][1], w[2 * i][2], w[2 * i][3], b[0], b[1]);
+            mma_16816<BF16>(acc[j], w[2 * i + 1][0], w[2 * i + 1][1], w[2 * i + 1][2], w[2 * i + 1][3], b[2], b[3]);
         }
-    }
-    // Experts with more tokens: their rows straight from memory, which holds
-    // them near (they are read for every 16 rows of the weights).
-#pragma unroll
-    for (int j = 1; j < NT; ++j) {
-        if (j * kMoeGroup >= s.tokens) break;
-        const uint16_t *row = token_row<DOWN>(a, c, s, j, g);
-        uint32_t b[4][2];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int at = k + i * 16 + h * 8;
-                b[i][h] = row && at < n ? __ldg(reinterpret_cast<const uint32_t *>(row + at + 2 * t)) : 0u;
-            }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mma_16816<BF16>(acc[j], w[i][0], w[i][1], w[i][2], w[i][3], b[i][0], b[i][1]);
     }
 }
 
@@ -483,51 +589,77 @@ __device__ __forceinline__ bool counted_last(int *count, const Sharers &w, int l
     return last;
 }
 
-constexpr int depth_of(int NT) { return NT == 8 ? 3 : 4; }
-template <bool DOWN, bool VEC, int NT>
-constexpr int smem_of()
-{
-    return kWarps * (depth_of(NT) * Stage<VEC>::kBytes + (DOWN ? NT * kMoeGroup * 17 * 4 : 0));
-}
-
 template <bool BF16, bool DOWN, bool VEC, int NT>
-__global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(const __grid_constant__ MoeArgs a)
+__global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(const __grid_constant__ MoeArgs a)
 {
-    constexpr int S = depth_of(NT);
+    using L = Layout<DOWN, VEC, NT>;
+    constexpr int S = L::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ Chosen c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    if (!DOWN) pdl_launch_dependents();
-    pdl_wait();
-    find_chosen(a, c, reinterpret_cast<uint32_t *>(smem));
+    float *weights = DOWN ? nullptr : reinterpret_cast<float *>(smem + L::kWarps * L::kWarp);
+    // Up waits for the router and lets down start only then, so that down may
+    // read the choice before it waits for up.
+    if (!DOWN) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+    find_chosen<L::kThreads>(a, c, *reinterpret_cast<ChosenScratch *>(smem), weights);
 
     const int n = DOWN ? a.F : a.K;
-    const int length = (n + 63) / 64;      // steps of a segment
-    const int64_t segments = static_cast<int64_t>(c.count) * (DOWN ? (a.K + 15) / 16 : (a.F + 7) / 8);
-    const int64_t total = segments * length;
-    int64_t share = (total + kMoeWorkers - 1) / kMoeWorkers;
-    if (share < kMoeMinShare) share = kMoeMinShare;
+    const int length = (n + 63) / 64, tiles = DOWN ? (a.K + 15) / 16 : (a.F + 7) / 8;
+    const int64_t total = static_cast<int64_t>(c.count) * tiles * length;
+    const int64_t share = max(static_cast<int64_t>(kMoeMinShare), (total + L::kWorkers - 1) / L::kWorkers);
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     const int64_t first = worker * share;
     if (first >= total) return;
     const int count = static_cast<int>(min(share, total - first));
 
-    const uint32_t ring = smem_u32(smem) + warp * (S * Stage<VEC>::kBytes);
-    // DOWN: the tokens' sums of the 16 rows under way, [token][17]
-    float *sums = reinterpret_cast<float *>(smem + kWarps * S * Stage<VEC>::kBytes) + warp * (NT * kMoeGroup * 17);
-    int64_t index = first / length, ahead = index;
-    int step = static_cast<int>(first - index * length), ahead_step = step;
-    Segment s = segment<DOWN>(a, c, index), f = s;
-    auto issue = [&](int stage) {
-        fetch<DOWN, VEC>(a, c, f, ahead_step * 64, ring + stage * Stage<VEC>::kBytes, lane);
-        if (++ahead_step == length) {
-            ahead_step = 0;
-            if (++ahead < segments) f = segment<DOWN>(a, c, ahead);
+    const uint32_t ring = smem_u32(smem) + warp * L::kWarp;
+    float *sums = reinterpret_cast<float *>(smem + warp * L::kWarp + S * L::kStage);
+    int *counts = a.counters + (DOWN ? kMoeWorkers : 0);
+    Segment s;
+    const int64_t index = first / length;
+    int step = static_cast<int>(first - index * length), ahead = step;
+    s.i = static_cast<int>(DOWN ? index % c.count : index / tiles);
+    s.tile = static_cast<int>(DOWN ? index / c.count : index % tiles);
+    tokens_of<DOWN>(c, s);
+    Segment f = s;
+    Copies<L> copies;
+    plan_copies<DOWN, VEC, L>(a, c, f, copies, lane);
+    copies.skip(step);
+    auto advance = [&] {
+        if (++ahead == length) {
+            ahead = 0;
+            if (next<DOWN>(c, f, tiles)) plan_copies<DOWN, VEC, L>(a, c, f, copies, lane);
         }
     };
+    if (DOWN) {
+        // The first stages' weights are on their way while up ends: the
+        // choice is known since up began.
+        const Segment f0 = f;
+        const Copies<L> copies0 = copies;
+        const int ahead0 = ahead;
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            if (i < count) {
+                copies.template weights<VEC>(ahead, ring + i * L::kStage, lane);
+                advance();
+            }
+        }
+        pdl_wait();
+        f = f0;
+        copies = copies0;
+        ahead = ahead0;
+    }
 #pragma unroll
     for (int i = 0; i < S; ++i) {
-        if (i < count) issue(i);
+        if (i < count) {
+            if (DOWN) copies.skip_weights();
+            else copies.template weights<VEC>(ahead, ring + i * L::kStage, lane);
+            copies.tokens(ahead, ring + i * L::kStage, lane);
+            advance();
+        }
         cp_async_commit();
     }
     float acc[NT][4];
@@ -536,31 +668,44 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(const __grid_consta
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[j][r] = 0.0f;
     if (DOWN) {
-        for (int i = lane; i < NT * kMoeGroup * 17; i += 32) sums[i] = 0.0f;
+        for (int i = lane; i < L::kMost * 17; i += 32) sums[i] = 0.0f;
         __syncwarp();
     }
-    // steps of the unit (a segment, or DOWN the segments of 16 rows)
+    // the unit: a segment, or DOWN the segments of 16 rows
     const int64_t unit = DOWN ? static_cast<int64_t>(c.count) * length : length;
-    int stage = 0;
+    int64_t begin = DOWN ? s.tile * unit : index * length;
+    int d0 = 0, d1 = 0, stage = 0;
+    bool fresh = true;
     for (int i = 0; i < count; ++i) {
+        if (!VEC && fresh) {
+            d0 = static_cast<int>((reinterpret_cast<uintptr_t>(weight_row<DOWN>(a, c, s, 0, g)) >> 1) & 7u);
+            d1 = static_cast<int>((reinterpret_cast<uintptr_t>(weight_row<DOWN>(a, c, s, 1, g)) >> 1) & 7u);
+            fresh = false;
+        }
         cp_async_wait<S - 1>();
         __syncwarp();
-        take<BF16, DOWN, VEC, NT>(acc, a, c, s, step * 64, ring + stage * Stage<VEC>::kBytes, lane);
+        take<BF16, DOWN, VEC, NT>(acc, s.tokens, n - step * 64, d0, d1, ring + stage * L::kStage, lane);
         __syncwarp();
-        if (i + S < count) issue(stage);
+        if (i + S < count) {
+            copies.template weights<VEC>(ahead, ring + stage * L::kStage, lane);
+            copies.tokens(ahead, ring + stage * L::kStage, lane);
+            advance();
+        }
         cp_async_commit();
         stage = stage + 1 == S ? 0 : stage + 1;
         const bool ends = ++step == length, done = i + 1 == count;
         if (!ends && !done) continue;
 
         // the segment's end, or the run's
-        const int64_t at = first + i + 1;                  // steps so far in the whole row
-        const int64_t begin = (at - 1) / unit * unit, end = begin + unit;
-        const bool whole = begin >= first && end <= at, close = at == end || done;
-        const Sharers w = sharers(begin, end, share);
-        const int64_t slot = static_cast<int64_t>(worker) * 2 + (worker == w.first ? 1 : 0);
+        const int64_t end = begin + unit, at = first + i + 1;
+        const bool close = at == end || done, whole = begin >= first && end <= at;
+        Sharers w = {0, 0};
+        int64_t slot = 0;
+        if (close && !whole) {
+            w = sharers(begin, end, share);
+            slot = static_cast<int64_t>(worker) * 2 + (worker == w.first ? 1 : 0);
+        }
         if (!DOWN) {
-            const int f0 = static_cast<int>(index - index / ((a.F + 7) / 8) * ((a.F + 7) / 8)) * 8;
             float2 v[NT];      // gate and up of row g for token t of each group
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
@@ -570,16 +715,17 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(const __grid_consta
             }
             bool finish = whole;
             if (!whole) {
-                float2 *part = reinterpret_cast<float2 *>(a.part_up) + slot * (NT * 32) + lane;
+                float2 *part = reinterpret_cast<float2 *>(a.parts) + slot * (NT * 32) + lane;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     if (j * kMoeGroup < s.tokens) part[j * 32] = v[j];
-                finish = counted_last(a.count_up, w, lane);
+                finish = counted_last(counts, w, lane);
                 if (finish) {
 #pragma unroll
                     for (int j = 0; j < NT; ++j) v[j] = make_float2(0.0f, 0.0f);
+#pragma unroll 4
                     for (int p = w.first; p <= w.last; ++p) {
-                        const float2 *from = reinterpret_cast<const float2 *>(a.part_up) +
+                        const float2 *from = reinterpret_cast<const float2 *>(a.parts) +
                                              (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (NT * 32) + lane;
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
@@ -596,15 +742,13 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(const __grid_consta
                 for (int j = 0; j < NT; ++j) {
                     const int r = j * kMoeGroup + t;
                     if (r >= s.tokens) continue;
-                    const int token = c.token[s.base + r];
-                    float p = 0.0f;
-                    for (int q = 0; q < a.top_k; ++q)
-                        if (a.ids[token * a.top_k + q] == c.expert[s.expert]) p = a.w[token * a.top_k + q];
                     // The token's weight goes into h, so that the last
                     // product is a plain sum over the experts.
-                    const float h = g < s.n0 ? p * (v[j].x / (1.0f + expf(-v[j].x)) * v[j].y) : 0.0f;
+                    const float h = weight_there<DOWN>(a, s, 0, g)
+                                        ? weights[s.base + r] * (v[j].x / (1.0f + expf(-v[j].x)) * v[j].y)
+                                        : 0.0f;
                     const uint2 parts = two_parts<BF16>(h, 0.0f);
-                    uint16_t *out = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(s.base + r) * 2 * a.Fp + f0 + g;
+                    uint16_t *out = static_cast<uint16_t *>(a.h) + static_cast<int64_t>(s.base + r) * 2 * a.Fp + s.tile * 8 + g;
                     out[0] = static_cast<uint16_t>(parts.x);
                     out[a.Fp] = static_cast<uint16_t>(parts.y);
                 }
@@ -623,18 +767,18 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(const __grid_consta
             }
             __syncwarp();
             if (close) {
-                const int row0 = static_cast<int>(begin / unit) * 16, values = a.M * 16;
+                const int row0 = s.tile * 16, values = a.M * 16;
                 bool finish = whole;
                 if (!whole) {
-                    float *part = a.part_down + slot * (NT * kMoeGroup * 16);
+                    float *part = a.parts + slot * (L::kMost * 16);
                     for (int v = lane; v < values; v += 32) part[v] = sums[(v >> 4) * 17 + (v & 15)];
-                    finish = counted_last(a.count_down, w, lane);
+                    finish = counted_last(counts, w, lane);
                     if (finish) {
                         for (int v = lane; v < values; v += 32) {
                             float x = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
                             for (int p = w.first; p <= w.last; ++p)
-                                x += __ldcg(a.part_down + (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (NT * kMoeGroup * 16) + v);
+                                x += __ldcg(a.parts + (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (L::kMost * 16) + v);
                             sums[(v >> 4) * 17 + (v & 15)] = x;
                         }
                     }
@@ -645,24 +789,26 @@ __global__ void __launch_bounds__(kMoeThreads, 2) moe_kernel(const __grid_consta
                             static_cast<uint16_t *>(a.y)[static_cast<int64_t>(v >> 4) * a.K + row0 + (v & 15)] =
                                 static_cast<uint16_t>(pack16<BF16>(sums[(v >> 4) * 17 + (v & 15)], 0.0f));
                 __syncwarp();
-                for (int v = lane; v < NT * kMoeGroup * 17; v += 32) sums[v] = 0.0f;
+                for (int v = lane; v < L::kMost * 17; v += 32) sums[v] = 0.0f;
                 __syncwarp();
             }
         }
         if (ends) {
             step = 0;
-            if (++index < segments) s = segment<DOWN>(a, c, index);
+            fresh = true;
+            if (at == end) begin = end;
+            next<DOWN>(c, s, tiles);
         }
     }
     cp_async_wait<0>();
 }
 
 template <typename F>
-cudaError_t launch(F *kern, unsigned grid, int cluster, size_t smem, bool after, const MoeArgs &a, cudaStream_t stream)
+cudaError_t launch(F *kern, unsigned grid, unsigned threads, int cluster, size_t smem, bool after, const MoeArgs &a, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kMoeThreads);
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -691,12 +837,11 @@ cudaError_t launch(F *kern, unsigned grid, int cluster, size_t smem, bool after,
 template <bool BF16, bool DOWN, bool VEC>
 cudaError_t product(const MoeArgs &a, cudaStream_t stream)
 {
-    switch (moe_groups(a.M)) {
-    case 1: return launch(moe_kernel<BF16, DOWN, VEC, 1>, kMoeCtas, 0, smem_of<DOWN, VEC, 1>(), true, a, stream);
-    case 2: return launch(moe_kernel<BF16, DOWN, VEC, 2>, kMoeCtas, 0, smem_of<DOWN, VEC, 2>(), true, a, stream);
-    case 4: return launch(moe_kernel<BF16, DOWN, VEC, 4>, kMoeCtas, 0, smem_of<DOWN, VEC, 4>(), true, a, stream);
-    default: return launch(moe_kernel<BF16, DOWN, VEC, 8>, kMoeCtas, 0, smem_of<DOWN, VEC, 8>(), true, a, stream);
-    }
+    using One = Layout<DOWN, VEC, 1>;
+    using Two = Layout<DOWN, VEC, 2>;
+    if (a.M <= kMoeGroup)
+        return launch(moe_kernel<BF16, DOWN, VEC, 1>, kMoeCtas, One::kThreads, 0, One::kBytes, true, a, stream);
+    return launch(moe_kernel<BF16, DOWN, VEC, 2>, kMoeCtas, Two::kThreads, 0, Two::kBytes, true, a, stream);
 }
 
 int status(const char *what, cudaError_t e) { return e == cudaSuccess ? 0 : record_cuda_error(what, e, cudaGetErrorString(e)); }
@@ -705,10 +850,10 @@ int status(const char *what, cudaError_t e) { return e == cudaSuccess ? 0 : reco
 
 int launch_moe_router(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream)
 {
-    const unsigned grid = static_cast<unsigned>(a.M * a.cluster);
+    const unsigned grid = static_cast<unsigned>(a.M * kMoeRouterCtas);
     const auto kern = bf16 ? (vec ? moe_router_kernel<true, true> : moe_router_kernel<true, false>)
                            : (vec ? moe_router_kernel<false, true> : moe_router_kernel<false, false>);
-    return status("expert router launch", launch(kern, grid, a.cluster, 0, false, a, stream));
+    return status("expert router launch", launch(kern, grid, kMoeThreads, kMoeRouterCtas, 0, false, a, stream));
 }
 
 int launch_moe_up(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream)

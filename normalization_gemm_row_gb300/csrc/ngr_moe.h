@@ -20,9 +20,11 @@ constexpr int kMoeWorkers = kMoeCtas * (kMoeThreads / 32);
 // rounded to the 16-bit type and what that rounding left out.
 constexpr int kMoeGroup = 4;
 constexpr int kMoeMinShare = 4;       // steps of a worker at least
+constexpr int kMoeCounters = 2 * kMoeWorkers;   // up, down: of a unit by its first worker
+constexpr int kMoeRouterCtas = 8;     // a cluster for each token
 
-// Groups that a kernel for M tokens has room for: 1, 2, 4 or 8.
-__host__ __device__ constexpr int moe_groups(int64_t M) { return M <= 4 ? 1 : M <= 8 ? 2 : M <= 16 ? 4 : 8; }
+constexpr int kMoeEntry = 2 * kMoeGroup;   // tokens that share one reading of an expert's weights
+constexpr int kMoeMaxEntries = kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / kMoeEntry;
 
 struct MoeArgs {
     const void *x, *gamma, *beta;     // [M, K], [K]
@@ -36,13 +38,14 @@ struct MoeArgs {
     void *h;                          // [M top_k, 2, Fp] weight x SiLU(gate) x up in two parts, likewise
     // A worker's parts of the units that it shares, the second place for the
     // unit that begins with it: up [workers][2][groups][32 lanes][gate, up],
-    // down [workers][2][tokens][16 rows], FP32.
-    float *part_up, *part_down;
-    int *count_up, *count_down;       // [workers], zeroed by the router
+    // down [workers][2][tokens][16 rows], FP32 (groups and tokens that there is
+    // room for: 1 and 4, or 2 and 32).  Up's are done with when
+    // down's are made.
+    float *parts;
+    int *counters;                    // [kMoeCounters], zeroed by the router
     int *err;
     int norm, M, K, F, E, top_k, renormalize;
     int Kp, Fp;                       // pitches, multiples of 64
-    int cluster;                      // CTAs that share a token's router row
     float eps;
 };
 

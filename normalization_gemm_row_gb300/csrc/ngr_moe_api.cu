@@ -30,7 +30,7 @@ int moe_sizes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
 }
 
 struct MoePlan {
-    size_t ids, w, a, h, part_up, part_down, count_up, count_down, total;
+    size_t ids, w, a, h, parts, counters, total;
     int64_t Kp, Fp;
 };
 
@@ -45,15 +45,12 @@ MoePlan moe_plan(int64_t M, int64_t K, int64_t F, int64_t top_k)
         off += (static_cast<size_t>(bytes) + 255) & ~static_cast<size_t>(255);
         return at;
     };
-    const int64_t groups = moe_groups(M);
     p.ids = take(M * top_k * 4);
     p.w = take(M * top_k * 4);
     p.a = take(M * 2 * p.Kp * 2);
     p.h = take(M * top_k * 2 * p.Fp * 2);
-    p.part_up = take(static_cast<int64_t>(kMoeWorkers) * 2 * groups * 32 * 8);
-    p.part_down = take(static_cast<int64_t>(kMoeWorkers) * 2 * groups * kMoeGroup * 16 * 4);
-    p.count_up = take(kMoeWorkers * 4);
-    p.count_down = take(kMoeWorkers * 4);
+    p.parts = take(static_cast<int64_t>(kMoeWorkers) * 2 * (M <= kMoeGroup ? kMoeGroup : kMoeMaxTokens) * 64);
+    p.counters = take(kMoeCounters * 4);
     p.total = off;
     return p;
 }
@@ -112,10 +109,8 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.w = reinterpret_cast<float *>(ws + p.w);
     a.a = ws + p.a;
     a.h = ws + p.h;
-    a.part_up = reinterpret_cast<float *>(ws + p.part_up);
-    a.part_down = reinterpret_cast<float *>(ws + p.part_down);
-    a.count_up = reinterpret_cast<int *>(ws + p.count_up);
-    a.count_down = reinterpret_cast<int *>(ws + p.count_down);
+    a.parts = reinterpret_cast<float *>(ws + p.parts);
+    a.counters = reinterpret_cast<int *>(ws + p.counters);
     a.err = reinterpret_cast<int *>(ws);
     a.norm = norm;
     a.M = static_cast<int>(M);
@@ -127,14 +122,13 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.Kp = static_cast<int>(p.Kp);
     a.Fp = static_cast<int>(p.Fp);
     a.eps = eps;
-    a.cluster = E <= 8 ? 1 : E <= 16 ? 2 : E <= 32 ? 4 : 8;   // an expert a warp, up to 64
     const bool bf16 = dtype == NGR_BF16;
     const bool vec_r = K % 8 == 0 && aligned(Wr, 16) && aligned(x, 16) && aligned(a.gamma, 16) && aligned(a.beta, 16);
     const bool vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
     const bool vec_f = F % 8 == 0 && aligned(Wd, 16);
     if (trace_mode())
-        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d router=%d CTAs a token%s%s\n",
-                     a.M, a.K, a.F, a.E, a.top_k, norm, a.cluster, vec_k ? "" : ", gate and up shifted",
+        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d%s%s\n",
+                     a.M, a.K, a.F, a.E, a.top_k, norm, vec_k ? "" : ", gate and up shifted",
                      vec_f ? "" : ", down shifted");
     call_begin();
     kernel_begin(stream);
