@@ -407,7 +407,8 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
  * their product with v; the order of every sum follows from the lengths alone
  * (the same call gives the same bits).  D is a multiple of 8 up to 256, every
  * pointer but lengths, lse and the table 16-byte aligned and every stride a
- * multiple of 8 elements.  Workspace (256-byte aligned):
+ * multiple of 8 elements; k and v each reach over 64 GiB at most
+ * (NGR_ERR_SHAPE).  Workspace (256-byte aligned):
  * ngr_paged_attention_workspace_bytes, with capacity = table_pages page_size.
  * The lengths stay on the device, so a captured call follows them. */
 int ngr_fused_paged_attention(const void *q, int64_t q_row_stride,

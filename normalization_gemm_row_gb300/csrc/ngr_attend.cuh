@@ -1,0 +1,686 @@
+// ngr_attend.cuh -- attention of one new token for each sequence over a paged
+// key-value cache.
+//
+//   s_j = scale q . k_j,  lse = log sum_j exp s_j,  out = sum_j exp(s_j - lse) v_j
+//
+// A key or value read serves the H / G query heads of its head: 2 H / G
+// operations a byte, so reading the cache bounds it.  The cache is streamed
+// once, by warps: each has a ring of stages in shared memory that
+// asynchronous copies of 16 tokens' keys and values fill, and takes them with
+// 16 x 8 x 16 matrix instructions, tokens (then dimensions) as the rows and 8
+// query heads as the columns, with a running maximum and sum.  (With heads as
+// rows, 8 heads would leave half of every instruction and of its registers
+// unused.)  The warps have nothing to wait for but their own copies: no
+// barrier.
+//
+// All items' tiles of 16 tokens (an item: a sequence and key head, and a block
+// of 16 query heads where there are more) stand in one row, which is cut into
+// equal runs, one a warp ("worker").  A batch of any lengths is balanced so,
+// and nothing but the device has to know the lengths.  An item that lies in
+// one run is finished there; the others' parts (FP32 sums, maximum, sum of
+// exponentials) are joined by a second kernel in the tokens' order, so a call
+// repeated gives the same bits.
+#pragma once
+
+#include "ngr.h"
+#include "ngr_entry.h"
+#include "ngr_internal.h"
+#include "ngr_kv.h"
+#include "ngr_mma.cuh"
+#include "ngr_ptx.cuh"
+
+namespace ngr {
+
+namespace {
+
+constexpr float kLn2 = 0.6931471805599453f;
+
+// A warp's ring: stages of 16 tokens' keys or values in turn, 192 KB over the
+// CTA's warps.
+template <int DP, int NB>
+struct Ring {
+    static constexpr int kWarps = attend_warps(DP, NB), kThreads = 32 * kWarps;
+    static constexpr int kStage = kAttendTile * DP * 2, kFit = 192 * 1024 / kWarps / kStage;
+    static constexpr int kStages = kFit < 6 ? kFit : 6, kBytes = kStages * kStage;
+    static_assert(kStages >= 3, "a tile's values and the next one's keys go while its keys are used");
+    // tiles that are under way at once
+    static constexpr int kTiles = 4;
+};
+
+// What a row of the batch has: its first token and how many.
+struct Span {
+    int start, n, tiles;
+    bool used;
+};
+__device__ __forceinline__ Span span_of(const AttendArgs &a, int b, bool *bad)
+{
+    int len = a.lengths[b];
+    Span s;
+    s.used = len >= 0;
+    if (len > a.kv.capacity) {
+        *bad = true;
+        len = static_cast<int>(a.kv.capacity);
+    }
+    s.start = a.window > 0 && len > a.window ? len - a.window : 0;
+    s.n = len > 0 ? len - s.start : 0;
+    // (a row without tokens is visited too: it has an output)
+    s.tiles = s.n > 0 ? (s.n + kAttendTile - 1) / kAttendTile : 1;
+    return s;
+}
+
+// A place in the row of tiles.
+struct Place {
+    int b, item, tile;     // sequence, item among the sequence's, tile of the item
+    Span s;
+};
+__device__ __forceinline__ void advance(const AttendArgs &a, Place &p, bool *bad)
+{
+    if (++p.tile < p.s.tiles) return;
+    p.tile = 0;
+    if (++p.item < a.G * a.blocks) return;
+    p.item = 0;
+    if (++p.b < a.B) p.s = span_of(a, p.b, bad);
+}
+
+// The entry of the table for a token of a tile, one in lane % 16, and its slot
+// in the page; kNone past the sequence's end.
+constexpr int kNone = -2147483647 - 1;
+__device__ __forceinline__ int page_entry(const AttendArgs &a, const Place &p, int lane, int *slot)
+{
+    const int j = p.tile * kAttendTile + (lane & 15);
+    if (j >= p.s.n) return kNone;
+    const int token = p.s.start + j;
+    const int page = a.kv.page_mul ? __umulhi(token, a.kv.page_mul) >> a.kv.page_sh : token;
+    *slot = token - page * a.kv.page_size;
+    return a.kv.table[p.b * a.kv.table_stride + page];
+}
+
+// Piece c of row r of a stage lies at c ^ turn(r), so that eight rows' pieces
+// of one column lie in all banks: the rows are P pieces apart, and 8 of them
+// fill the 8 places of 16 bytes modulo 128.
+template <int DP>
+__device__ __forceinline__ constexpr int turn(int r)
+{
+    static_assert(DP / 8 % 8 == 0 || DP / 8 % 8 == 2 || DP / 8 % 8 == 4, "");
+    return DP / 8 % 8 == 0 ? r & 7 : DP / 8 % 8 == 4 ? (r >> 1) & 3 : (r >> 2) & 1;
+}
+
+// A lane's 16-byte pieces of a tile's rows, D / 8 a row: piece lane + 32 i.
+// FULL: D = DP.
+template <int DP, bool FULL>
+struct Pieces {
+    static constexpr int kEach = DP / 8, kMost = kAttendTile * kEach / 32;
+    // a lane's pieces lie in one column, kRows rows apart
+    static constexpr bool kColumn = FULL && 32 % kEach == 0;
+    static constexpr int kRows = kColumn ? 32 / kEach : 1, kHeld = kColumn ? 1 : kMost;
+    int count;                              // of all the tile's
+    int at[kHeld], row[kHeld], col[kHeld];  // in the stage; the token; the piece of its row
+    __device__ __forceinline__ Pieces(int D, int lane)
+    {
+        const int each = FULL ? kEach : D / 8;
+        count = kAttendTile * each;
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) {
+            const int p = min(i * 32 + lane, count - 1), r = p / each, c = p - r * each;
+            at[i] = r * (DP * 2) + ((c ^ turn<DP>(r)) << 4);
+            row[i] = r;
+            col[i] = c;
+        }
+    }
+    __device__ __forceinline__ int at_of(int i) const
+    {
+        // (the first row is below kRows, whose multiples' bits are apart from it)
+        return kColumn ? (at[0] ^ (turn<DP>(i * kRows) << 4)) + i * kRows * DP * 2 : at[kColumn ? 0 : i];
+    }
+    __device__ __forceinline__ int row_of(int i) const { return kColumn ? row[0] + i * kRows : row[kColumn ? 0 : i]; }
+    __device__ __forceinline__ int col_of(int i) const { return col[kColumn ? 0 : i]; }
+};
+constexpr uint32_t kNowhere = 0xffffffffu;
+// The rows at these offsets (one in lane % 16, in 16-byte units) to a stage;
+// zeros for those nowhere, if not `all` are somewhere.
+template <int DP, bool FULL>
+__device__ __forceinline__ void fetch(const void *cache, const Pieces<DP, FULL> &p, uint32_t offset, bool all, uint32_t stage,
+                                      int lane)
+{
+    using P = Pieces<DP, FULL>;
+    const uint4 *from = static_cast<const uint4 *>(cache) + (P::kColumn ? p.col_of(0) : 0);
+    if (all) {
+#pragma unroll
+        for (int i = 0; i < P::kMost; ++i) {
+            if (!FULL && i * 32 >= p.count) break;
+            const uint32_t at = __shfl_sync(0xffffffffu, offset, p.row_of(i)) + (P::kColumn ? 0 : p.col_of(i));
+            if (FULL || i * 32 + lane < p.count) cp_async16(stage + p.at_of(i), from + at);
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < P::kMost; ++i) {
+        if (!FULL && i * 32 >= p.count) break;
+        const uint32_t at = __shfl_sync(0xffffffffu, offset, p.row_of(i));
+        const bool there = at != kNowhere;
+        if (FULL || i * 32 + lane < p.count)
+            cp_async16(stage + p.at_of(i), from + (there ? at + (P::kColumn ? 0 : p.col_of(i)) : 0u), there);
+    }
+}
+
+// NB: blocks of 8 query heads that a warp takes at once, 1 or 2.
+template <bool BF16, int DP, int NB, bool FULL>
+__global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(const __grid_constant__ AttendArgs a)
+{
+    using R = Ring<DP, NB>;
+    constexpr int kWarps = R::kWarps, kThreads = R::kThreads, S = R::kStages;
+    constexpr int kSteps = DP / 16;
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ long long before[kThreads + 1];
+    __shared__ long long warp_total[kWarps];
+    __shared__ uint32_t seen[kWarps][R::kTiles];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    const int items = a.G * a.blocks;
+    pdl_launch_dependents();
+    // (columns from D on are zeros, which no copy touches)
+    if (!FULL)
+        for (int i = threadIdx.x; i < kWarps * R::kBytes / 16; i += kThreads)
+            reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+
+    // Tiles before each run of `each` sequences.
+    const int each = (a.B + kThreads - 1) / kThreads;
+    bool bad = false;
+    {
+        long long mine = 0;
+        for (int i = 0; i < each; ++i) {
+            const int b = static_cast<int>(threadIdx.x) * each + i;
+            if (b < a.B) mine += static_cast<long long>(span_of(a, b, &bad).tiles) * items;
+        }
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+        }
+        if (lane == 31) warp_total[warp] = incl;
+        __syncthreads();
+        long long base = 0;
+        for (int w = 0; w < warp; ++w) base += warp_total[w];
+        before[threadIdx.x + 1] = base + incl;
+        if (threadIdx.x == 0) before[0] = 0;
+        __syncthreads();
+    }
+    bad = false;      // (counted by whoever works on the sequence)
+    const long long total = before[kThreads];
+    long long share = (total + a.workers - 1) / a.workers;
+    if (share < a.min_share) share = a.min_share;
+    // Neighbouring runs on different SMs: a few runs have an SM each.
+    const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+    const long long first = worker * share;
+    long long left = total - first;
+    const int count = static_cast<int>(left <= 0 ? 0 : left < share ? left : share);
+    AttendJob job = {-1, -1, 0, 0};
+
+    if (count > 0) {
+        Place c;
+        {
+            int lo = 0, hi = kThreads;       // before[lo] <= first < before[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (before[mid] <= first) lo = mid;
+                else hi = mid;
+            }
+            long long at = before[lo];
+            int b = lo * each;
+            Span s = span_of(a, b, &bad);
+            while (at + static_cast<long long>(s.tiles) * items <= first) {
+                at += static_cast<long long>(s.tiles) * items;
+                s = span_of(a, ++b, &bad);
+            }
+            c.b = b;
+            c.s = s;
+            c.item = static_cast<int>((first - at) / s.tiles);
+            c.tile = static_cast<int>((first - at) - static_cast<long long>(c.item) * s.tiles);
+        }
+        Place f = c;
+        const Pieces<DP, FULL> pieces(a.D, lane);
+        const uint32_t base = smem_u32(ring) + warp * R::kBytes;
+        // Keys and values go by turns; the values' offsets are kept from the
+        // keys'.  What the cursor f does not reach is an empty group.
+        uint32_t k_at = kNowhere, v_at = kNowhere;
+        bool all = false;                  // the tile has all its tokens
+        int left = count, issued = 0;      // tiles to issue, issued
+        auto locate = [&](int entry, int slot) {
+            k_at = v_at = kNowhere;
+            if (entry != kNone) {
+                if (entry >= 0 && entry < a.kv.pages) {
+                    const uint32_t head = a.blocks == 1 ? f.item : f.item / a.blocks;
+                    k_at = entry * a.k_page + slot * a.k_token + head * a.k_head;
+                    v_at = a.alike ? k_at : entry * a.v_page + slot * a.v_token + head * a.v_head;
+                } else {
+                    bad = true;
+                }
+            }
+        };
+        auto issue_keys = [&](int entry, int slot, int stage) {
+            if (left > 0) {
+                locate(entry, slot);
+                const uint32_t there = __ballot_sync(0xffffffffu, k_at != kNowhere);
+                all = there == 0xffffffffu;
+                if (lane == 0) seen[warp][issued % R::kTiles] = there;
+                fetch<DP, FULL>(a.kv.k, pieces, k_at, all, base + stage * R::kStage, lane);
+                advance(a, f, &bad);
+                ++issued;
+            }
+            --left;
+            cp_async_commit();
+        };
+        auto issue_values = [&](int stage) {      // of the tile whose keys went last
+            if (left >= 0) fetch<DP, FULL>(a.kv.v, pieces, v_at, all, base + stage * R::kStage, lane);
+            cp_async_commit();
+        };
+        auto entry_ahead = [&](int *slot) { return left > 0 ? page_entry(a, f, lane, slot) : kNone; };
+#pragma unroll
+        for (int i = 0; i < S; ++i) {
+            if (i % 2 == 0) {
+                int slot = 0;
+                const int entry = entry_ahead(&slot);
+                issue_keys(entry, slot, i);
+            } else {
+                issue_values(i);
+            }
+        }
+
+        // of dimension block j, head block n: dimensions 16 j + g (o[0], o[1])
+        // and 16 j + g + 8, heads 8 n + 2t and the next; maximum and this
+        // lane's share of the sum of each of those heads
+        float o[kSteps][NB][4], top[NB][2], sum[NB][2];
+        uint32_t q[kSteps][NB][2];
+        bool fresh = true;         // a new item
+        bool whole = c.tile == 0;  // this worker has the item's beginning
+        int stage = 0;
+        for (int i = 0; i < count; ++i) {
+            int slot = 0;
+            const int entry = entry_ahead(&slot);
+            if (fresh) {
+                const int kv_head = c.item / a.blocks, block = c.item - kv_head * a.blocks;
+                const int rows = min(kAttendRows, a.group - block * kAttendRows);
+                const uint16_t *from = static_cast<const uint16_t *>(a.q) + c.b * a.q_row +
+                                       (kv_head * a.group + block * kAttendRows) * a.q_head;
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = 8 * n + g, d = k * 16 + h * 8 + 2 * t;
+                            q[k][n][h] = r < rows && d < a.D ? *reinterpret_cast<const uint32_t *>(from + r * a.q_head + d) : 0u;
+                        }
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) o[k][n][e] = 0.0f;
+                    }
+                    top[n][0] = top[n][1] = -INFINITY;
+                    sum[n][0] = sum[n][1] = 0.0f;
+                }
+                fresh = false;
+            }
+            cp_async_wait<S - 1>();
+            __syncwarp();
+            const uint32_t there = seen[warp][i % R::kTiles] & 0xffffu;
+
+            // scores of tokens g (z[0], z[1]) and g + 8 with heads 2t, 2t + 1
+            float z[NB][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[n][e] = 0.0f;
+            {
+                const int r = lane & 15, half = lane >> 4;
+                const uint32_t row = base + stage * R::kStage + r * (DP * 2);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t w[4];
+                    ldmatrix4(w, row + (((2 * k + half) ^ turn<DP>(r)) << 4));
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) mma_16816<BF16>(z[n], w[0], w[1], w[2], w[3], q[k][n][0], q[k][n][1]);
+                }
+            }
+            __syncwarp();
+            if (S % 2 == 0) issue_keys(entry, slot, stage);
+            else issue_values(stage);
+            stage = stage + 1 == S ? 0 : stage + 1;
+            // in units of log 2, those that are not there out
+            bool more = false;
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) z[n][e] *= a.scale2;
+            if (there != 0xffffu) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (!((there >> (g + (e >> 1) * 8)) & 1u)) z[n][e] = -INFINITY;
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) more = more || z[n][e] > top[n][e & 1];
+            // Only where a head's maximum grows is it exchanged.
+            if (__any_sync(0xffffffffu, more)) {
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float high = fmaxf(z[n][h], z[n][2 + h]);
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) high = fmaxf(high, __shfl_xor_sync(0xffffffffu, high, x));
+                        const float to = fmaxf(top[n][h], high);
+                        const float by = to == top[n][h] ? 1.0f : exp2_fast(top[n][h] - to);
+                        top[n][h] = to;
+                        sum[n][h] *= by;
+#pragma unroll
+                        for (int k = 0; k < kSteps; ++k) {
+                            o[k][n][h] *= by;
+                            o[k][n][2 + h] *= by;
+                        }
+                    }
+            }
+            // The weights go to the second product in the inputs' type: half
+            // a step off each, as independent roundings that average out
+            // (their sum is of the unrounded ones).
+            uint32_t p[NB][2];
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    // (nothing seen so far: 2^(-inf - 0) = 0)
+                    const float off = top[n][e & 1] == -INFINITY ? 0.0f : top[n][e & 1];
+                    z[n][e] = exp2_fast(z[n][e] - off);
+                    sum[n][e & 1] += z[n][e];
+                }
+                p[n][0] = transpose8(pack16<BF16>(z[n][0], z[n][1]));
+                p[n][1] = transpose8(pack16<BF16>(z[n][2], z[n][3]));
+            }
+            cp_async_wait<S - 1>();
+            __syncwarp();
+            {
+                const int r = lane & 7, tokens = (lane >> 4) << 3, half = (lane >> 3) & 1;
+                const uint32_t row = base + stage * R::kStage + (tokens + r) * (DP * 2);
+#pragma unroll
+                for (int k = 0; k < kSteps; ++k) {
+                    uint32_t w[4];
+                    ldmatrix4_t(w, row + (((2 * k + half) ^ turn<DP>(r)) << 4));
+#pragma unroll
+                    for (int n = 0; n < NB; ++n) mma_16816<BF16>(o[k][n], w[0], w[1], w[2], w[3], p[n][0], p[n][1]);
+                }
+            }
+            __syncwarp();
+            if (S % 2 == 0) issue_values(stage);
+            else issue_keys(entry, slot, stage);
+            stage = stage + 1 == S ? 0 : stage + 1;
+
+            const bool ends = c.tile + 1 == c.s.tiles;
+            if (ends || i + 1 == count) {
+                const int kv_head = c.item / a.blocks, block = c.item - kv_head * a.blocks;
+                const int rows = min(kAttendRows, a.group - block * kAttendRows);
+                const int head = kv_head * a.group + block * kAttendRows;
+#pragma unroll
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int x = 4; x < 32; x <<= 1) sum[n][h] += __shfl_xor_sync(0xffffffffu, sum[n][h], x);
+                if (ends && whole) {
+                    if (c.s.used) {
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int r = 8 * n + 2 * t + h;
+                                if (r >= rows) continue;
+                                const float total = sum[n][h], by = total == 0.0f ? 0.0f : 1.0f / total;
+                                const int64_t at = static_cast<int64_t>(c.b) * a.H + head + r;
+                                uint16_t *out = static_cast<uint16_t *>(a.out) + at * a.D;
+#pragma unroll
+                                for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e)
+                                        if (k * 16 + e * 8 < a.D)
+                                            out[k * 16 + e * 8 + g] =
+                                                static_cast<uint16_t>(pack16<BF16>(o[k][n][2 * e + h] * by, 0.0f));
+                                if (a.lse && g == 0) a.lse[at] = total == 0.0f ? -INFINITY : top[n][h] * kLn2 + logf(total);
+                            }
+                    }
+                    if (a.slot_by_item && lane == 0)
+                        a.jobs[static_cast<int64_t>(c.b) * items + c.item] = AttendJob{-1, -1, 0, 0};
+                } else {
+                    const int64_t part = (static_cast<int64_t>(worker) * 2 + (whole ? 1 : 0)) * a.part_rows;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const int r = 8 * n + 2 * t + h;
+                            if (r >= rows) continue;
+                            if (g == 0) a.part_ml[part + r] = make_float2(top[n][h], sum[n][h]);
+                            float *po = a.part_o + (part + r) * DP + g;
+#pragma unroll
+                            for (int k = 0; k < kSteps; ++k) {
+                                po[k * 16] = o[k][n][h];
+                                po[k * 16 + 8] = o[k][n][2 + h];
+                            }
+                        }
+                    if (whole) {      // the others' parts follow
+                        const long long end = first + i + (c.s.tiles - c.tile);
+                        job = AttendJob{worker, static_cast<int>((end - 1) / share), c.b, c.item};
+                        if (a.slot_by_item && lane == 0) a.jobs[static_cast<int64_t>(c.b) * items + c.item] = job;
+                    }
+                }
+                fresh = whole = true;
+            }
+            advance(a, c, &bad);
+        }
+        cp_async_wait<0>();
+    }
+    if (!a.slot_by_item && lane == 0) a.jobs[worker] = job;
+    const bool any = __any_sync(0xffffffffu, bad);
+    if (lane == 0) a.flags[worker] = any;
+}
+
+// The parts of an item that several workers share.  Up to 32 parts (a batch)
+// a warp takes a row by itself, its parts' weights in its lanes; more (few
+// long sequences) are taken by all warps of a block together, a row of blocks
+// for each row.
+constexpr int kJoinWarps = 16, kJoinHeld = 4;
+
+template <int N>
+__device__ __forceinline__ void add_scaled(float4 (&to)[N], const float4 (&v)[N], float w)
+{
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        to[e].x = fmaf(w, v[e].x, to[e].x);
+        to[e].y = fmaf(w, v[e].y, to[e].y);
+        to[e].z = fmaf(w, v[e].z, to[e].z);
+        to[e].w = fmaf(w, v[e].w, to[e].w);
+    }
+}
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a)
+{
+    extern __shared__ float weight[];     // [workers][weight, weight x sum]
+    __shared__ __align__(16) float sums[kJoinWarps][DP];
+    __shared__ float red[kJoinWarps];
+    constexpr int kEach = (DP / 4 + 31) / 32;      // 16-byte pieces of a part's row that a lane has
+    auto has = [&](int e) { return (e * 32 + (static_cast<int>(threadIdx.x) & 31)) * 4 < DP; };
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    pdl_wait();
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        int bad = 0;
+        for (int w = threadIdx.x; w < a.workers; w += 32 * kJoinWarps) bad |= a.flags[w];
+        const int any = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.err = any ? kDevErrPage : 0;
+    }
+    const AttendJob job = a.jobs[blockIdx.x];
+    if (job.first < 0) return;
+    const int kv_head = job.item / a.blocks, block = job.item - kv_head * a.blocks;
+    const int rows = min(kAttendRows, a.group - block * kAttendRows), parts = job.last - job.first + 1;
+    const int64_t head0 = static_cast<int64_t>(job.row) * a.H + kv_head * a.group + block * kAttendRows;
+    auto part = [&](int i, int row) { return (static_cast<int64_t>(job.first + i) * 2 + (i == 0 ? 1 : 0)) * a.part_rows + row; };
+    auto load = [&](float4 (&v)[kEach], int i, int row) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            v[e] = has(e) ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + part(i, row) * DP) + e * 32 + lane)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    };
+
+    if (parts <= 32) {
+        if (blockIdx.y > 0) return;
+        for (int row = warp; row < rows; row += kJoinWarps) {
+            const float2 ml = lane < parts ? a.part_ml[part(lane, row)] : make_float2(-INFINITY, 0.0f);
+            float top = ml.x;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float w = exp2_fast(ml.x - (top == -INFINITY ? 0.0f : top));
+            float total = w * ml.y;
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+            float4 acc[kEach] = {};
+#pragma unroll 4
+            for (int i = 0; i < parts; ++i) {
+                const float wi = __shfl_sync(0xffffffffu, w, i);
+                float4 v[kEach];
+                load(v, i, row);
+                add_scaled(acc, v, wi);
+            }
+            const float by = total == 0.0f ? 0.0f : 1.0f / total;
+            uint16_t *out = static_cast<uint16_t *>(a.out) + (head0 + row) * a.D;
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                if ((e * 32 + lane) * 4 < a.D)
+                    *reinterpret_cast<uint2 *>(out + (e * 32 + lane) * 4) =
+                        make_uint2(pack16<BF16>(acc[e].x * by, acc[e].y * by), pack16<BF16>(acc[e].z * by, acc[e].w * by));
+            if (a.lse && lane == 0) a.lse[head0 + row] = total == 0.0f ? -INFINITY : top * kLn2 + logf(total);
+        }
+        return;
+    }
+    for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+        // A warp's first sums are on their way before their weights are known.
+        float4 held[kJoinHeld][kEach];
+#pragma unroll
+        for (int h = 0; h < kJoinHeld; ++h)
+            if (warp + h * kJoinWarps < parts) load(held[h], warp + h * kJoinWarps, row);
+        float top = -INFINITY;
+        for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) top = fmaxf(top, a.part_ml[part(i, row)].x);
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        if (lane == 0) red[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinWarps; ++w) top = fmaxf(top, red[w]);
+        const float off = top == -INFINITY ? 0.0f : top;
+        for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) {
+            const float2 ml = a.part_ml[part(i, row)];
+            const float w = exp2_fast(ml.x - off);
+            weight[2 * i] = w;
+            weight[2 * i + 1] = w * ml.y;
+        }
+        __syncthreads();
+        // (every warp sums the denominators the same way)
+        float total = 0.0f;
+        for (int i = lane; i < parts; i += 32) total += weight[2 * i + 1];
+#pragma unroll
+        for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+        {
+            float4 acc[kEach] = {};
+#pragma unroll
+            for (int h = 0; h < kJoinHeld; ++h)
+                if (warp + h * kJoinWarps < parts) add_scaled(acc, held[h], weight[2 * (warp + h * kJoinWarps)]);
+#pragma unroll 4
+            for (int i = warp + kJoinHeld * kJoinWarps; i < parts; i += kJoinWarps) {
+                float4 v[kEach];
+                load(v, i, row);
+                add_scaled(acc, v, weight[2 * i]);
+            }
+#pragma unroll
+            for (int e = 0; e < kEach; ++e)
+                if (has(e)) *reinterpret_cast<float4 *>(&sums[warp][(e * 32 + lane) * 4]) = acc[e];
+        }
+        __syncthreads();
+        const float by = total == 0.0f ? 0.0f : 1.0f / total;
+        if (threadIdx.x < DP / 2 && static_cast<int>(threadIdx.x) * 2 < a.D) {
+            float x = 0.0f, y = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; ++w) {
+                x += sums[w][2 * threadIdx.x];
+                y += sums[w][2 * threadIdx.x + 1];
+            }
+            *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.out) + (head0 + row) * a.D + 2 * threadIdx.x) =
+                pack16<BF16>(x * by, y * by);
+        }
+        if (a.lse && threadIdx.x == 0) a.lse[head0 + row] = total == 0.0f ? -INFINITY : top * kLn2 + logf(total);
+    }
+}
+
+template <bool BF16, int DP, int NB, bool FULL>
+cudaError_t attend(const AttendArgs &a, cudaStream_t stream)
+{
+    using R = Ring<DP, NB>;
+    constexpr int kSmem = R::kWarps * R::kBytes;
+    // (an attribute of the device's copy of the function: set at every call,
+    // as the current device may be another)
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<BF16, DP, NB, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+    attend_kernel<BF16, DP, NB, FULL><<<a.workers / R::kWarps, R::kThreads, kSmem, stream>>>(a);
+    return cudaGetLastError();
+}
+template <bool BF16, int DP, bool PADDED>
+cudaError_t attend(const AttendArgs &a, cudaStream_t stream)
+{
+    if constexpr (PADDED) {
+        if (a.D < DP)
+            return attend_heads(a.group) == 1 ? attend<BF16, DP, 1, false>(a, stream) : attend<BF16, DP, 2, false>(a, stream);
+    }
+    return attend_heads(a.group) == 1 ? attend<BF16, DP, 1, true>(a, stream) : attend<BF16, DP, 2, true>(a, stream);
+}
+
+template <bool BF16, int DP>
+cudaError_t join(const AttendArgs &a, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    // (blocks for single rows where there are few jobs, which are the long ones)
+    const int apart = 1024 / a.slots;
+    cfg.gridDim = dim3(static_cast<unsigned>(a.slots),
+                       static_cast<unsigned>(apart < 1 ? 1 : apart < a.part_rows ? apart : a.part_rows));
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.workers) * 2 * sizeof(float);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_join_kernel<BF16, DP>, a);
+}
+
+template <bool BF16>
+cudaError_t by_dim(bool joining, const AttendArgs &a, cudaStream_t stream)
+{
+    switch (attend_dim(a.D)) {
+    case 64: return joining ? join<BF16, 64>(a, stream) : attend<BF16, 64, true>(a, stream);
+    case 80: return joining ? join<BF16, 80>(a, stream) : attend<BF16, 80, false>(a, stream);
+    case 96: return joining ? join<BF16, 96>(a, stream) : attend<BF16, 96, false>(a, stream);
+    case 128: return joining ? join<BF16, 128>(a, stream) : attend<BF16, 128, true>(a, stream);
+    case 192: return joining ? join<BF16, 192>(a, stream) : attend<BF16, 192, false>(a, stream);
+    default: return joining ? join<BF16, 256>(a, stream) : attend<BF16, 256, true>(a, stream);
+    }
+}
+
+}  // namespace
+
+// (one translation unit for each type, which defines its name and kind)
+#define NGR_JOINED2(a, b) a##b
+#define NGR_JOINED(a, b) NGR_JOINED2(a, b)
+int NGR_JOINED(launch_attend_, NGR_ATTEND_TYPE)(bool joining, const AttendArgs &a, cudaStream_t stream)
+{
+    const cudaError_t e = by_dim<NGR_ATTEND_BF16>(joining, a, stream);
+    return e == cudaSuccess ? 0 : record_cuda_error(joining ? "paged attention join launch" : "paged attention launch", e, cudaGetErrorString(e));
+}
+
+}  // namespace ngr

@@ -1,6 +1,6 @@
 // ngr_kv.h -- argument blocks of the paged key-value cache's kernels: the
 // rotated append (ngr_append.cu) and the attention of one new token
-// (ngr_attend.cu).  Not installed.
+// (ngr_attend.cuh).  Not installed.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -19,6 +19,9 @@ struct KvView {
     int64_t table_stride;
     int64_t capacity;     // tokens that a row of the table has room for
     int pages, page_size, rows;
+    // token / page_size for 31-bit tokens: the high word of the product with
+    // page_mul shifted down by page_sh (page_mul 0: pages of one token)
+    uint32_t page_mul, page_sh;
 };
 
 struct AppendArgs {
@@ -53,6 +56,9 @@ struct AttendJob {
 
 struct AttendArgs {
     KvView kv;
+    // the view's strides in 16-byte units: no offset passes 32 bits
+    uint32_t k_page, k_token, k_head, v_page, v_token, v_head;
+    bool alike;               // v's are k's
     const void *q;
     int64_t q_row, q_head;
     const int *lengths;
@@ -73,10 +79,21 @@ struct AttendArgs {
     int *err;
 };
 
-// The padded head dimension (64, 128 or 256) and the warps of a CTA for it.
-inline int attend_dim(int64_t D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-inline int attend_warps(int dim) { return dim == 256 ? 4 : 8; }
-int launch_attend(bool bf16, const AttendArgs &a, cudaStream_t stream);
-int launch_attend_join(bool bf16, const AttendArgs &a, cudaStream_t stream);
+// The padded head dimension (the kernels are built for these), the blocks of 8 query heads a
+// warp takes at once, and the warps of a CTA: as many as their registers (64
+// for the sums of 8 heads and 256 dimensions) leave room for.
+inline int attend_dim(int64_t D)
+{
+    return D == 80 || D == 96 || D == 192 ? static_cast<int>(D) : D <= 64 ? 64 : D <= 128 ? 128 : 256;
+}
+inline int attend_heads(int64_t group) { return group <= 8 ? 1 : 2; }
+constexpr int attend_warps(int dim, int heads) { return dim * heads <= 128 ? 16 : dim * heads <= 256 ? 8 : 4; }
+// The main kernel, or (joining) the one that joins its parts.
+int launch_attend_bf16(bool joining, const AttendArgs &a, cudaStream_t stream);
+int launch_attend_f16(bool joining, const AttendArgs &a, cudaStream_t stream);
+inline int launch_attend(bool bf16, bool joining, const AttendArgs &a, cudaStream_t stream)
+{
+    return bf16 ? launch_attend_bf16(joining, a, stream) : launch_attend_f16(joining, a, stream);
+}
 
 }  // namespace ngr

@@ -1,5 +1,5 @@
 // ngr_kv_api.cu -- entry points of the paged key-value cache (ngr_append.cu,
-// ngr_attend.cu): argument checks, workspace layout, how many workers.
+// ngr_attend.cuh): argument checks, workspace layout, how many workers.
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -48,7 +48,24 @@ int kv_view(const ngr_kv_cache *c, int64_t G, KvView *v)
     v->pages = static_cast<int>(c->pages);
     v->page_size = static_cast<int>(c->page_size);
     v->rows = static_cast<int>(c->table_rows);
+    // ceil(2^(31 + s) / page_size) with 2^s the next power of two: exact below 2^31
+    v->page_mul = v->page_sh = 0;
+    if (c->page_size > 1) {
+        int s = 1;
+        while ((int64_t(1) << s) < c->page_size) ++s;
+        v->page_mul = static_cast<uint32_t>(((uint64_t(1) << (31 + s)) + c->page_size - 1) / c->page_size);
+        v->page_sh = static_cast<uint32_t>(s - 1);
+    }
     return NGR_OK;
+}
+
+// The last of a view's heads, in 16-byte units, is below 2^32 - 1 (strides
+// are multiples of 8 elements).
+bool within_32(int64_t page, int64_t token, int64_t head, const KvView &v, int64_t G)
+{
+    const double last = static_cast<double>(page / 8) * (v.pages - 1) + static_cast<double>(token / 8) * (v.page_size - 1) +
+                        static_cast<double>(head / 8) * static_cast<double>(G - 1);
+    return last < 4294967295.0;
 }
 
 // Elements that every address of these strides is a multiple of: 8, 4, 2 or 1.
@@ -71,8 +88,9 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
 {
     AttendPlan p;
     std::memset(&p, 0, sizeof(p));
-    const int dim = attend_dim(D), warps = attend_warps(dim);
-    const int64_t group = H / G, longest = window > 0 ? std::min(window, capacity) : capacity;
+    const int64_t group = H / G;
+    const int dim = attend_dim(D), warps = attend_warps(dim, attend_heads(group));
+    const int64_t longest = window > 0 ? std::min(window, capacity) : capacity;
     p.blocks = (group + kAttendRows - 1) / kAttendRows;
     p.items = B * G * p.blocks;
     p.part_rows = std::min<int64_t>(group, kAttendRows);
@@ -242,6 +260,16 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
         granule({q, a.kv.k, a.kv.v}, {q_row_stride, q_head_stride, a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv.v_page,
                                       a.kv.v_token, a.kv.v_head}) != 8)
         return NGR_ERR_ALIGN;
+    if (!within_32(a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv, G) ||
+        !within_32(a.kv.v_page, a.kv.v_token, a.kv.v_head, a.kv, G))
+        return NGR_ERR_SHAPE;
+    a.k_page = static_cast<uint32_t>(a.kv.k_page / 8);
+    a.k_token = static_cast<uint32_t>(a.kv.k_token / 8);
+    a.k_head = static_cast<uint32_t>(a.kv.k_head / 8);
+    a.v_page = static_cast<uint32_t>(a.kv.v_page / 8);
+    a.v_token = static_cast<uint32_t>(a.kv.v_token / 8);
+    a.v_head = static_cast<uint32_t>(a.kv.v_head / 8);
+    a.alike = a.k_page == a.v_page && a.k_token == a.v_token && a.k_head == a.v_head;
     const AttendPlan p = attend_plan(B, H, G, D, std::min(a.kv.capacity, kMax31), window);
     if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
@@ -279,11 +307,11 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     const bool bf16 = dtype == NGR_BF16;
     call_begin();
     kernel_begin(stream);
-    rc = launch_attend(bf16, a, stream);
+    rc = launch_attend(bf16, false, a, stream);
     kernel_end(stream);
     if (rc == NGR_OK) {
         kernel_begin(stream);
-        rc = launch_attend_join(bf16, a, stream);
+        rc = launch_attend(bf16, true, a, stream);
         kernel_end(stream);
     }
     return call_end(rc, workspace, stream);

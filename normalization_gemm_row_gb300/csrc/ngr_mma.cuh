@@ -34,6 +34,15 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 2^x, off by a few steps of 2^-24 (the hardware's approximation; results
+// below 2^-126 are 0).
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // Four 8 x 8 matrices of 16-bit elements from shared memory; lane i gives the
 // address of row i % 8 of matrix i / 8.  `_t`: each transposed.
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t saddr)
@@ -51,11 +60,24 @@ __device__ __forceinline__ void ldmatrix4_t(uint32_t (&r)[4], uint32_t saddr)
                  : "memory");
 }
 
+// An 8 x 8 matrix of 16-bit elements spread over a warp (lane 4 r + c holds row
+// r, columns 2c and 2c + 1), transposed.
+__device__ __forceinline__ uint32_t transpose8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+
 // 16 bytes to shared memory behind the thread's back; zeros where !there
 // (nothing is read then).
 __device__ __forceinline__ void cp_async16(uint32_t saddr, const void *src, bool there)
 {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(saddr), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async16(uint32_t saddr, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(saddr), "l"(src) : "memory");
 }
 // The same for a stream whose next bytes are wanted soon: L2 fetches 256.
 __device__ __forceinline__ void cp_async16_ahead(uint32_t saddr, const void *src, bool there)
