@@ -18,6 +18,7 @@ from __future__ import annotations
 import ctypes
 import functools
 import os
+import struct
 import threading
 
 import torch
@@ -846,54 +847,56 @@ def fused_linear_cross_entropy_backward(dloss, lse, x, W, target, logit_scale=1.
     return dx, dW
 
 
-def _kv_cache(x, k_cache, v_cache, block_table):
-    """(KvCache, G, D) of caches [pages, page_size, G, D] and a block table
-    [rows, pages a row], of x's type and device."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+_CODES = {torch.float16: NGR_F16, torch.bfloat16: NGR_BF16}
+_pack_cache = struct.Struct("=QQqqqqqqqqQqqq").pack      # ngr_kv_cache
+
+
+def _kv_cache(dtype, index, k_cache, v_cache, block_table):
+    """(an ngr_kv_cache's bytes, G, D, tokens a row of the table has room for)
+    of caches [pages, page_size, G, D] of this type on device ``index`` and a
+    block table [rows, pages a row]."""
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError("the caches must be [pages, page_size, heads, dim] and alike")
-    if k_cache.dtype is not x.dtype or v_cache.dtype is not x.dtype:
+    if k_cache.dtype is not dtype or v_cache.dtype is not dtype:
         raise TypeError("all tensors must share one dtype")
     if block_table.dtype is not torch.int32:
         raise TypeError("block_table must be int32")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [rows, pages a row]")
-    index = x.get_device()
     if index < 0:
         raise ValueError("all tensors must be CUDA tensors")
     if k_cache.get_device() != index or v_cache.get_device() != index or block_table.get_device() != index:
         raise ValueError("all tensors must be on one CUDA device")
-    pages, size, G, D = k_cache.shape
+    pages, size, G, D = shape
     kp, kt, kh, kd = k_cache.stride()
     vp, vt, vh, vd = v_cache.stride()
     rows, width = block_table.shape
     step, one = block_table.stride()
     if (D > 1 and (kd != 1 or vd != 1)) or (width > 1 and one != 1):
         raise ValueError("the last dimension of the caches and of block_table must be contiguous")
-    return KvCache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, kp, kt, kh, vp, vt, vh,
-                   block_table.data_ptr(), rows, width, step), G, D
+    return (_pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, kp, kt, kh, vp, vt, vh,
+                        block_table.data_ptr(), rows, width, step), G, D, width * size)
 
 
-def _int32(what, device_index, n, *ts):
-    """The others (None left out) are contiguous int32 vectors of n entries."""
-    for t in ts:
-        if t is None:
-            continue
-        if t.dtype is not torch.int32:
-            raise TypeError(f"{what} must be int32")
-        if t.dim() != 1 or t.shape[0] != n or t.get_device() != device_index or not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous on the tensors' device, with one entry per token")
+def _int32(what, index, n, t):
+    """t is a contiguous int32 vector of n entries on device ``index``."""
+    if t.dtype is not torch.int32:
+        raise TypeError(f"{what} must be int32")
+    if t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous on the tensors' device, with one entry per token")
 
 
-def _heads_last(what, x, t, tokens, heads, dim):
-    """t's token and head strides, t [tokens, heads, dim] of x's type and device."""
-    if t.dtype is not x.dtype:
+def _heads_last(what, dtype, index, t, tokens, heads, dim):
+    """t's token and head strides, t [tokens, heads, dim] of this type and device."""
+    if t.dtype is not dtype:
         raise TypeError("all tensors must share one dtype")
-    if t.get_device() != x.get_device():
+    if t.get_device() != index:
         raise ValueError("all tensors must be on one CUDA device")
-    if t.dim() != 3 or t.shape[0] != tokens or (heads is not None and t.shape[1] != heads) or t.shape[2] != dim:
+    if t.shape != (tokens, heads, dim):
         raise ValueError(f"{what} must be [tokens, heads, dim], with the caches' dim (and heads, for k and v)")
     a, b, c = t.stride()
-    if dim > 1 and c != 1:
+    if c != 1 and dim > 1:
         raise ValueError(f"{what} must have contiguous heads")
     return a, b
 
@@ -915,21 +918,23 @@ def fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows
     is not there is left out as well; only the GPU sees it: to learn of it
     pass a ``workspace`` (256 bytes) and ask ``check_workspace``, or set
     NGR_DEBUG=1."""
-    code = _dtype_code(k)
-    cache, G, D = _kv_cache(k, k_cache, v_cache, block_table)
+    dtype, index = k.dtype, k.get_device()
+    code = _CODES[dtype] if dtype in _CODES else _dtype_code(k)
+    cache, G, D, _ = _kv_cache(dtype, index, k_cache, v_cache, block_table)
     T = k.shape[0]
-    index = k.get_device()
-    kt, kh = _heads_last("k", k, k, T, G, D)
-    vt, vh = _heads_last("v", k, v, T, G, D)
+    kt, kh = _heads_last("k", dtype, index, k, T, G, D)
+    vt, vh = _heads_last("v", dtype, index, v, T, G, D)
     H = qt = qh = ot = oh = 0
     if q is not None:
-        qt, qh = _heads_last("q", k, q, T, None, D)
-        H = q.shape[1]
+        H = q.shape[1] if q.dim() == 3 else 0
+        qt, qh = _heads_last("q", dtype, index, q, T, H, D)
         if q_out is not None:
-            ot, oh = _heads_last("q_out", k, q_out, T, H, D)
+            ot, oh = _heads_last("q_out", dtype, index, q_out, T, H, D)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _int32("positions and rows", index, T, positions, rows)
+    _int32("positions", index, T, positions)
+    if rows is not None:
+        _int32("rows", index, T, rows)
     rot = 0
     if inv_freq is not None:
         if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != index
@@ -941,14 +946,15 @@ def fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows
                      interleaved, q_out, workspace)
         return got[0]
     if q is not None and q_out is None:
-        q_out = torch.empty((T, H, D), dtype=q.dtype, device=q.device)
+        q_out = torch.empty((T, H, D), dtype=dtype, device=k.device)
         ot, oh = H * D, D
+    nbytes = 0
     if workspace is not None or _debug():
         workspace = _scratch(256, k.device, workspace)
+        nbytes = workspace.numel() * workspace.element_size()
     rc = lib().ngr_fused_rope_append_kv(
-        _ptr(q), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, ctypes.addressof(cache), positions.data_ptr(),
-        _ptr(rows), _ptr(inv_freq), rot, 1 if interleaved else 0, T, H, G, D, code, _ptr(q_out), ot, oh,
-        _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
+        _ptr(q), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, cache, positions.data_ptr(), _ptr(rows),
+        _ptr(inv_freq), rot, 1 if interleaved else 0, T, H, G, D, code, _ptr(q_out), ot, oh, _ptr(workspace), nbytes,
         _current_stream_handle(index))
     if rc != 0:
         raise NgrError(rc, "fused_rope_append_kv")
@@ -961,6 +967,7 @@ def _append_there(q, k, v, k_cache, v_cache, block_table, positions, rows, inv_f
                                  workspace, stream),)
 
 
+@functools.lru_cache(maxsize=1)         # (the library asks once, too)
 def _debug():
     """NGR_DEBUG: calls report what their kernels found."""
     return os.environ.get("NGR_DEBUG", "0") not in ("", "0")
@@ -980,17 +987,19 @@ def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     was (in ``out`` and ``lse`` when given).  A length beyond the table, or a
     page that is not there, is seen by the GPU alone, which leaves those tokens
     out: pass a ``workspace`` and ask ``check_workspace``, or set NGR_DEBUG=1."""
-    code = _dtype_code(q)
-    cache, G, D = _kv_cache(q, k_cache, v_cache, block_table)
-    B = q.shape[0]
-    index = q.get_device()
-    qr, qh = _heads_last("q", q, q, B, None, D)
-    H = q.shape[1]
+    dtype, index = q.dtype, q.get_device()
+    code = _CODES[dtype] if dtype in _CODES else _dtype_code(q)
+    cache, G, D, capacity = _kv_cache(dtype, index, k_cache, v_cache, block_table)
+    shape = q.shape
+    if len(shape) != 3:
+        raise ValueError("q must be [B, H, D]")
+    B, H, _ = shape
+    qr, qh = _heads_last("q", dtype, index, q, B, H, D)
     _int32("lengths", index, B, lengths)
-    if out is not None and (out.shape != q.shape or out.dtype is not q.dtype or out.get_device() != index
+    if out is not None and (out.shape != shape or out.dtype is not dtype or out.get_device() != index
                             or not out.is_contiguous()):
         raise ValueError("out must be contiguous, with q's shape, type and device")
-    if lse is not None and (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or lse.get_device() != index
+    if lse is not None and (lse.shape != (B, H) or lse.dtype is not torch.float32 or lse.get_device() != index
                             or not lse.is_contiguous()):
         raise ValueError("lse must be contiguous float32 [B, H] on q's device")
     if not _here(q, stream):
@@ -999,15 +1008,15 @@ def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
         return got if return_lse else got[0]
     if scale is None:
         scale = D ** -0.5
+    device = q.device
     if out is None:
-        out = torch.empty((B, H, D), dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=dtype, device=device)
     if lse is None and return_lse:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
-    ws = _scratch(ngr_paged_attention_workspace_bytes(B, H, G, D, cache.table_pages * cache.page_size, window),
-                  q.device, workspace)
+        lse = torch.empty((B, H), dtype=torch.float32, device=device)
+    ws = _scratch(ngr_paged_attention_workspace_bytes(B, H, G, D, capacity, window), device, workspace)
     rc = lib().ngr_fused_paged_attention(
-        q.data_ptr(), qr, qh, ctypes.addressof(cache), lengths.data_ptr(), scale, window, B, H, G, D, code,
-        out.data_ptr(), _ptr(lse), ws.data_ptr(), ws.numel() * ws.element_size(), _current_stream_handle(index))
+        q.data_ptr(), qr, qh, cache, lengths.data_ptr(), scale, window, B, H, G, D, code, out.data_ptr(), _ptr(lse),
+        ws.data_ptr(), ws.numel() * ws.element_size(), _current_stream_handle(index))
     if rc != 0:
         raise NgrError(rc, "fused_paged_attention")
     return (out, lse) if return_lse else out

@@ -6,9 +6,9 @@
 //   or (2i, 2i + 1) interleaved; dimensions from rot on are copied.
 //
 // Every element is read once and written once, so memory bounds it: 2 (H + 2 G)
-// D elements a token.  A thread moves one pair of 16-byte pieces (a unit),
-// whose loads start before the position and the page are known, so that
-// a block waits for memory twice (position, table) and not three times.
+// D elements a token.  A thread moves pairs of 16-byte pieces (units), whose
+// loads start before the position and the page are known, so that a block
+// waits for memory twice (position, table) and not three times.
 #include "ngr.h"
 #include "ngr_entry.h"
 #include "ngr_internal.h"
@@ -59,21 +59,24 @@ template <> struct Piece<4> { using T = uint2; };
 template <> struct Piece<2> { using T = uint32_t; };
 template <> struct Piece<1> { using T = uint16_t; };
 
-template <bool BF16>
-__device__ __forceinline__ float to_f(uint16_t v)
+// Two elements of a piece (or its only one) as floats, and back.
+template <bool BF16, int VEC>
+__device__ __forceinline__ float2 get2(const uint16_t (&e)[VEC], int i)
 {
-    if (BF16) return __uint_as_float(static_cast<uint32_t>(v) << 16);
-    return __half2float(__ushort_as_half(v));
+    return unpack16<BF16>(VEC > 1 ? reinterpret_cast<const uint32_t *>(e)[i / 2] : static_cast<uint32_t>(e[0]));
 }
-template <bool BF16>
-__device__ __forceinline__ uint16_t from_f(float v)
+template <bool BF16, int VEC>
+__device__ __forceinline__ void set2(uint16_t (&e)[VEC], int i, float x, float y)
 {
-    return static_cast<uint16_t>(pack16<BF16>(v, 0.0f));
+    const uint32_t v = pack16<BF16>(x, y);
+    if (VEC > 1) reinterpret_cast<uint32_t *>(e)[i / 2] = v;
+    else e[0] = static_cast<uint16_t>(v);
 }
 
 // The units of a head: of each, two pieces of VEC elements from `first` and
-// `second` on (second < 0: one piece).  Pair units rotate the pieces against
-// one another, inner units each within itself; others are copied.
+// `second` on (second < 0: one piece; first past D: none).  Pair units rotate
+// the pieces against one another, inner units each within itself; others are
+// copied.
 enum { kCopy = 0, kPair = 1, kInner = 2 };
 struct Unit {
     int first, second, kind;
@@ -123,25 +126,28 @@ __device__ __forceinline__ int page_of(const AppendArgs &a, int t, int position,
     return page;
 }
 
-template <bool BF16, int VEC, bool INTERLEAVED>
+// A block has one token: its threads stand for `a.units` units of
+// threads / a.units heads, EACH times over, so that a thread's units are the
+// same one of different heads and turn by the same angles.
+template <bool BF16, int VEC, bool INTERLEAVED, int EACH>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a)
 {
     using P = typename Piece<VEC>::T;
     union Data {
         P p;
         uint16_t e[VEC];
+        __device__ Data() {}
     };
+    constexpr int kAngles = INTERLEAVED && VEC > 1 ? VEC / 2 : VEC;     // of a piece
     __shared__ float2 turn[kAttendMaxDim / 2];
+    const int threads = static_cast<int>(blockDim.x);
     if (a.err && blockIdx.x == 0) {
         // The error word by one block: the others leave bad tokens out, and
         // without a launch of its own nothing could clear the word for them.
         bool bad = false;
-        for (int t = threadIdx.x; t < a.T; t += kAppendThreads) page_of(a, t, a.positions[t], &bad);
-        if (__syncthreads_or(bad) == 0) {
-            if (threadIdx.x == 0) *a.err = 0;
-        } else if (threadIdx.x == 0) {
-            *a.err = kDevErrPage;
-        }
+        for (int t = threadIdx.x; t < a.T; t += threads) page_of(a, t, a.positions[t], &bad);
+        const int any = __syncthreads_or(bad);
+        if (threadIdx.x == 0) *a.err = any ? kDevErrPage : 0;
         return;
     }
     const unsigned block = blockIdx.x - (a.err ? 1u : 0u);
@@ -149,87 +155,92 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const int part = static_cast<int>(block - static_cast<unsigned>(t) * a.blocks_per_token);
     const int position = a.positions[t];
 
-    int i = part * kAppendThreads + static_cast<int>(threadIdx.x);
-    const int per = units_of_head(VEC, INTERLEAVED, a.D, a.rot), turned = (a.H + a.G) * per;
-    const bool any_turned = part * kAppendThreads < turned;
-    const uint16_t *src = nullptr;
-    int head = 0, what = 3;     // 0 q, 1 k, 2 v, 3 nothing
-    Unit u = {0, -1, kCopy};
-    if (i < turned) {
-        head = i / per;
-        u = unit_of<VEC, INTERLEAVED>(i - head * per, a.D, a.rot);
-        what = head < a.H ? 0 : 1;
-        if (what == 0) {
-            src = static_cast<const uint16_t *>(a.q) + t * a.q_token + head * a.q_head;
-        } else {
-            head -= a.H;
-            src = static_cast<const uint16_t *>(a.k) + t * a.k_token + head * a.k_head;
-        }
-    } else {
-        i -= turned;
-        const int each = units_of_head(VEC, false, a.D, 0);
-        if (i < a.G * each) {
-            head = i / each;
-            u = unit_of<VEC, false>(i - head * each, a.D, 0);
-            what = 2;
-            src = static_cast<const uint16_t *>(a.v) + t * a.v_token + head * a.v_head;
-        }
-    }
-    Data x, y;
-    if (src) {
-        x.p = *reinterpret_cast<const P *>(src + u.first);
-        if (u.second >= 0) y.p = *reinterpret_cast<const P *>(src + u.second);
+    const int step = threads / a.units, row = static_cast<int>(threadIdx.x) / a.units;
+    const int i = static_cast<int>(threadIdx.x) - row * a.units, first = part * step * EACH + row;
+    const Unit turned = unit_of<VEC, INTERLEAVED>(i, a.D, a.rot), plain = unit_of<VEC, false>(i, a.D, 0);
+    Data x[EACH], y[EACH];
+#pragma unroll
+    for (int n = 0; n < EACH; ++n) {
+        const int head = first + n * step;
+        const uint16_t *src;
+        if (head < a.H) src = static_cast<const uint16_t *>(a.q) + t * a.q_token + head * a.q_head;
+        else if (head < a.H + a.G) src = static_cast<const uint16_t *>(a.k) + t * a.k_token + (head - a.H) * a.k_head;
+        else if (head < a.H + 2 * a.G) src = static_cast<const uint16_t *>(a.v) + t * a.v_token + (head - a.H - a.G) * a.v_head;
+        else continue;
+        const Unit &u = head < a.H + a.G ? turned : plain;
+        if (u.first < a.D) x[n].p = *reinterpret_cast<const P *>(src + u.first);
+        if (u.second >= 0) y[n].p = *reinterpret_cast<const P *>(src + u.second);
     }
     bool bad = false;
     const int page = page_of(a, t, position, &bad);
     if (page < 0) return;      // (the whole block: it has one token)
-    if (any_turned) {
-        for (int f = threadIdx.x; f < a.rot / 2; f += kAppendThreads) turn[f] = rotation(a.inv_freq[f], position);
-        __syncthreads();
+    for (int f = threadIdx.x; f < a.rot / 2; f += threads) turn[f] = rotation(a.inv_freq[f], position);
+    __syncthreads();
+    // the angles of the pieces, one after the other in `turn`
+    constexpr int kTurned = INTERLEAVED && VEC > 1 ? 2 : 1;     // pieces that have angles of their own
+    float2 cs[kTurned][kAngles];
+    bool turns[kTurned];
+#pragma unroll
+    for (int h = 0; h < kTurned; ++h) {
+        const int at = h ? turned.second : turned.first;
+        turns[h] = turned.kind == kInner ? at >= 0 && at < a.rot : turned.kind == kPair;
+        const int from = turned.kind == kInner || INTERLEAVED ? at / 2 : at;
+#pragma unroll
+        for (int e = 0; e < kAngles; ++e) cs[h][e] = turns[h] ? turn[from + e] : make_float2(1.0f, 0.0f);
     }
-    if (!src) return;
-    if (u.kind == kPair) {
+    const int64_t slot = position - position / a.kv.page_size * a.kv.page_size;
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-            const float2 cs = turn[INTERLEAVED ? u.first / 2 : u.first + e];
-            const float p = to_f<BF16>(x.e[e]), q = to_f<BF16>(y.e[e]);
-            x.e[e] = from_f<BF16>(p * cs.x - q * cs.y);
-            y.e[e] = from_f<BF16>(p * cs.y + q * cs.x);
-        }
-    } else if (INTERLEAVED && VEC > 1 && u.kind == kInner) {
+    for (int n = 0; n < EACH; ++n) {
+        const int head = first + n * step;
+        uint16_t *dst;
+        if (head < a.H)
+            dst = static_cast<uint16_t *>(a.q_out) + t * a.qo_token + head * a.qo_head;
+        else if (head < a.H + a.G)
+            dst = static_cast<uint16_t *>(a.kv.k) + page * a.kv.k_page + slot * a.kv.k_token + (head - a.H) * a.kv.k_head;
+        else if (head < a.H + 2 * a.G)
+            dst = static_cast<uint16_t *>(a.kv.v) + page * a.kv.v_page + slot * a.kv.v_token + (head - a.H - a.G) * a.kv.v_head;
+        else
+            break;
+        const bool is_v = head >= a.H + a.G;
+        if (!is_v) {
+            if constexpr (INTERLEAVED && VEC > 1) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            Data &d = h ? y : x;
-            const int at = h ? u.second : u.first;
-            if (at < 0 || at >= a.rot) continue;
+                for (int h = 0; h < 2; ++h) {
+                    if (!turns[h]) continue;
+                    Data &d = h ? y[n] : x[n];
 #pragma unroll
-            for (int e = 0; e + 1 < VEC; e += 2) {
-                const float2 cs = turn[(at + e) / 2];
-                const float p = to_f<BF16>(d.e[e]), q = to_f<BF16>(d.e[e + 1]);
-                d.e[e] = from_f<BF16>(p * cs.x - q * cs.y);
-                d.e[e + 1] = from_f<BF16>(p * cs.y + q * cs.x);
+                    for (int e = 0; e < VEC; e += 2) {
+                        const float2 v = get2<BF16>(d.e, e), c = cs[h][e / 2];
+                        set2<BF16>(d.e, e, v.x * c.x - v.y * c.y, v.x * c.y + v.y * c.x);
+                    }
+                }
+            } else if (turns[0]) {
+#pragma unroll
+                for (int e = 0; e < VEC; e += 2) {
+                    const float2 p = get2<BF16>(x[n].e, e), q = get2<BF16>(y[n].e, e);
+                    const float2 c = cs[0][e], d = cs[0][VEC > 1 ? e + 1 : e];
+                    set2<BF16>(x[n].e, e, p.x * c.x - q.x * c.y, p.y * d.x - q.y * d.y);
+                    set2<BF16>(y[n].e, e, p.x * c.y + q.x * c.x, p.y * d.y + q.y * d.x);
+                }
             }
         }
+        const Unit &u = is_v ? plain : turned;
+        if (u.first < a.D) *reinterpret_cast<P *>(dst + u.first) = x[n].p;
+        if (u.second >= 0) *reinterpret_cast<P *>(dst + u.second) = y[n].p;
     }
-    uint16_t *dst;
-    if (what == 0) {
-        dst = static_cast<uint16_t *>(a.q_out) + t * a.qo_token + head * a.qo_head;
-    } else {
-        const int64_t slot = position - position / a.kv.page_size * a.kv.page_size;
-        dst = what == 1 ? static_cast<uint16_t *>(a.kv.k) + page * a.kv.k_page + slot * a.kv.k_token + head * a.kv.k_head
-                        : static_cast<uint16_t *>(a.kv.v) + page * a.kv.v_page + slot * a.kv.v_token + head * a.kv.v_head;
-    }
-    *reinterpret_cast<P *>(dst + u.first) = x.p;
-    if (u.second >= 0) *reinterpret_cast<P *>(dst + u.second) = y.p;
 }
 
 template <bool BF16, int VEC>
 void launch(bool interleaved, const AppendArgs &a, unsigned grid, cudaStream_t stream)
 {
-    if (interleaved)
-        append_kernel<BF16, VEC, true><<<grid, kAppendThreads, 0, stream>>>(a);
-    else
-        append_kernel<BF16, VEC, false><<<grid, kAppendThreads, 0, stream>>>(a);
+    const unsigned threads = static_cast<unsigned>(a.threads);
+    if (a.each > 1) {
+        if (interleaved) append_kernel<BF16, VEC, true, kAppendEach><<<grid, threads, 0, stream>>>(a);
+        else append_kernel<BF16, VEC, false, kAppendEach><<<grid, threads, 0, stream>>>(a);
+    } else {
+        if (interleaved) append_kernel<BF16, VEC, true, 1><<<grid, threads, 0, stream>>>(a);
+        else append_kernel<BF16, VEC, false, 1><<<grid, threads, 0, stream>>>(a);
+    }
 }
 template <bool BF16>
 void launch(int vec, bool interleaved, const AppendArgs &a, unsigned grid, cudaStream_t stream)
@@ -242,10 +253,11 @@ void launch(int vec, bool interleaved, const AppendArgs &a, unsigned grid, cudaS
 
 }  // namespace
 
-int64_t append_units(int vec, bool interleaved, int64_t H, int64_t G, int64_t D, int64_t rot)
+int append_units(int vec, bool interleaved, int64_t D, int64_t rot)
 {
-    const int d = static_cast<int>(D), r = static_cast<int>(rot);
-    return (H + G) * units_of_head(vec, interleaved, d, r) + G * units_of_head(vec, false, d, 0);
+    const int d = static_cast<int>(D), turned = units_of_head(vec, interleaved, d, static_cast<int>(rot));
+    const int plain = units_of_head(vec, false, d, 0);
+    return turned > plain ? turned : plain;
 }
 
 int launch_append(bool bf16, int vec, bool interleaved, const AppendArgs &a, cudaStream_t stream)

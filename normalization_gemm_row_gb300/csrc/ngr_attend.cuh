@@ -20,6 +20,9 @@
 // one run is finished there; the others' parts (FP32 sums, maximum, sum of
 // exponentials) are joined by a second kernel in the tokens' order, so a call
 // repeated gives the same bits.
+//
+// Few items of short contexts take a CTA each ("solo"): its warps share the
+// item's tiles and join their parts in shared memory, without a second launch.
 #pragma once
 
 #include "ngr.h"
@@ -28,6 +31,8 @@
 #include "ngr_kv.h"
 #include "ngr_mma.cuh"
 #include "ngr_ptx.cuh"
+
+#include <type_traits>
 
 namespace ngr {
 
@@ -163,17 +168,77 @@ __device__ __forceinline__ void fetch(const void *cache, const Pieces<DP, FULL> 
     }
 }
 
+// One row of an item's output from at most 32 parts, by a warp: ml(i) is part
+// i's (maximum, sum), o(i, at) its sums of dimensions at to at + 3.
+template <bool BF16, int DP, typename Ml, typename O>
+__device__ __forceinline__ void join_row(const AttendArgs &a, int parts, int64_t head, Ml ml, O o)
+{
+    constexpr int kEach = (DP / 4 + 31) / 32;
+    const int lane = threadIdx.x & 31;
+    const float2 mine = lane < parts ? ml(lane) : make_float2(-INFINITY, 0.0f);
+    float top = mine.x;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+    const float w = exp2_fast(mine.x - (top == -INFINITY ? 0.0f : top));
+    float total = w * mine.y;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
+    float4 acc[kEach] = {};
+#pragma unroll 4
+    for (int i = 0; i < parts; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int at = (e * 32 + lane) * 4;
+            if (at >= DP) break;
+            const float4 v = o(i, at);
+            acc[e].x = fmaf(wi, v.x, acc[e].x);
+            acc[e].y = fmaf(wi, v.y, acc[e].y);
+            acc[e].z = fmaf(wi, v.z, acc[e].z);
+            acc[e].w = fmaf(wi, v.w, acc[e].w);
+        }
+    }
+    const float by = total == 0.0f ? 0.0f : 1.0f / total;
+    uint16_t *out = static_cast<uint16_t *>(a.out) + head * a.D;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e)
+        if ((e * 32 + lane) * 4 < a.D)
+            *reinterpret_cast<uint2 *>(out + (e * 32 + lane) * 4) =
+                make_uint2(pack16<BF16>(acc[e].x * by, acc[e].y * by), pack16<BF16>(acc[e].z * by, acc[e].w * by));
+    if (a.lse && lane == 0) a.lse[head] = total == 0.0f ? -INFINITY : top * kLn2 + logf(total);
+}
+
+// The error word by one block: lengths beyond the table, and pages that are
+// not there, of all rows.
+__device__ __forceinline__ void check_pages(const AttendArgs &a)
+{
+    bool bad = false;
+    for (int b = 0; b < a.B; ++b) {
+        const Span s = span_of(a, b, &bad);
+        if (s.n == 0) continue;
+        for (int i = s.start / a.kv.page_size + static_cast<int>(threadIdx.x); i <= (s.start + s.n - 1) / a.kv.page_size;
+             i += static_cast<int>(blockDim.x)) {
+            const int page = a.kv.table[b * a.kv.table_stride + i];
+            bad = bad || page < 0 || page >= a.kv.pages;
+        }
+    }
+    const int any = __syncthreads_or(bad);
+    if (threadIdx.x == 0) *a.err = any ? kDevErrPage : 0;
+}
+
 // NB: blocks of 8 query heads that a warp takes at once, 1 or 2.
-template <bool BF16, int DP, int NB, bool FULL>
+template <bool BF16, int DP, int NB, bool FULL, bool SOLO>
 __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(const __grid_constant__ AttendArgs a)
 {
     using R = Ring<DP, NB>;
     constexpr int kWarps = R::kWarps, kThreads = R::kThreads, S = R::kStages;
     constexpr int kSteps = DP / 16;
     extern __shared__ __align__(128) uint8_t ring[];
-    __shared__ long long before[kThreads + 1];
-    __shared__ long long warp_total[kWarps];
+    __shared__ long long before[SOLO ? 1 : kThreads + 1];
+    __shared__ long long warp_total[SOLO ? 1 : kWarps];
     __shared__ uint32_t seen[kWarps][R::kTiles];
+    __shared__ float2 solo_ml[SOLO ? kWarps : 1][kAttendRows];
+    static_assert(kAttendRows / 2 * NB * DP * 4 <= R::kBytes, "a part in a warp's ring");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int items = a.G * a.blocks;
@@ -183,10 +248,25 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         for (int i = threadIdx.x; i < kWarps * R::kBytes / 16; i += kThreads)
             reinterpret_cast<uint4 *>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
 
-    // Tiles before each run of `each` sequences.
-    const int each = (a.B + kThreads - 1) / kThreads;
     bool bad = false;
-    {
+    Place c;
+    long long share = 1, first = 0;
+    int worker = warp, count;
+    if constexpr (SOLO) {
+        if (static_cast<int>(blockIdx.x) == a.B * items) {      // a block that only looks for bad pages
+            check_pages(a);
+            return;
+        }
+        c.b = static_cast<int>(blockIdx.x) / items;
+        c.item = static_cast<int>(blockIdx.x) - c.b * items;
+        c.s = span_of(a, c.b, &bad);
+        share = (c.s.tiles + kWarps - 1) / kWarps;
+        c.tile = worker * static_cast<int>(share);
+        count = max(0, min(static_cast<int>(share), c.s.tiles - c.tile));
+        if (!FULL) __syncthreads();
+    } else {
+        // Tiles before each run of `each` sequences.
+        const int each = (a.B + kThreads - 1) / kThreads;
         long long mine = 0;
         for (int i = 0; i < each; ++i) {
             const int b = static_cast<int>(threadIdx.x) * each + i;
@@ -205,21 +285,16 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         before[threadIdx.x + 1] = base + incl;
         if (threadIdx.x == 0) before[0] = 0;
         __syncthreads();
-    }
-    bad = false;      // (counted by whoever works on the sequence)
-    const long long total = before[kThreads];
-    long long share = (total + a.workers - 1) / a.workers;
-    if (share < a.min_share) share = a.min_share;
-    // Neighbouring runs on different SMs: a few runs have an SM each.
-    const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-    const long long first = worker * share;
-    long long left = total - first;
-    const int count = static_cast<int>(left <= 0 ? 0 : left < share ? left : share);
-    AttendJob job = {-1, -1, 0, 0};
-
-    if (count > 0) {
-        Place c;
-        {
+        bad = false;      // (counted by whoever works on the sequence)
+        const long long total = before[kThreads];
+        share = (total + a.workers - 1) / a.workers;
+        if (share < a.min_share) share = a.min_share;
+        // Neighbouring runs on different SMs: a few runs have an SM each.
+        worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
+        first = worker * share;
+        const long long left = total - first;
+        count = static_cast<int>(left <= 0 ? 0 : left < share ? left : share);
+        if (count > 0) {
             int lo = 0, hi = kThreads;       // before[lo] <= first < before[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
@@ -238,6 +313,11 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             c.item = static_cast<int>((first - at) / s.tiles);
             c.tile = static_cast<int>((first - at) - static_cast<long long>(c.item) * s.tiles);
         }
+    }
+    AttendJob job = {-1, -1, 0, 0};
+    const Place at_start = c;      // solo: the CTA's item
+
+    if (count > 0) {
         Place f = c;
         const Pieces<DP, FULL> pieces(a.D, lane);
         const uint32_t base = smem_u32(ring) + warp * R::kBytes;
@@ -246,7 +326,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         uint32_t k_at = kNowhere, v_at = kNowhere;
         bool all = false;                  // the tile has all its tokens
         int left = count, issued = 0;      // tiles to issue, issued
-        auto locate = [&](int entry, int slot) {
+        auto locate = [&](const Place &f, int entry, int slot) {
             k_at = v_at = kNowhere;
             if (entry != kNone) {
                 if (entry >= 0 && entry < a.kv.pages) {
@@ -258,14 +338,13 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                 }
             }
         };
-        auto issue_keys = [&](int entry, int slot, int stage) {
+        auto issue_keys = [&](const Place &f, int entry, int slot, int stage) {
             if (left > 0) {
-                locate(entry, slot);
+                locate(f, entry, slot);
                 const uint32_t there = __ballot_sync(0xffffffffu, k_at != kNowhere);
                 all = there == 0xffffffffu;
                 if (lane == 0) seen[warp][issued % R::kTiles] = there;
                 fetch<DP, FULL>(a.kv.k, pieces, k_at, all, base + stage * R::kStage, lane);
-                advance(a, f, &bad);
                 ++issued;
             }
             --left;
@@ -276,14 +355,21 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             cp_async_commit();
         };
         auto entry_ahead = [&](int *slot) { return left > 0 ? page_entry(a, f, lane, slot) : kNone; };
+        {
+            // The first tiles' table entries are asked for together.
+            constexpr int kFirst = (S + 1) / 2;
+            Place at[kFirst];
+            int entry[kFirst], slot[kFirst] = {};
 #pragma unroll
-        for (int i = 0; i < S; ++i) {
-            if (i % 2 == 0) {
-                int slot = 0;
-                const int entry = entry_ahead(&slot);
-                issue_keys(entry, slot, i);
-            } else {
-                issue_values(i);
+            for (int j = 0; j < kFirst; ++j) {
+                at[j] = f;
+                entry[j] = j < count ? page_entry(a, f, lane, &slot[j]) : kNone;
+                if (j < count) advance(a, f, &bad);
+            }
+#pragma unroll
+            for (int i = 0; i < S; ++i) {
+                if (i % 2 == 0) issue_keys(at[i / 2], entry[i / 2], slot[i / 2], i);
+                else issue_values(i);
             }
         }
 
@@ -293,7 +379,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         float o[kSteps][NB][4], top[NB][2], sum[NB][2];
         uint32_t q[kSteps][NB][2];
         bool fresh = true;         // a new item
-        bool whole = c.tile == 0;  // this worker has the item's beginning
+        bool whole = !SOLO && c.tile == 0;  // this worker has the item's beginning
         int stage = 0;
         for (int i = 0; i < count; ++i) {
             int slot = 0;
@@ -342,7 +428,22 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                 }
             }
             __syncwarp();
-            if (S % 2 == 0) issue_keys(entry, slot, stage);
+            auto next_keys = [&] {
+                issue_keys(f, entry, slot, stage);
+                if (left >= 0) {
+                    advance(a, f, &bad);
+                    // a new item's queries on their way, for when its first tile is taken
+                    if (f.tile == 0 && left > 0 && lane < kAttendRows) {
+                        const int kv_head = f.item / a.blocks, block = f.item - kv_head * a.blocks;
+                        const int r = kv_head * a.group + block * kAttendRows + lane;
+                        if (lane < min(kAttendRows, a.group - block * kAttendRows))
+#pragma unroll
+                            for (int d = 0; d < DP * 2; d += 128)
+                                asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint8_t *>(a.q) + (f.b * a.q_row + r * a.q_head) * 2 + d));
+                    }
+                }
+            };
+            if (S % 2 == 0) next_keys();
             else issue_values(stage);
             stage = stage + 1 == S ? 0 : stage + 1;
             // in units of log 2, those that are not there out
@@ -413,7 +514,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             }
             __syncwarp();
             if (S % 2 == 0) issue_values(stage);
-            else issue_keys(entry, slot, stage);
+            else next_keys();
             stage = stage + 1 == S ? 0 : stage + 1;
 
             const bool ends = c.tile + 1 == c.s.tiles;
@@ -427,7 +528,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) sum[n][h] += __shfl_xor_sync(0xffffffffu, sum[n][h], x);
-                if (ends && whole) {
+                if (!SOLO && ends && whole) {
                     if (c.s.used) {
 #pragma unroll
                         for (int n = 0; n < NB; ++n)
@@ -452,14 +553,20 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                         a.jobs[static_cast<int64_t>(c.b) * items + c.item] = AttendJob{-1, -1, 0, 0};
                 } else {
                     const int64_t part = (static_cast<int64_t>(worker) * 2 + (whole ? 1 : 0)) * a.part_rows;
+                    if (SOLO) {      // (the ring is empty: its copies are done)
+                        cp_async_wait<0>();
+                        __syncwarp();
+                    }
+                    float2 *part_ml = SOLO ? solo_ml[SOLO ? warp : 0] : a.part_ml + part;
+                    float *part_o = SOLO ? reinterpret_cast<float *>(ring + warp * R::kBytes) : a.part_o + part * DP;
 #pragma unroll
                     for (int n = 0; n < NB; ++n)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const int r = 8 * n + 2 * t + h;
                             if (r >= rows) continue;
-                            if (g == 0) a.part_ml[part + r] = make_float2(top[n][h], sum[n][h]);
-                            float *po = a.part_o + (part + r) * DP + g;
+                            if (g == 0) part_ml[r] = make_float2(top[n][h], sum[n][h]);
+                            float *po = part_o + r * DP + g;
 #pragma unroll
                             for (int k = 0; k < kSteps; ++k) {
                                 po[k * 16] = o[k][n][h];
@@ -477,6 +584,19 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             advance(a, c, &bad);
         }
         cp_async_wait<0>();
+    }
+    if constexpr (SOLO) {
+        __syncthreads();
+        const int kv_head = at_start.item / a.blocks, block = at_start.item - kv_head * a.blocks;
+        const int rows = min(kAttendRows, a.group - block * kAttendRows);
+        const int parts = (at_start.s.tiles + static_cast<int>(share) - 1) / static_cast<int>(share);
+        if (!at_start.s.used) return;
+        for (int row = warp; row < rows; row += kWarps)
+            join_row<BF16, DP>(
+                a, parts, static_cast<int64_t>(at_start.b) * a.H + kv_head * a.group + block * kAttendRows + row,
+                [&](int i) { return solo_ml[i][row]; },
+                [&](int i, int at) { return *reinterpret_cast<const float4 *>(ring + i * R::kBytes + (row * DP + at) * 4); });
+        return;
     }
     if (!a.slot_by_item && lane == 0) a.jobs[worker] = job;
     const bool any = __any_sync(0xffffffffu, bad);
@@ -532,32 +652,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
 
     if (parts <= 32) {
         if (blockIdx.y > 0) return;
-        for (int row = warp; row < rows; row += kJoinWarps) {
-            const float2 ml = lane < parts ? a.part_ml[part(lane, row)] : make_float2(-INFINITY, 0.0f);
-            float top = ml.x;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
-            const float w = exp2_fast(ml.x - (top == -INFINITY ? 0.0f : top));
-            float total = w * ml.y;
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) total += __shfl_xor_sync(0xffffffffu, total, x);
-            float4 acc[kEach] = {};
-#pragma unroll 4
-            for (int i = 0; i < parts; ++i) {
-                const float wi = __shfl_sync(0xffffffffu, w, i);
-                float4 v[kEach];
-                load(v, i, row);
-                add_scaled(acc, v, wi);
-            }
-            const float by = total == 0.0f ? 0.0f : 1.0f / total;
-            uint16_t *out = static_cast<uint16_t *>(a.out) + (head0 + row) * a.D;
-#pragma unroll
-            for (int e = 0; e < kEach; ++e)
-                if ((e * 32 + lane) * 4 < a.D)
-                    *reinterpret_cast<uint2 *>(out + (e * 32 + lane) * 4) =
-                        make_uint2(pack16<BF16>(acc[e].x * by, acc[e].y * by), pack16<BF16>(acc[e].z * by, acc[e].w * by));
-            if (a.lse && lane == 0) a.lse[head0 + row] = total == 0.0f ? -INFINITY : top * kLn2 + logf(total);
-        }
+        for (int row = warp; row < rows; row += kJoinWarps)
+            join_row<BF16, DP>(
+                a, parts, head0 + row, [&](int i) { return a.part_ml[part(i, row)]; },
+                [&](int i, int at) { return __ldcg(reinterpret_cast<const float4 *>(a.part_o + part(i, row) * DP + at)); });
         return;
     }
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
@@ -618,26 +716,26 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
     }
 }
 
-template <bool BF16, int DP, int NB, bool FULL>
+template <bool BF16, int DP, int NB, bool FULL, bool SOLO>
 cudaError_t attend(const AttendArgs &a, cudaStream_t stream)
 {
     using R = Ring<DP, NB>;
     constexpr int kSmem = R::kWarps * R::kBytes;
     // (an attribute of the device's copy of the function: set at every call,
     // as the current device may be another)
-    cudaError_t e = cudaFuncSetAttribute(attend_kernel<BF16, DP, NB, FULL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    cudaError_t e = cudaFuncSetAttribute(attend_kernel<BF16, DP, NB, FULL, SOLO>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
-    attend_kernel<BF16, DP, NB, FULL><<<a.workers / R::kWarps, R::kThreads, kSmem, stream>>>(a);
+    attend_kernel<BF16, DP, NB, FULL, SOLO><<<SOLO ? a.B * a.G * a.blocks + 1 : a.workers / R::kWarps, R::kThreads, kSmem, stream>>>(a);
     return cudaGetLastError();
 }
-template <bool BF16, int DP, bool PADDED>
+template <bool BF16, int DP, bool PADDED, bool SOLO>
 cudaError_t attend(const AttendArgs &a, cudaStream_t stream)
 {
     if constexpr (PADDED) {
         if (a.D < DP)
-            return attend_heads(a.group) == 1 ? attend<BF16, DP, 1, false>(a, stream) : attend<BF16, DP, 2, false>(a, stream);
+            return attend_heads(a.group) == 1 ? attend<BF16, DP, 1, false, SOLO>(a, stream) : attend<BF16, DP, 2, false, SOLO>(a, stream);
     }
-    return attend_heads(a.group) == 1 ? attend<BF16, DP, 1, true>(a, stream) : attend<BF16, DP, 2, true>(a, stream);
+    return attend_heads(a.group) == 1 ? attend<BF16, DP, 1, true, SOLO>(a, stream) : attend<BF16, DP, 2, true, SOLO>(a, stream);
 }
 
 template <bool BF16, int DP>
@@ -659,28 +757,33 @@ cudaError_t join(const AttendArgs &a, cudaStream_t stream)
     return cudaLaunchKernelEx(&cfg, attend_join_kernel<BF16, DP>, a);
 }
 
-template <bool BF16>
-cudaError_t by_dim(bool joining, const AttendArgs &a, cudaStream_t stream)
+// Calls f with the padded dimension, and whether smaller ones share it.
+template <typename F>
+cudaError_t by_dim(int64_t D, F f)
 {
-    switch (attend_dim(a.D)) {
-    case 64: return joining ? join<BF16, 64>(a, stream) : attend<BF16, 64, true>(a, stream);
-    case 80: return joining ? join<BF16, 80>(a, stream) : attend<BF16, 80, false>(a, stream);
-    case 96: return joining ? join<BF16, 96>(a, stream) : attend<BF16, 96, false>(a, stream);
-    case 128: return joining ? join<BF16, 128>(a, stream) : attend<BF16, 128, true>(a, stream);
-    case 192: return joining ? join<BF16, 192>(a, stream) : attend<BF16, 192, false>(a, stream);
-    default: return joining ? join<BF16, 256>(a, stream) : attend<BF16, 256, true>(a, stream);
+    switch (attend_dim(D)) {
+    case 64: return f(std::integral_constant<int, 64>(), std::true_type());
+    case 80: return f(std::integral_constant<int, 80>(), std::false_type());
+    case 96: return f(std::integral_constant<int, 96>(), std::false_type());
+    case 128: return f(std::integral_constant<int, 128>(), std::true_type());
+    case 192: return f(std::integral_constant<int, 192>(), std::false_type());
+    default: return f(std::integral_constant<int, 256>(), std::true_type());
     }
 }
 
-}  // namespace
-
-// (one translation unit for each type, which defines its name and kind)
-#define NGR_JOINED2(a, b) a##b
-#define NGR_JOINED(a, b) NGR_JOINED2(a, b)
-int NGR_JOINED(launch_attend_, NGR_ATTEND_TYPE)(bool joining, const AttendArgs &a, cudaStream_t stream)
+template <bool BF16, bool SOLO>
+int run_attend(const AttendArgs &a, cudaStream_t stream)
 {
-    const cudaError_t e = by_dim<NGR_ATTEND_BF16>(joining, a, stream);
-    return e == cudaSuccess ? 0 : record_cuda_error(joining ? "paged attention join launch" : "paged attention launch", e, cudaGetErrorString(e));
+    const cudaError_t e = by_dim(a.D, [&](auto dim, auto padded) { return attend<BF16, dim(), padded(), SOLO>(a, stream); });
+    return e == cudaSuccess ? 0 : record_cuda_error("paged attention launch", e, cudaGetErrorString(e));
 }
+template <bool BF16>
+int run_join(const AttendArgs &a, cudaStream_t stream)
+{
+    const cudaError_t e = by_dim(a.D, [&](auto dim, auto) { return join<BF16, dim()>(a, stream); });
+    return e == cudaSuccess ? 0 : record_cuda_error("paged attention join launch", e, cudaGetErrorString(e));
+}
+
+}  // namespace
 
 }  // namespace ngr

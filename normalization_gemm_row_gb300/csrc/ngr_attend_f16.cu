@@ -1,4 +1,7 @@
 // ngr_attend_f16.cu -- the paged attention's kernels for f16.
-#define NGR_ATTEND_TYPE f16
-#define NGR_ATTEND_BF16 false
 #include "ngr_attend.cuh"
+
+namespace ngr {
+int launch_attend_f16(const AttendArgs &a, cudaStream_t stream) { return run_attend<false, false>(a, stream); }
+int launch_attend_join_f16(const AttendArgs &a, cudaStream_t stream) { return run_join<false>(a, stream); }
+}  // namespace ngr

@@ -33,13 +33,14 @@ struct AppendArgs {
     const float *inv_freq;
     int *err;                 // null: nothing is reported
     int T, H, G, D, rot;
-    int blocks_per_token;
+    int units, blocks_per_token, threads, each;     // units of a head; of `each` heads a thread
 };
-constexpr int kAppendThreads = 256;
+constexpr int kAppendThreads = 256;    // a block, at most
+constexpr int kAppendEach = 4;         // heads a thread of a large call
 // vec: elements that one access moves (8, 4, 2 or 1).
 int launch_append(bool bf16, int vec, bool interleaved, const AppendArgs &a, cudaStream_t stream);
-// Units (thread's work) of one token, of which a block takes kAppendThreads.
-int64_t append_units(int vec, bool interleaved, int64_t H, int64_t G, int64_t D, int64_t rot);
+// Units (pairs of accesses) of a head, at most kAppendThreads.
+int append_units(int vec, bool interleaved, int64_t D, int64_t rot);
 
 constexpr int kAttendMaxDim = 256;
 constexpr int kAttendRows = 16;    // query heads of one key head that a warp takes at once
@@ -88,12 +89,11 @@ inline int attend_dim(int64_t D)
 }
 inline int attend_heads(int64_t group) { return group <= 8 ? 1 : 2; }
 constexpr int attend_warps(int dim, int heads) { return dim * heads <= 128 ? 16 : dim * heads <= 256 ? 8 : 4; }
-// The main kernel, or (joining) the one that joins its parts.
-int launch_attend_bf16(bool joining, const AttendArgs &a, cudaStream_t stream);
-int launch_attend_f16(bool joining, const AttendArgs &a, cudaStream_t stream);
-inline int launch_attend(bool bf16, bool joining, const AttendArgs &a, cudaStream_t stream)
-{
-    return bf16 ? launch_attend_bf16(joining, a, stream) : launch_attend_f16(joining, a, stream);
-}
+int launch_attend_bf16(const AttendArgs &a, cudaStream_t stream);
+int launch_attend_f16(const AttendArgs &a, cudaStream_t stream);
+int launch_attend_solo_bf16(const AttendArgs &a, cudaStream_t stream);
+int launch_attend_solo_f16(const AttendArgs &a, cudaStream_t stream);
+int launch_attend_join_bf16(const AttendArgs &a, cudaStream_t stream);
+int launch_attend_join_f16(const AttendArgs &a, cudaStream_t stream);
 
 }  // namespace ngr

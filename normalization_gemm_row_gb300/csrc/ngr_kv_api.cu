@@ -15,6 +15,9 @@ namespace ngr {
 namespace {
 
 constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
+// Units of a call that are several to a thread: as many as the SMs have room
+// for threads, twice over.
+constexpr int64_t kAppendMany = int64_t(2) * 152 * 2048;
 // Fewer tiles than this are not worth a worker of their own.
 constexpr int64_t kMinShare = 2;
 
@@ -77,7 +80,11 @@ int granule(std::initializer_list<const void *> bases, std::initializer_list<int
     return static_cast<int>(bits & -bits);
 }
 
+// Contexts whose items take a CTA each: tiles of each of its warps at most.
+constexpr int64_t kSoloTiles = 6;
+
 struct AttendPlan {
+    bool solo;
     int64_t workers, slots, part_rows, blocks, items;
     size_t flags, jobs, ml, o, total;
 };
@@ -95,6 +102,9 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
     p.items = B * G * p.blocks;
     p.part_rows = std::min<int64_t>(group, kAttendRows);
     const int64_t tiles = (longest + kAttendTile - 1) / kAttendTile;
+    p.total = 256;
+    p.solo = p.items <= kAttendSms && tiles <= kSoloTiles * warps;
+    if (p.solo) return p;
     const double all = static_cast<double>(p.items) * static_cast<double>(tiles);
     const int64_t ctas = all >= static_cast<double>(kAttendSms * kMinShare)
                              ? kAttendSms
@@ -215,10 +225,17 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride, int64_t q_he
     a.G = static_cast<int>(G);
     a.D = static_cast<int>(D);
     a.rot = static_cast<int>(rot);
-    const int64_t units = append_units(vec, interleaved != 0, H, G, D, rot);
-    const int64_t blocks = (units + kAppendThreads - 1) / kAppendThreads;
-    if (units > kMax31 - kAppendThreads || blocks > (kMax31 - 1) / T) return NGR_ERR_SHAPE;
+    // Few tokens spread over as many blocks as they fill; of many a thread
+    // takes several heads, whose loads are under way together and whose
+    // angles are the same.
+    const int64_t all = H + 2 * G;
+    a.units = append_units(vec, interleaved != 0, D, rot);
+    if (all > kMax31 / 256) return NGR_ERR_SHAPE;
+    a.each = all * a.units * T >= kAppendMany ? kAppendEach : 1;
+    const int64_t at_once = (kAppendThreads / a.units) * a.each, blocks = (all + at_once - 1) / at_once;
+    if (blocks > (kMax31 - 1) / T) return NGR_ERR_SHAPE;
     a.blocks_per_token = static_cast<int>(blocks);
+    a.threads = static_cast<int>((all + blocks * a.each - 1) / (blocks * a.each)) * a.units;
     if (trace_mode())
         std::fprintf(stderr, "ngr: rotated append T=%d H=%d G=%d D=%d rot=%d%s page=%d elements at once=%d blocks a token=%d\n",
                      a.T, a.H, a.G, a.D, a.rot, interleaved ? " interleaved" : "", a.kv.page_size, vec, a.blocks_per_token);
@@ -302,16 +319,18 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     a.part_o = reinterpret_cast<float *>(ws + p.o);
     a.err = reinterpret_cast<int *>(ws);
     if (trace_mode())
-        std::fprintf(stderr, "ngr: paged attention B=%d H=%d G=%d D=%d page=%d window=%d dim=%d workers=%d jobs=%d\n", a.B, a.H,
-                     a.G, a.D, a.kv.page_size, a.window, attend_dim(D), a.workers, a.slots);
+        std::fprintf(stderr, "ngr: paged attention B=%d H=%d G=%d D=%d page=%d window=%d dim=%d %s=%d jobs=%d\n", a.B, a.H,
+                     a.G, a.D, a.kv.page_size, a.window, attend_dim(D), p.solo ? "items" : "workers",
+                     p.solo ? static_cast<int>(p.items) : a.workers, a.slots);
     const bool bf16 = dtype == NGR_BF16;
     call_begin();
     kernel_begin(stream);
-    rc = launch_attend(bf16, false, a, stream);
+    rc = p.solo ? (bf16 ? launch_attend_solo_bf16(a, stream) : launch_attend_solo_f16(a, stream))
+                : (bf16 ? launch_attend_bf16(a, stream) : launch_attend_f16(a, stream));
     kernel_end(stream);
-    if (rc == NGR_OK) {
+    if (rc == NGR_OK && !p.solo) {
         kernel_begin(stream);
-        rc = launch_attend(bf16, true, a, stream);
+        rc = bf16 ? launch_attend_join_bf16(a, stream) : launch_attend_join_f16(a, stream);
         kernel_end(stream);
     }
     return call_end(rc, workspace, stream);
