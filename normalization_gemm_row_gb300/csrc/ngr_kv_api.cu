@@ -33,10 +33,6 @@ int kv_view(const ngr_kv_cache *c, int64_t G, KvView *v)
         c->table_rows > kMax31 || c->table_pages <= 0 || c->table_pages > kMax31)
         return NGR_ERR_SHAPE;
     if (!aligned(c->table, 4) || !aligned(c->k, 2) || !aligned(c->v, 2)) return NGR_ERR_ALIGN;
-    // (rows of the table may be a view of wider ones; tokens may be in any order in memory)
-    if ((c->table_rows > 1 && c->table_stride < c->table_pages) || c->k_page_stride < 0 || c->k_token_stride < 0 ||
-        c->k_head_stride < 0 || c->v_page_stride < 0 || c->v_token_stride < 0 || c->v_head_stride < 0)
-        return NGR_ERR_ARG;
     v->k = c->k;
     v->v = c->v;
     v->k_page = step(c->k_page_stride, c->pages);
@@ -45,6 +41,10 @@ int kv_view(const ngr_kv_cache *c, int64_t G, KvView *v)
     v->v_page = step(c->v_page_stride, c->pages);
     v->v_token = step(c->v_token_stride, c->page_size);
     v->v_head = step(c->v_head_stride, G);
+    // (rows of the table may be parts of wider ones)
+    if ((c->table_rows > 1 && c->table_stride < c->table_pages) ||
+        (v->k_page | v->k_token | v->k_head | v->v_page | v->v_token | v->v_head) < 0)
+        return NGR_ERR_ARG;
     v->table = c->table;
     v->table_stride = c->table_stride;
     v->capacity = c->table_pages * c->page_size;
