@@ -41,8 +41,6 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kWarps = kMoeThreads / 32;
-
 // ------------------------------------------------------------------ rows
 __device__ __forceinline__ uint4 zero4() { return make_uint4(0u, 0u, 0u, 0u); }
 
@@ -84,6 +82,16 @@ __device__ __forceinline__ uint2 two_parts(float x, float y)
     return make_uint2(hi, pack16<BF16>(fabsf(h.x) < INFINITY ? x - h.x : 0.0f, fabsf(h.y) < INFINITY ? y - h.y : 0.0f));
 }
 
+// ---------------------------------------------------------------- router
+// A cluster of a.router CTAs (8, or 16 for many experts) for a token.  Its CTAs share the experts, each
+// with the token's normalized row in FP32, a piece at a time; the first CTA
+// gathers the logits and chooses.  Bound by the latency of what it does one
+// after the other: row, statistics, logits, choice.
+constexpr int kRouterPiece = 8192;
+constexpr int kRouterPitch = kRouterPiece / 8 + 1;
+constexpr int kRouterThreads = 512, kRouterWarps = kRouterThreads / 32;
+constexpr int kRouterAtOnce = 2;      // experts of a warp
+
 __device__ __forceinline__ float block_sum(float v, float *red)
 {
 #pragma unroll
@@ -93,17 +101,9 @@ __device__ __forceinline__ float block_sum(float v, float *red)
     __syncthreads();
     v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w];
+    for (int w = 0; w < kRouterWarps; ++w) v += red[w];
     return v;
 }
-
-// ---------------------------------------------------------------- router
-// A cluster of kMoeRouterCtas for a token.  Its CTAs share the experts, each
-// with the token's normalized row in FP32, a piece at a time; the first CTA
-// gathers the logits and chooses.  Bound by the latency of what it does one
-// after the other: row, statistics, logits, choice.
-constexpr int kRouterPiece = 8192;
-constexpr int kRouterPitch = kRouterPiece / 8 + 1;
 
 // A float as an unsigned number of the same order, NaN as -inf.
 __device__ __forceinline__ uint32_t order_of(float v)
@@ -113,63 +113,63 @@ __device__ __forceinline__ uint32_t order_of(float v)
 }
 
 template <bool BF16, bool VEC>
-__global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_constant__ MoeArgs a)
+__global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid_constant__ MoeArgs a)
 {
     // column k of a piece at [k % 8][k / 8]: a lane's 8 columns lie in 8 rows
     __shared__ float row[8 * kRouterPitch];
     __shared__ float logit[kMoeMaxExperts];
-    __shared__ float mine[kMoeMaxExperts / kMoeRouterCtas][kWarps];     // parts of the CTA's experts' logits
-    __shared__ float red[kWarps];
+    __shared__ float mine[kMoeMaxExperts / 8][kRouterWarps];     // parts of the CTA's experts' logits
+    __shared__ float red[kRouterWarps];
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = static_cast<int>(cluster.block_rank());
-    const int m = static_cast<int>(blockIdx.x) / kMoeRouterCtas;
+    const int m = static_cast<int>(blockIdx.x) / a.router;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint16_t *x = static_cast<const uint16_t *>(a.x) + static_cast<int64_t>(m) * a.K;
     const uint16_t *gamma = static_cast<const uint16_t *>(a.gamma), *beta = static_cast<const uint16_t *>(a.beta);
     pdl_launch_dependents();
     cluster.barrier_arrive();      // (waited for before the first one's memory is written: it has to have started)
-    // The CTA's experts rank, rank + 8, ...: a warp takes one, or a part of
+    // The CTA's experts rank, rank + a.router, ...: a warp takes one, or a part of
     // one's row where they are fewer than the warps.
-    const int experts = rank < a.E ? (a.E - rank + kMoeRouterCtas - 1) / kMoeRouterCtas : 0;
-    const int split = experts >= 8 ? 1 : experts >= 4 ? 2 : experts >= 2 ? 4 : 8;
+    const int experts = rank < a.E ? (a.E - rank + a.router - 1) / a.router : 0;
+    const int split = experts >= 16 ? 1 : experts >= 8 ? 2 : experts >= 4 ? 4 : experts >= 2 ? 8 : 16;
     // What is read last is on its way to L2 first.
-    for (int i = warp / split; i < experts; i += kWarps / split) {
-        const char *wr = static_cast<const char *>(a.Wr) + (static_cast<int64_t>(i) * kMoeRouterCtas + rank) * a.K * 2;
+    for (int i = warp / split; i < experts; i += kRouterWarps / split) {
+        const char *wr = static_cast<const char *>(a.Wr) + (static_cast<int64_t>(i) * a.router + rank) * a.K * 2;
         for (int at = (warp % split * 32 + lane) * 128; at < a.K * 2; at += split * 32 * 128)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(wr + at));
     }
     if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-    for (int i = static_cast<int>(blockIdx.x) * kMoeThreads + threadIdx.x; i < kMoeCounters;
-         i += static_cast<int>(gridDim.x) * kMoeThreads)
+    for (int i = static_cast<int>(blockIdx.x) * kRouterThreads + threadIdx.x; i < kMoeCounters;
+         i += static_cast<int>(gridDim.x) * kRouterThreads)
         a.counters[i] = 0;
 
-    uint4 held[kRouterPiece / 8 / kMoeThreads];      // the row, if it is no longer than a piece
-    uint4 held_gamma[kRouterPiece / 8 / kMoeThreads];
+    uint4 held[kRouterPiece / 8 / kRouterThreads];      // the row, if it is no longer than a piece
+    uint4 held_gamma[kRouterPiece / 8 / kRouterThreads];
     const bool short_row = a.K <= kRouterPiece;
     if (short_row && a.norm != kNormNone) {
 #pragma unroll
-        for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i)
-            held_gamma[i] = row8<VEC>(gamma, (i * kMoeThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
+        for (int i = 0; i < kRouterPiece / 8 / kRouterThreads; ++i)
+            held_gamma[i] = row8<VEC>(gamma, (i * kRouterThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
     }
     if (short_row) {
 #pragma unroll
-        for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i)
-            held[i] = row8<VEC>(x, (i * kMoeThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
+        for (int i = 0; i < kRouterPiece / 8 / kRouterThreads; ++i)
+            held[i] = row8<VEC>(x, (i * kRouterThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
     }
     // f(values, column) over the row, 8 columns a thread at a time
     auto over_row = [&](auto f) {
         float v[8];
         if (short_row) {
 #pragma unroll
-            for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i) {
-                const int k = (i * kMoeThreads + static_cast<int>(threadIdx.x)) * 8;
+            for (int i = 0; i < kRouterPiece / 8 / kRouterThreads; ++i) {
+                const int k = (i * kRouterThreads + static_cast<int>(threadIdx.x)) * 8;
                 if (k >= a.K) break;
                 unpack8<BF16>(held[i], v);
                 f(v, k);
             }
         } else {
 #pragma unroll 4
-            for (int k = threadIdx.x * 8; k < a.K; k += kMoeThreads * 8) {
+            for (int k = threadIdx.x * 8; k < a.K; k += kRouterThreads * 8) {
                 unpack8<BF16>(row8<VEC>(x, k, a.K), v);
                 f(v, k);
             }
@@ -195,13 +195,13 @@ __global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_co
         });
         scale = 1.0f / sqrtf(block_sum(s, red) / a.K + a.eps);
     }
-    for (int i = threadIdx.x; i < kMoeMaxExperts / kMoeRouterCtas * kWarps; i += kMoeThreads) mine[i / kWarps][i % kWarps] = 0.0f;
+    for (int i = threadIdx.x; i < kMoeMaxExperts / 8 * kRouterWarps; i += kRouterThreads) mine[i / kRouterWarps][i % kRouterWarps] = 0.0f;
     for (int k0 = 0; k0 < a.K; k0 += kRouterPiece) {
         const int n = min(kRouterPiece, a.K - k0);
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kRouterPiece / 8 / kMoeThreads; ++i) {
-            const int c = i * kMoeThreads + static_cast<int>(threadIdx.x), k = k0 + c * 8;
+        for (int i = 0; i < kRouterPiece / 8 / kRouterThreads; ++i) {
+            const int c = i * kRouterThreads + static_cast<int>(threadIdx.x), k = k0 + c * 8;
             if (c * 8 >= n) break;
             float v[8];
             unpack8<BF16>(short_row ? held[i] : row8<VEC>(x, k, a.K), v);
@@ -227,29 +227,49 @@ __global__ void __launch_bounds__(kMoeThreads) moe_router_kernel(const __grid_co
             }
         }
         __syncthreads();
-        for (int i = warp / split; i < experts; i += kWarps / split) {
-            float z = 0.0f;
-            const uint16_t *wr = static_cast<const uint16_t *>(a.Wr) + (static_cast<int64_t>(i) * kMoeRouterCtas + rank) * a.K;
+        // several experts of a warp at once: their rows' loads together, the
+        // token's columns read once
+        for (int i0 = warp / split; i0 < experts; i0 += kRouterAtOnce * kRouterWarps / split) {
+            float z[kRouterAtOnce] = {};
+            const uint16_t *wr[kRouterAtOnce];
+#pragma unroll
+            for (int u = 0; u < kRouterAtOnce; ++u) {
+                const int i = min(i0 + u * (kRouterWarps / split), experts - 1);
+                wr[u] = static_cast<const uint16_t *>(a.Wr) + (static_cast<int64_t>(i) * a.router + rank) * a.K;
+            }
 #pragma unroll 8
             for (int c = warp % split * 32 + lane; c * 8 < n; c += split * 32) {
-                float w[8];
-                unpack8<BF16>(row8<VEC>(wr, k0 + c * 8, a.K), w);
+                uint4 d[kRouterAtOnce];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) z = fmaf(w[j], row[j * kRouterPitch + c], z);
+                for (int u = 0; u < kRouterAtOnce; ++u) d[u] = row8<VEC>(wr[u], k0 + c * 8, a.K);
+                float r[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) r[j] = row[j * kRouterPitch + c];
+#pragma unroll
+                for (int u = 0; u < kRouterAtOnce; ++u) {
+                    float w[8];
+                    unpack8<BF16>(d[u], w);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z[u] = fmaf(w[j], r[j], z[u]);
+                }
             }
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-            if (lane == 0) mine[i][warp % split] += z;
+            for (int u = 0; u < kRouterAtOnce; ++u) {
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
+                const int i = i0 + u * (kRouterWarps / split);
+                if (lane == 0 && i < experts) mine[i][warp % split] += z[u];
+            }
         }
     }
     cluster.barrier_wait();
     float *logits = cluster.map_shared_rank(logit, 0);
     __syncthreads();
-    for (int i = threadIdx.x; i < experts; i += kMoeThreads) {
+    for (int i = threadIdx.x; i < experts; i += kRouterThreads) {
         float z = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) z += mine[i][w];
-        logits[i * kMoeRouterCtas + rank] = z;
+        for (int w = 0; w < kRouterWarps; ++w) z += mine[i][w];
+        logits[i * a.router + rank] = z;
     }
     cluster.sync();
     if (rank != 0 || warp != 0) return;
@@ -322,9 +342,17 @@ template <int THREADS>
 __device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenScratch &x, float *p)
 {
     const int lane = threadIdx.x & 31, all = a.M * a.top_k;
+    // a thread's choices, most calls' only ones held
+    const int i0 = threadIdx.x;
+    int id0 = 0;
+    float w0 = 0.0f;
+    if (i0 < all) {
+        id0 = __ldcg(a.ids + i0);
+        if (p) w0 = __ldcg(a.w + i0);
+    }
     for (int e = threadIdx.x; e < a.E; e += THREADS) x.tokens[e] = 0u;
     __syncthreads();
-    for (int i = threadIdx.x; i < all; i += THREADS) atomicOr(&x.tokens[__ldcg(a.ids + i)], 1u << (i / a.top_k));
+    for (int i = i0; i < all; i += THREADS) atomicOr(&x.tokens[i == i0 ? id0 : __ldcg(a.ids + i)], 1u << (i / a.top_k));
     __syncthreads();
     if (threadIdx.x < 32) {
         int n = 0, rows = 0;
@@ -356,9 +384,9 @@ __device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenS
     }
     __syncthreads();
     if (p) {
-        for (int i = threadIdx.x; i < all; i += THREADS) {
-            const int e = __ldcg(a.ids + i), m = i / a.top_k;
-            p[x.base[e] + __popc(x.tokens[e] & ((1u << m) - 1u))] = __ldcg(a.w + i);
+        for (int i = i0; i < all; i += THREADS) {
+            const int e = i == i0 ? id0 : __ldcg(a.ids + i), m = i / a.top_k;
+            p[x.base[e] + __popc(x.tokens[e] & ((1u << m) - 1u))] = i == i0 ? w0 : __ldcg(a.w + i);
         }
     }
     __syncthreads();
@@ -589,6 +617,45 @@ __device__ __forceinline__ bool counted_last(int *count, const Sharers &w, int l
     return last;
 }
 
+// The parts of 16 rows' sums for all tokens, added in the workers' order into
+// sums [token][17].  A part is M x 4 pieces of 16 bytes: few tokens' are read
+// several at a time, each by some of the lanes.
+template <typename L>
+__device__ __forceinline__ void gather_parts(const MoeArgs &a, const Sharers &w, float *sums, int lane)
+{
+    const float4 *parts = reinterpret_cast<const float4 *>(a.parts);
+    const int each = a.M == 1 ? 4 : a.M == 2 ? 8 : a.M <= 4 ? 16 : 32;     // lanes of a part
+    const int group = lane / each, groups = 32 / each;
+    for (int v0 = 0; v0 < a.M * 4; v0 += each) {
+        const int v = v0 + lane % each;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (v < a.M * 4) {
+#pragma unroll 8
+            for (int p = w.first + group; p <= w.last; p += groups) {
+                const float4 y = __ldcg(parts + (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (L::kMost * 4) + v);
+                x.x += y.x;
+                x.y += y.y;
+                x.z += y.z;
+                x.w += y.w;
+            }
+        }
+        for (int o = 16; o >= each; o >>= 1) {
+            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
+            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
+            x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
+            x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+        }
+        if (group == 0 && v < a.M * 4) {
+            float *to = sums + (v >> 2) * 17 + (v & 3) * 4;
+            to[0] = x.x;
+            to[1] = x.y;
+            to[2] = x.z;
+            to[3] = x.w;
+        }
+    }
+    __syncwarp();
+}
+
 template <bool BF16, bool DOWN, bool VEC, int NT>
 __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(const __grid_constant__ MoeArgs a)
 {
@@ -770,18 +837,14 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
                 const int row0 = s.tile * 16, values = a.M * 16;
                 bool finish = whole;
                 if (!whole) {
-                    float *part = a.parts + slot * (L::kMost * 16);
-                    for (int v = lane; v < values; v += 32) part[v] = sums[(v >> 4) * 17 + (v & 15)];
-                    finish = counted_last(counts, w, lane);
-                    if (finish) {
-                        for (int v = lane; v < values; v += 32) {
-                            float x = 0.0f;
-#pragma unroll 8
-                            for (int p = w.first; p <= w.last; ++p)
-                                x += __ldcg(a.parts + (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (L::kMost * 16) + v);
-                            sums[(v >> 4) * 17 + (v & 15)] = x;
-                        }
+                    // (16-byte pieces: M tokens x 4 of them)
+                    float4 *part = reinterpret_cast<float4 *>(a.parts) + slot * (L::kMost * 4);
+                    for (int v = lane; v < a.M * 4; v += 32) {
+                        const float *from = sums + (v >> 2) * 17 + (v & 3) * 4;
+                        part[v] = make_float4(from[0], from[1], from[2], from[3]);
                     }
+                    finish = counted_last(counts, w, lane);
+                    if (finish) gather_parts<L>(a, w, sums, lane);
                 }
                 if (finish)
                     for (int v = lane; v < values; v += 32)
@@ -826,6 +889,10 @@ cudaError_t launch(F *kern, unsigned grid, unsigned threads, int cluster, size_t
     }
     cfg.attrs = attr;
     cfg.numAttrs = static_cast<unsigned>(n);
+    if (cluster > 8) {      // a size that has to be asked for
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
     if (smem > 0) {
         // (an attribute of the current device's copy of the function)
         const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
@@ -850,10 +917,10 @@ int status(const char *what, cudaError_t e) { return e == cudaSuccess ? 0 : reco
 
 int launch_moe_router(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream)
 {
-    const unsigned grid = static_cast<unsigned>(a.M * kMoeRouterCtas);
+    const unsigned grid = static_cast<unsigned>(a.M * a.router);
     const auto kern = bf16 ? (vec ? moe_router_kernel<true, true> : moe_router_kernel<true, false>)
                            : (vec ? moe_router_kernel<false, true> : moe_router_kernel<false, false>);
-    return status("expert router launch", launch(kern, grid, kMoeThreads, kMoeRouterCtas, 0, false, a, stream));
+    return status("expert router launch", launch(kern, grid, kRouterThreads, a.router, 0, false, a, stream));
 }
 
 int launch_moe_up(bool bf16, bool vec, const MoeArgs &a, cudaStream_t stream)

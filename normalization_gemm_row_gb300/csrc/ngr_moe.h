@@ -21,7 +21,6 @@ constexpr int kMoeWorkers = kMoeCtas * (kMoeThreads / 32);
 constexpr int kMoeGroup = 4;
 constexpr int kMoeMinShare = 4;       // steps of a worker at least
 constexpr int kMoeCounters = 2 * kMoeWorkers;   // up, down: of a unit by its first worker
-constexpr int kMoeRouterCtas = 8;     // a cluster for each token
 
 constexpr int kMoeEntry = 2 * kMoeGroup;   // tokens that share one reading of an expert's weights
 constexpr int kMoeMaxEntries = kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / kMoeEntry;
@@ -46,6 +45,7 @@ struct MoeArgs {
     int *err;
     int norm, M, K, F, E, top_k, renormalize;
     int Kp, Fp;                       // pitches, multiples of 64
+    int router;                       // CTAs of the cluster that takes a token's routing
     float eps;
 };
 

@@ -18,6 +18,9 @@ constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
 static_assert(NGR_MOE_MAX_M == kMoeMaxTokens && NGR_MOE_MAX_EXPERTS == kMoeMaxExperts && NGR_MOE_MAX_TOP_K == kMoeMaxTopK,
               "ngr.h and the kernels agree");
 
+// More experts than this take clusters of 16 CTAs in the router.
+constexpr int64_t kMoeManyExperts = 64;
+
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
 
@@ -122,6 +125,7 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.Kp = static_cast<int>(p.Kp);
     a.Fp = static_cast<int>(p.Fp);
     a.eps = eps;
+    a.router = E > kMoeManyExperts ? 16 : 8;
     const bool bf16 = dtype == NGR_BF16;
     const bool vec_r = K % 8 == 0 && aligned(Wr, 16) && aligned(x, 16) && aligned(a.gamma, 16) && aligned(a.beta, 16);
     const bool vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
