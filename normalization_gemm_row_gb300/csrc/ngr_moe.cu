@@ -128,21 +128,12 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
     const uint16_t *gamma = static_cast<const uint16_t *>(a.gamma), *beta = static_cast<const uint16_t *>(a.beta);
     pdl_launch_dependents();
     cluster.barrier_arrive();      // (waited for before the first one's memory is written: it has to have started)
-    // The CTA's experts rank, rank + a.router, ...: a warp takes one, or a part of
-    // one's row where they are fewer than the warps.
+    // The CTA's experts rank, rank + a.router, ...: a warp takes two at once,
+    // or a part of their rows where there are fewer pairs than warps.
     const int experts = rank < a.E ? (a.E - rank + a.router - 1) / a.router : 0;
-    const int split = experts >= 16 ? 1 : experts >= 8 ? 2 : experts >= 4 ? 4 : experts >= 2 ? 8 : 16;
-    // What is read last is on its way to L2 first.
-    for (int i = warp / split; i < experts; i += kRouterWarps / split) {
-        const char *wr = static_cast<const char *>(a.Wr) + (static_cast<int64_t>(i) * a.router + rank) * a.K * 2;
-        for (int at = (warp % split * 32 + lane) * 128; at < a.K * 2; at += split * 32 * 128)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(wr + at));
-    }
-    if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
-    for (int i = static_cast<int>(blockIdx.x) * kRouterThreads + threadIdx.x; i < kMoeCounters;
-         i += static_cast<int>(gridDim.x) * kRouterThreads)
-        a.counters[i] = 0;
-
+    const int pairs = (experts + kRouterAtOnce - 1) / kRouterAtOnce;      // one a warp, or a part of its rows
+    const int split = pairs >= 16 ? 1 : pairs >= 8 ? 2 : pairs >= 4 ? 4 : pairs >= 2 ? 8 : 16;
+    const int slots = kRouterWarps / split, mine_of = warp / split, part = warp % split;
     uint4 held[kRouterPiece / 8 / kRouterThreads];      // the row, if it is no longer than a piece
     uint4 held_gamma[kRouterPiece / 8 / kRouterThreads];
     const bool short_row = a.K <= kRouterPiece;
@@ -156,6 +147,16 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
         for (int i = 0; i < kRouterPiece / 8 / kRouterThreads; ++i)
             held[i] = row8<VEC>(x, (i * kRouterThreads + static_cast<int>(threadIdx.x)) * 8, a.K);
     }
+    // What is read last is on its way to L2 meanwhile.
+    for (int i = mine_of; i < experts; i += slots) {
+        const char *wr = static_cast<const char *>(a.Wr) + (static_cast<int64_t>(i) * a.router + rank) * a.K * 2;
+        for (int at = (part * 32 + lane) * 128; at < a.K * 2; at += split * 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(wr + at));
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *a.err = 0;
+    for (int i = static_cast<int>(blockIdx.x) * kRouterThreads + threadIdx.x; i < kMoeCounters;
+         i += static_cast<int>(gridDim.x) * kRouterThreads)
+        a.counters[i] = 0;
     // f(values, column) over the row, 8 columns a thread at a time
     auto over_row = [&](auto f) {
         float v[8];
@@ -229,19 +230,16 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
         __syncthreads();
         // several experts of a warp at once: their rows' loads together, the
         // token's columns read once
-        for (int i0 = warp / split; i0 < experts; i0 += kRouterAtOnce * kRouterWarps / split) {
+        for (int i0 = mine_of; i0 < experts; i0 += kRouterAtOnce * slots) {
             float z[kRouterAtOnce] = {};
-            const uint16_t *wr[kRouterAtOnce];
-#pragma unroll
-            for (int u = 0; u < kRouterAtOnce; ++u) {
-                const int i = min(i0 + u * (kRouterWarps / split), experts - 1);
-                wr[u] = static_cast<const uint16_t *>(a.Wr) + (static_cast<int64_t>(i) * a.router + rank) * a.K;
-            }
+            const uint16_t *wr = static_cast<const uint16_t *>(a.Wr) + (static_cast<int64_t>(i0) * a.router + rank) * a.K;
+            const int64_t next = static_cast<int64_t>(slots) * a.router * a.K;
+            const bool both = i0 + slots < experts;
 #pragma unroll 8
-            for (int c = warp % split * 32 + lane; c * 8 < n; c += split * 32) {
+            for (int c = part * 32 + lane; c * 8 < n; c += split * 32) {
                 uint4 d[kRouterAtOnce];
-#pragma unroll
-                for (int u = 0; u < kRouterAtOnce; ++u) d[u] = row8<VEC>(wr[u], k0 + c * 8, a.K);
+                d[0] = row8<VEC>(wr, k0 + c * 8, a.K);
+                d[1] = both ? row8<VEC>(wr + next, k0 + c * 8, a.K) : zero4();
                 float r[8];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) r[j] = row[j * kRouterPitch + c];
@@ -257,8 +255,7 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
             for (int u = 0; u < kRouterAtOnce; ++u) {
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) z[u] += __shfl_xor_sync(0xffffffffu, z[u], o);
-                const int i = i0 + u * (kRouterWarps / split);
-                if (lane == 0 && i < experts) mine[i][warp % split] += z[u];
+                if (lane == 0 && (u == 0 || both)) mine[i0 + u * slots][part] += z[u];
             }
         }
     }
@@ -283,31 +280,57 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
     for (int e = lane; e < a.E; e += 32) all += expf(logit[e] - top);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-    uint32_t taken = 0;            // of this lane's experts
-    float p = 0.0f, sum = 0.0f;    // lane s: choice s
-    int id = 0;
-    for (int s = 0; s < a.top_k; ++s) {
-        // the largest logit that is left, of equal ones the lowest expert's;
-        // NaN counts as -inf, so that there is always a choice
-        uint32_t best = 0;         // (below any logit's order)
-        int at = kMoeMaxExperts;
-        for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
-            const uint32_t v = order_of(logit[e]);
-            if (!((taken >> i) & 1u) && v > best) {
-                best = v;
-                at = e;
-            }
+    // The largest logit that is left, of equal ones the lowest expert's; NaN
+    // counts as -inf, so that there is always a choice.  (Any logit's order is
+    // above 0.)
+    int id = 0;                    // lane s: choice s
+    auto choose = [&](auto best_of, auto take) {
+        for (int s = 0; s < a.top_k; ++s) {
+            uint32_t best = 0;
+            int at = kMoeMaxExperts;
+            best_of(best, at);
+            const uint32_t most = __reduce_max_sync(0xffffffffu, best);
+            at = __reduce_min_sync(0xffffffffu, best == most ? at : kMoeMaxExperts);
+            if ((at & 31) == lane) take(at >> 5);
+            if (lane == s) id = at;
         }
-        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-        at = __reduce_min_sync(0xffffffffu, best == most ? at : kMoeMaxExperts);
-        if ((at & 31) == lane) taken |= 1u << (at >> 5);
-        const float q = expf(logit[at] - top) / all;
-        sum += q;
-        if (lane == s) {
-            p = q;
-            id = at;
-        }
+    };
+    constexpr int kHeld = 8;
+    if (a.E <= 32 * kHeld) {
+        uint32_t order[kHeld];
+#pragma unroll
+        for (int i = 0; i < kHeld; ++i) order[i] = lane + 32 * i < a.E ? order_of(logit[lane + 32 * i]) : 0u;
+        choose(
+            [&](uint32_t &best, int &at) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i)
+                    if (order[i] > best) {
+                        best = order[i];
+                        at = lane + 32 * i;
+                    }
+            },
+            [&](int t) {
+#pragma unroll
+                for (int i = 0; i < kHeld; ++i)
+                    if (i == t) order[i] = 0u;
+            });
+    } else {
+        uint32_t taken = 0;        // of this lane's experts
+        choose(
+            [&](uint32_t &best, int &at) {
+                for (int e = lane, i = 0; e < a.E; e += 32, ++i) {
+                    const uint32_t v = order_of(logit[e]);
+                    if (!((taken >> i) & 1u) && v > best) {
+                        best = v;
+                        at = e;
+                    }
+                }
+            },
+            [&](int t) { taken |= 1u << t; });
     }
+    float p = lane < a.top_k ? expf(logit[id] - top) / all : 0.0f, sum = p;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane < a.top_k) {
         if (a.renormalize) p /= sum;
         const int i = m * a.top_k + lane;
