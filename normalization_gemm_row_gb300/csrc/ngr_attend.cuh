@@ -14,9 +14,10 @@
 // barrier.
 //
 // All items' tiles of 16 tokens (an item: a sequence and key head, and a block
-// of 16 query heads where there are more) stand in one row, which is cut into
-// equal runs, one a warp ("worker").  A batch of any lengths is balanced so,
-// and nothing but the device has to know the lengths.  An item that lies in
+// of 16 query heads where there are more) stand in one row, with a place more
+// before each item for what its beginning costs, and the row is cut into equal
+// runs, one a warp ("worker").  A batch of any lengths is balanced so, and
+// nothing but the device has to know the lengths.  An item that lies in
 // one run is finished there; the others' parts (FP32 sums, maximum, sum of
 // exponentials) are joined by a second kernel in the tokens' order, so a call
 // repeated gives the same bits.
@@ -73,18 +74,26 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, bool *bad)
     return s;
 }
 
-// A place in the row of tiles.
+// Places of the row before each item's tiles: taking up an item (queries,
+// output) costs about as much as a tile (37 rows of 12 heads, some of them
+// with a tile alone: the worker of those ended at 50 us, the others at 35).
+constexpr int kItemPlaces = 1;
+
+// A tile of the row.
 struct Place {
     int b, item, tile;     // sequence, item among the sequence's, tile of the item
     Span s;
 };
-__device__ __forceinline__ void advance(const AttendArgs &a, Place &p, bool *bad)
+// On to the next one; returns how many places further it is.
+__device__ __forceinline__ int advance(const AttendArgs &a, Place &p, bool *bad)
 {
-    if (++p.tile < p.s.tiles) return;
+    if (++p.tile < p.s.tiles) return 1;
     p.tile = 0;
-    if (++p.item < a.G * a.blocks) return;
-    p.item = 0;
-    if (++p.b < a.B) p.s = span_of(a, p.b, bad);
+    if (++p.item == a.G * a.blocks) {
+        p.item = 0;
+        if (++p.b < a.B) p.s = span_of(a, p.b, bad);
+    }
+    return 1 + kItemPlaces;
 }
 
 // The entry of the table for a token of a tile, one in lane % 16, and its slot
@@ -250,8 +259,8 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
 
     bool bad = false;
     Place c;
-    long long share = 1, first = 0;
-    int worker = warp, count;
+    long long share = 1, place = 0, end = 0;      // the worker's run: from tile c's place up to `end`
+    int worker = warp;
     if constexpr (SOLO) {
         if (static_cast<int>(blockIdx.x) == a.B * items) {      // a block that only looks for bad pages
             check_pages(a);
@@ -262,7 +271,8 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         c.s = span_of(a, c.b, &bad);
         share = (c.s.tiles + kWarps - 1) / kWarps;
         c.tile = worker * static_cast<int>(share);
-        count = max(0, min(static_cast<int>(share), c.s.tiles - c.tile));
+        place = c.tile;
+        end = min(place + share, static_cast<long long>(c.s.tiles));
         if (!FULL) __syncthreads();
     } else {
         // Tiles before each run of `each` sequences.
@@ -270,7 +280,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         long long mine = 0;
         for (int i = 0; i < each; ++i) {
             const int b = static_cast<int>(threadIdx.x) * each + i;
-            if (b < a.B) mine += static_cast<long long>(span_of(a, b, &bad).tiles) * items;
+            if (b < a.B) mine += static_cast<long long>(span_of(a, b, &bad).tiles + kItemPlaces) * items;
         }
         long long incl = mine;
 #pragma unroll
@@ -291,41 +301,44 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         if (share < a.min_share) share = a.min_share;
         // Neighbouring runs on different SMs: a few runs have an SM each.
         worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-        first = worker * share;
-        const long long left = total - first;
-        count = static_cast<int>(left <= 0 ? 0 : left < share ? left : share);
-        if (count > 0) {
-            int lo = 0, hi = kThreads;       // before[lo] <= first < before[hi]
+        place = worker * share;
+        end = min(place + share, total);
+        if (place < end) {
+            int lo = 0, hi = kThreads;       // before[lo] <= place < before[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
-                if (before[mid] <= first) lo = mid;
+                if (before[mid] <= place) lo = mid;
                 else hi = mid;
             }
             long long at = before[lo];
             int b = lo * each;
             Span s = span_of(a, b, &bad);
-            while (at + static_cast<long long>(s.tiles) * items <= first) {
-                at += static_cast<long long>(s.tiles) * items;
+            while (at + static_cast<long long>(s.tiles + kItemPlaces) * items <= place) {
+                at += static_cast<long long>(s.tiles + kItemPlaces) * items;
                 s = span_of(a, ++b, &bad);
             }
             c.b = b;
             c.s = s;
-            c.item = static_cast<int>((first - at) / s.tiles);
-            c.tile = static_cast<int>((first - at) - static_cast<long long>(c.item) * s.tiles);
+            c.item = static_cast<int>((place - at) / (s.tiles + kItemPlaces));
+            at += static_cast<long long>(c.item) * (s.tiles + kItemPlaces) + kItemPlaces;      // of the item's first tile
+            c.tile = static_cast<int>(max(0LL, place - at));
+            place = at + c.tile;
         }
     }
     AttendJob job = {-1, -1, 0, 0};
     const Place at_start = c;      // solo: the CTA's item
 
-    if (count > 0) {
+    if (place < end) {
         Place f = c;
+        long long f_place = place;
         const Pieces<DP, FULL> pieces(a.D, lane);
         const uint32_t base = smem_u32(ring) + warp * R::kBytes;
         // Keys and values go by turns; the values' offsets are kept from the
         // keys'.  What the cursor f does not reach is an empty group.
         uint32_t k_at = kNowhere, v_at = kNowhere;
         bool all = false;                  // the tile has all its tokens
-        int left = count, issued = 0;      // tiles to issue, issued
+        bool real = false;                 // the last keys issued were a tile's
+        int issued = 0;                    // tiles
         auto locate = [&](const Place &f, int entry, int slot) {
             k_at = v_at = kNowhere;
             if (entry != kNone) {
@@ -338,8 +351,9 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                 }
             }
         };
-        auto issue_keys = [&](const Place &f, int entry, int slot, int stage) {
-            if (left > 0) {
+        auto issue_keys = [&](const Place &f, long long f_at, int entry, int slot, int stage) {
+            real = f_at < end;
+            if (real) {
                 locate(f, entry, slot);
                 const uint32_t there = __ballot_sync(0xffffffffu, k_at != kNowhere);
                 all = there == 0xffffffffu;
@@ -347,28 +361,29 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                 fetch<DP, FULL>(a.kv.k, pieces, k_at, all, base + stage * R::kStage, lane);
                 ++issued;
             }
-            --left;
             cp_async_commit();
         };
         auto issue_values = [&](int stage) {      // of the tile whose keys went last
-            if (left >= 0) fetch<DP, FULL>(a.kv.v, pieces, v_at, all, base + stage * R::kStage, lane);
+            if (real) fetch<DP, FULL>(a.kv.v, pieces, v_at, all, base + stage * R::kStage, lane);
             cp_async_commit();
         };
-        auto entry_ahead = [&](int *slot) { return left > 0 ? page_entry(a, f, lane, slot) : kNone; };
+        auto entry_ahead = [&](int *slot) { return f_place < end ? page_entry(a, f, lane, slot) : kNone; };
         {
             // The first tiles' table entries are asked for together.
             constexpr int kFirst = (S + 1) / 2;
             Place at[kFirst];
+            long long place_of[kFirst];
             int entry[kFirst], slot[kFirst] = {};
 #pragma unroll
             for (int j = 0; j < kFirst; ++j) {
                 at[j] = f;
-                entry[j] = j < count ? page_entry(a, f, lane, &slot[j]) : kNone;
-                if (j < count) advance(a, f, &bad);
+                place_of[j] = f_place;
+                entry[j] = entry_ahead(&slot[j]);
+                if (f_place < end) f_place += advance(a, f, &bad);
             }
 #pragma unroll
             for (int i = 0; i < S; ++i) {
-                if (i % 2 == 0) issue_keys(at[i / 2], entry[i / 2], slot[i / 2], i);
+                if (i % 2 == 0) issue_keys(at[i / 2], place_of[i / 2], entry[i / 2], slot[i / 2], i);
                 else issue_values(i);
             }
         }
@@ -381,7 +396,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         bool fresh = true;         // a new item
         bool whole = !SOLO && c.tile == 0;  // this worker has the item's beginning
         int stage = 0;
-        for (int i = 0; i < count; ++i) {
+        for (int i = 0; place < end; ++i) {
             int slot = 0;
             const int entry = entry_ahead(&slot);
             if (fresh) {
@@ -429,11 +444,11 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             }
             __syncwarp();
             auto next_keys = [&] {
-                issue_keys(f, entry, slot, stage);
-                if (left >= 0) {
-                    advance(a, f, &bad);
+                issue_keys(f, f_place, entry, slot, stage);
+                if (real) {
+                    f_place += advance(a, f, &bad);
                     // a new item's queries on their way, for when its first tile is taken
-                    if (f.tile == 0 && left > 0 && lane < kAttendRows) {
+                    if (f.tile == 0 && f_place < end && lane < kAttendRows) {
                         const int kv_head = f.item / a.blocks, block = f.item - kv_head * a.blocks;
                         const int r = kv_head * a.group + block * kAttendRows + lane;
                         if (lane < min(kAttendRows, a.group - block * kAttendRows))
@@ -518,7 +533,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             stage = stage + 1 == S ? 0 : stage + 1;
 
             const bool ends = c.tile + 1 == c.s.tiles;
-            if (ends || i + 1 == count) {
+            if (ends || place + 1 >= end) {
                 const int kv_head = c.item / a.blocks, block = c.item - kv_head * a.blocks;
                 const int rows = min(kAttendRows, a.group - block * kAttendRows);
                 const int head = kv_head * a.group + block * kAttendRows;
@@ -574,14 +589,14 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                             }
                         }
                     if (whole) {      // the others' parts follow
-                        const long long end = first + i + (c.s.tiles - c.tile);
-                        job = AttendJob{worker, static_cast<int>((end - 1) / share), c.b, c.item};
+                        const long long last = place + (c.s.tiles - 1 - c.tile);
+                        job = AttendJob{worker, static_cast<int>(last / share), c.b, c.item};
                         if (a.slot_by_item && lane == 0) a.jobs[static_cast<int64_t>(c.b) * items + c.item] = job;
                     }
                 }
                 fresh = whole = true;
             }
-            advance(a, c, &bad);
+            place += advance(a, c, &bad);
         }
         cp_async_wait<0>();
     }

@@ -105,10 +105,11 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
     p.total = 256;
     p.solo = p.items <= kAttendSms && tiles <= kSoloTiles * warps;
     if (p.solo) return p;
-    const double all = static_cast<double>(p.items) * static_cast<double>(tiles);
+    // (a place more for each item: kItemPlaces)
+    const double all = static_cast<double>(p.items) * static_cast<double>(tiles + 1);
     const int64_t ctas = all >= static_cast<double>(kAttendSms * kMinShare)
                              ? kAttendSms
-                             : std::max<int64_t>(1, (p.items * tiles + kMinShare - 1) / kMinShare);
+                             : std::max<int64_t>(1, (p.items * (tiles + 1) + kMinShare - 1) / kMinShare);
     p.workers = ctas * warps;
     p.slots = std::min(p.items, p.workers);
     size_t off = 256;
