@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
 // a warp takes a row by itself, its parts' weights in its lanes; more (few
 // long sequences) are taken by all warps of a block together, a row of blocks
 // for each row.
-constexpr int kJoinWarps = 16, kJoinHeld = 4;
+constexpr int kJoinWarps = 16, kJoinHeld = 8;
 
 template <int N>
 __device__ __forceinline__ void add_scaled(float4 (&to)[N], const float4 (&v)[N], float w)

@@ -567,17 +567,16 @@ __device__ __forceinline__ void plan_copies(const MoeArgs &a, const Chosen &c, c
         p.token_steps[i] = row ? (n - col + 63) >> 6 : 0;
     }
 }
-// A 32-bit operand word of a row off the 16-byte boundary: columns e, e + 1 of
-// the stage's row whose first word starts `d` elements before column 0.
-__device__ __forceinline__ uint32_t pair_at(uint32_t row, int d, int e)
+// The 32-bit operand word at `at` of a row off the 16-byte boundary: from there
+// if its columns start with a word, else (shift 16) from the middle of it to
+// that of the next.  (Both are read: neighbouring rows' distances differ, and
+// a branch would part the warp.)
+__device__ __forceinline__ uint32_t pair_at(uint32_t at, uint32_t shift)
 {
-    const int at = d + e;
-    uint32_t lo;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(row + (at >> 1) * 4) : "memory");
-    if (!(at & 1)) return lo;
-    uint32_t hi;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(hi) : "r"(row + (at >> 1) * 4 + 4) : "memory");
-    return __funnelshift_r(lo, hi, 16);
+    uint32_t lo, hi;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(at) : "memory");
+    asm volatile("ld.shared.u32 %0, [%1 + 4];" : "=r"(hi) : "r"(at) : "memory");
+    return __funnelshift_r(lo, hi, shift);
 }
 
 // The products of one step, `left` columns from the row's end.  d0, d1: how
@@ -593,17 +592,26 @@ __device__ __forceinline__ void take(float (&acc)[NT][4], int tokens, int left, 
 #pragma unroll
         for (int i = 0; i < 4; ++i) ldmatrix4(w[i], stage + r * 128 + (((2 * i + half) ^ (r & 7)) << 4));
     } else {
-        const uint32_t row0 = stage + g * 144, row1 = stage + (g + 8) * 144;
+        const uint32_t at0 = stage + g * 144 + (d0 >> 1) * 4 + t * 4, at1 = stage + (g + 8) * 144 + (d1 >> 1) * 4 + t * 4;
+        const uint32_t shift0 = (d0 & 1) * 16, shift1 = (d1 & 1) * 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const int e = i * 16 + h * 8 + 2 * t;
-                // (what follows the row's end belongs to the next row)
-                const uint32_t keep = (e < left ? 0xFFFFu : 0u) | (e + 1 < left ? 0xFFFF0000u : 0u);
-                w[i][2 * h] = pair_at(row0, d0, e) & keep;
-                w[i][2 * h + 1] = pair_at(row1, d1, e) & keep;
+                w[i][2 * h] = pair_at(at0 + i * 32 + h * 16, shift0);
+                w[i][2 * h + 1] = pair_at(at1 + i * 32 + h * 16, shift1);
             }
+        if (left < 64) {      // what follows the row's end belongs to the next row
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int e = i * 16 + h * 8 + 2 * t;
+                    const uint32_t keep = (e < left ? 0xFFFFu : 0u) | (e + 1 < left ? 0xFFFF0000u : 0u);
+                    w[i][2 * h] &= keep;
+                    w[i][2 * h + 1] &= keep;
+                }
+        }
     }
 #pragma unroll
     for (int j = 0; j < L::kGroups; ++j) {
