@@ -866,39 +866,41 @@ def _kv_cache(dtype, index, k_cache, v_cache, block_table):
         raise ValueError("block_table must be [rows, pages a row]")
     if index < 0:
         raise ValueError("all tensors must be CUDA tensors")
-    if k_cache.get_device() != index or v_cache.get_device() != index or block_table.get_device() != index:
+    if not k_cache.get_device() == v_cache.get_device() == block_table.get_device() == index:
         raise ValueError("all tensors must be on one CUDA device")
     pages, size, G, D = shape
     kp, kt, kh, kd = k_cache.stride()
     vp, vt, vh, vd = v_cache.stride()
     rows, width = block_table.shape
     step, one = block_table.stride()
-    if (D > 1 and (kd != 1 or vd != 1)) or (width > 1 and one != 1):
+    if (kd != 1 or vd != 1) and D > 1 or one != 1 and width > 1:
         raise ValueError("the last dimension of the caches and of block_table must be contiguous")
     return (_pack_cache(k_cache.data_ptr(), v_cache.data_ptr(), pages, size, kp, kt, kh, vp, vt, vh,
                         block_table.data_ptr(), rows, width, step), G, D, width * size)
 
 
 def _int32(what, index, n, t):
-    """t is a contiguous int32 vector of n entries on device ``index``."""
+    """The address of t, a contiguous int32 vector of n entries on device ``index``."""
     if t.dtype is not torch.int32:
         raise TypeError(f"{what} must be int32")
     if t.shape != (n,) or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous on the tensors' device, with one entry per token")
+    return t.data_ptr()
 
 
-def _heads_last(what, dtype, index, t, tokens, heads, dim):
-    """t's token and head strides, t [tokens, heads, dim] of this type and device."""
+def _heads_last(what, dtype, index, t, shape):
+    """The address of t and its token and head strides; t of this type, device
+    and shape [tokens, heads, dim]."""
     if t.dtype is not dtype:
         raise TypeError("all tensors must share one dtype")
     if t.get_device() != index:
         raise ValueError("all tensors must be on one CUDA device")
-    if t.shape != (tokens, heads, dim):
+    if t.shape != shape:
         raise ValueError(f"{what} must be [tokens, heads, dim], with the caches' dim (and heads, for k and v)")
     a, b, c = t.stride()
-    if c != 1 and dim > 1:
+    if c != 1 and shape[2] > 1:
         raise ValueError(f"{what} must have contiguous heads")
-    return a, b
+    return t.data_ptr(), a, b
 
 
 def fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows=None, inv_freq=None,
@@ -922,40 +924,40 @@ def fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows
     code = _CODES[dtype] if dtype in _CODES else _dtype_code(k)
     cache, G, D, _ = _kv_cache(dtype, index, k_cache, v_cache, block_table)
     T = k.shape[0]
-    kt, kh = _heads_last("k", dtype, index, k, T, G, D)
-    vt, vh = _heads_last("v", dtype, index, v, T, G, D)
-    H = qt = qh = ot = oh = 0
+    kv_shape = (T, G, D)
+    k_at, kt, kh = _heads_last("k", dtype, index, k, kv_shape)
+    v_at, vt, vh = _heads_last("v", dtype, index, v, kv_shape)
+    q_at, o_at, H, qt, qh, ot, oh = None, None, 0, 0, 0, 0, 0
     if q is not None:
         H = q.shape[1] if q.dim() == 3 else 0
-        qt, qh = _heads_last("q", dtype, index, q, T, H, D)
+        shape = (T, H, D)
+        q_at, qt, qh = _heads_last("q", dtype, index, q, shape)
         if q_out is not None:
-            ot, oh = _heads_last("q_out", dtype, index, q_out, T, H, D)
+            o_at, ot, oh = _heads_last("q_out", dtype, index, q_out, shape)
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _int32("positions", index, T, positions)
-    if rows is not None:
-        _int32("rows", index, T, rows)
-    rot = 0
+    positions_at = _int32("positions", index, T, positions)
+    rows_at = _int32("rows", index, T, rows) if rows is not None else None
+    inv_at, rot = None, 0
     if inv_freq is not None:
         if (inv_freq.dtype is not torch.float32 or inv_freq.dim() != 1 or inv_freq.get_device() != index
                 or not inv_freq.is_contiguous()):
             raise ValueError("inv_freq must be a contiguous float32 vector on the tensors' device")
-        rot = 2 * inv_freq.shape[0]
+        inv_at, rot = inv_freq.data_ptr(), 2 * inv_freq.shape[0]
     if not _here(k, stream):
         got = _there(_append_there, k, stream, q, k, v, k_cache, v_cache, block_table, positions, rows, inv_freq,
                      interleaved, q_out, workspace)
         return got[0]
     if q is not None and q_out is None:
-        q_out = torch.empty((T, H, D), dtype=dtype, device=k.device)
-        ot, oh = H * D, D
-    nbytes = 0
+        q_out = torch.empty(shape, dtype=dtype, device=k.device)
+        o_at, ot, oh = q_out.data_ptr(), H * D, D
+    ws_at, nbytes = None, 0
     if workspace is not None or _debug():
         workspace = _scratch(256, k.device, workspace)
-        nbytes = workspace.numel() * workspace.element_size()
-    rc = lib().ngr_fused_rope_append_kv(
-        _ptr(q), qt, qh, k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, cache, positions.data_ptr(), _ptr(rows),
-        _ptr(inv_freq), rot, 1 if interleaved else 0, T, H, G, D, code, _ptr(q_out), ot, oh, _ptr(workspace), nbytes,
-        _current_stream_handle(index))
+        ws_at, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    rc = (_lib or lib()).ngr_fused_rope_append_kv(
+        q_at, qt, qh, k_at, kt, kh, v_at, vt, vh, cache, positions_at, rows_at, inv_at, rot, 1 if interleaved else 0,
+        T, H, G, D, code, o_at, ot, oh, ws_at, nbytes, _current_stream_handle(index))
     if rc != 0:
         raise NgrError(rc, "fused_rope_append_kv")
     return q_out
@@ -994,8 +996,8 @@ def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     if len(shape) != 3:
         raise ValueError("q must be [B, H, D]")
     B, H, _ = shape
-    qr, qh = _heads_last("q", dtype, index, q, B, H, D)
-    _int32("lengths", index, B, lengths)
+    q_at, qr, qh = _heads_last("q", dtype, index, q, (B, H, D))
+    lengths_at = _int32("lengths", index, B, lengths)
     if out is not None and (out.shape != shape or out.dtype is not dtype or out.get_device() != index
                             or not out.is_contiguous()):
         raise ValueError("out must be contiguous, with q's shape, type and device")
@@ -1014,8 +1016,8 @@ def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     if lse is None and return_lse:
         lse = torch.empty((B, H), dtype=torch.float32, device=device)
     ws = _scratch(ngr_paged_attention_workspace_bytes(B, H, G, D, capacity, window), device, workspace)
-    rc = lib().ngr_fused_paged_attention(
-        q.data_ptr(), qr, qh, cache, lengths.data_ptr(), scale, window, B, H, G, D, code, out.data_ptr(), _ptr(lse),
+    rc = (_lib or lib()).ngr_fused_paged_attention(
+        q_at, qr, qh, cache, lengths_at, scale, window, B, H, G, D, code, out.data_ptr(), _ptr(lse),
         ws.data_ptr(), ws.numel() * ws.element_size(), _current_stream_handle(index))
     if rc != 0:
         raise NgrError(rc, "fused_paged_attention")
