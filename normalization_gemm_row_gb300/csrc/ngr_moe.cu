@@ -343,8 +343,8 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
 
 // -------------------------------------------------------------- products
 // The experts that somebody chose, in order, for every CTA in its shared
-// memory; one that more than kMoeEntry tokens chose stands there once for
-// each kMoeEntry of them, and its weights' second reader finds them in L2 (it
+// memory; one that more than ENTRY tokens chose stands there once for each
+// ENTRY of them, and its weights' second reader finds them in L2 (it
 // runs at the same time).  So every step costs the same, whatever the choice:
 // with all of an expert's tokens in one entry the runs with the busiest
 // experts kept the others waiting (down at 32 tokens, 32 experts of 4096 x
@@ -361,7 +361,7 @@ struct ChosenScratch {
     uint16_t base[kMoeMaxExperts];                     // by expert
 };
 // `p`, if not null, takes the weight of each row of h.
-template <int THREADS>
+template <int THREADS, int ENTRY>
 __device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenScratch &x, float *p)
 {
     const int lane = threadIdx.x & 31, all = a.M * a.top_k;
@@ -382,7 +382,7 @@ __device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenS
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const uint32_t t = e0 + lane < a.E ? x.tokens[e0 + lane] : 0u;
             if (__ballot_sync(0xffffffffu, t != 0u) == 0u) continue;
-            const int mine = __popc(t), entries = (mine + kMoeEntry - 1) / kMoeEntry;
+            const int mine = __popc(t), entries = (mine + ENTRY - 1) / ENTRY;
             int incl = mine | entries << 16;      // both sums at once
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -392,10 +392,10 @@ __device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenS
             if (t != 0u) {
                 int at = n + (incl >> 16) - entries, r = rows + (incl & 0xFFFF) - mine, left = mine;
                 x.base[e0 + lane] = static_cast<uint16_t>(r);
-                for (int i = 0; i < entries; ++i, ++at, left -= kMoeEntry) {
+                for (int i = 0; i < entries; ++i, ++at, left -= ENTRY) {
                     c.expert[at] = static_cast<uint16_t>(e0 + lane);
-                    c.base[at] = static_cast<uint16_t>(r + i * kMoeEntry);
-                    c.tokens[at] = static_cast<uint8_t>(min(left, kMoeEntry));
+                    c.base[at] = static_cast<uint16_t>(r + i * ENTRY);
+                    c.tokens[at] = static_cast<uint8_t>(min(left, ENTRY));
                 }
                 for (uint32_t bits = t; bits; bits &= bits - 1u) c.token[r++] = static_cast<uint8_t>(__ffs(bits) - 1);
             }
@@ -415,15 +415,15 @@ __device__ __forceinline__ void find_chosen(const MoeArgs &a, Chosen &c, ChosenS
     __syncthreads();
 }
 
-// How one kernel is laid out, with room for NT groups of tokens in an entry:
-// 1 if the call has no more tokens, else 2.
+// How one kernel is laid out, with room for NT groups of tokens in an entry.
+constexpr int moe_warps(bool down, int nt) { return nt == 4 ? 5 : nt == 2 && down ? 7 : 8; }
 template <bool DOWN, bool VEC, int NT>
 struct Layout {
     static constexpr int kStages = NT == 1 ? 4 : 3;
     // A stage: a step's 16 weight rows of 128 bytes, or of the nine 16-byte
     // words that they lie in where rows are off the boundary, and 8 token
     // rows of 128 bytes a group.
-    static constexpr int kGroups = NT;
+    static constexpr int kGroups = NT, kEntry = NT * kMoeGroup;
     static constexpr int kPitch = VEC ? 128 : 144, kCopies = VEC ? 4 : 5;
     static constexpr int kTokens = 16 * kPitch, kStage = kTokens + NT * 1024;
     // DOWN: the tokens' sums of the 16 rows under way, [token][17]
@@ -431,7 +431,7 @@ struct Layout {
     static constexpr int kSums = DOWN ? kMost * 17 * 4 : 0;
     static constexpr int kWarp = kStages * kStage + kSums;
     // Two CTAs have to fit into an SM's shared memory.
-    static constexpr int kWarps = DOWN && NT == 2 ? 7 : 8, kThreads = 32 * kWarps, kWorkers = kMoeCtas * kWarps;
+    static constexpr int kWarps = moe_warps(DOWN, NT), kThreads = 32 * kWarps, kWorkers = kMoeCtas * kWarps;
     static constexpr int kWeights = DOWN ? 0 : kMost * kMoeMaxTopK * 4;
     static constexpr int kBytes = kWarps * kWarp + kWeights;
     static_assert(kWarps * kWarp >= static_cast<int>(sizeof(ChosenScratch)), "the rings hold it first");
@@ -528,6 +528,15 @@ struct Copies {
     {
 #pragma unroll
         for (int i = 0; i < L::kCopies; ++i) from[i] += 64;
+    }
+    // On to the next 8 rows of the same experts' weights, of n elements, behind
+    // a segment's `length` steps: the rows' distances from the boundary stay.
+    __device__ __forceinline__ void next_rows(int n, int length)
+    {
+#pragma unroll
+        for (int i = 0; i < L::kCopies; ++i) from[i] += 8 * static_cast<int64_t>(n) - length * 64;
+#pragma unroll
+        for (int i = 0; i < 2 * L::kGroups; ++i) token[i] -= length * 64;
     }
     __device__ __forceinline__ void skip(int steps)
     {
@@ -650,45 +659,58 @@ __device__ __forceinline__ bool counted_last(int *count, const Sharers &w, int l
 
 // The parts of 16 rows' sums for all tokens, added in the workers' order into
 // sums [token][17].  A part is M x 4 pieces of 16 bytes: few tokens' are read
-// several at a time, each by some of the lanes.
-template <typename L>
-__device__ __forceinline__ void gather_parts(const MoeArgs &a, const Sharers &w, float *sums, int lane)
+// several at a time, each by some of the lanes; of many a lane reads several
+// pieces at a time.
+template <int PIECES>
+__device__ __forceinline__ void gather_pieces(const MoeArgs &a, const Sharers &w, float *sums, int lane, int each)
 {
     const float4 *parts = reinterpret_cast<const float4 *>(a.parts);
-    const int each = a.M == 1 ? 4 : a.M == 2 ? 8 : a.M <= 4 ? 16 : 32;     // lanes of a part
-    const int group = lane / each, groups = 32 / each;
-    for (int v0 = 0; v0 < a.M * 4; v0 += each) {
-        const int v = v0 + lane % each;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (v < a.M * 4) {
-#pragma unroll 8
-            for (int p = w.first + group; p <= w.last; p += groups) {
-                const float4 y = __ldcg(parts + (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (L::kMost * 4) + v);
-                x.x += y.x;
-                x.y += y.y;
-                x.z += y.z;
-                x.w += y.w;
+    const int pitch = a.part_bytes / 16, group = lane / each, groups = 32 / each, v = lane % each;
+    float4 x[PIECES] = {};
+#pragma unroll 4
+    for (int p = w.first + group; p <= w.last; p += groups) {
+        const float4 *from = parts + (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * pitch + v;
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            if (v + i * 32 < a.M * 4) {
+                const float4 y = __ldcg(from + i * 32);
+                x[i].x += y.x;
+                x[i].y += y.y;
+                x[i].z += y.z;
+                x[i].w += y.w;
             }
         }
-        for (int o = 16; o >= each; o >>= 1) {
-            x.x += __shfl_xor_sync(0xffffffffu, x.x, o);
-            x.y += __shfl_xor_sync(0xffffffffu, x.y, o);
-            x.z += __shfl_xor_sync(0xffffffffu, x.z, o);
-            x.w += __shfl_xor_sync(0xffffffffu, x.w, o);
+    }
+    for (int o = 16; o >= each; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < PIECES; ++i) {
+            x[i].x += __shfl_xor_sync(0xffffffffu, x[i].x, o);
+            x[i].y += __shfl_xor_sync(0xffffffffu, x[i].y, o);
+            x[i].z += __shfl_xor_sync(0xffffffffu, x[i].z, o);
+            x[i].w += __shfl_xor_sync(0xffffffffu, x[i].w, o);
         }
-        if (group == 0 && v < a.M * 4) {
-            float *to = sums + (v >> 2) * 17 + (v & 3) * 4;
-            to[0] = x.x;
-            to[1] = x.y;
-            to[2] = x.z;
-            to[3] = x.w;
+    }
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+        const int at = v + i * 32;
+        if (group == 0 && at < a.M * 4) {
+            float *to = sums + (at >> 2) * 17 + (at & 3) * 4;
+            to[0] = x[i].x;
+            to[1] = x[i].y;
+            to[2] = x[i].z;
+            to[3] = x[i].w;
         }
     }
     __syncwarp();
 }
+__device__ __forceinline__ void gather_parts(const MoeArgs &a, const Sharers &w, float *sums, int lane)
+{
+    if (a.M <= 8) gather_pieces<1>(a, w, sums, lane, a.M == 1 ? 4 : a.M == 2 ? 8 : a.M <= 4 ? 16 : 32);
+    else gather_pieces<4>(a, w, sums, lane, 32);
+}
 
 template <bool BF16, bool DOWN, bool VEC, int NT>
-__global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(const __grid_constant__ MoeArgs a)
+__global__ void __launch_bounds__(32 * moe_warps(DOWN, NT), 2) moe_kernel(const __grid_constant__ MoeArgs a)
 {
     using L = Layout<DOWN, VEC, NT>;
     constexpr int S = L::kStages;
@@ -702,12 +724,15 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
         pdl_wait();
         pdl_launch_dependents();
     }
-    find_chosen<L::kThreads>(a, c, *reinterpret_cast<ChosenScratch *>(smem), weights);
+    find_chosen<L::kThreads, L::kEntry>(a, c, *reinterpret_cast<ChosenScratch *>(smem), weights);
 
     const int n = DOWN ? a.F : a.K;
     const int length = (n + 63) / 64, tiles = DOWN ? (a.K + 15) / 16 : (a.F + 7) / 8;
     const int64_t total = static_cast<int64_t>(c.count) * tiles * length;
-    const int64_t share = max(static_cast<int64_t>(kMoeMinShare), (total + L::kWorkers - 1) / L::kWorkers);
+    // (steps of a unit: a segment, or DOWN the segments of 16 rows)
+    const int64_t unit = DOWN ? static_cast<int64_t>(c.count) * length : length;
+    const int64_t share = max(max(static_cast<int64_t>(kMoeMinShare), (unit + kMoeMaxSharers - 2) / (kMoeMaxSharers - 1)),
+                              (total + L::kWorkers - 1) / L::kWorkers);
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     const int64_t first = worker * share;
     if (first >= total) return;
@@ -729,7 +754,11 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
     auto advance = [&] {
         if (++ahead == length) {
             ahead = 0;
-            if (next<DOWN>(c, f, tiles)) plan_copies<DOWN, VEC, L>(a, c, f, copies, lane);
+            const int i = f.i;
+            if (next<DOWN>(c, f, tiles)) {
+                if (!DOWN && f.i == i && f.tile + 1 < tiles) copies.next_rows(n, length);
+                else plan_copies<DOWN, VEC, L>(a, c, f, copies, lane);
+            }
         }
     };
     if (DOWN) {
@@ -769,8 +798,6 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
         for (int i = lane; i < L::kMost * 17; i += 32) sums[i] = 0.0f;
         __syncwarp();
     }
-    // the unit: a segment, or DOWN the segments of 16 rows
-    const int64_t unit = DOWN ? static_cast<int64_t>(c.count) * length : length;
     int64_t begin = DOWN ? s.tile * unit : index * length;
     int d0 = 0, d1 = 0, stage = 0;
     bool fresh = true;
@@ -813,7 +840,7 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
             }
             bool finish = whole;
             if (!whole) {
-                float2 *part = reinterpret_cast<float2 *>(a.parts) + slot * (NT * 32) + lane;
+                float2 *part = reinterpret_cast<float2 *>(a.parts) + slot * (a.part_bytes / 8) + lane;
 #pragma unroll
                 for (int j = 0; j < NT; ++j)
                     if (j * kMoeGroup < s.tokens) part[j * 32] = v[j];
@@ -824,7 +851,7 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
 #pragma unroll 4
                     for (int p = w.first; p <= w.last; ++p) {
                         const float2 *from = reinterpret_cast<const float2 *>(a.parts) +
-                                             (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (NT * 32) + lane;
+                                             (static_cast<int64_t>(p) * 2 + (p == w.first ? 1 : 0)) * (a.part_bytes / 8) + lane;
 #pragma unroll
                         for (int j = 0; j < NT; ++j)
                             if (j * kMoeGroup < s.tokens) {
@@ -869,13 +896,13 @@ __global__ void __launch_bounds__(32 * (DOWN && NT == 2 ? 7 : 8), 2) moe_kernel(
                 bool finish = whole;
                 if (!whole) {
                     // (16-byte pieces: M tokens x 4 of them)
-                    float4 *part = reinterpret_cast<float4 *>(a.parts) + slot * (L::kMost * 4);
+                    float4 *part = reinterpret_cast<float4 *>(a.parts) + slot * (a.part_bytes / 16);
                     for (int v = lane; v < a.M * 4; v += 32) {
                         const float *from = sums + (v >> 2) * 17 + (v & 3) * 4;
                         part[v] = make_float4(from[0], from[1], from[2], from[3]);
                     }
                     finish = counted_last(counts, w, lane);
-                    if (finish) gather_parts<L>(a, w, sums, lane);
+                    if (finish) gather_parts(a, w, sums, lane);
                 }
                 if (finish)
                     for (int v = lane; v < values; v += 32)
@@ -932,14 +959,21 @@ cudaError_t launch(F *kern, unsigned grid, unsigned threads, int cluster, size_t
     return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
+template <bool BF16, bool DOWN, bool VEC, int NT>
+cudaError_t product(const MoeArgs &a, cudaStream_t stream)
+{
+    using L = Layout<DOWN, VEC, NT>;
+    return launch(moe_kernel<BF16, DOWN, VEC, NT>, kMoeCtas, L::kThreads, 0, L::kBytes, true, a, stream);
+}
+
 template <bool BF16, bool DOWN, bool VEC>
 cudaError_t product(const MoeArgs &a, cudaStream_t stream)
 {
-    using One = Layout<DOWN, VEC, 1>;
-    using Two = Layout<DOWN, VEC, 2>;
-    if (a.M <= kMoeGroup)
-        return launch(moe_kernel<BF16, DOWN, VEC, 1>, kMoeCtas, One::kThreads, 0, One::kBytes, true, a, stream);
-    return launch(moe_kernel<BF16, DOWN, VEC, 2>, kMoeCtas, Two::kThreads, 0, Two::kBytes, true, a, stream);
+    switch (a.groups) {
+    case 1: return product<BF16, DOWN, VEC, 1>(a, stream);
+    case 2: return product<BF16, DOWN, VEC, 2>(a, stream);
+    default: return product<BF16, DOWN, VEC, 4>(a, stream);
+    }
 }
 
 int status(const char *what, cudaError_t e) { return e == cudaSuccess ? 0 : record_cuda_error(what, e, cudaGetErrorString(e)); }

@@ -22,8 +22,15 @@ constexpr int kMoeGroup = 4;
 constexpr int kMoeMinShare = 4;       // steps of a worker at least
 constexpr int kMoeCounters = 2 * kMoeWorkers;   // up, down: of a unit by its first worker
 
-constexpr int kMoeEntry = 2 * kMoeGroup;   // tokens that share one reading of an expert's weights
-constexpr int kMoeMaxEntries = kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / kMoeEntry;
+// Groups of tokens that share one reading of an expert's weights: 1 if the
+// call has no more, 2 (nearly all experts' of a batch that spreads over many),
+// or 4 where an expert has more than six on average, so that 8 would often
+// not hold them.
+inline int moe_groups(int64_t M, int64_t E, int64_t top_k) { return M <= kMoeGroup ? 1 : M > 2 * kMoeGroup && M * top_k > 6 * E ? 4 : 2; }
+constexpr int kMoeMaxEntries = kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / (2 * kMoeGroup);
+// Runs that share a unit at most: the last to finish adds their parts, at
+// about 0.2 us each.
+constexpr int kMoeMaxSharers = 24;
 
 struct MoeArgs {
     const void *x, *gamma, *beta;     // [M, K], [K]
@@ -36,15 +43,16 @@ struct MoeArgs {
     void *a;                          // [M, 2, Kp] normalized rows in two parts, zeros up to a multiple of 8
     void *h;                          // [M top_k, 2, Fp] weight x SiLU(gate) x up in two parts, likewise
     // A worker's parts of the units that it shares, the second place for the
-    // unit that begins with it: up [workers][2][groups][32 lanes][gate, up],
-    // down [workers][2][tokens][16 rows], FP32 (groups and tokens that there is
-    // room for: 1 and 4, or 2 and 32).  Up's are done with when
+    // unit that begins with it: part_bytes each: up [groups][32 lanes][gate,
+    // up], down [tokens][16 rows], FP32.  Up's are done with when
     // down's are made.
     float *parts;
+    int part_bytes;
     int *counters;                    // [kMoeCounters], zeroed by the router
     int *err;
     int norm, M, K, F, E, top_k, renormalize;
     int Kp, Fp;                       // pitches, multiples of 64
+    int groups;                       // see moe_groups
     int router;                       // CTAs of the cluster that takes a token's routing
     float eps;
 };

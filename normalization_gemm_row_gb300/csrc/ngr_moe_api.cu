@@ -13,7 +13,6 @@ namespace ngr {
 
 namespace {
 
-constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
 
 static_assert(NGR_MOE_MAX_M == kMoeMaxTokens && NGR_MOE_MAX_EXPERTS == kMoeMaxExperts && NGR_MOE_MAX_TOP_K == kMoeMaxTopK,
               "ngr.h and the kernels agree");
@@ -34,10 +33,11 @@ int moe_sizes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
 
 struct MoePlan {
     size_t ids, w, a, h, parts, counters, total;
-    int64_t Kp, Fp;
+    int64_t Kp, Fp, part_bytes;
+    int groups;
 };
 
-MoePlan moe_plan(int64_t M, int64_t K, int64_t F, int64_t top_k)
+MoePlan moe_plan(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
 {
     MoePlan p;
     p.Kp = up_to(K, 64);
@@ -52,7 +52,9 @@ MoePlan moe_plan(int64_t M, int64_t K, int64_t F, int64_t top_k)
     p.w = take(M * top_k * 4);
     p.a = take(M * 2 * p.Kp * 2);
     p.h = take(M * top_k * 2 * p.Fp * 2);
-    p.parts = take(static_cast<int64_t>(kMoeWorkers) * 2 * (M <= kMoeGroup ? kMoeGroup : kMoeMaxTokens) * 64);
+    p.groups = moe_groups(M, E, top_k);
+    p.part_bytes = std::max<int64_t>(p.groups * 256, M * 64);
+    p.parts = take(static_cast<int64_t>(kMoeWorkers) * 2 * p.part_bytes);
     p.counters = take(kMoeCounters * 4);
     p.total = off;
     return p;
@@ -69,7 +71,7 @@ extern "C" {
 size_t ngr_moe_swiglu_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
 {
     if (moe_sizes(M, K, F, E, top_k) != NGR_OK) return 0;
-    return moe_plan(M, K, F, top_k).total;
+    return moe_plan(M, K, F, E, top_k).total;
 }
 
 int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void *beta, const void *Wr, const void *Wg,
@@ -89,7 +91,7 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     for (const void *p : {x, gamma, beta, Wr, Wg, Wu, Wd, static_cast<const void *>(y)})
         if (!aligned(p, 2)) return NGR_ERR_ALIGN;
     if (!aligned(experts, 4) || !aligned(weights, 4)) return NGR_ERR_ALIGN;
-    const MoePlan p = moe_plan(M, K, F, top_k);
+    const MoePlan p = moe_plan(M, K, F, E, top_k);
     if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;
     int sms = 0;
@@ -113,6 +115,8 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.a = ws + p.a;
     a.h = ws + p.h;
     a.parts = reinterpret_cast<float *>(ws + p.parts);
+    a.part_bytes = static_cast<int>(p.part_bytes);
+    a.groups = p.groups;
     a.counters = reinterpret_cast<int *>(ws + p.counters);
     a.err = reinterpret_cast<int *>(ws);
     a.norm = norm;
@@ -131,8 +135,8 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     const bool vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
     const bool vec_f = F % 8 == 0 && aligned(Wd, 16);
     if (trace_mode())
-        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d%s%s\n",
-                     a.M, a.K, a.F, a.E, a.top_k, norm, vec_k ? "" : ", gate and up shifted",
+        std::fprintf(stderr, "ngr: experts M=%d K=%d F=%d E=%d top_k=%d norm=%d groups=%d%s%s\n",
+                     a.M, a.K, a.F, a.E, a.top_k, norm, a.groups, vec_k ? "" : ", gate and up shifted",
                      vec_f ? "" : ", down shifted");
     call_begin();
     kernel_begin(stream);

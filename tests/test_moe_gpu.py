@@ -51,6 +51,20 @@ def test_experts(E, top_k):
     run(6, 64, 40, E, top_k, F16, seed=E + top_k)
 
 
+@pytest.mark.parametrize("M,E,top_k", [(12, 2, 1), (12, 2, 2), (24, 3, 2), (32, 1, 1), (32, 4, 4), (32, 5, 3), (17, 4, 2), (9, 1, 1)])
+@pytest.mark.parametrize("K,F", [(128, 96), (61, 45), (64, 1000)])
+def test_few_experts_of_many_tokens(M, E, top_k, K, F):
+    """More tokens an expert than share one reading of its weights."""
+    run(M, K, F, E, top_k, BF16, seed=M + E)
+
+
+@pytest.mark.parametrize("K,F", [(16, 3000), (130, 2500), (3000, 16), (8, 9), (200, 4544)])
+@pytest.mark.parametrize("M", [1, 19])
+def test_long_thin_experts(M, K, F):
+    """Units of one step, and units that many workers share."""
+    run(M, K, F, 8, 4, F16, seed=K)
+
+
 def test_everybody_chooses_the_same_and_everybody_apart():
     d = R.case(32, 128, 96, 40, BF16, seed=3, norm=0)
     d["Wr"].zero_()

@@ -157,7 +157,7 @@ for data, call in S.CALLS[:3]:
 LINES = [r"ngr: rotated append T=64 H=8 G=4 D=64 rot=64 page=16 elements at once=8 blocks a token=\d+",
          r"ngr: paged attention B=90 H=8 G=2 D=64 page=16 window=0 dim=64 workers=\d+ jobs=\d+",
          r"ngr: paged attention B=3 H=8 G=2 D=64 page=16 window=0 dim=64 items=6 jobs=0",
-         r"ngr: experts M=9 K=256 F=320 E=12 top_k=3 norm=2"]
+         r"ngr: experts M=9 K=256 F=320 E=12 top_k=3 norm=2 groups=2"]
 
 
 def test_trace_and_debug():
