@@ -621,8 +621,11 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
 // The parts of an item that several workers share.  Up to 32 parts (a batch)
 // a warp takes a row by itself, its parts' weights in its lanes; more (few
 // long sequences) are taken by all warps of a block together, a row of blocks
-// for each row.
-constexpr int kJoinWarps = 16, kJoinHeld = 8;
+// for each row; HELD of its parts a warp has under way at once.  8 where items
+// have many parts on average (131072 tokens of 8 key heads: 98.9 -> 97.4 us
+// with 8 instead of 4), else 4, whose registers let more blocks run (64 rows of
+// 8192 tokens: the join 12 us instead of 17).
+constexpr int kJoinWarps = 16;
 
 template <int N>
 __device__ __forceinline__ void add_scaled(float4 (&to)[N], const float4 (&v)[N], float w)
@@ -636,7 +639,7 @@ __device__ __forceinline__ void add_scaled(float4 (&to)[N], const float4 (&v)[N]
     }
 }
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, int HELD>
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a)
 {
     extern __shared__ float weight[];     // [workers][weight, weight x sum]
@@ -675,9 +678,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
     }
     for (int row = blockIdx.y; row < rows; row += gridDim.y) {
         // A warp's first sums are on their way before their weights are known.
-        float4 held[kJoinHeld][kEach];
+        float4 held[HELD][kEach];
 #pragma unroll
-        for (int h = 0; h < kJoinHeld; ++h)
+        for (int h = 0; h < HELD; ++h)
             if (warp + h * kJoinWarps < parts) load(held[h], warp + h * kJoinWarps, row);
         float top = -INFINITY;
         for (int i = threadIdx.x; i < parts; i += 32 * kJoinWarps) top = fmaxf(top, a.part_ml[part(i, row)].x);
@@ -703,10 +706,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
         {
             float4 acc[kEach] = {};
 #pragma unroll
-            for (int h = 0; h < kJoinHeld; ++h)
+            for (int h = 0; h < HELD; ++h)
                 if (warp + h * kJoinWarps < parts) add_scaled(acc, held[h], weight[2 * (warp + h * kJoinWarps)]);
 #pragma unroll 4
-            for (int i = warp + kJoinHeld * kJoinWarps; i < parts; i += kJoinWarps) {
+            for (int i = warp + HELD * kJoinWarps; i < parts; i += kJoinWarps) {
                 float4 v[kEach];
                 load(v, i, row);
                 add_scaled(acc, v, weight[2 * i]);
@@ -769,7 +772,7 @@ cudaError_t join(const AttendArgs &a, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_join_kernel<BF16, DP>, a);
+    return cudaLaunchKernelEx(&cfg, a.slots * 32 <= a.workers ? attend_join_kernel<BF16, DP, 8> : attend_join_kernel<BF16, DP, 4>, a);
 }
 
 // Calls f with the padded dimension, and whether smaller ones share it.
