@@ -342,9 +342,7 @@ size_t ngr_linear_cross_entropy_workspace_bytes(int backward, int64_t M,
  * the sequence in row b lies in page table[b][j / page_size], slot j %
  * page_size; a row's first table_pages entries count, and only those that the
  * sequence's tokens need are looked at.  A cache without pages, [B, S, G, D],
- * is pages = B of page_size = S with the table 0, 1, ..., B - 1.
- * (The pages name keeping the cache in segments that attention reads piece by
- * piece: [OPS], KV-cache-aware incremental attention.) */
+ * is pages = B of page_size = S with the table 0, 1, ..., B - 1. */
 typedef struct {
     void *k, *v;
     int64_t pages, page_size;
@@ -434,9 +432,10 @@ size_t ngr_paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t G,
  * gamma, beta and eps as in ngr_fused_norm_swiglu.  The choice is returned in
  * experts (int32 [M, top_k], largest first) and weights (FP32 [M, top_k]) when
  * they are not NULL.  The router works in FP32 throughout; the experts'
- * products take a, and p times the gated product, rounded to `dtype`, and
+ * products take a, and p times the gated product, in two parts of `dtype` (the
+ * value rounded and what that left out; within `dtype`'s range), and
  * accumulate in FP32; y is rounded once.  Only chosen experts' weights are
- * read, each once.  A token whose router's logits hold a NaN has y = NaN.
+ * read.  A token whose router's logits hold a NaN has y = NaN.
  * Any K and F up to NGR_MOE_MAX_WIDTH, any 2-byte alignment (16-byte aligned
  * weights with K, F multiples of 8 take 16-byte loads).  y may be x's memory.
  * Sums have a fixed order.  Workspace (256-byte aligned):
