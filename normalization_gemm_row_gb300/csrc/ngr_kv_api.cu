@@ -16,9 +16,12 @@ namespace {
 
 constexpr int64_t kMax31 = (int64_t(1) << 31) - 1;
 // Units of a call that are several to a thread: as many as the SMs have room
-// for threads, twice over.
+// for threads, twice over.  Four heads a thread against one: 8192 tokens of 80
+// heads of 128 64 and 84 us, 2048 tokens of 48 heads 10.5 and 16.6; calls
+// below this would leave SMs without a block.
 constexpr int64_t kAppendMany = int64_t(2) * 152 * 2048;
-// Fewer tiles than this are not worth a worker of their own.
+// Fewer tiles than this are not worth a worker of their own: one row of 4096
+// tokens, 8 key heads: 14.5 us, with 1 15.2, with 4 14.6.
 constexpr int64_t kMinShare = 2;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }

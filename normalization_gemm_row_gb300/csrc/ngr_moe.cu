@@ -6,18 +6,19 @@
 //   h = p SiLU(a Wg^T) (a Wu^T) for a token and chosen expert,
 //   y = sum over the chosen experts of h Wd^T.
 //
-// A chosen expert's three weights are read once, 6 F K bytes, for the few
-// tokens that chose it: reading them bounds the layer.  The weights go
-// straight from memory into the operands of 16 x 8 x 16 matrix instructions,
-// their rows as the instruction's rows and the tokens as its columns: a lane
-// reads 16 contiguous bytes of a row, and the contraction is taken in the
-// order that this gives, for both operands alike.
+// A chosen expert's three weights, 6 F K bytes, serve the few tokens that
+// chose it: reading them bounds the layer.  Each warp has a ring of stages in
+// shared memory that its own asynchronous copies fill with weights and token
+// rows, and takes them with 16 x 8 x 16 matrix instructions, the weight's rows
+// as the instruction's rows and the tokens as its columns; it waits for
+// nothing but its own copies.  (Weights loaded straight into the operands: 802
+// us where the rings take 362, below.)
 //
 // The steps of a product (64 columns of 16 weight rows) over all chosen
 // experts stand in one row that is cut into equal runs, one a warp
 // ("worker"), so that any number of experts and any sizes keep every warp
-// busy to the end; only the device knows the choice.  A worker's loads run
-// kDepth steps ahead, past the ends of units too.  A unit (16 rows' results)
+// busy to the end; only the device knows the choice.  A worker's copies run
+// some steps ahead, past the ends of units too.  A unit (16 rows' results)
 // that several workers share is put together, in the workers' order, by the
 // one that finishes last: the others leave their parts in memory and count.
 //
@@ -25,6 +26,9 @@
 // to the 16-bit type and what that left out, so that rounding a and h costs
 // no accuracy (a single rounding of each doubled y's error, 1.7e-3 to 3.4e-3
 // in bf16), for no bytes of weights more.
+//
+// bf16, 32 tokens, 6 of 64 experts of 4096 x 1536: 362 us, gate and up 249 us
+// (6.4 TB/s), down 125; one token, 2 of 8 experts of 4096 x 14336: 125 us.
 #include "ngr.h"
 #include "ngr_entry.h"
 #include "ngr_internal.h"
@@ -83,10 +87,11 @@ __device__ __forceinline__ uint2 two_parts(float x, float y)
 }
 
 // ---------------------------------------------------------------- router
-// A cluster of a.router CTAs (8, or 16 for many experts) for a token.  Its CTAs share the experts, each
-// with the token's normalized row in FP32, a piece at a time; the first CTA
-// gathers the logits and chooses.  Bound by the latency of what it does one
-// after the other: row, statistics, logits, choice.
+// A cluster of a.router CTAs (8, or 16 for many experts) for a token.  Its
+// CTAs share the experts, each with the token's normalized row in FP32, a
+// piece at a time; the first CTA gathers the logits and chooses.  Bound by the
+// latency of what it does one after the other: row, statistics, logits,
+// choice (10 us at 32 tokens of 4096, 32 experts, memory's caches flushed).
 constexpr int kRouterPiece = 8192;
 constexpr int kRouterPitch = kRouterPiece / 8 + 1;
 constexpr int kRouterThreads = 512, kRouterWarps = kRouterThreads / 32;
@@ -348,8 +353,9 @@ __global__ void __launch_bounds__(kRouterThreads) moe_router_kernel(const __grid
 // runs at the same time).  So every step costs the same, whatever the choice:
 // with all of an expert's tokens in one entry the runs with the busiest
 // experts kept the others waiting (down at 32 tokens, 32 experts of 4096 x
-// 1536: a third of the warps' time).  The rows of h stand by expert and then
-// by token.
+// 1536: a third of the warps' time; 433 us in all for the 32 tokens and 64
+// experts above, against 362).  The rows of h stand by expert and then by
+// token.
 struct Chosen {
     uint16_t expert[kMoeMaxEntries], base[kMoeMaxEntries];
     uint8_t tokens[kMoeMaxEntries];

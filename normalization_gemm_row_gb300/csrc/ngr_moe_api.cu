@@ -13,11 +13,13 @@ namespace ngr {
 
 namespace {
 
-
 static_assert(NGR_MOE_MAX_M == kMoeMaxTokens && NGR_MOE_MAX_EXPERTS == kMoeMaxExperts && NGR_MOE_MAX_TOP_K == kMoeMaxTopK,
               "ngr.h and the kernels agree");
 
-// More experts than this take clusters of 16 CTAs in the router.
+// More experts than this take clusters of 16 CTAs in the router: 8 tokens, 128
+// experts 97 us with 16, 98.5 with 8; one token, 256 experts of 7168 x 2048
+// 142 and 146; but 32 tokens, 64 experts 366 and 361, as 512 CTAs of the
+// router are more than fit at once.
 constexpr int64_t kMoeManyExperts = 64;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
