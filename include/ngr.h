@@ -394,10 +394,11 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
  * over the lengths[b] tokens of table row b (the new token's own among them,
  * if it was appended), or the last `window` of them (0: all).  Query head h
  * uses key head h / (H / G); H is a multiple of G.  q is [B, H, D] by its row
- * and head strides in elements, out [B, H, D] dense, lse FP32 [B, H] or NULL
- * (it joins results over parts of a context).  lengths[b] = 0 gives out = 0
- * and lse = -inf, and so do scores that are all -inf; a negative length is a row that is not in use, whose out
- * and lse are left as they were.  A length beyond table_pages page_size counts
+ * and head strides in elements, out [B, H, D] dense (q's own memory, if q is
+ * dense too, or apart from it), lse FP32 [B, H] or NULL (it joins results over
+ * parts of a context).  lengths[b] = 0 gives out = 0 and lse = -inf, and so do
+ * scores that are all -inf; a negative length is a row that is not in use,
+ * whose out and lse are left as they were.  A length beyond table_pages page_size counts
  * as that, a page that is not there as if its tokens were not, and either is
  * reported by the workspace's error word as NGR_ERR_ARG.  What the cache holds
  * beside the sequences' tokens is not looked at (it may be NaN).  Scores,

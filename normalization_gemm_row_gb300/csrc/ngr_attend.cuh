@@ -222,17 +222,23 @@ __device__ __forceinline__ void join_row(const AttendArgs &a, int parts, int64_t
 }
 
 // The error word by one block: lengths beyond the table, and pages that are
-// not there, of all rows.
+// not there, of all rows.  8 lanes take a row, 8 entries each at once, so that
+// the block is done before those that attend (150 rows of 2000 tokens one
+// after the other, a block wide: 108 us).
 __device__ __forceinline__ void check_pages(const AttendArgs &a)
 {
+    constexpr int kLanes = 8, kHeld = 8;
     bool bad = false;
-    for (int b = 0; b < a.B; ++b) {
+    for (int b = static_cast<int>(threadIdx.x) / kLanes; b < a.B; b += static_cast<int>(blockDim.x) / kLanes) {
         const Span s = span_of(a, b, &bad);
         if (s.n == 0) continue;
-        for (int i = s.start / a.kv.page_size + static_cast<int>(threadIdx.x); i <= (s.start + s.n - 1) / a.kv.page_size;
-             i += static_cast<int>(blockDim.x)) {
-            const int page = a.kv.table[b * a.kv.table_stride + i];
-            bad = bad || page < 0 || page >= a.kv.pages;
+        const int last = (s.start + s.n - 1) / a.kv.page_size;
+        for (int64_t i = s.start / a.kv.page_size + static_cast<int>(threadIdx.x) % kLanes; i <= last; i += kLanes * kHeld) {
+            int page[kHeld];
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h) page[h] = i + h * kLanes <= last ? a.kv.table[b * a.kv.table_stride + i + h * kLanes] : 0;
+#pragma unroll
+            for (int h = 0; h < kHeld; ++h) bad = bad || page[h] < 0 || page[h] >= a.kv.pages;
         }
     }
     const int any = __syncthreads_or(bad);

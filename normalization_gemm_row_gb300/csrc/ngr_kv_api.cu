@@ -83,8 +83,14 @@ int granule(std::initializer_list<const void *> bases, std::initializer_list<int
     return static_cast<int>(bits & -bits);
 }
 
-// Contexts whose items take a CTA each: tiles of each of its warps at most.
-constexpr int64_t kSoloTiles = 6;
+// Contexts whose items take a CTA each: tiles of each of its warps at most, 6
+// or a sixth of the items.  Few items leave SMs idle, but there is no second
+// launch and nothing to join.  64 query heads on 8 of 128, alone against
+// split, memory's caches flushed: one row of 1000 tokens 16.5 us (split 17.5),
+// of 2040 21.7 (17.5); 12 rows of 4000 49 (56), 16 of 2040 36 (46), 16 of
+// 4000 61 (71); 16 of 400 to 4000 44 (46).  The longest row sets the time
+// (one of 8000 tokens 54 us, split 24), so the longest tables stay split.
+constexpr int64_t kSoloTiles = 6, kSoloItems = 6;
 
 struct AttendPlan {
     bool solo;
@@ -106,7 +112,8 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
     p.part_rows = std::min<int64_t>(group, kAttendRows);
     const int64_t tiles = (longest + kAttendTile - 1) / kAttendTile;
     p.total = 256;
-    p.solo = p.items <= kAttendSms && tiles <= kSoloTiles * warps;
+    // (a block more looks for bad pages)
+    p.solo = p.items < kAttendSms && tiles <= std::max(kSoloTiles, p.items / kSoloItems) * warps;
     if (p.solo) return p;
     // (a place more for each item: kItemPlaces)
     const double all = static_cast<double>(p.items) * static_cast<double>(tiles + 1);

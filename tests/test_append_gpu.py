@@ -213,3 +213,21 @@ def test_bad_tokens_are_left_out_and_reported(what):
     ngr.fused_rope_append_kv(q, k, v, kc, vc, table.cuda(), positions.cuda(), rows=rows.cuda())
     assert torch.equal(vc[table[0, 0].item(), 3], v[0])
     assert torch.equal(vc[3], before[3]) or what == "row past the table"
+
+
+@pytest.mark.parametrize("layout", ["heads", "wide", "pages inside"])
+def test_values_in_another_layout_than_keys(layout):
+    """The strides of the two caches are their own."""
+    g = R.generator(6)
+    k, v = torch.randn((4, 3, 64), generator=g).to(BF16), torch.randn((4, 3, 64), generator=g).to(BF16)
+    kc = torch.zeros((5, 16, 3, 64), dtype=BF16, device="cuda")
+    vc = R.to_cuda(R.cache_like(5, 16, 3, 64, BF16, layout, g, fill=0.0)[1])
+    table = torch.tensor([[4, 1], [0, 3]], dtype=torch.int32)
+    rows, pos = torch.tensor([0, 0, 1, 1], dtype=torch.int32), torch.tensor([15, 16, 3, 31], dtype=torch.int32)
+    ngr.fused_rope_append_kv(None, k.cuda(), v.cuda(), kc, vc, table.cuda(), pos.cuda(), rows=rows.cuda())
+    page, slot = table[rows.long(), pos.long() // 16].long(), pos.long() % 16
+    for got, new in ((kc.cpu(), k), (vc.cpu(), v)):
+        assert torch.equal(got[page, slot], new)
+        got = got.clone()
+        got[page, slot] = 0
+        assert (got == 0).all()

@@ -212,3 +212,56 @@ def test_joined_by_lse():
     extra = R.U[F16] * sum((o * torch.exp(l - total)[..., None]).abs() for o, l in parts)
     assert ((out - want[0]).abs() <= 2 * want[2] + extra).all()
     assert ((total - want[1]).abs() <= 2 * want[3] + 1e-6).all()
+
+
+@pytest.mark.parametrize("page_size", [1, 16])
+@pytest.mark.parametrize("B", [1, 140, 200])
+def test_bad_pages_of_many_rows_are_reported(B, page_size):
+    """Any row's last page, or its length: found in batches of every size, and only then."""
+    lengths = [40 + b % 300 for b in range(B)]
+    for row in sorted({0, B // 2, B - 1}):
+        for what in ("none", "page", "length"):
+            d = data(lengths, 4, 1, 64, page_size, BF16, dirty=False, seed=row)
+            if what == "page":
+                d["table"][row, (lengths[row] - 1) // page_size] = d["k"].shape[0]
+            elif what == "length":
+                d["table"][row] = 0
+                d["lengths"][row] = d["table"].shape[1] * page_size + 1
+            n = ngr.binding.ngr_paged_attention_workspace_bytes(B, 4, 1, 64, d["table"].shape[1] * page_size, 0)
+            ws = torch.full((n,), 255, dtype=torch.uint8, device="cuda")
+            out, lse = call(d, workspace=ws)
+            R.check_attention(out, lse, R.attention(d["q"], d["k"], d["v"], d["table"], d["lengths"], 0.125), what)
+            if what == "none":
+                ngr.check_workspace(ws)
+            else:
+                with pytest.raises(ngr.NgrError) as e:
+                    ngr.check_workspace(ws)
+                assert e.value.status == -9
+
+
+@pytest.mark.parametrize("lengths,H,G,D", [([2500] * 18, 16, 8, 64), ([2000] * 3 + [1, 0, 1700] * 5, 8, 8, 128), ([700] * 151, 2, 1, 256),
+                                           ([700] * 152, 2, 1, 256), ([900, 3, 16] * 8, 40, 2, 256)])
+def test_batches_that_nearly_fill_the_device(lengths, H, G, D):
+    check(data(lengths, H, G, D, 32, F16, seed=len(lengths)))
+
+
+def test_values_in_another_layout_than_keys():
+    """The strides of k and v are their own."""
+    for lengths in ([100, 3, 61], [700] * 60):
+        d = data(lengths, 8, 4, 64, 16, BF16, layout="tokens")
+        for layout in ("heads", "wide", "pages inside"):
+            other = R.cache_like(d["k"].shape[0], 16, 4, 64, BF16, layout, R.generator(1), fill=0.0)[1]
+            d["v"] = other.copy_(d["v"])
+            check(d, what=layout)
+
+
+def test_output_in_the_queries_place():
+    for lengths in ([100, 0, -1, 61], [5000, 40] + [300] * 100):
+        d = data(lengths, 16, 4, 64, 16, F16)
+        want, want_lse = call(d, out=torch.zeros_like(d["q"], device="cuda"))
+        q = d["q"].cuda()
+        out, lse = ngr.fused_paged_attention(q, R.to_cuda(d["k"]), R.to_cuda(d["v"]), d["table"].cuda(), d["lengths"].cuda(), out=q,
+                                             return_lse=True)
+        used = d["lengths"] >= 0
+        assert out is q and torch.equal(q.cpu()[used], want.cpu()[used]) and torch.equal(lse.cpu()[used], want_lse.cpu()[used])
+        assert torch.equal(q.cpu()[~used], d["q"][~used])
