@@ -16,11 +16,12 @@ namespace {
 static_assert(NGR_MOE_MAX_M == kMoeMaxTokens && NGR_MOE_MAX_EXPERTS == kMoeMaxExperts && NGR_MOE_MAX_TOP_K == kMoeMaxTopK,
               "ngr.h and the kernels agree");
 
-// More experts than this take clusters of 16 CTAs in the router: 8 tokens, 128
-// experts 97 us with 16, 98.5 with 8; one token, 256 experts of 7168 x 2048
-// 142 and 146; but 32 tokens, 64 experts 366 and 361, as 512 CTAs of the
-// router are more than fit at once.
-constexpr int64_t kMoeManyExperts = 64;
+// More experts than this take clusters of 16 CTAs in the router, if the tokens
+// are few enough for each CTA to have an SM: 8 tokens, 512 experts 118 us with
+// 16, 122.7 with 8; 128 experts 97 and 98.5; one token, 256 experts of 7168 x
+// 2048 142 and 146; but 32 tokens, 512 experts 331 and 323.5; 12 tokens, 128
+// experts 131 and 129.
+constexpr int64_t kMoeManyExperts = 64, kMoeFewTokens = 9;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
@@ -131,7 +132,7 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     a.Kp = static_cast<int>(p.Kp);
     a.Fp = static_cast<int>(p.Fp);
     a.eps = eps;
-    a.router = E > kMoeManyExperts ? 16 : 8;
+    a.router = E > kMoeManyExperts && M <= kMoeFewTokens ? 16 : 8;
     const bool bf16 = dtype == NGR_BF16;
     const bool vec_r = K % 8 == 0 && aligned(Wr, 16) && aligned(x, 16) && aligned(a.gamma, 16) && aligned(a.beta, 16);
     const bool vec_k = K % 8 == 0 && aligned(Wg, 16) && aligned(Wu, 16);
