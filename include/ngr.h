@@ -408,7 +408,8 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
  * pointer but lengths, lse and the table 16-byte aligned and every stride a
  * multiple of 8 elements; k and v each reach over 64 GiB at most
  * (NGR_ERR_SHAPE).  Workspace (256-byte aligned):
- * ngr_paged_attention_workspace_bytes, with capacity = table_pages page_size.
+ * ngr_paged_attention_workspace_bytes, with capacity = table_pages page_size
+ * (one is enough for smaller batches, tables and windows).
  * The lengths stay on the device, so a captured call follows them. */
 int ngr_fused_paged_attention(const void *q, int64_t q_row_stride,
                               int64_t q_head_stride, const ngr_kv_cache *cache,

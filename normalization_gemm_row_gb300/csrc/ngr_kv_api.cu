@@ -114,7 +114,9 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
     p.total = 256;
     // (a block more looks for bad pages)
     p.solo = p.items < kAttendSms && tiles <= std::max(kSoloTiles, p.items / kSoloItems) * warps;
-    if (p.solo) return p;
+    // Longer tables' batches have a split's workspace all the same, so that one
+    // for a batch is enough for smaller batches, which are split.
+    if (p.solo && tiles <= kSoloTiles * warps) return p;
     // (a place more for each item: kItemPlaces)
     const double all = static_cast<double>(p.items) * static_cast<double>(tiles + 1);
     const int64_t ctas = all >= static_cast<double>(kAttendSms * kMinShare)

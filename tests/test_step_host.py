@@ -163,3 +163,20 @@ def test_helpers_refuse_on_the_cpu():
                              gamma=torch.zeros(7, dtype=torch.float16))
     with pytest.raises(ValueError, match="CUDA"):
         pkg.fused_moe_swiglu(t, torch.zeros((3, 8), dtype=torch.float16), w, w, w.transpose(1, 2).contiguous(), 1)
+
+
+@pytest.mark.parametrize("H,G,D", [(64, 8, 128), (4, 1, 64), (40, 2, 256), (12, 12, 80)])
+@pytest.mark.parametrize("capacity", [16, 1000, 2048, 5000, 40000])
+def test_a_workspace_is_enough_for_smaller_batches_and_tables(H, G, D, capacity):
+    size = B.ngr_paged_attention_workspace_bytes
+    of_batches = [size(n, H, G, D, capacity, 0) for n in range(1, 200)]
+    assert of_batches == sorted(of_batches)
+    for n in (1, 7, 100):
+        assert size(n, H, G, D, capacity, 0) <= size(n, H, G, D, 2 * capacity, 0)
+        assert size(n, H, G, D, capacity, 500) <= size(n, H, G, D, capacity, 0)
+
+
+@pytest.mark.parametrize("K,F,E,top_k", [(64, 96, 8, 2), (4096, 1536, 64, 6), (1000, 2001, 13, 3), (192, 4544, 4, 4)])
+def test_experts_workspace_is_enough_for_fewer_tokens(K, F, E, top_k):
+    sizes = [B.ngr_moe_swiglu_workspace_bytes(m, K, F, E, top_k) for m in range(1, 33)]
+    assert sizes == sorted(sizes)
