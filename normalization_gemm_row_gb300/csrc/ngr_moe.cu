@@ -737,7 +737,15 @@ __global__ void __launch_bounds__(32 * moe_warps(DOWN, NT), 2) moe_kernel(const 
     const int64_t total = static_cast<int64_t>(c.count) * tiles * length;
     // (steps of a unit: a segment, or DOWN the segments of 16 rows)
     const int64_t unit = DOWN ? static_cast<int64_t>(c.count) * length : length;
-    const int64_t share = max(max(static_cast<int64_t>(kMoeMinShare), (unit + kMoeMaxSharers - 2) / (kMoeMaxSharers - 1)),
+    // Steps of a worker: at least as many as a unit then has workers, whose
+    // last one adds their parts at about a step's time each (down's parts of
+    // fewer than 8 tokens: several at once, in that measure).  19 tokens, 4 of
+    // 8 experts of 192 x 4544 (12 units of down): 43 us, of half or twice as
+    // many workers 50 and 46, without this limit 98; 29 tokens, 5 of 122 of 156
+    // x 3958 (10 units): 148 us, 165 and 158, at 24 workers 194; one token, 2 of
+    // 8 of 256 x 16384: 29 us, as with 8 tokens' measure 31.
+    const float cost = DOWN && a.M < 8 ? static_cast<float>(a.M) * 0.125f : 1.0f;
+    const int64_t share = max(max(static_cast<int64_t>(kMoeMinShare), static_cast<int64_t>(sqrtf(cost * static_cast<float>(unit)))),
                               (total + L::kWorkers - 1) / L::kWorkers);
     const int worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
     const int64_t first = worker * share;

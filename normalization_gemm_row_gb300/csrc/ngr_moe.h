@@ -35,10 +35,6 @@ inline int moe_groups(int64_t M, int64_t E, int64_t top_k)
     return M <= kMoeGroup ? 1 : M > 2 * kMoeGroup && M * top_k > 6 * E ? 4 : 2;
 }
 constexpr int kMoeMaxEntries = kMoeMaxExperts + kMoeMaxTokens * kMoeMaxTopK / (2 * kMoeGroup);
-// Runs that share a unit at most: the last to finish adds their parts, at
-// about 0.2 us each.  19 tokens, 4 of 8 experts of 192 x 4544 (12 units of
-// down): 44 us with 24, 52 with 12, 45 with 48, 98 without a limit.
-constexpr int kMoeMaxSharers = 24;
 
 struct MoeArgs {
     const void *x, *gamma, *beta;     // [M, K], [K]

@@ -139,3 +139,10 @@ def test_shapes_and_repeats():
     assert torch.equal(y, again)
     none = ngr.fused_moe_swiglu(x[:0], d2["Wr"], d2["Wg"], d2["Wu"], d2["Wd"], 2, norm=2, gamma=d2["gamma"])
     assert none.shape == (0, 3, 128)
+
+
+@pytest.mark.parametrize("M,E,top_k", [(1, 3, 1), (2, 16, 4), (8, 16, 4), (29, 20, 5), (32, 24, 6)])
+@pytest.mark.parametrize("F", [6000, 6001])
+def test_rows_that_many_workers_share(M, E, top_k, F):
+    """A few rows of down's result, each of them from thousands of steps."""
+    run(M, 40, F, E, top_k, BF16, seed=M + F)
