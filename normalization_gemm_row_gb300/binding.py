@@ -983,7 +983,8 @@ def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     (out, lse), lse float32 [B, H] the log of the sum of the exponentials of
     the scores.  scale is 1 / sqrt(D) by default.  The caches and the table
     as in ``fused_rope_append_kv``, at 16-byte steps; D a multiple of 8 up to
-    256; H a multiple of the caches' heads.  ``out`` may be q itself.
+    256; H a multiple of the caches' heads, at most 9728 times as many.
+    ``out`` may be q itself.
 
     A length of 0 gives 0 and -inf; a row with a negative length is left as it
     was (in ``out`` and ``lse`` when given).  A length beyond the table, or a

@@ -13,20 +13,23 @@
 // unused.)  The warps have nothing to wait for but their own copies: no
 // barrier.
 //
-// All items' tiles of 16 tokens (an item: a sequence and key head, and a block
-// of 16 query heads where there are more) stand in one row, with a place more
-// before each item for what its beginning costs, and the row is cut into equal
-// runs, one a warp ("worker").  A batch of any lengths is balanced so, and
-// nothing but the device has to know the lengths.  An item that lies in
-// one run is finished there; the others' parts (FP32 sums, maximum, sum of
-// exponentials) are joined by a second kernel in the tokens' order, so a call
-// repeated gives the same bits.
+// The sequences' tiles of 16 tokens stand in one row, with a place more before
+// each sequence for what its beginning costs, and the row is cut into equal
+// runs.  A group of warps ("workers") takes a run, a warp for each key head
+// (and block of 16 query heads where there are more).  A batch of any lengths
+// is balanced so, and nothing but the device has to know the lengths; and what
+// is read at a time lies together: the heads of a token share lines of L2 (64
+// rows of 8000 tokens, 8 key heads of 80: 213 us; with the items' tiles in one
+// row, head after head, 329, as much as with 128 dimensions).  An item (a sequence and key head) that lies in one run is
+// finished there; the others' parts (FP32 sums, maximum, sum of exponentials)
+// are joined by a second kernel in the tokens' order, so a call repeated gives
+// the same bits.
 //
 // Few items of short contexts take a CTA each ("solo"): its warps share the
 // item's tiles and join their parts in shared memory, without a second launch.
 //
-// bf16, 64 query heads on 8 of 128: 64 rows of 2048 to 8192 tokens 213 us (6.3
-// TB/s), one of 131072 tokens 97 us (5.5 TB/s, of which 7 are the join), one
+// bf16, 64 query heads on 8 of 128: 64 rows of 2048 to 8192 tokens 212 us (6.3
+// TB/s), one of 131072 tokens 94 us (5.7 TB/s, of which 7 are the join), one
 // of 1000 tokens 12.5 us.
 #pragma once
 
@@ -78,12 +81,12 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, bool *bad)
     return s;
 }
 
-// Places of the row before each item's tiles: taking up an item (queries,
+// Places of the row before each sequence's tiles: taking up an item (queries,
 // output) costs about as much as a tile (37 rows of 12 heads, some of them
 // with a tile alone: the worker of those ended at 50 us, the others at 35).
 constexpr int kItemPlaces = 1;
 
-// A tile of the row.
+// A tile of the row, for one of the items.
 struct Place {
     int b, item, tile;     // sequence, item among the sequence's, tile of the item
     Span s;
@@ -93,10 +96,7 @@ __device__ __forceinline__ int advance(const AttendArgs &a, Place &p, bool *bad)
 {
     if (++p.tile < p.s.tiles) return 1;
     p.tile = 0;
-    if (++p.item == a.G * a.blocks) {
-        p.item = 0;
-        if (++p.b < a.B) p.s = span_of(a, p.b, bad);
-    }
+    if (++p.b < a.B) p.s = span_of(a, p.b, bad);
     return 1 + kItemPlaces;
 }
 
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
     bool bad = false;
     Place c;
     long long share = 1, place = 0, end = 0;      // the worker's run: from tile c's place up to `end`
-    int worker = warp;
+    int worker = warp, group = 0;
     if constexpr (SOLO) {
         if (static_cast<int>(blockIdx.x) == a.B * items) {      // a block that only looks for bad pages
             check_pages(a);
@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         long long mine = 0;
         for (int i = 0; i < each; ++i) {
             const int b = static_cast<int>(threadIdx.x) * each + i;
-            if (b < a.B) mine += static_cast<long long>(span_of(a, b, &bad).tiles + kItemPlaces) * items;
+            if (b < a.B) mine += span_of(a, b, &bad).tiles + kItemPlaces;
         }
         long long incl = mine;
 #pragma unroll
@@ -307,12 +307,18 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         __syncthreads();
         bad = false;      // (counted by whoever works on the sequence)
         const long long total = before[kThreads];
-        share = (total + a.workers - 1) / a.workers;
+        share = (total + a.groups - 1) / a.groups;
         if (share < a.min_share) share = a.min_share;
-        // Neighbouring runs on different SMs: a few runs have an SM each.
-        worker = warp * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x);
-        place = worker * share;
-        end = min(place + share, total);
+        // Few workers spread over the SMs, a group's by fours (64 rows of 2048
+        // to 8192 tokens 212.5 us, each on an SM of its own 217, eights 217).
+        constexpr int kTogether = 4;
+        worker = ((warp / kTogether) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * kTogether + warp % kTogether;
+        c.item = worker % items;
+        group = worker / items;
+        if (group < a.groups) {
+            place = group * share;
+            end = min(place + share, total);
+        }
         if (place < end) {
             int lo = 0, hi = kThreads;       // before[lo] <= place < before[hi]
             while (hi - lo > 1) {
@@ -323,14 +329,13 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             long long at = before[lo];
             int b = lo * each;
             Span s = span_of(a, b, &bad);
-            while (at + static_cast<long long>(s.tiles + kItemPlaces) * items <= place) {
-                at += static_cast<long long>(s.tiles + kItemPlaces) * items;
+            while (at + s.tiles + kItemPlaces <= place) {
+                at += s.tiles + kItemPlaces;
                 s = span_of(a, ++b, &bad);
             }
             c.b = b;
             c.s = s;
-            c.item = static_cast<int>((place - at) / (s.tiles + kItemPlaces));
-            at += static_cast<long long>(c.item) * (s.tiles + kItemPlaces) + kItemPlaces;      // of the item's first tile
+            at += kItemPlaces;      // of the first tile
             c.tile = static_cast<int>(max(0LL, place - at));
             place = at + c.tile;
         }
@@ -577,7 +582,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                     if (a.slot_by_item && lane == 0)
                         a.jobs[static_cast<int64_t>(c.b) * items + c.item] = AttendJob{-1, -1, 0, 0};
                 } else {
-                    const int64_t part = (static_cast<int64_t>(worker) * 2 + (whole ? 1 : 0)) * a.part_rows;
+                    const int64_t part = ((static_cast<int64_t>(c.item) * a.groups + group) * 2 + (whole ? 1 : 0)) * a.part_rows;
                     if (SOLO) {      // (the ring is empty: its copies are done)
                         cp_async_wait<0>();
                         __syncwarp();
@@ -600,7 +605,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                         }
                     if (whole) {      // the others' parts follow
                         const long long last = place + (c.s.tiles - 1 - c.tile);
-                        job = AttendJob{worker, static_cast<int>(last / share), c.b, c.item};
+                        job = AttendJob{group, static_cast<int>(last / share), c.b, c.item};
                         if (a.slot_by_item && lane == 0) a.jobs[static_cast<int64_t>(c.b) * items + c.item] = job;
                     }
                 }
@@ -652,7 +657,7 @@ __device__ __forceinline__ void add_scaled(float4 (&to)[N], const float4 (&v)[N]
 template <bool BF16, int DP, int HELD>
 __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __grid_constant__ AttendArgs a)
 {
-    extern __shared__ float weight[];     // [workers][weight, weight x sum]
+    extern __shared__ float weight[];     // [groups][weight, weight x sum]
     __shared__ __align__(16) float sums[kJoinWarps][DP];
     __shared__ float red[kJoinWarps];
     constexpr int kEach = (DP / 4 + 31) / 32;      // 16-byte pieces of a part's row that a lane has
@@ -663,14 +668,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const __gr
         int bad = 0;
         for (int w = threadIdx.x; w < a.workers; w += 32 * kJoinWarps) bad |= a.flags[w];
         const int any = __syncthreads_or(bad);
-        if (threadIdx.x == 0) *a.err = any ? kDevErrPage : 0;
+        if (threadIdx.x == 0 && (any || !a.err_keep)) *a.err = any ? kDevErrPage : 0;
     }
     const AttendJob job = a.jobs[blockIdx.x];
     if (job.first < 0) return;
     const int kv_head = job.item / a.blocks, block = job.item - kv_head * a.blocks;
     const int rows = min(kAttendRows, a.group - block * kAttendRows), parts = job.last - job.first + 1;
     const int64_t head0 = static_cast<int64_t>(job.row) * a.H + kv_head * a.group + block * kAttendRows;
-    auto part = [&](int i, int row) { return (static_cast<int64_t>(job.first + i) * 2 + (i == 0 ? 1 : 0)) * a.part_rows + row; };
+    auto part = [&](int i, int row) {
+        return ((static_cast<int64_t>(job.item) * a.groups + job.first + i) * 2 + (i == 0 ? 1 : 0)) * a.part_rows + row;
+    };
     auto load = [&](float4 (&v)[kEach], int i, int row) {
 #pragma unroll
         for (int e = 0; e < kEach; ++e)
@@ -775,7 +782,7 @@ cudaError_t join(const AttendArgs &a, cudaStream_t stream)
     cfg.gridDim = dim3(static_cast<unsigned>(a.slots),
                        static_cast<unsigned>(apart < 1 ? 1 : apart < a.part_rows ? apart : a.part_rows));
     cfg.blockDim = dim3(32 * kJoinWarps);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.workers) * 2 * sizeof(float);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.groups) * 2 * sizeof(float);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -94,7 +94,8 @@ constexpr int64_t kSoloTiles = 6, kSoloItems = 6;
 
 struct AttendPlan {
     bool solo;
-    int64_t workers, slots, part_rows, blocks, items;
+    int64_t at_once;      // key heads of a launch
+    int64_t workers, groups, slots, part_rows, blocks, items;
     size_t flags, jobs, ml, o, total;
 };
 
@@ -108,7 +109,9 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
     const int dim = attend_dim(D), warps = attend_warps(dim, attend_heads(group));
     const int64_t longest = window > 0 ? std::min(window, capacity) : capacity;
     p.blocks = (group + kAttendRows - 1) / kAttendRows;
-    p.items = B * G * p.blocks;
+    // (so many heads that not each can have a worker take several launches)
+    p.at_once = std::min(G, std::max<int64_t>(1, kAttendSms * warps / p.blocks));
+    p.items = B * p.at_once * p.blocks;
     p.part_rows = std::min<int64_t>(group, kAttendRows);
     const int64_t tiles = (longest + kAttendTile - 1) / kAttendTile;
     p.total = 256;
@@ -123,6 +126,7 @@ AttendPlan attend_plan(int64_t B, int64_t H, int64_t G, int64_t D, int64_t capac
                              ? kAttendSms
                              : std::max<int64_t>(1, (p.items * (tiles + 1) + kMinShare - 1) / kMinShare);
     p.workers = ctas * warps;
+    p.groups = p.workers / (p.at_once * p.blocks);
     p.slots = std::min(p.items, p.workers);
     size_t off = 256;
     auto take = [&](size_t bytes) {
@@ -150,6 +154,7 @@ int attend_sizes(int64_t B, int64_t H, int64_t G, int64_t D)
     const int rc = heads(H, G, D, true);
     if (rc != NGR_OK) return rc;
     if (D % 8 != 0 || B < 0 || B > kMax31 || (B > 0 && H > kMax31 / B)) return NGR_ERR_SHAPE;
+    if (H / G > kAttendMaxGroup) return NGR_ERR_SHAPE;
     return NGR_OK;
 }
 
@@ -317,15 +322,13 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     a.window = static_cast<int>(std::min(window, kMax31));
     a.B = static_cast<int>(B);
     a.H = static_cast<int>(H);
-    a.G = static_cast<int>(G);
     a.D = static_cast<int>(D);
     a.group = static_cast<int>(H / G);
     a.blocks = static_cast<int>(p.blocks);
     a.workers = static_cast<int>(p.workers);
+    a.groups = static_cast<int>(p.groups);
     a.min_share = static_cast<int>(kMinShare);
     a.part_rows = static_cast<int>(p.part_rows);
-    a.slots = static_cast<int>(p.slots);
-    a.slot_by_item = p.items <= p.workers;
     a.flags = reinterpret_cast<int *>(ws + p.flags);
     a.jobs = reinterpret_cast<AttendJob *>(ws + p.jobs);
     a.part_ml = reinterpret_cast<float2 *>(ws + p.ml);
@@ -333,18 +336,29 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     a.err = reinterpret_cast<int *>(ws);
     if (trace_mode())
         std::fprintf(stderr, "ngr: paged attention B=%d H=%d G=%d D=%d page=%d window=%d dim=%d %s=%d jobs=%d\n", a.B, a.H,
-                     a.G, a.D, a.kv.page_size, a.window, attend_dim(D), p.solo ? "items" : "workers",
-                     p.solo ? static_cast<int>(p.items) : a.workers, a.slots);
+                     static_cast<int>(G), a.D, a.kv.page_size, a.window, attend_dim(D), p.solo ? "items" : "workers",
+                     p.solo ? static_cast<int>(p.items) : a.workers, static_cast<int>(p.slots));
     const bool bf16 = dtype == NGR_BF16;
     call_begin();
-    kernel_begin(stream);
-    rc = p.solo ? (bf16 ? launch_attend_solo_bf16(a, stream) : launch_attend_solo_f16(a, stream))
-                : (bf16 ? launch_attend_bf16(a, stream) : launch_attend_f16(a, stream));
-    kernel_end(stream);
-    if (rc == NGR_OK && !p.solo) {
+    for (int64_t g = 0; g < G && rc == NGR_OK; g += p.at_once) {
+        a.G = static_cast<int>(std::min(p.at_once, G - g));
+        a.q = static_cast<const uint16_t *>(q) + g * a.group * q_head_stride;
+        a.kv.k = static_cast<uint16_t *>(const_cast<void *>(cache->k)) + g * a.kv.k_head;
+        a.kv.v = static_cast<uint16_t *>(const_cast<void *>(cache->v)) + g * a.kv.v_head;
+        a.out = static_cast<uint16_t *>(out) + g * a.group * D;
+        a.lse = lse ? lse + g * a.group : nullptr;
+        a.slots = static_cast<int>(std::min(B * a.G * p.blocks, p.workers));
+        a.slot_by_item = B * a.G * p.blocks <= p.workers;
+        a.err_keep = g > 0;
         kernel_begin(stream);
-        rc = bf16 ? launch_attend_join_bf16(a, stream) : launch_attend_join_f16(a, stream);
+        rc = p.solo ? (bf16 ? launch_attend_solo_bf16(a, stream) : launch_attend_solo_f16(a, stream))
+                    : (bf16 ? launch_attend_bf16(a, stream) : launch_attend_f16(a, stream));
         kernel_end(stream);
+        if (rc == NGR_OK && !p.solo) {
+            kernel_begin(stream);
+            rc = bf16 ? launch_attend_join_bf16(a, stream) : launch_attend_join_f16(a, stream);
+            kernel_end(stream);
+        }
     }
     return call_end(rc, workspace, stream);
 }

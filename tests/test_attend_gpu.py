@@ -265,3 +265,15 @@ def test_output_in_the_queries_place():
         used = d["lengths"] >= 0
         assert out is q and torch.equal(q.cpu()[used], want.cpu()[used]) and torch.equal(lse.cpu()[used], want_lse.cpu()[used])
         assert torch.equal(q.cpu()[~used], d["q"][~used])
+
+
+@pytest.mark.parametrize("G,group,D", [(700, 9, 136), (1300, 1, 192), (608, 9, 256), (2500, 1, 16)])
+def test_more_heads_than_the_device_has_warps(G, group, D):
+    d = data([70, 3, 0], G * group, G, D, 16, F16, seed=G, dirty=False)
+    check(d)
+    d["table"][1, 0] = d["k"].shape[0]
+    n = ngr.binding.ngr_paged_attention_workspace_bytes(3, G * group, G, D, d["table"].shape[1] * 16, 0)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    call(d, workspace=ws)
+    with pytest.raises(ngr.NgrError):
+        ngr.check_workspace(ws)

@@ -180,3 +180,10 @@ def test_a_workspace_is_enough_for_smaller_batches_and_tables(H, G, D, capacity)
 def test_experts_workspace_is_enough_for_fewer_tokens(K, F, E, top_k):
     sizes = [B.ngr_moe_swiglu_workspace_bytes(m, K, F, E, top_k) for m in range(1, 33)]
     assert sizes == sorted(sizes)
+
+
+@host_only
+def test_query_heads_of_a_key_head():
+    wide = cache(k_token_stride=64, k_head_stride=64, v_token_stride=64, v_head_stride=64)
+    assert attend(wide, H=9729, G=1, q_row=9729 * 64) == SHAPE
+    assert passes(attend(wide, H=9728, G=1, q_row=9728 * 64))
