@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
         share = (total + a.groups - 1) / a.groups;
         if (share < a.min_share) share = a.min_share;
         // Few workers spread over the SMs, a group's by fours (64 rows of 2048
-        // to 8192 tokens 212.5 us, each on an SM of its own 217, eights 217).
+        // to 8192 tokens 212.5 us, each on an SM of its own 217; eights as fours).
         constexpr int kTogether = 4;
         worker = ((warp / kTogether) * static_cast<int>(gridDim.x) + static_cast<int>(blockIdx.x)) * kTogether + warp % kTogether;
         c.item = worker % items;
