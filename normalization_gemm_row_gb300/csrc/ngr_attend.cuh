@@ -47,6 +47,14 @@ namespace ngr {
 namespace {
 
 constexpr float kLn2 = 0.6931471805599453f;
+// What the softmax weights are multiplied by for their product with v, and the
+// sums divided by in the end.  A weight is at most 1, of the run's largest: in
+// fp16 those below 2^-14 would be subnormal and those below 2^-25 gone, while
+// the sum of the exponentials counts them (27000 tokens at e^-17.3 of one of
+// weight 1: 1.6e-3 in their place of 8.3e-4).  Times 2^15 all are normal from
+// 2^-29 on.
+template <bool BF16>
+constexpr float kWeightScale = BF16 ? 1.0f : 32768.0f;
 
 // A warp's ring: stages of 16 tokens' keys or values in turn, 192 KB over the
 // CTA's warps.
@@ -525,6 +533,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                     const float off = top[n][e & 1] == -INFINITY ? 0.0f : top[n][e & 1];
                     z[n][e] = exp2_fast(z[n][e] - off);
                     sum[n][e & 1] += z[n][e];
+                    z[n][e] *= kWeightScale<BF16>;
                 }
                 p[n][0] = transpose8(pack16<BF16>(z[n][0], z[n][1]));
                 p[n][1] = transpose8(pack16<BF16>(z[n][2], z[n][3]));
@@ -558,6 +567,14 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int x = 4; x < 32; x <<= 1) sum[n][h] += __shfl_xor_sync(0xffffffffu, sum[n][h], x);
+                if (!BF16) {
+#pragma unroll
+                    for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[k][n][e] *= 1.0f / kWeightScale<BF16>;
+                }
                 if (!SOLO && ends && whole) {
                     if (c.s.used) {
 #pragma unroll
