@@ -402,9 +402,10 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
  * as that, a page that is not there as if its tokens were not, and either is
  * reported by the workspace's error word as NGR_ERR_ARG.  What the cache holds
  * beside the sequences' tokens is not looked at (it may be NaN).  Scores,
- * softmax and sums are FP32, the softmax weights are rounded to `dtype` for
- * their product with v; the order of every sum follows from the lengths alone
- * (the same call gives the same bits).  H / G is at most 9728.  D is a multiple of 8 up to 256, every
+ * softmax and sums are FP32, the softmax weights go into their product with v
+ * in two parts of `dtype` (the value rounded and what that left out); the order
+ * of every sum follows from the lengths alone (the same call gives the same
+ * bits).  H / G is at most 9728.  D is a multiple of 8 up to 256, every
  * pointer but lengths, lse and the table 16-byte aligned and every stride a
  * multiple of 8 elements; k and v each reach over 64 GiB at most
  * (NGR_ERR_SHAPE).  Workspace (256-byte aligned):

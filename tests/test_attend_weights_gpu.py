@@ -50,3 +50,13 @@ SHAPES = [(1000, 3, 2), (3000, 40, 3000), (27000, 5, 1)]
 def test_many_small_weights_in_fp16(n, at, rows, score, D):
     """Weights down to e^-20 of the largest keep their share: each is off by at most half a step of fp16, relative."""
     one_and_many(n, at, D, score, F16, rows, R.U[F16], f"{n} tokens")
+
+
+@pytest.mark.parametrize("n,at,rows", SHAPES)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 80, 256])
+def test_equal_weights_between_two_steps(n, at, rows, dtype, D):
+    """Weights of the other tokens that are all half a step above a power of two (a little less): two parts hold them,
+    each off by half a step of half a step; one part would take their sum half a step down."""
+    score = -math.log((1 + 0.98 * R.U[dtype]) / 32)
+    one_and_many(n, at, D, score, dtype, rows, R.U[dtype] ** 2, f"{n} tokens")
