@@ -436,9 +436,9 @@ size_t ngr_paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t G,
  * experts (int32 [M, top_k], largest first) and weights (FP32 [M, top_k]) when
  * they are not NULL.  The router works in FP32 throughout; the experts'
  * products take a, and p times the gated product, in two parts of `dtype` (the
- * value rounded and what that left out; within `dtype`'s range), and
- * accumulate in FP32; y is rounded once.  Only chosen experts' weights are
- * read.  A token whose router's logits hold a NaN has y = NaN.
+ * value rounded and what that left out; in fp16 up to 2^24 in size and to 2^-28
+ * near 0), and accumulate in FP32; y is rounded once.  Only chosen experts'
+ * weights are read.  A token whose router's logits hold a NaN has y = NaN.
  * Any K and F up to NGR_MOE_MAX_WIDTH, any 2-byte alignment (16-byte aligned
  * weights with K, F multiples of 8 take 16-byte loads).  y may be x's memory.
  * Sums have a fixed order.  Workspace (256-byte aligned):

@@ -76,14 +76,33 @@ __device__ __forceinline__ void unpack8(const uint4 &d, float (&v)[8])
     }
 }
 
-// Two values as their rounded parts and what the rounding left out.
+// Two values as their rounded parts and what the rounding left out.  fp16's
+// narrow range is moved for it: the value is taken times 2^-8, so that up to
+// 2^24 fits, and the second part times 2^11 more, as it is that much smaller.
+// Both together are off by at most 2^-22 of the value, or 2^-28.  (Without the
+// scales what passed 65504 was infinite, and a value below 2^-14 had no second
+// part: it was up to 2^-25 off.)
+template <bool BF16>
+constexpr float kValueScale = BF16 ? 1.0f : 1.0f / 256.0f;
+template <bool BF16>
+constexpr float kLowScale = BF16 ? 1.0f : 2048.0f;
 template <bool BF16>
 __device__ __forceinline__ uint2 two_parts(float x, float y)
 {
+    x *= kValueScale<BF16>;
+    y *= kValueScale<BF16>;
     const uint32_t hi = pack16<BF16>(x, y);
     const float2 h = unpack16<BF16>(hi);
     // (an infinity has no second part)
-    return make_uint2(hi, pack16<BF16>(fabsf(h.x) < INFINITY ? x - h.x : 0.0f, fabsf(h.y) < INFINITY ? y - h.y : 0.0f));
+    return make_uint2(hi, pack16<BF16>(fabsf(h.x) < INFINITY ? (x - h.x) * kLowScale<BF16> : 0.0f,
+                                       fabsf(h.y) < INFINITY ? (y - h.y) * kLowScale<BF16> : 0.0f));
+}
+// A sum of products with values in two parts, from those with each of them.
+template <bool BF16>
+__device__ __forceinline__ float both_parts(float hi, float lo)
+{
+    if (BF16) return hi + lo;
+    return fmaf(lo, 1.0f / kLowScale<BF16>, hi) * (1.0f / kValueScale<BF16>);
 }
 
 // ---------------------------------------------------------------- router
@@ -848,7 +867,7 @@ __global__ void __launch_bounds__(32 * moe_warps(DOWN, NT), 2) moe_kernel(const 
             float2 v[NT];      // gate and up of row g for token t of each group
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
-                v[j] = make_float2(acc[j][0] + acc[j][1], acc[j][2] + acc[j][3]);
+                v[j] = make_float2(both_parts<BF16>(acc[j][0], acc[j][1]), both_parts<BF16>(acc[j][2], acc[j][3]));
 #pragma unroll
                 for (int r = 0; r < 4; ++r) acc[j][r] = 0.0f;
             }
@@ -898,8 +917,8 @@ __global__ void __launch_bounds__(32 * moe_warps(DOWN, NT), 2) moe_kernel(const 
                 const int r = j * kMoeGroup + t;
                 if (r < s.tokens) {
                     float *to = sums + c.token[s.base + r] * 17;
-                    to[g] += acc[j][0] + acc[j][1];
-                    to[g + 8] += acc[j][2] + acc[j][3];
+                    to[g] += both_parts<BF16>(acc[j][0], acc[j][1]);
+                    to[g + 8] += both_parts<BF16>(acc[j][2], acc[j][3]);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) acc[j][q] = 0.0f;
