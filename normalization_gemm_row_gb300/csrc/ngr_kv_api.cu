@@ -4,6 +4,7 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <numeric>
 
 #include "ngr.h"
 #include "ngr_entry.h"
@@ -81,6 +82,41 @@ int granule(std::initializer_list<const void *> bases, std::initializer_list<int
     for (const void *p : bases) bits |= static_cast<int64_t>(reinterpret_cast<uintptr_t>(p) >> 1);
     for (int64_t s : steps) bits |= s;
     return static_cast<int>(bits & -bits);
+}
+
+// What a tensor occupies: pieces of `bytes`, `count` of them at steps of
+// `step` in each dimension (bytes, not negative).
+struct Places {
+    uintptr_t at;
+    int64_t bytes;
+    int64_t count[2], step[2];
+
+    Places(const void *p, int64_t piece, int64_t n0, int64_t s0, int64_t n1 = 1, int64_t s1 = 0)
+        : at(reinterpret_cast<uintptr_t>(p)), bytes(piece), count{n0, n1}, step{s0, s1}
+    {
+        // pieces that follow one another are one
+        for (int i = 0; i < 2; ++i)
+            for (int d = 0; d < 2; ++d)
+                if (count[d] > 1 && (step[d] == bytes || step[d] == 0)) {
+                    if (step[d]) bytes *= count[d];
+                    count[d] = 1;
+                }
+        for (int d = 0; d < 2; ++d)
+            if (count[d] == 1) step[d] = 0;
+    }
+    uintptr_t end() const { return at + bytes + (count[0] - 1) * step[0] + (count[1] - 1) * step[1]; }
+};
+// Whether two tensors share no byte: one lies behind the other, or all steps
+// are multiples of some distance within which the pieces lie apart (parts of
+// one array's rows, say).
+bool apart(const Places &a, const Places &b)
+{
+    if (a.end() <= b.at || b.end() <= a.at) return true;
+    int64_t period = 0;
+    for (int64_t s : {a.step[0], a.step[1], b.step[0], b.step[1]}) period = std::gcd(period, s);
+    if (period == 0) return false;
+    const int64_t p = period, off = static_cast<int64_t>((b.at % p + p - a.at % p) % p);
+    return off >= a.bytes && off + b.bytes <= p;
 }
 
 // Contexts whose items take a CTA each: tiles of each of its warps at most, 6
@@ -295,6 +331,12 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
         granule({q, a.kv.k, a.kv.v}, {q_row_stride, q_head_stride, a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv.v_page,
                                       a.kv.v_token, a.kv.v_head}) != 8)
         return NGR_ERR_ALIGN;
+    // Each query is read by its own item's warps, which then write its place
+    // in out: in q's memory only where both lie alike.
+    const Places q_at(q, D * 2, H, q_head_stride * 2, B, q_row_stride * 2), out_at(out, B * H * D * 2, 1, 0);
+    const bool in_place = q == out && (H == 1 || q_head_stride == D) && (B == 1 || q_row_stride == H * D);
+    if (!in_place && !apart(q_at, out_at)) return NGR_ERR_ARG;
+    if (lse && (!apart(q_at, Places(lse, B * H * 4, 1, 0)) || !apart(out_at, Places(lse, B * H * 4, 1, 0)))) return NGR_ERR_ARG;
     if (!within_32(a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv, G) ||
         !within_32(a.kv.v_page, a.kv.v_token, a.kv.v_head, a.kv, G))
         return NGR_ERR_SHAPE;
