@@ -362,7 +362,10 @@ typedef struct {
  *   q_out[t] = rotated q[t];  the cache's slot of (row, positions[t]) takes
  *   the rotated k[t] and v[t] as it is.
  * q, q_out are [T, H, D], k, v [T, G, D] by their token and head strides in
- * elements (parts of one QKV row, say); q_out may be q itself with q's strides.
+ * elements (parts of one QKV row, say); q_out may be q itself with q's strides,
+ * or lies apart from q, k and v.  NGR_ERR_ARG if it does not, or if elements of
+ * q_out or of the caches share their places with one another (steps that lie
+ * within what smaller steps span; k and v of the cache over each other).
  * q may be NULL (H and q_out are not looked at).  rows[t] is the token's row
  * of the block table (NULL: row t).  A token with a negative position is left
  * out: nothing of it is written.  A token whose row, position or page is not

@@ -4,7 +4,9 @@
 #include <cmath>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <numeric>
+#include <utility>
 
 #include "ngr.h"
 #include "ngr_entry.h"
@@ -85,38 +87,59 @@ int granule(std::initializer_list<const void *> bases, std::initializer_list<int
 }
 
 // What a tensor occupies: pieces of `bytes`, `count` of them at steps of
-// `step` in each dimension (bytes, not negative).
+// `step` in each dimension (bytes, not negative), the smaller steps first.
 struct Places {
+    static constexpr int kDims = 3;
     uintptr_t at;
-    int64_t bytes;
-    int64_t count[2], step[2];
+    int64_t bytes, count[kDims], step[kDims];
+    int dims = 0;
 
-    Places(const void *p, int64_t piece, int64_t n0, int64_t s0, int64_t n1 = 1, int64_t s1 = 0)
-        : at(reinterpret_cast<uintptr_t>(p)), bytes(piece), count{n0, n1}, step{s0, s1}
+    // dimensions as {entries, step in elements of `size` bytes}
+    Places(const void *p, int64_t piece, int64_t size, std::initializer_list<std::pair<int64_t, int64_t>> of)
+        : at(reinterpret_cast<uintptr_t>(p)), bytes(piece * size)
     {
-        // pieces that follow one another are one
-        for (int i = 0; i < 2; ++i)
-            for (int d = 0; d < 2; ++d)
-                if (count[d] > 1 && (step[d] == bytes || step[d] == 0)) {
-                    if (step[d]) bytes *= count[d];
-                    count[d] = 1;
-                }
-        for (int d = 0; d < 2; ++d)
-            if (count[d] == 1) step[d] = 0;
+        for (const auto &d : of) {
+            if (d.first <= 1 || d.second == 0) continue;
+            int i = dims++;
+            for (; i > 0 && step[i - 1] > d.second * size; --i) {
+                step[i] = step[i - 1];
+                count[i] = count[i - 1];
+            }
+            step[i] = d.second * size;
+            count[i] = d.first;
+        }
     }
-    uintptr_t end() const { return at + bytes + (count[0] - 1) * step[0] + (count[1] - 1) * step[1]; }
+    // from the first byte to behind the last, of the first n dimensions
+    int64_t extent(int n) const
+    {
+        int64_t e = bytes;
+        for (int i = 0; i < n; ++i) e += (count[i] - 1) * step[i];
+        return e;
+    }
+    // Every piece lies behind those of smaller steps: none shares a byte with another.
+    bool nested() const
+    {
+        for (int i = 0; i < dims; ++i)
+            if (step[i] < extent(i)) return false;
+        return true;
+    }
 };
-// Whether two tensors share no byte: one lies behind the other, or all steps
-// are multiples of some distance within which the pieces lie apart (parts of
-// one array's rows, say).
+// Whether two tensors share no byte: one lies behind the other, or what the
+// smaller steps span lies apart within a distance that all others are
+// multiples of (parts of one array's rows or pages, say).
 bool apart(const Places &a, const Places &b)
 {
-    if (a.end() <= b.at || b.end() <= a.at) return true;
-    int64_t period = 0;
-    for (int64_t s : {a.step[0], a.step[1], b.step[0], b.step[1]}) period = std::gcd(period, s);
-    if (period == 0) return false;
-    const int64_t p = period, off = static_cast<int64_t>((b.at % p + p - a.at % p) % p);
-    return off >= a.bytes && off + b.bytes <= p;
+    if (a.at + a.extent(a.dims) <= b.at || b.at + b.extent(b.dims) <= a.at) return true;
+    for (int i = a.dims; i >= 0; --i)
+        for (int j = b.dims; j >= 0; --j) {
+            int64_t period = 0;
+            for (int d = i; d < a.dims; ++d) period = std::gcd(period, a.step[d]);
+            for (int d = j; d < b.dims; ++d) period = std::gcd(period, b.step[d]);
+            if (period == 0) continue;
+            const int64_t off = static_cast<int64_t>((b.at % period + period - a.at % period) % period);
+            if (off >= a.extent(i) && off + b.extent(j) <= period) return true;
+        }
+    return false;
 }
 
 // Contexts whose items take a CTA each: tiles of each of its warps at most, 6
@@ -243,13 +266,23 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride, int64_t q_he
         return NGR_ERR_ARG;
     // what is written has a place of its own for every element
     const KvView &kv = a.kv;
-    if ((q && T > 1 && q_out_token_stride == 0) || (H > 1 && q_out_head_stride < D) ||
-        (G > 1 && (kv.k_head < D || kv.v_head < D)) || (kv.page_size > 1 && (kv.k_token < D || kv.v_token < D)) ||
-        (kv.pages > 1 && (kv.k_page < D || kv.v_page < D)))
+    const Places k_cache(kv.k, D, 2, {{G, kv.k_head}, {kv.page_size, kv.k_token}, {kv.pages, kv.k_page}}),
+        v_cache(kv.v, D, 2, {{G, kv.v_head}, {kv.page_size, kv.v_token}, {kv.pages, kv.v_page}});
+    if ((q && T > 1 && q_out_token_stride == 0) || (H > 1 && q_out_head_stride == 0) || (G > 1 && (kv.k_head == 0 || kv.v_head == 0)) ||
+        (kv.page_size > 1 && (kv.k_token == 0 || kv.v_token == 0)) || (kv.pages > 1 && (kv.k_page == 0 || kv.v_page == 0)))
         return NGR_ERR_ARG;
-    // q_out in q's memory: the same elements in the same places
-    if (q && q == q_out && (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride))
-        return NGR_ERR_ARG;
+    if (!k_cache.nested() || !v_cache.nested() || !apart(k_cache, v_cache)) return NGR_ERR_ARG;
+    if (q) {
+        const Places out(q_out, D, 2, {{H, q_out_head_stride}, {T, q_out_token_stride}});
+        if (!out.nested()) return NGR_ERR_ARG;
+        if (q == q_out) {      // the same elements in the same places
+            if (q_token_stride != q_out_token_stride || q_head_stride != q_out_head_stride) return NGR_ERR_ARG;
+        } else if (!apart(out, Places(q, D, 2, {{H, q_head_stride}, {T, q_token_stride}})) ||
+                   !apart(out, Places(k, D, 2, {{G, k_head_stride}, {T, k_token_stride}})) ||
+                   !apart(out, Places(v, D, 2, {{G, v_head_stride}, {T, v_token_stride}}))) {
+            return NGR_ERR_ARG;
+        }
+    }
     int vec = granule({q, k, v, q_out, a.kv.k, a.kv.v},
                       {D, q_token_stride, q_head_stride, k_token_stride, k_head_stride, v_token_stride, v_head_stride,
                        q_out_token_stride, q_out_head_stride, a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv.v_page,
@@ -333,10 +366,10 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
         return NGR_ERR_ALIGN;
     // Each query is read by its own item's warps, which then write its place
     // in out: in q's memory only where both lie alike.
-    const Places q_at(q, D * 2, H, q_head_stride * 2, B, q_row_stride * 2), out_at(out, B * H * D * 2, 1, 0);
+    const Places q_at(q, D, 2, {{H, q_head_stride}, {B, q_row_stride}}), out_at(out, B * H * D, 2, {}), lse_at(lse, B * H, 4, {});
     const bool in_place = q == out && (H == 1 || q_head_stride == D) && (B == 1 || q_row_stride == H * D);
     if (!in_place && !apart(q_at, out_at)) return NGR_ERR_ARG;
-    if (lse && (!apart(q_at, Places(lse, B * H * 4, 1, 0)) || !apart(out_at, Places(lse, B * H * 4, 1, 0)))) return NGR_ERR_ARG;
+    if (lse && (!apart(q_at, lse_at) || !apart(out_at, lse_at))) return NGR_ERR_ARG;
     if (!within_32(a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv, G) ||
         !within_32(a.kv.v_page, a.kv.v_token, a.kv.v_head, a.kv, G))
         return NGR_ERR_SHAPE;

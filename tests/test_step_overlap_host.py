@@ -39,3 +39,48 @@ def test_attention_refuses_outputs_over_queries(kw):
     dict(q_row=640, out=A + 3 * 640 * 2 + ROW)])
 def test_attention_takes_outputs_apart_from_queries(kw):
     assert passes(attend(**kw))
+
+
+# The cache of test_step_host: 10 pages of 16 tokens of 2 heads of 64; a page is 2048 elements.
+@pytest.mark.parametrize("kw", [
+    dict(k_page_stride=1024), dict(v_page_stride=2047 - 63), dict(v_page_stride=64), dict(k_token_stride=64), dict(v_token_stride=96),
+    dict(k_page_stride=128, k_token_stride=128 * 9),                    # pages inside tokens, of too few
+    dict(v=A), dict(v=A + 128), dict(v=A + 10 * 2048 * 2 - 16), dict(v=A - 64),
+    dict(k_page_stride=4096, v_page_stride=4096, v=A + 2048),           # v's pages half over k's
+    dict(k_head_stride=128, v_head_stride=128, k_token_stride=256, v_token_stride=256, k_page_stride=4096, v_page_stride=4096, v=A + 256)])
+def test_append_refuses_caches_with_shared_places(kw):
+    assert append(cache(**kw)) == ARG
+
+
+@host_only
+@pytest.mark.parametrize("kw", [
+    dict(v=A + 10 * 2048 * 2), dict(k_page_stride=2048 + 8),
+    dict(k_page_stride=4096, v_page_stride=4096, v=A + 2048 * 2),       # [pages, 2, tokens, heads, dim]
+    dict(k_token_stride=256, v_token_stride=256, k_page_stride=4096, v_page_stride=4096, v=A + 256),     # [pages, tokens, 2, ...]
+    dict(k_head_stride=128, v_head_stride=128, k_token_stride=256, v_token_stride=256, k_page_stride=4096, v_page_stride=4096, v=A + 128),
+    dict(k_head_stride=1024, k_token_stride=64, k_page_stride=4096, v_page_stride=4096, v=A + 2048 * 2),  # k by heads, v by tokens
+    dict(k_token_stride=144, k_head_stride=72, k_page_stride=4352, v_page_stride=4352, v=A + 2304 * 2),   # k padded, in one page
+    dict(k_page_stride=128, k_token_stride=128 * 10),                   # pages inside tokens
+    dict(pages=1, k_page_stride=1), dict(page_size=1, k_token_stride=1, v_token_stride=0)])
+def test_append_takes_caches_whose_places_are_apart(kw):
+    assert passes(append(cache(**kw)))
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out_token=511), dict(q_out_token=64), dict(q_out_token=1), dict(q_out_head=96, q_out_token=512), dict(q_out_head=200, q_out_token=64),
+    dict(q=OTHER + 2), dict(q=OTHER - 4 * ROW + 2), dict(q=OTHER + 16, q_token=512), dict(k=OTHER), dict(v=OTHER + 4 * ROW - 2),
+    dict(q=OTHER - HEAD, q_token=640, q_out_token=640)])
+def test_append_refuses_rotated_queries_over_inputs_or_themselves(kw):
+    assert append(**kw) == ARG
+
+
+@host_only
+@pytest.mark.parametrize("kw", [
+    dict(q=OTHER), dict(q=OTHER + 4 * ROW), dict(k=OTHER - 4 * 2 * HEAD), dict(q_out_head=256, q_out_token=64),
+    dict(T=1, q_out_token=1), dict(T=1, H=1, q_out_head=1),
+    # parts of rows of 2048: q, then q_out, k and v behind them
+    dict(q=FAR, q_token=2048, q_out=FAR + ROW, q_out_token=2048, k=FAR + 2 * ROW, k_token=2048, v=FAR + 2 * ROW + 2 * HEAD, v_token=2048),
+    # heads of q and of q_out in turn
+    dict(q=FAR, q_head=128, q_token=1024, q_out=FAR + HEAD, q_out_head=128, q_out_token=1024)])
+def test_append_takes_rotated_queries_apart(kw):
+    assert passes(append(**kw))
