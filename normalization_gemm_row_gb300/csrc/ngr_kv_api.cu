@@ -68,13 +68,14 @@ int kv_view(const ngr_kv_cache *c, int64_t G, KvView *v)
     return NGR_OK;
 }
 
-// The last of a view's heads, in 16-byte units, is below 2^32 - 1 (strides
-// are multiples of 8 elements).
-bool within_32(int64_t page, int64_t token, int64_t head, const KvView &v, int64_t G)
+// All of a view's 16-byte units, counted from its start, have numbers of 32
+// bits, and its last head starts below the largest, which stands for none
+// (strides are multiples of 8 elements).
+bool within_32(int64_t page, int64_t token, int64_t head, const KvView &v, int64_t G, int64_t D)
 {
     const double last = static_cast<double>(page / 8) * (v.pages - 1) + static_cast<double>(token / 8) * (v.page_size - 1) +
                         static_cast<double>(head / 8) * static_cast<double>(G - 1);
-    return last < 4294967295.0;
+    return last < 4294967295.0 && last + static_cast<double>(D / 8) <= 4294967296.0;
 }
 
 // Elements that every address of these strides is a multiple of: 8, 4, 2 or 1.
@@ -370,8 +371,8 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     const bool in_place = q == out && (H == 1 || q_head_stride == D) && (B == 1 || q_row_stride == H * D);
     if (!in_place && !apart(q_at, out_at)) return NGR_ERR_ARG;
     if (lse && (!apart(q_at, lse_at) || !apart(out_at, lse_at))) return NGR_ERR_ARG;
-    if (!within_32(a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv, G) ||
-        !within_32(a.kv.v_page, a.kv.v_token, a.kv.v_head, a.kv, G))
+    if (!within_32(a.kv.k_page, a.kv.k_token, a.kv.k_head, a.kv, G, D) ||
+        !within_32(a.kv.v_page, a.kv.v_token, a.kv.v_head, a.kv, G, D))
         return NGR_ERR_SHAPE;
     a.k_page = static_cast<uint32_t>(a.kv.k_page / 8);
     a.k_token = static_cast<uint32_t>(a.kv.k_token / 8);
