@@ -550,25 +550,36 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             {
                 const int r = lane & 7, tokens = (lane >> 4) << 3, half = (lane >> 3) & 1;
                 const uint32_t row = base + stage * R::kStage + (tokens + r) * (DP * 2);
-                // Two dimension blocks at once, so that no product waits for
-                // the one before it on the same sums: the weights' second part
-                // takes 64 rows of 2048 to 8192 tokens from 210.5 to 211.3 us
-                // (one block at once 215.5), 16 rows of 8000, 16 heads to a
-                // key head of 256, from 133 to 141.
-                constexpr int kAtOnce = 2;
+                // A tile's sums are a chain of their own, for the sake of long
+                // ones (mma_16816_from_zero).  Four dimension blocks at once,
+                // so that few products wait for one before them: 64 rows of
+                // 2048 to 8192 tokens 213 us (with the weights in one part and
+                // one long chain 211), 16 rows of 8000, 16 heads to a key head
+                // of 192, 99 (two blocks at once 103, one 121), of 256 151 (one
+                // part, one chain 133).
+                constexpr int kAtOnce = 4;
 #pragma unroll
                 for (int k0 = 0; k0 < kSteps; k0 += kAtOnce) {
                     uint32_t w[kAtOnce][4];
 #pragma unroll
                     for (int k = 0; k < kAtOnce && k0 + k < kSteps; ++k)
                         ldmatrix4_t(w[k], row + (((2 * (k0 + k) + half) ^ turn<DP>(r)) << 4));
+                    float d[kAtOnce][NB][4];
 #pragma unroll
                     for (int part = 0; part < 2; ++part)
 #pragma unroll
                         for (int k = 0; k < kAtOnce && k0 + k < kSteps; ++k)
 #pragma unroll
-                            for (int n = 0; n < NB; ++n)
-                                mma_16816<BF16>(o[k0 + k][n], w[k][0], w[k][1], w[k][2], w[k][3], p[part][n][0], p[part][n][1]);
+                            for (int n = 0; n < NB; ++n) {
+                                if (part == 0) mma_16816_from_zero<BF16>(d[k][n], w[k][0], w[k][1], w[k][2], w[k][3], p[0][n][0], p[0][n][1]);
+                                else mma_16816<BF16>(d[k][n], w[k][0], w[k][1], w[k][2], w[k][3], p[1][n][0], p[1][n][1]);
+                            }
+#pragma unroll
+                    for (int k = 0; k < kAtOnce && k0 + k < kSteps; ++k)
+#pragma unroll
+                        for (int n = 0; n < NB; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) o[k0 + k][n][e] += d[k][n][e];
                 }
             }
             __syncwarp();

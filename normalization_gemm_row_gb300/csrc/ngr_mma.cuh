@@ -34,6 +34,29 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
             : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// d = a b.
+//
+// The instruction adds its 16 products and d as integers: each addend is cut
+// off at 2^-25 of the largest one's power of two, the sum at 2^-23 of its own.
+// Both cuts go toward zero, so a long chain of them on one sum drifts (a
+// warp's sums over 55000 tiles of 16 tokens: 1.6 % low).  Long sums are made of
+// short chains instead, which begin here and are added by rounding additions.
+template <bool BF16>
+__device__ __forceinline__ void mma_16816_from_zero(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                    uint32_t b0, uint32_t b1)
+{
+    if (BF16)
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+            : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+            : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // 2^x, off by a few steps of 2^-24 (the hardware's approximation; results
 // below 2^-126 are 0).
 __device__ __forceinline__ float exp2_fast(float x)
