@@ -84,8 +84,10 @@ __device__ __forceinline__ Span span_of(const AttendArgs &a, int b, bool *bad)
     }
     s.start = a.window > 0 && len > a.window ? len - a.window : 0;
     s.n = len > 0 ? len - s.start : 0;
-    // (a row without tokens is visited too: it has an output)
-    s.tiles = s.n > 0 ? (s.n + kAttendTile - 1) / kAttendTile : 1;
+    // (a row without tokens is visited too: it has an output; a row may have
+    // 2^31 - 1 tokens, so nothing is added to n: the last tile's last token is
+    // number 2^31 - 1)
+    s.tiles = s.n > 0 ? s.n / kAttendTile + (s.n % kAttendTile != 0) : 1;
     return s;
 }
 
