@@ -111,7 +111,8 @@ __device__ __forceinline__ int advance(const AttendArgs &a, Place &p, bool *bad)
 }
 
 // The entry of the table for a token of a tile, one in lane % 16, and its slot
-// in the page; kNone past the sequence's end.
+// in the page; kNone past the sequence's end, which no entry is (negative ones
+// are no pages, and -1 then).
 constexpr int kNone = -2147483647 - 1;
 __device__ __forceinline__ int page_entry(const AttendArgs &a, const Place &p, int lane, int *slot)
 {
@@ -120,7 +121,7 @@ __device__ __forceinline__ int page_entry(const AttendArgs &a, const Place &p, i
     const int token = p.s.start + j;
     const int page = a.kv.page_mul ? __umulhi(token, a.kv.page_mul) >> a.kv.page_sh : token;
     *slot = token - page * a.kv.page_size;
-    return a.kv.table[p.b * a.kv.table_stride + page];
+    return max(a.kv.table[p.b * a.kv.table_stride + page], -1);
 }
 
 // Piece c of row r of a stage lies at c ^ turn(r), so that eight rows' pieces
