@@ -479,8 +479,9 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                         const int r = kv_head * a.group + block * kAttendRows + lane;
                         if (lane < min(kAttendRows, a.group - block * kAttendRows))
 #pragma unroll
-                            for (int d = 0; d < DP * 2; d += 128)
-                                asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint8_t *>(a.q) + (f.b * a.q_row + r * a.q_head) * 2 + d));
+                            for (int d = 0; d < DP * 2; d += 128)      // (of the head alone: what follows the last may be nobody's)
+                                if (FULL || d < a.D * 2)
+                                    asm volatile("prefetch.global.L1 [%0];" ::"l"(static_cast<const uint8_t *>(a.q) + (f.b * a.q_row + r * a.q_head) * 2 + d));
                     }
                 }
             };
