@@ -371,7 +371,8 @@ typedef struct {
  * out: nothing of it is written.  A token whose row, position or page is not
  * there is left out too, and the workspace's error word reports NGR_ERR_ARG.
  * Two tokens of one call in one slot: one of them is kept, in each piece of
- * its row either.  Angles are reduced exactly (2^-64 of a turn a position),
+ * its row either.  Angles are reduced exactly (to 2^-62 of a turn a position, for
+ * any finite inv_freq; others give NaN),
  * the rotation is FP32 and rounded once.  inv_freq is FP32 [rot / 2],
  * positions and rows are int32 [T].  D up to 256; any alignment (16-byte
  * aligned heads, rows and pages take 16-byte accesses).  The workspace

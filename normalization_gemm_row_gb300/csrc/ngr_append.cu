@@ -21,26 +21,31 @@ namespace ngr {
 namespace {
 
 // f / (2 pi) modulo 1 as a 64-bit fraction: the 24-bit significand times the
-// first 128 bits of 1 / (2 pi), shifted by f's exponent.  A position times
-// this, modulo 2^64, is the angle in turns to 2^-64 of a turn per position:
-// the product position x f in FP32 would be 2^-7 off at position 2^17, and
-// FP64 has a sixty-fourth of FP32's rate here.  (0 from 2^88 on.)
+// first 192 bits of 1 / (2 pi), shifted by f's exponent, which is at most 104.
+// Off by less than 2^-62, for any finite f.  A position times this, modulo
+// 2^64, is the angle in turns: the product position x f in FP32 would be 2^-7
+// off at position 2^17, and FP64 has a sixty-fourth of FP32's rate here.
 __device__ __forceinline__ unsigned long long turn_fraction(float f)
 {
-    constexpr unsigned long long kHi = 0x28be60db9391054aull, kLo = 0x7f09d5f47d4d3770ull;
+    constexpr unsigned long long k2 = 0x28be60db9391054aull, k1 = 0x7f09d5f47d4d3770ull, k0 = 0x36d8a5664f10e410ull;
     const uint32_t bits = __float_as_uint(f);
     const int e = static_cast<int>((bits >> 23) & 255u);
     const unsigned long long m = (bits & 0x7FFFFFu) | (e ? 0x800000u : 0u);
-    const int r = 64 - ((e ? e : 1) - 150);
-    const unsigned long long p0 = m * kLo, c = __umul64hi(m, kLo), mid = m * kHi, p1 = mid + c,
-                             p2 = __umul64hi(m, kHi) + (p1 < mid ? 1u : 0u);
-    unsigned long long lo = 0, hi = 0;      // the words that the shift by r leaves, before its last r % 64 bits
-    if (r >= 0) {
-        const int w = r >> 6;
-        lo = w == 0 ? p0 : w == 1 ? p1 : w == 2 ? p2 : 0;
-        hi = w == 0 ? p1 : w == 1 ? p2 : 0;
-    }
-    const int b = r & 63;
+    const int r = 128 - ((e ? e : 1) - 150);      // 24 and more, for finite f
+    // the product's words: its shift by r leaves those from number r / 64 on
+    unsigned long long p[6] = {m * k0, 0, 0, 0, 0, 0};
+    const unsigned long long mid1 = m * k1, mid2 = m * k2;
+    p[1] = mid1 + __umul64hi(m, k0);
+    p[2] = mid2 + __umul64hi(m, k1) + (p[1] < mid1 ? 1u : 0u);
+    p[3] = __umul64hi(m, k2) + (p[2] < mid2 ? 1u : 0u);
+    const int w = r >> 6, b = r & 63;
+    unsigned long long lo = 0, hi = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+        if (i == w) {
+            lo = p[i];
+            hi = p[i + 1];
+        }
     const unsigned long long u = (lo >> b) | (b ? hi << (64 - b) : 0);
     return bits >> 31 ? 0 - u : u;
 }
