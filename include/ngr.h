@@ -409,10 +409,11 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
  * softmax and sums are FP32, the softmax weights go into their product with v
  * in two parts of `dtype` (the value rounded and what that left out); the order
  * of every sum follows from the lengths alone (the same call gives the same
- * bits).  H / G is at most 9728.  D is a multiple of 8 up to 256, every
- * pointer but lengths, lse and the table 16-byte aligned and every stride a
- * multiple of 8 elements; k and v each reach over 64 GiB at most
- * (NGR_ERR_SHAPE; heads of 8 16 bytes less).  Workspace (256-byte aligned):
+ * bits).  scale is at most 2^127 in size (NGR_ERR_ARG), H / G at most 9728.  D
+ * is a multiple of 8 up to 256, every pointer but lengths, lse and the table
+ * 16-byte aligned and every stride a multiple of 8 elements; k and v each reach
+ * over 64 GiB at most (NGR_ERR_SHAPE; heads of 8 16 bytes less).  Workspace
+ * (256-byte aligned):
  * ngr_paged_attention_workspace_bytes, with capacity = table_pages page_size
  * (one is enough for smaller batches, tables and windows).
  * The lengths stay on the device, so a captured call follows them. */

@@ -350,7 +350,8 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     if (dtype != NGR_F16 && dtype != NGR_BF16) return NGR_ERR_DTYPE;
     int rc = attend_sizes(B, H, G, D);
     if (rc != NGR_OK) return rc;
-    if (!std::isfinite(scale) || window < 0) return NGR_ERR_ARG;
+    const float scale2 = scale * 1.4426950408889634f;      // of exponents of 2
+    if (!std::isfinite(scale2) || window < 0) return NGR_ERR_ARG;
     if (B == 0) return NGR_OK;
     if (!q || !lengths || !out) return NGR_ERR_NULL;
     AttendArgs a;
@@ -394,7 +395,7 @@ int ngr_fused_paged_attention(const void *q, int64_t q_row_stride, int64_t q_hea
     a.lengths = lengths;
     a.out = out;
     a.lse = lse;
-    a.scale2 = scale * 1.4426950408889634f;
+    a.scale2 = scale2;
     a.window = static_cast<int>(std::min(window, kMax31));
     a.B = static_cast<int>(B);
     a.H = static_cast<int>(H);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import normalization_gemm_row_gb300 as pkg
-from test_step_host import SHAPE, attend, cache, passes
+from test_step_host import ARG, SHAPE, attend, cache, passes
 
 UNITS = 1 << 32      # 16-byte units of 64 GiB
 
@@ -47,3 +47,11 @@ def test_the_smallest_heads_end_a_unit_earlier():
     if not torch.cuda.is_available():
         assert passes(call(reaching(UNITS - 2, 8, "k"), 8))
     assert call(reaching(UNITS - 1, 8, "k"), 8) == SHAPE
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scales_whose_exponents_of_2_pass_fp32(sign):
+    """(the kernels' exponentials are of 2: times log2 e, such a scale would be infinite)"""
+    assert attend(scale=sign * 3e38) == ARG and attend(scale=sign * float("inf")) == ARG
+    if not torch.cuda.is_available():
+        assert passes(attend(scale=sign * 2.0 ** 127)) and passes(attend(scale=sign * 1e-45)) and passes(attend(scale=0.0))
