@@ -4,7 +4,7 @@ bound on every error's size, without the single roundings that
 moe_reference.py admits."""
 import torch
 
-from moe_reference import TINY, U, chain as router_chain, normalized
+from moe_reference import TINY, U, case as make_case, chain as router_chain, normalized, separate
 
 FLOOR = {torch.float16: 2.0 ** -28, torch.bfloat16: 2.0 ** -126}
 
@@ -15,10 +15,11 @@ def two_parts(x, dtype):
 
 
 def chain(n):
-    """A sum of n products in FP32, 16 at a time, relative to the sum S of their sizes.  An addition of 16 is off by at
-    most 2^-22 of what it has so far, on average S / 2: n / 16 of them 2^-23 n / 16.  A row's parts of at least sqrt(n /
-    64) steps are joined by as many additions; 16 more for the two columns, tokens' sums and the like."""
-    return (n / 16 + (n / 64) ** 0.5 + 16) * 2.0 ** -23
+    """A sum of n products, relative to the sum S of their sizes.  A matrix instruction adds 16 of them to what is there:
+    it cuts the 17 addends off at 2^-25 of the largest's power of two and their sum at 2^-23, together below 2^-20.5 of
+    the sizes so far, on average of S / 2.  A row's parts of at least sqrt(n / 64) steps are joined by as many rounding
+    additions; 16 more for the two columns, tokens' sums and the like."""
+    return n / 16 * 2.0 ** -21.5 + ((n / 64) ** 0.5 + 16) * 2.0 ** -24
 
 
 def reference(d, top_k, norm=2, eps=1e-5, renormalize=True):
@@ -50,3 +51,30 @@ def reference(d, top_k, norm=2, eps=1e-5, renormalize=True):
         y[m] += h @ wd.t()
         tol[m] += (dh + chain(F * top_k) * h.abs()) @ wd.abs().t()
     return y, order, p, tol + U[dtype] * y.abs() + TINY[dtype], tol_p
+
+
+# (M, K, F, E, top_k): ordinary sizes, widths that end inside a step or off the 16-byte boundary, rows of down's result
+# that many workers share
+CASES = [(5, 256, 192, 8, 2), (6, 64, 40, 33, 5), (32, 61, 45, 5, 3), (7, 65, 63, 6, 2), (4, 1000, 2001, 5, 2), (4, 1001, 500, 5, 2),
+         (19, 130, 2500, 8, 4), (4, 4100, 72, 5, 2), (4, 8200, 40, 5, 2), (29, 40, 6001, 20, 5), (2, 40, 6000, 16, 4)]
+
+
+def case(M, K, F, E, top_k, dtype, norm=2):
+    """Inputs whose last columns weigh the more, so that one that is lost shows: their share of the results is about 8 /
+    sqrt(K) and 8 / sqrt(F) of them."""
+    d = make_case(M, K, F, E, dtype, seed=M + K + F, norm=norm)
+    d["x" if norm == 0 else "gamma"][..., -1] *= 8
+    d["Wd"][..., -1] *= 8
+    return separate(d, top_k, norm)
+
+
+def sparse_case(M, K, F, E, top_k, dtype, norm=2):
+    """Inputs of which three columns of K and of F count, the first, a middle one and the last: nothing averages out, so
+    that a single rounding of a or of h shows."""
+    d = make_case(M, K, F, E, dtype, seed=2 * (M + K + F) + norm, norm=norm)
+    few_k, few_f = ([0, n // 2, n - 1] for n in (K, F))
+    x, wd = torch.zeros_like(d["x"]), torch.zeros_like(d["Wd"])
+    x[:, few_k] = d["x"][:, few_k] * (1.0 if norm else K ** 0.5)
+    wd[..., few_f] = d["Wd"][..., few_f]
+    d["x"], d["Wd"] = x, wd
+    return separate(d, top_k, norm)

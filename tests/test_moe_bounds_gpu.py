@@ -38,3 +38,17 @@ def test_fp16_values_beyond_the_ends_of_its_range(M, K, F, E, top_k):
             d["Wr"] = (d["Wr"].double() * 500).to(F16)
             d = R.separate(d, top_k, norm)
         check(d, top_k, norm, str(by))
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("norm", [0, 1, 2])
+@pytest.mark.parametrize("M,K,F,E,top_k", B.CASES)
+def test_every_column_counts(M, K, F, E, top_k, norm, dtype):
+    check(B.case(M, K, F, E, top_k, dtype, norm), top_k, norm)
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("norm", [0, 2])
+@pytest.mark.parametrize("M,K,F,E,top_k", B.CASES)
+def test_both_parts_count(M, K, F, E, top_k, norm, dtype):
+    check(B.sparse_case(M, K, F, E, top_k, dtype, norm), top_k, norm)
