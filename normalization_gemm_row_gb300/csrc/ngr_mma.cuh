@@ -127,6 +127,15 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi)
     const __half2 v = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&v);
 }
+// The same, cut off toward zero.
+template <bool BF16>
+__device__ __forceinline__ uint32_t cut16(float lo, float hi)
+{
+    if (BF16) return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 template <bool BF16>
 __device__ __forceinline__ float2 unpack16(uint32_t v)
 {

@@ -56,7 +56,34 @@ def test_many_small_weights_in_fp16(n, at, rows, score, D):
 @pytest.mark.parametrize("dtype", [F16, BF16])
 @pytest.mark.parametrize("D", [64, 80, 256])
 def test_equal_weights_between_two_steps(n, at, rows, dtype, D):
-    """Weights of the other tokens that are all half a step above a power of two (a little less): two parts hold them,
-    each off by half a step of half a step; one part would take their sum half a step down."""
+    """Weights of the other tokens that are all half a step above a power of two (a little less): two parts hold them;
+    one part would take their sum half a step down."""
     score = -math.log((1 + 0.98 * R.U[dtype]) / 32)
-    one_and_many(n, at, D, score, dtype, rows, R.U[dtype] ** 2, f"{n} tokens")
+    one_and_many(n, at, D, score, dtype, rows, B.two_parts(dtype), f"{n} tokens")
+
+
+@pytest.mark.parametrize("lengths", [[100, 33], [3000, 1] + [200] * 150, [90000]])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("D", [64, 80, 256])
+def test_infinite_values(lengths, dtype, D):
+    """An infinite value is its dimension's result, for every head and whatever the token's weight; both signs are NaN;
+    the other dimensions are as they were."""
+    g = R.generator(D)
+    table, pages = R.pages_for(lengths, 16, g)
+    k, v = R.cache_like(pages, 16, 2, D, dtype, "tokens", g)
+    q = torch.randn((len(lengths), 8, D), generator=g).to(dtype)
+    n = torch.tensor(lengths, dtype=torch.int32)
+    want = R.attention(q, k, v, table, n, D ** -0.5)
+    wild = [3, 17, 40]
+    for b, size in enumerate(lengths):
+        for at in {0, size // 3, size - 1}:
+            page = table[b, at // 16]
+            v[page, at % 16, :, 3] = float("inf")
+            v[page, at % 16, :, 17] = -float("inf")
+            v[page, at % 16, :, 40] = float("inf") if at else -float("inf")
+    out = ngr.fused_paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), n.cuda()).cpu()
+    assert (out[..., 3] == float("inf")).all() and (out[..., 17] == -float("inf")).all()
+    several = n > 3
+    assert torch.isnan(out[several][..., 40]).all()
+    tame = [d for d in range(D) if d not in wild]
+    assert ((out.double() - want[0]).abs() <= want[2])[..., tame].all()
