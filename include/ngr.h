@@ -439,7 +439,7 @@ size_t ngr_paged_attention_workspace_bytes(int64_t B, int64_t H, int64_t G,
  * x and y are [M, K], Wr [E, K], Wg and Wu [E, F, K], Wd [E, K, F]; norm,
  * gamma, beta and eps as in ngr_fused_norm_swiglu.  The choice is returned in
  * experts (int32 [M, top_k], largest first) and weights (FP32 [M, top_k]) when
- * they are not NULL.  The router works in FP32 throughout; the experts'
+ * they are not NULL (apart from one another, x and y: NGR_ERR_ARG otherwise).  The router works in FP32 throughout; the experts'
  * products take a, and p times the gated product, in two parts of `dtype` (the
  * value rounded and what that left out; in fp16 up to 2^24 in size and to 2^-28
  * near 0), and accumulate in FP32; y is rounded once.  Only chosen experts'

@@ -24,6 +24,12 @@ static_assert(NGR_MOE_MAX_M == kMoeMaxTokens && NGR_MOE_MAX_EXPERTS == kMoeMaxEx
 constexpr int64_t kMoeManyExperts = 64, kMoeFewTokens = 9;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+// Whether two arrays share no byte (a null one does not).
+bool apart(const void *p, size_t p_bytes, const void *q, size_t q_bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return !p || !q || a + p_bytes <= b || b + q_bytes <= a;
+}
 int64_t up_to(int64_t v, int64_t n) { return (v + n - 1) / n * n; }
 
 int moe_sizes(int64_t M, int64_t K, int64_t F, int64_t E, int64_t top_k)
@@ -94,6 +100,12 @@ int ngr_fused_moe_swiglu(int norm, const void *x, const void *gamma, const void 
     for (const void *p : {x, gamma, beta, Wr, Wg, Wu, Wd, static_cast<const void *>(y)})
         if (!aligned(p, 2)) return NGR_ERR_ALIGN;
     if (!aligned(experts, 4) || !aligned(weights, 4)) return NGR_ERR_ALIGN;
+    // x is read to its end before y is written, but while the choice is; what
+    // is returned is apart from one another.
+    const size_t rows = static_cast<size_t>(M * K) * 2, choices = static_cast<size_t>(M * top_k) * 4;
+    if (!apart(experts, choices, x, rows) || !apart(weights, choices, x, rows) || !apart(experts, choices, y, rows) ||
+        !apart(weights, choices, y, rows) || !apart(experts, choices, weights, choices))
+        return NGR_ERR_ARG;
     const MoePlan p = moe_plan(M, K, F, E, top_k);
     if (!workspace || workspace_bytes < p.total) return NGR_ERR_WORKSPACE;
     if (!aligned(workspace, 256)) return NGR_ERR_ALIGN;

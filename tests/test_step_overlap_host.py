@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import normalization_gemm_row_gb300 as pkg
-from test_step_host import A, ARG, OTHER, append, attend, cache, passes
+from test_step_host import A, ARG, OTHER, append, attend, cache, moe, passes
 
 FAR = 0x40000000
 
@@ -84,3 +84,18 @@ def test_append_refuses_rotated_queries_over_inputs_or_themselves(kw):
     dict(q=FAR, q_head=128, q_token=1024, q_out=FAR + HEAD, q_out_head=128, q_out_token=1024)])
 def test_append_takes_rotated_queries_apart(kw):
     assert passes(append(**kw))
+
+
+# The experts' layer of test_step_host: 4 tokens of 64 elements (512 bytes), 2 choices each (32 bytes).
+@pytest.mark.parametrize("kw", [
+    dict(experts=A), dict(weights=A), dict(experts=A + 508), dict(weights=A - 28), dict(y=OTHER, experts=OTHER + 4),
+    dict(y=OTHER, weights=OTHER), dict(y=OTHER, experts=A + 4), dict(experts=OTHER, weights=OTHER), dict(experts=OTHER, weights=OTHER + 28)])
+def test_experts_refuse_a_choice_over_rows_or_weights(kw):
+    assert moe(**kw) == ARG
+
+
+@host_only
+@pytest.mark.parametrize("kw", [
+    dict(experts=A + 512), dict(weights=A - 32), dict(experts=OTHER, weights=OTHER + 32), dict(weights=OTHER), dict(y=A + 16, experts=OTHER)])
+def test_experts_take_a_choice_apart(kw):
+    assert passes(moe(**kw))
