@@ -400,11 +400,12 @@ int ngr_fused_rope_append_kv(const void *q, int64_t q_token_stride,
  * uses key head h / (H / G); H is a multiple of G.  q is [B, H, D] by its row
  * and head strides in elements, out [B, H, D] dense (q's own memory, if q is
  * dense too, or apart from it: NGR_ERR_ARG otherwise), lse FP32 [B, H], apart
- * from both, or NULL (it joins results over parts of a context).  lengths[b] = 0 gives out = 0 and lse = -inf, and so do
- * scores that are all -inf; a negative length is a row that is not in use,
- * whose out and lse are left as they were.  A length beyond table_pages page_size counts
- * as that, a page that is not there as if its tokens were not, and either is
- * reported by the workspace's error word as NGR_ERR_ARG.  What the cache holds
+ * from both, or NULL (it joins results over parts of a context).
+ * lengths[b] = 0 gives out = 0 and lse = -inf, and so do scores that are all
+ * -inf; a negative length is a row that is not in use, whose out and lse are
+ * left as they were.  A length beyond table_pages page_size counts as that, a
+ * page that is not there as if its tokens were not, and either is reported by
+ * the workspace's error word as NGR_ERR_ARG.  What the cache holds
  * beside the sequences' tokens is not looked at (it may be NaN).  Scores,
  * softmax and sums are FP32, the softmax weights go into their product with v
  * in two parts of `dtype` (the value rounded and what that left out); the order

@@ -669,8 +669,9 @@ def _scratch(nbytes, device, workspace):
 def check_workspace(workspace, stream=None):
     """Wait for ``stream`` (by default the current one of the workspace's
     device) and raise NgrError if a kernel of the last call with this
-    workspace reported an error: a target outside the vocabulary, or a wait
-    that ran out.  The report is cleared."""
+    workspace reported an error: a target outside the vocabulary, a page,
+    position or table row that is not there, or a wait that ran out.  The
+    report is cleared."""
     if not workspace.is_cuda:
         raise ValueError("the workspace must be a CUDA tensor")
     handle = _stream(stream) if stream is not None else _current_stream_handle(workspace.get_device())
@@ -916,10 +917,10 @@ def fused_rope_append_kv(q, k, v, k_cache, v_cache, block_table, positions, rows
     table.  inv_freq, float32 [rot / 2], gives the angles (None: no rotation);
     the first rot dimensions are turned in pairs (i, i + rot / 2), or (2i, 2i +
     1) with ``interleaved``.  A token with a negative position is left out,
-    its row of q_out and its slot included.  One whose row, position or page
-    is not there is left out as well; only the GPU sees it: to learn of it
-    pass a ``workspace`` (256 bytes) and ask ``check_workspace``, or set
-    NGR_DEBUG=1."""
+    its slot and its row of q_out included (which is undefined where q_out is
+    not given).  One whose row, position or page is not there is left out as
+    well; only the GPU sees it: to learn of it pass a ``workspace`` (256 bytes)
+    and ask ``check_workspace``, or set NGR_DEBUG=1."""
     dtype, index = k.dtype, k.get_device()
     code = _CODES[dtype] if dtype in _CODES else _dtype_code(k)
     cache, G, D, _ = _kv_cache(dtype, index, k_cache, v_cache, block_table)
@@ -987,7 +988,7 @@ def fused_paged_attention(q, k_cache, v_cache, block_table, lengths, scale=None,
     ``out`` may be q itself.
 
     A length of 0 gives 0 and -inf; a row with a negative length is left as it
-    was (in ``out`` and ``lse`` when given).  A length beyond the table, or a
+    was in ``out`` and ``lse`` (and is undefined where they are not given).  A length beyond the table, or a
     page that is not there, is seen by the GPU alone, which leaves those tokens
     out: pass a ``workspace`` and ask ``check_workspace``, or set NGR_DEBUG=1."""
     dtype, index = q.dtype, q.get_device()

@@ -19,18 +19,23 @@
 // (and block of 16 query heads where there are more).  A batch of any lengths
 // is balanced so, and nothing but the device has to know the lengths; and what
 // is read at a time lies together: the heads of a token share lines of L2 (64
-// rows of 8000 tokens, 8 key heads of 80: 213 us; with the items' tiles in one
-// row, head after head, 329, as much as with 128 dimensions).  An item (a sequence and key head) that lies in one run is
-// finished there; the others' parts (FP32 sums, maximum, sum of exponentials)
-// are joined by a second kernel in the tokens' order, so a call repeated gives
-// the same bits.
+// rows of 8000 tokens, 8 key heads of 80: 215 us; with the items' tiles in one
+// row, head after head, 329, as much as with 128 dimensions).  An item (a
+// sequence and key head) that lies in one run is finished there; the others'
+// parts (FP32 sums, maximum, sum of exponentials) are joined by a second kernel
+// in the tokens' order, so a call repeated gives the same bits.
 //
 // Few items of short contexts take a CTA each ("solo"): its warps share the
 // item's tiles and join their parts in shared memory, without a second launch.
 //
-// bf16, 64 query heads on 8 of 128: 64 rows of 2048 to 8192 tokens 212 us (6.3
-// TB/s), one of 131072 tokens 94 us (5.7 TB/s, of which 7 are the join), one
-// of 1000 tokens 12.5 us.
+// Scores, maxima, exponentials and sums are FP32.  A softmax weight goes into
+// its product with v in two parts of the inputs' type, and a tile's products
+// are added to the sums by rounding additions, not by the instruction's own
+// long chain.
+//
+// bf16, 64 query heads on 8 of 128: 64 rows of 2048 to 8192 tokens 213 us (6.3
+// TB/s), one of 131072 tokens 95 us (5.6 TB/s, of which 7 are the join), one
+// of 1000 tokens 14 us.
 #pragma once
 
 #include "ngr.h"

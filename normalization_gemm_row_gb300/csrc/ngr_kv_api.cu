@@ -148,8 +148,11 @@ bool apart(const Places &a, const Places &b)
 // launch and nothing to join.  64 query heads on 8 of 128, alone against
 // split, memory's caches flushed: one row of 1000 tokens 16.5 us (split 17.5),
 // of 2040 21.7 (17.5); 12 rows of 4000 49 (56), 16 of 2040 36 (46), 16 of
-// 4000 61 (71); 16 of 400 to 4000 44 (46).  The longest row sets the time
-// (one of 8000 tokens 54 us, split 24), so the longest tables stay split.
+// 4000 61 (71); 16 of 400 to 4000 44 (46); 16 of 100 11 (17).  The longest row
+// sets the time, and only the table's room is known here, not the lengths: one
+// row of 2000 among 15 of 100 25 us (split 19), of 4000 37.5 (23), of 1500
+// among 7 of 50 21 (19).  With longer tables that would cost more than even
+// batches gain (one of 8000 tokens 54 us, split 24): they stay split.
 constexpr int64_t kSoloTiles = 6, kSoloItems = 6;
 
 struct AttendPlan {
