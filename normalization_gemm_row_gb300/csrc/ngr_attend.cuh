@@ -535,10 +535,11 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
             // tokens of equal scores have weights that are all off alike, by
             // up to half a step, which the sum of the unrounded ones does not
             // have: as much again as the output's own rounding.)  The second
-            // part's last bit is set, so that both are above 0 and an infinite
-            // value gives its infinity, not one minus another or times 0.
-            // Together they are off by at most 3 x 2^-15 of the weight (fp16 3
-            // x 2^-21, or 3 x 2^-40 of the largest where its steps end).
+            // part's last bit is set where the first is not 0, so that both are
+            // above 0 and an infinite value gives its infinity, not one minus
+            // another or times 0.  Together they are off by at most 3 x 2^-15
+            // of the weight (fp16 3 x 2^-21, or 3 x 2^-40 of the largest where
+            // its steps end); a weight of 0 is 0.
             uint32_t p[2][NB][2];
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(32 * attend_warps(DP, NB), 1) attend_kernel(co
                     const uint32_t high = cut16<BF16>(z[n][2 * h], z[n][2 * h + 1]);
                     const float2 v = unpack16<BF16>(high);
                     p[0][n][h] = transpose8(high);
-                    p[1][n][h] = transpose8(pack16<BF16>(z[n][2 * h] - v.x, z[n][2 * h + 1] - v.y) | 0x10001u);
+                    p[1][n][h] = transpose8(pack16<BF16>(z[n][2 * h] - v.x, z[n][2 * h + 1] - v.y) | __vminu2(high, 0x10001u));
                 }
             }
             cp_async_wait<S - 1>();

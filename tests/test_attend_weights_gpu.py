@@ -87,3 +87,29 @@ def test_infinite_values(lengths, dtype, D):
     assert torch.isnan(out[several][..., 40]).all()
     tame = [d for d in range(D) if d not in wild]
     assert ((out.double() - want[0]).abs() <= want[2])[..., tame].all()
+
+
+@pytest.mark.parametrize("n,rows", [(1000, 2), (8192, 2600), (60000, 1)])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("far", ["infinitely", "beyond the smallest weight"])
+def test_tokens_without_weight_have_none(n, rows, dtype, far):
+    """Keys whose score is -inf, or 100 below the others', with fp16's largest values: nothing of them counts."""
+    page, D = 64, 64
+    pages = -(-n // page)
+    k = torch.zeros((pages, page, 1, D), dtype=dtype)
+    k[..., 0] = -float("inf") if far == "infinitely" else -100
+    v = torch.full((pages, page, 1, D), 65504.0, dtype=dtype)
+    few = torch.linspace(0.5, 2, D).to(dtype)
+    for at in (0, n // 3, n - 1):
+        k[at // page, at % page, 0, 0] = 0
+        v[at // page, at % page, 0] = few
+    q = torch.zeros((rows, 2, D), dtype=dtype)
+    q[..., 0] = 1
+    table = torch.arange(pages, dtype=torch.int32).repeat(rows, 1)
+    lengths = torch.full((rows,), n, dtype=torch.int32)
+    out, lse = ngr.fused_paged_attention(q.cuda(), k.cuda(), v.cuda(), table.cuda(), lengths.cuda(), scale=1.0, return_lse=True)
+    # three weights of 1, each off by 3 x 2^-15 (fp16 2^-21) at most and alike, whose sum is divided by 3 and rounded
+    # (e^-100 x 65504 x n is below 1e-33)
+    want = few.double()
+    assert ((out.double().cpu() - want).abs() <= (R.U[dtype] + B.two_parts(dtype) + 2.0 ** -21) * want).all()
+    assert ((lse.cpu() - math.log(3)).abs() <= 2.0 ** -20).all()
